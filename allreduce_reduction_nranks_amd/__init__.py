@@ -12,6 +12,7 @@ raises -- there is no fallback path.
 """
 from __future__ import annotations
 
+import builtins
 import ctypes
 import os
 import threading
@@ -58,6 +59,7 @@ def load_library() -> ctypes.CDLL:
             raise RuntimeError("libmrr.so is not built (%s); run __graft_entry__.build()" % LIB_PATH)
         L = ctypes.CDLL(LIB_PATH)
         vp, sz, i, u32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_uint32
+        f32 = ctypes.c_float
         pp = ctypes.POINTER(vp)
         sigs = {
             "mrr_allreduce_rsag": ([pp, pp, sz, i, i, vp], i),
@@ -80,6 +82,9 @@ def load_library() -> ctypes.CDLL:
             "mrr_fp8b15_to_f32": ([vp, vp, sz, vp], i),
             "mrr_f16_to_fp8b15": ([vp, vp, sz, vp], i),
             "mrr_f32_to_fp8b15": ([vp, vp, sz, vp], i),
+            "mrr_layernorm_fwd": ([pp, i, vp, vp, vp, vp, vp, vp, vp, sz, sz, sz, sz, f32, i, i, vp], i),
+            "mrr_layernorm_bwd_workspace_bytes": ([sz, sz], sz),
+            "mrr_layernorm_bwd": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, sz, sz, sz, i, i, vp, sz, vp], i),
             "mrr_stream_copy": ([vp, vp, sz, vp], i),
             "mrr_rank_buffer_pitch": ([sz, i], sz),
             "mrr_status_string": ([i], ctypes.c_char_p),
@@ -377,6 +382,88 @@ def mrr_f16_to_fp8b15(src, dst, n, stream=None) -> int:
 def mrr_f32_to_fp8b15(src, dst, n, stream=None) -> int:
     _codec_room(src, 4, dst, 1, n)
     return load_library().mrr_f32_to_fp8b15(_ptr(src), _ptr(dst), n, _stream(stream))
+
+
+def _matrix_bytes(rows, cols, ld, esize) -> int:
+    """Bytes from the first element to the last of rows x cols elements, rows ld apart."""
+    return ((rows - 1) * ld + cols) * esize if rows > 0 and cols > 0 else 0
+
+
+def _span(x) -> int:
+    """Bytes from a tensor's first element to its last, strides counted."""
+    if x.is_contiguous():
+        return x.nbytes
+    if x.numel() == 0:
+        return 0
+    return (1 + builtins.sum((n - 1) * s for n, s in zip(x.shape, x.stride()))) * x.element_size()
+
+
+def _rows_room(x, nbytes: int, what: str) -> None:
+    """_room() for an argument whose rows may lie apart: a view of a wider tensor
+    counts with its strides."""
+    if x is not None and not isinstance(x, int) and x.nbytes < nbytes and _span(x) < nbytes:
+        raise ValueError("%s spans %d bytes, the call needs %d" % (what, _span(x), nbytes))
+
+
+def _rows_ptrs(xs, n: int, nbytes, what: str):
+    """_rank_ptrs() for per-rank matrices; nbytes[r] is what entry r has to span."""
+    if xs is None:
+        return None
+    if len(xs) < n:
+        raise ValueError("%s has %d entries, nranks is %d" % (what, len(xs), n))
+    for r in range(n):
+        if xs[r] is not None and type(xs[r]) is not int and xs[r].nbytes < nbytes[r]:
+            _rows_room(xs[r], nbytes[r], "%s[%d]" % (what, r))
+    return (_VP * len(xs))(*[_ptr(x) for x in xs])
+
+
+def _wtype(dtype, wdtype) -> int:
+    w = _dt(wdtype)
+    return _dt(dtype) if w == MRR_AUTO else w
+
+
+def mrr_layernorm_fwd(inputs, nranks, residual, weight, bias, sum, out, mean, rstd, rows, cols,
+                      ld_in, ld_out, eps, dtype, wdtype="auto", stream=None) -> int:
+    t, tw = _dt(dtype), _wtype(dtype, wdtype)
+    nin, nout = (_matrix_bytes(rows, cols, ld, _ESIZE.get(t, 0)) for ld in (ld_in, ld_out))
+    wb = cols * _ESIZE.get(tw, 0)
+    _rows_room(residual, nin, "residual")
+    _room(weight, wb, "weight")
+    _room(bias, wb, "bias")
+    _rows_room(sum, nout, "sum")
+    _rows_room(out, nout, "out")
+    _room(mean, 4 * rows, "mean")
+    _room(rstd, 4 * rows, "rstd")
+    return load_library().mrr_layernorm_fwd(
+        _rows_ptrs(inputs, nranks, [nin] * max(0, nranks), "inputs"), nranks, _ptr(residual), _ptr(weight), _ptr(bias),
+        _ptr(sum), _ptr(out), _ptr(mean), _ptr(rstd), rows, cols, ld_in, ld_out, eps, t, tw,
+        _stream(stream))
+
+
+def mrr_layernorm_bwd_workspace_bytes(rows, cols) -> int:
+    return load_library().mrr_layernorm_bwd_workspace_bytes(rows, cols)
+
+
+def mrr_layernorm_bwd(dout, sum, weight, mean, rstd, dresidual, dsum, dweight, dbias, rows, cols,
+                      ld_in, ld_out, dtype, wdtype="auto", workspace=None, workspace_bytes=0,
+                      stream=None) -> int:
+    t, tw = _dt(dtype), _wtype(dtype, wdtype)
+    nin, nout = (_matrix_bytes(rows, cols, ld, _ESIZE.get(t, 0)) for ld in (ld_in, ld_out))
+    wb = cols * _ESIZE.get(tw, 0)
+    _rows_room(dout, nin, "dout")
+    _rows_room(sum, nin, "sum")
+    _room(weight, wb, "weight")
+    _room(mean, 4 * rows, "mean")
+    _room(rstd, 4 * rows, "rstd")
+    _rows_room(dresidual, nin, "dresidual")
+    _rows_room(dsum, nout, "dsum")
+    _room(dweight, wb, "dweight")
+    _room(dbias, wb, "dbias")
+    _room(workspace, workspace_bytes, "workspace")
+    return load_library().mrr_layernorm_bwd(
+        _ptr(dout), _ptr(sum), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dresidual), _ptr(dsum),
+        _ptr(dweight), _ptr(dbias), rows, cols, ld_in, ld_out, t, tw, _ptr(workspace),
+        workspace_bytes, _stream(stream))
 
 
 def mrr_stream_copy(src, dst, nbytes, stream=None) -> int:

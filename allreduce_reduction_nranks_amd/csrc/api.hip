@@ -9,6 +9,7 @@
 
 #include "mrr_device.hpp"
 #include "mrr_internal.hpp"
+#include "mrr_ops.hpp"
 
 namespace mrr {
 
@@ -240,6 +241,67 @@ namespace mrr {
 hipError_t launch_stream_copy(const void* src, void* dst, size_t nbytes, hipStream_t stream);
 }  // namespace mrr
 
+namespace mrr {
+// ---------------------------------------------------------------------------
+// Operators on rows: shared checks.
+// ---------------------------------------------------------------------------
+constexpr size_t kMaxRows = (size_t)1 << 31;
+constexpr size_t kMaxCols = (size_t)1 << 20;
+constexpr size_t kMaxLd = (size_t)1 << 31;
+
+static bool float_type(int t) { return t == kF32 || t == kF16 || t == kBF16; }
+
+// A matrix that a call reads or writes: `rows` rows of `width` bytes, `pitch`
+// bytes apart.  Null or empty: absent.
+struct Mat {
+  const void* p;
+  size_t rows, width, pitch;
+  Range range() const {
+    return {(uintptr_t)p, (uintptr_t)p + (p && rows && width ? (rows - 1) * pitch + width : 0)};
+  }
+};
+
+static Mat vec(const void* p, size_t bytes) { return {p, 1, bytes, bytes}; }
+
+// Two matrices of one pitch whose rows lie side by side (columns of one wider
+// buffer) share no byte although their ranges overlap.
+static bool overlaps(const Mat& a, const Mat& b) {
+  const Range x = a.range(), y = b.range();
+  if (x.lo == x.hi || y.lo == y.hi || !overlaps(x, y)) return false;
+  if (a.pitch != b.pitch || a.rows < 2 || b.rows < 2) return true;
+  const uintptr_t d = (y.lo >= x.lo ? y.lo - x.lo : a.pitch - (x.lo - y.lo) % a.pitch) % a.pitch;
+  return d < a.width || a.pitch - d < b.width;
+}
+
+static bool same(const Mat& a, const Mat& b) {
+  return a.p == b.p && a.rows == b.rows && a.width == b.width && (a.pitch == b.pitch || a.rows < 2);
+}
+
+// An output may be exactly one of the first `in_place` inputs; any other
+// overlap with an input or another output is refused.
+static bool bad_overlap(const Mat* ins, int nin, int in_place, const Mat* outs, int nout) {
+  for (int k = 0; k < nout; ++k) {
+    for (int i = 0; i < nin; ++i)
+      if (overlaps(outs[k], ins[i]) && !(i < in_place && same(outs[k], ins[i]))) return true;
+    for (int j = 0; j < k; ++j)
+      if (overlaps(outs[k], outs[j])) return true;
+  }
+  return false;
+}
+
+// Types and sizes of a layer norm call; MRR_OK, or the refusal.
+static mrr_status norm_shape(const char* fn, size_t rows, size_t cols, size_t ld_in, size_t ld_out,
+                             int t, int* tw) {
+  if (*tw == MRR_AUTO) *tw = t;
+  if (!float_type(t) || (*tw != t && *tw != kF32)) return refuse(MRR_EUNSUPPORTED, fn, "type");
+  if (cols == 0 || cols > kMaxCols) return refuse(MRR_EINVAL, fn, "cols out of range");
+  if (rows > kMaxRows) return refuse(MRR_EINVAL, fn, "rows out of range");
+  if (ld_in < cols || ld_in > kMaxLd || ld_out < cols || ld_out > kMaxLd)
+    return refuse(MRR_EINVAL, fn, "row stride out of range");
+  return MRR_OK;
+}
+}  // namespace mrr
+
 using namespace mrr;
 
 extern "C" {
@@ -251,7 +313,7 @@ const char* mrr_status_string(mrr_status s) {
     case MRR_EUNSUPPORTED: return "MRR_EUNSUPPORTED: rank count or type combination not supported";
     case MRR_EALIGN: return "MRR_EALIGN: pointer misaligned";
     case MRR_EOVERLAP: return "MRR_EOVERLAP: output overlaps another buffer";
-    case MRR_ESCRATCH: return "MRR_ESCRATCH: packet scratch too small";
+    case MRR_ESCRATCH: return "MRR_ESCRATCH: scratch or workspace too small";
     case MRR_ETIMEDOUT: return "MRR_ETIMEDOUT: packet poll exceeded max_spins";
     case MRR_EHIP: return "MRR_EHIP: HIP runtime error";
   }
@@ -752,6 +814,110 @@ mrr_status mrr_f16_to_fp8b15(const uint16_t* in, uint8_t* out, size_t n, void* s
 }
 mrr_status mrr_f32_to_fp8b15(const float* in, uint8_t* out, size_t n, void* stream) {
   return codec(3, in, 4, out, 1, n, stream, "mrr_f32_to_fp8b15");
+}
+
+mrr_status mrr_layernorm_fwd(const void* const* inputs, int nranks, const void* residual,
+                             const void* weight, const void* bias, void* sum, void* out,
+                             float* mean, float* rstd, size_t rows, size_t cols, size_t ld_in,
+                             size_t ld_out, float eps, mrr_dtype dtype, mrr_dtype wdtype,
+                             void* stream) {
+  static const char* fn = "mrr_layernorm_fwd";
+  const int t = dtype;
+  int tw = wdtype;
+  if (nranks < 1 || nranks > kMaxRanks) return refuse(MRR_EUNSUPPORTED, fn, "nranks out of range");
+  if (mrr_status st = norm_shape(fn, rows, cols, ld_in, ld_out, t, &tw)) return st;
+  if (!(eps >= 0.0f)) return refuse(MRR_EINVAL, fn, "eps");
+  if (rows == 0) return MRR_OK;
+  if (!inputs || !out) return refuse(MRR_EINVAL, fn, "null pointer");
+  NormFwdArgs a{};
+  const size_t e = tsize(t), ew = tsize(tw);
+  Mat ins[kMaxRanks + 3];
+  int nin = 0;
+  for (int r = 0; r < nranks; ++r) {
+    if (!inputs[r]) return refuse(MRR_EINVAL, fn, "null rank pointer");
+    if (!aligned(inputs[r], e)) return refuse(MRR_EALIGN, fn, "element alignment");
+    a.in[r] = inputs[r];
+    ins[nin++] = {inputs[r], rows, cols * e, ld_in * e};
+  }
+  ins[nin++] = {residual, rows, cols * e, ld_in * e};
+  const int in_place = nin;
+  ins[nin++] = vec(weight, cols * ew);
+  ins[nin++] = vec(bias, cols * ew);
+  const Mat outs[4] = {{sum, rows, cols * e, ld_out * e}, {out, rows, cols * e, ld_out * e},
+                       vec(mean, rows * 4), vec(rstd, rows * 4)};
+  if (!aligned(residual, e) || !aligned(sum, e) || !aligned(out, e) || !aligned(weight, ew) ||
+      !aligned(bias, ew) || !aligned(mean, 4) || !aligned(rstd, 4))
+    return refuse(MRR_EALIGN, fn, "element alignment");
+  if (bad_overlap(ins, nin, in_place, outs, 4)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
+  a.residual = residual;
+  a.weight = weight;
+  a.bias = bias;
+  a.sum = sum;
+  a.out = out;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.rows = rows;
+  a.ld_in = ld_in;
+  a.ld_out = ld_out;
+  a.cols = (uint32_t)cols;
+  a.nranks = nranks;
+  a.eps = eps;
+  a.wf32 = tw == kF32;
+  return hip_status(launch_norm_fwd(a, t, (hipStream_t)stream), fn);
+}
+
+size_t mrr_layernorm_bwd_workspace_bytes(size_t rows, size_t cols) {
+  if (cols == 0 || cols > kMaxCols || rows > kMaxRows) return 0;
+  return (size_t)norm_bwd_groups(rows, (uint32_t)cols) * 2 * cols * sizeof(float);
+}
+
+mrr_status mrr_layernorm_bwd(const void* dout, const void* sum, const void* weight,
+                             const float* mean, const float* rstd, const void* dresidual,
+                             void* dsum, void* dweight, void* dbias, size_t rows, size_t cols,
+                             size_t ld_in, size_t ld_out, mrr_dtype dtype, mrr_dtype wdtype,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  static const char* fn = "mrr_layernorm_bwd";
+  const int t = dtype;
+  int tw = wdtype;
+  if (mrr_status st = norm_shape(fn, rows, cols, ld_in, ld_out, t, &tw)) return st;
+  if (!dsum && !dweight && !dbias) return refuse(MRR_EINVAL, fn, "no output");
+  const bool params = dweight || dbias;
+  if (rows == 0 && !params) return MRR_OK;
+  if (rows && (!dout || !sum || !mean || !rstd)) return refuse(MRR_EINVAL, fn, "null pointer");
+  const size_t e = tsize(t), ew = tsize(tw), need = mrr_layernorm_bwd_workspace_bytes(rows, cols);
+  const Mat x{nullptr, rows, cols * e, ld_in * e};
+  const Mat ins[6] = {{dout, x.rows, x.width, x.pitch}, {sum, x.rows, x.width, x.pitch},
+                      {dresidual, x.rows, x.width, x.pitch}, vec(weight, cols * ew),
+                      vec(mean, rows * 4), vec(rstd, rows * 4)};
+  const Mat outs[4] = {{dsum, rows, cols * e, ld_out * e}, vec(dweight, cols * ew), vec(dbias, cols * ew),
+                       vec(params ? workspace : nullptr, need)};
+  if (!aligned(dout, e) || !aligned(sum, e) || !aligned(dresidual, e) || !aligned(dsum, e) ||
+      !aligned(weight, ew) || !aligned(dweight, ew) || !aligned(dbias, ew) || !aligned(mean, 4) ||
+      !aligned(rstd, 4))
+    return refuse(MRR_EALIGN, fn, "element alignment");
+  if (params && need) {
+    if (!workspace) return refuse(MRR_EINVAL, fn, "null workspace");
+    if (!aligned(workspace, 16)) return refuse(MRR_EALIGN, fn, "workspace 16 bytes");
+    if (workspace_bytes < need) return refuse(MRR_ESCRATCH, fn, "workspace too small");
+  }
+  if (bad_overlap(ins, 6, 3, outs, 4)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
+  NormBwdArgs a{};
+  a.dout = dout;
+  a.sum = sum;
+  a.weight = weight;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.dresidual = dresidual;
+  a.dsum = dsum;
+  a.dweight = dweight;
+  a.dbias = dbias;
+  a.partial = (float*)workspace;
+  a.rows = rows;
+  a.ld_in = ld_in;
+  a.ld_out = ld_out;
+  a.cols = (uint32_t)cols;
+  a.wf32 = tw == kF32;
+  return hip_status(launch_norm_bwd(a, t, (hipStream_t)stream), fn);
 }
 
 mrr_status mrr_stream_copy(const void* src, void* dst, size_t nbytes, void* stream) {

@@ -70,7 +70,7 @@ typedef enum mrr_status {
   MRR_EUNSUPPORTED = 2, /* rank count or type combination not provided */
   MRR_EALIGN = 3,       /* a pointer not aligned as the entry point requires */
   MRR_EOVERLAP = 4,     /* an output overlaps another buffer other than its own input */
-  MRR_ESCRATCH = 5,     /* packet scratch smaller than mrr_packet_scratch_bytes() */
+  MRR_ESCRATCH = 5,     /* scratch or workspace smaller than its _bytes() function says */
   MRR_ETIMEDOUT = 6,    /* (device error word only) a packet poll exceeded max_spins */
   MRR_EHIP = 7          /* the HIP runtime refused the launch */
 } mrr_status;
@@ -401,6 +401,69 @@ mrr_status mrr_fp8b15_to_f16(const uint8_t* in, uint16_t* out, size_t n, void* s
 mrr_status mrr_fp8b15_to_f32(const uint8_t* in, float* out, size_t n, void* stream);
 mrr_status mrr_f16_to_fp8b15(const uint16_t* in, uint8_t* out, size_t n, void* stream);
 mrr_status mrr_f32_to_fp8b15(const float* in, uint8_t* out, size_t n, void* stream);
+
+/* --------------------------------------------------------------------------
+ * Layer norm of a rank sum: what consumes the N partial results of a
+ * row-parallel product, with the residual of the layer.
+ *
+ *   h[i][c]  = round_dtype( x_0 + x_1 + ... + x_{nranks-1} + residual )
+ *   y[i][c]  = round_dtype( (h - mean_i) * rstd_i * weight[c] + bias[c] )
+ *   mean_i = mean over c of h[i][c]; rstd_i = 1 / sqrt(var_i + eps), var_i the
+ *   mean of (h - mean_i)^2 (biased)
+ * summed in rank order in f32, the residual last; statistics in f32, of the
+ * rounded h.
+ *
+ * inputs:    host array of nranks (1..32) device pointers to rows x cols
+ *            elements of dtype (F32 | F16 | BF16), rows ld_in elements apart;
+ *            they may overlap each other.
+ * residual:  as an input; NULL = none.
+ * weight, bias: cols elements of wdtype: F32, or the data type (AUTO);
+ *            NULL = 1 and 0.
+ * sum:       receives h, rows ld_out elements apart; NULL = not stored.
+ * out:       receives y, rows ld_out elements apart.
+ * mean, rstd: receive rows f32 values each; NULL = not stored.
+ * sum and out may each be exactly one of the inputs or the residual, when
+ * ld_in == ld_out; any other overlap of an output gives MRR_EOVERLAP.
+ * Pointers are aligned to their element (MRR_EALIGN); no call is slower by
+ * much for less than 16 bytes.
+ * Errors: MRR_EUNSUPPORTED for another type or nranks outside [1, 32];
+ * MRR_EINVAL for null pointers, cols 0 or over 2^20, ld_in or ld_out below
+ * cols or over 2^31, rows over 2^31 or an eps that is negative or NaN.
+ * rows == 0 launches nothing.
+ * ------------------------------------------------------------------------ */
+mrr_status mrr_layernorm_fwd(const void* const* inputs, int nranks, const void* residual,
+                             const void* weight, const void* bias, void* sum, void* out,
+                             float* mean, float* rstd, size_t rows, size_t cols, size_t ld_in,
+                             size_t ld_out, float eps, mrr_dtype dtype, mrr_dtype wdtype,
+                             void* stream);
+
+/* --------------------------------------------------------------------------
+ * Gradient of mrr_layernorm_fwd.  With xhat = (h - mean) * rstd and
+ * g = dout * weight, mean() over a row:
+ *   dsum    = round( rstd * (g - mean(g) - xhat * mean(g * xhat)) + dresidual )
+ *   dweight = round( sum over rows of dout * xhat )
+ *   dbias   = round( sum over rows of dout )
+ * dsum is the gradient of every input and of the residual alike (each enters
+ * the sum with factor 1).  Sums are f32 and taken in a fixed order: the same
+ * call gives the same bits.
+ *
+ * dout, sum (the forward's h), dresidual (the gradient that h receives from
+ * elsewhere, NULL = none): rows ld_in elements apart; dsum: rows ld_out apart.
+ * mean, rstd: the forward's.  weight as in the forward; dweight, dbias: cols
+ * elements of wdtype.  dsum, dweight and dbias may be NULL, not all three.
+ * dsum may be exactly dout, sum or dresidual when ld_in == ld_out.
+ * workspace: device, 16-byte aligned, mrr_layernorm_bwd_workspace_bytes(rows,
+ * cols) bytes at least (else MRR_ESCRATCH), contents irrelevant before and
+ * after; needed only with dweight or dbias.
+ * rows == 0 sets dweight and dbias to zero.  Errors as in the forward.
+ * ------------------------------------------------------------------------ */
+size_t mrr_layernorm_bwd_workspace_bytes(size_t rows, size_t cols);
+
+mrr_status mrr_layernorm_bwd(const void* dout, const void* sum, const void* weight,
+                             const float* mean, const float* rstd, const void* dresidual,
+                             void* dsum, void* dweight, void* dbias, size_t rows, size_t cols,
+                             size_t ld_in, size_t ld_out, mrr_dtype dtype, mrr_dtype wdtype,
+                             void* workspace, size_t workspace_bytes, void* stream);
 
 /* --------------------------------------------------------------------------
  * Copy-kernel calibration (measurement aid, not part of the reduction).
