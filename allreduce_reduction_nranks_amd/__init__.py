@@ -59,7 +59,7 @@ def load_library() -> ctypes.CDLL:
             raise RuntimeError("libmrr.so is not built (%s); run __graft_entry__.build()" % LIB_PATH)
         L = ctypes.CDLL(LIB_PATH)
         vp, sz, i, u32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_uint32
-        f32 = ctypes.c_float
+        f32, i64, psz = ctypes.c_float, ctypes.c_int64, ctypes.POINTER(sz)
         pp = ctypes.POINTER(vp)
         sigs = {
             "mrr_allreduce_rsag": ([pp, pp, sz, i, i, vp], i),
@@ -85,6 +85,9 @@ def load_library() -> ctypes.CDLL:
             "mrr_layernorm_fwd": ([pp, i, vp, vp, vp, vp, vp, vp, vp, sz, sz, sz, sz, f32, i, i, vp], i),
             "mrr_layernorm_bwd_workspace_bytes": ([sz, sz], sz),
             "mrr_layernorm_bwd": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, sz, sz, sz, i, i, vp, sz, vp], i),
+            "mrr_linear_xent_workspace_bytes": ([sz, sz, psz, i, i, i], sz),
+            "mrr_linear_xent_fwd": ([vp, pp, psz, i, vp, i64, vp, vp, sz, sz, sz, sz, i, vp, sz, vp], i),
+            "mrr_linear_xent_bwd": ([vp, pp, psz, i, vp, i64, vp, vp, sz, vp, pp, sz, sz, sz, sz, i, vp, sz, vp], i),
             "mrr_stream_copy": ([vp, vp, sz, vp], i),
             "mrr_rank_buffer_pitch": ([sz, i], sz),
             "mrr_status_string": ([i], ctypes.c_char_p),
@@ -464,6 +467,53 @@ def mrr_layernorm_bwd(dout, sum, weight, mean, rstd, dresidual, dsum, dweight, d
         _ptr(dout), _ptr(sum), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dresidual), _ptr(dsum),
         _ptr(dweight), _ptr(dbias), rows, cols, ld_in, ld_out, t, tw, _ptr(workspace),
         workspace_bytes, _stream(stream))
+
+
+def _sizes(rows, n: int):
+    if rows is None:
+        return None
+    if len(rows) < n:
+        raise ValueError("rows has %d entries, nranks is %d" % (len(rows), n))
+    return (ctypes.c_size_t * max(1, len(rows)))(*rows)
+
+
+def mrr_linear_xent_workspace_bytes(tokens, cols, rows, nranks, dtype, backward) -> int:
+    return load_library().mrr_linear_xent_workspace_bytes(tokens, cols, _sizes(rows, nranks), nranks, _dt(dtype),
+                                                          1 if backward else 0)
+
+
+def mrr_linear_xent_fwd(hidden, weights, rows, nranks, targets, ignore_index, loss, lse, tokens, cols,
+                        ld_hidden, ld_weight, dtype, workspace=None, workspace_bytes=0, stream=None) -> int:
+    t, e = _dt(dtype), _ESIZE.get(_dt(dtype), 0)
+    sizes = _sizes(rows, nranks)
+    _rows_room(hidden, _matrix_bytes(tokens, cols, ld_hidden, e), "hidden")
+    _room(targets, 8 * tokens, "targets")
+    _room(loss, 4 * tokens, "loss")
+    _room(lse, 4 * tokens, "lse")
+    _room(workspace, workspace_bytes, "workspace")
+    need = [_matrix_bytes(n, cols, ld_weight, e) for n in rows[:max(0, nranks)]] if rows is not None else []
+    return load_library().mrr_linear_xent_fwd(
+        _ptr(hidden), _rows_ptrs(weights, len(need), need, "weights"), sizes, nranks, _ptr(targets), ignore_index,
+        _ptr(loss), _ptr(lse), tokens, cols, ld_hidden, ld_weight, t, _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def mrr_linear_xent_bwd(hidden, weights, rows, nranks, targets, ignore_index, lse, dloss, dloss_stride, dhidden,
+                        dweights, tokens, cols, ld_hidden, ld_weight, dtype, workspace=None, workspace_bytes=0,
+                        stream=None) -> int:
+    t, e = _dt(dtype), _ESIZE.get(_dt(dtype), 0)
+    sizes = _sizes(rows, nranks)
+    nh = _matrix_bytes(tokens, cols, ld_hidden, e)
+    _rows_room(hidden, nh, "hidden")
+    _room(targets, 8 * tokens, "targets")
+    _room(lse, 4 * tokens, "lse")
+    _rows_room(dloss, 4 * ((tokens - 1) * dloss_stride + 1) if tokens > 0 else 0, "dloss")
+    _rows_room(dhidden, nh, "dhidden")
+    _room(workspace, workspace_bytes, "workspace")
+    need = [_matrix_bytes(n, cols, ld_weight, e) for n in rows[:max(0, nranks)]] if rows is not None else []
+    return load_library().mrr_linear_xent_bwd(
+        _ptr(hidden), _rows_ptrs(weights, len(need), need, "weights"), sizes, nranks, _ptr(targets), ignore_index,
+        _ptr(lse), _ptr(dloss), dloss_stride, _ptr(dhidden), _rows_ptrs(dweights, len(need), need, "dweights"), tokens,
+        cols, ld_hidden, ld_weight, t, _ptr(workspace), workspace_bytes, _stream(stream))
 
 
 def mrr_stream_copy(src, dst, nbytes, stream=None) -> int:

@@ -248,6 +248,8 @@ namespace mrr {
 constexpr size_t kMaxRows = (size_t)1 << 31;
 constexpr size_t kMaxCols = (size_t)1 << 20;
 constexpr size_t kMaxLd = (size_t)1 << 31;
+constexpr size_t kMaxTokens = (size_t)1 << 24;
+constexpr size_t kMaxVocab = (size_t)1 << 30;
 
 static bool float_type(int t) { return t == kF32 || t == kF16 || t == kBF16; }
 
@@ -918,6 +920,153 @@ mrr_status mrr_layernorm_bwd(const void* dout, const void* sum, const void* weig
   a.cols = (uint32_t)cols;
   a.wf32 = tw == kF32;
   return hip_status(launch_norm_bwd(a, t, (hipStream_t)stream), fn);
+}
+
+// Sizes and types of a cross entropy call; MRR_OK, or the refusal.
+static mrr_status xent_shape(const char* fn, const size_t* rows, int nranks, size_t tokens, size_t cols, int t,
+                             uint64_t* vocab) {
+  if (nranks < 1 || nranks > kMaxRanks) return refuse(MRR_EUNSUPPORTED, fn, "nranks out of range");
+  if (!float_type(t)) return refuse(MRR_EUNSUPPORTED, fn, "type");
+  if (!rows) return refuse(MRR_EINVAL, fn, "null rows");
+  if (cols == 0 || cols > kMaxCols) return refuse(MRR_EINVAL, fn, "cols out of range");
+  if (tokens > kMaxTokens) return refuse(MRR_EINVAL, fn, "tokens out of range");
+  *vocab = 0;
+  for (int r = 0; r < nranks; ++r) {
+    if (rows[r] > kMaxVocab) return refuse(MRR_EINVAL, fn, "rows out of range");
+    *vocab += rows[r];
+  }
+  if (*vocab == 0 || *vocab > kMaxVocab) return refuse(MRR_EINVAL, fn, "vocabulary out of range");
+  return MRR_OK;
+}
+
+size_t mrr_linear_xent_workspace_bytes(size_t tokens, size_t cols, const size_t* rows, int nranks,
+                                       mrr_dtype dtype, int backward) {
+  uint64_t vocab;
+  if (tokens == 0 || xent_shape("mrr_linear_xent_workspace_bytes", rows, nranks, tokens, cols, dtype, &vocab))
+    return 0;
+  return xent_plan((uint32_t)tokens, (uint32_t)cols, rows, nranks, dtype, backward != 0).bytes;
+}
+
+// What the two passes share: the operands' checks.
+static mrr_status xent_operands(const char* fn, const void* hidden, const void* const* weights, const size_t* rows,
+                                int nranks, const int64_t* targets, size_t tokens, size_t cols, size_t ld_hidden,
+                                size_t ld_weight, int t, void* workspace, size_t workspace_bytes, size_t need,
+                                Mat* ins, int* nin) {
+  const size_t e = tsize(t);
+  if (ld_hidden < cols || ld_hidden > kMaxLd || ld_weight < cols || ld_weight > kMaxLd)
+    return refuse(MRR_EINVAL, fn, "row stride out of range");
+  if (!hidden || !weights || !targets || !workspace) return refuse(MRR_EINVAL, fn, "null pointer");
+  if (!aligned(hidden, e) || !aligned(targets, 8)) return refuse(MRR_EALIGN, fn, "element alignment");
+  if (!aligned(workspace, 16)) return refuse(MRR_EALIGN, fn, "workspace 16 bytes");
+  if (workspace_bytes < need) return refuse(MRR_ESCRATCH, fn, "workspace too small");
+  ins[(*nin)++] = {hidden, tokens, cols * e, ld_hidden * e};
+  ins[(*nin)++] = vec(targets, tokens * 8);
+  for (int r = 0; r < nranks; ++r) {
+    if (rows[r] == 0) continue;
+    if (!weights[r]) return refuse(MRR_EINVAL, fn, "null weight shard");
+    if (!aligned(weights[r], e)) return refuse(MRR_EALIGN, fn, "element alignment");
+    ins[(*nin)++] = {weights[r], rows[r], cols * e, ld_weight * e};
+  }
+  return MRR_OK;
+}
+
+mrr_status mrr_linear_xent_fwd(const void* hidden, const void* const* weights, const size_t* rows,
+                               int nranks, const int64_t* targets, int64_t ignore_index,
+                               float* loss, float* lse, size_t tokens, size_t cols,
+                               size_t ld_hidden, size_t ld_weight, mrr_dtype dtype,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  static const char* fn = "mrr_linear_xent_fwd";
+  const int t = dtype;
+  uint64_t vocab;
+  if (mrr_status st = xent_shape(fn, rows, nranks, tokens, cols, t, &vocab)) return st;
+  if (tokens == 0) return MRR_OK;
+  if (!loss && !lse) return refuse(MRR_EINVAL, fn, "no output");
+  Mat ins[kMaxRanks + 2];
+  int nin = 0;
+  const size_t need = xent_plan((uint32_t)tokens, (uint32_t)cols, rows, nranks, t, false).bytes;
+  if (mrr_status st = xent_operands(fn, hidden, weights, rows, nranks, targets, tokens, cols, ld_hidden, ld_weight, t,
+                                    workspace, workspace_bytes, need, ins, &nin))
+    return st;
+  if (!aligned(loss, 4) || !aligned(lse, 4)) return refuse(MRR_EALIGN, fn, "element alignment");
+  const Mat outs[3] = {vec(loss, tokens * 4), vec(lse, tokens * 4), vec(workspace, need)};
+  if (bad_overlap(ins, nin, 0, outs, 3)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
+  XentCall c{};
+  c.hidden = hidden;
+  c.weights = weights;
+  c.rows = rows;
+  c.nranks = nranks;
+  c.targets = targets;
+  c.ignore = ignore_index;
+  c.loss = loss;
+  c.lse_out = lse;
+  c.tokens = (uint32_t)tokens;
+  c.cols = (uint32_t)cols;
+  c.ld_hidden = ld_hidden;
+  c.ld_weight = ld_weight;
+  c.workspace = workspace;
+  return hip_status(launch_xent_fwd(c, t, (hipStream_t)stream), fn);
+}
+
+mrr_status mrr_linear_xent_bwd(const void* hidden, const void* const* weights, const size_t* rows,
+                               int nranks, const int64_t* targets, int64_t ignore_index,
+                               const float* lse, const float* dloss, size_t dloss_stride,
+                               void* dhidden, void* const* dweights, size_t tokens, size_t cols,
+                               size_t ld_hidden, size_t ld_weight, mrr_dtype dtype,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  static const char* fn = "mrr_linear_xent_bwd";
+  const int t = dtype;
+  uint64_t vocab;
+  if (mrr_status st = xent_shape(fn, rows, nranks, tokens, cols, t, &vocab)) return st;
+  const size_t e = tsize(t);
+  Mat outs[kMaxRanks + 2];
+  int nout = 0;
+  outs[nout++] = {dhidden, tokens, cols * e, ld_hidden * e};
+  bool wanted = dhidden != nullptr;
+  for (int r = 0; dweights && r < nranks; ++r) {
+    if (!dweights[r] || !rows[r]) continue;
+    if (!aligned(dweights[r], e)) return refuse(MRR_EALIGN, fn, "element alignment");
+    outs[nout++] = {dweights[r], rows[r], cols * e, ld_weight * e};
+    wanted = true;
+  }
+  if (!wanted) return refuse(MRR_EINVAL, fn, "no output");
+  Mat ins[kMaxRanks + 4];
+  int nin = 0;
+  const size_t need =
+      tokens ? xent_plan((uint32_t)tokens, (uint32_t)cols, rows, nranks, t, true).bytes : 0;
+  if (tokens == 0) {
+    if (ld_weight < cols || ld_weight > kMaxLd) return refuse(MRR_EINVAL, fn, "row stride out of range");
+    if (bad_overlap(ins, 0, 0, outs, nout)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
+  } else {
+    if (mrr_status st = xent_operands(fn, hidden, weights, rows, nranks, targets, tokens, cols, ld_hidden, ld_weight, t,
+                                      workspace, workspace_bytes, need, ins, &nin))
+      return st;
+    if (!lse || !dloss) return refuse(MRR_EINVAL, fn, "null pointer");
+    if (dloss_stride > kMaxLd) return refuse(MRR_EINVAL, fn, "dloss stride out of range");
+    if (!aligned(lse, 4) || !aligned(dloss, 4) || !aligned(dhidden, e)) return refuse(MRR_EALIGN, fn, "element alignment");
+    ins[nin++] = vec(lse, tokens * 4);
+    ins[nin++] = vec(dloss, ((tokens - 1) * dloss_stride + 1) * 4);
+    outs[nout++] = vec(workspace, need);
+    // the hidden states, first of ins, are copied before anything is written
+    if (bad_overlap(ins, nin, 1, outs, nout)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
+  }
+  XentCall c{};
+  c.hidden = hidden;
+  c.weights = weights;
+  c.rows = rows;
+  c.nranks = nranks;
+  c.targets = targets;
+  c.ignore = ignore_index;
+  c.lse = lse;
+  c.dloss = dloss;
+  c.dloss_stride = dloss_stride;
+  c.dhidden = dhidden;
+  c.dweights = dweights;
+  c.tokens = (uint32_t)tokens;
+  c.cols = (uint32_t)cols;
+  c.ld_hidden = ld_hidden;
+  c.ld_weight = ld_weight;
+  c.workspace = workspace;
+  return hip_status(launch_xent_bwd(c, t, (hipStream_t)stream), fn);
 }
 
 mrr_status mrr_stream_copy(const void* src, void* dst, size_t nbytes, void* stream) {

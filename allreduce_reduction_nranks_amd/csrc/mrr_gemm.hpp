@@ -1,0 +1,218 @@
+// mrr_gemm.hpp -- the tile product that the cross entropy kernels share: one
+// workgroup computes D[m][n] = sum over k of A[m][k] B[n][k] for a tile of
+// 256 m by BN n in f32, from 16-bit operands, and hands each wave its part.
+//
+// An operand lies in memory either with k contiguous ("row": a row for each m)
+// or with m contiguous ("col": a row for each k).  Both reach LDS by loads that
+// bypass registers (16 bytes a lane, a wave's 1 KiB contiguous in LDS), 64 k a
+// stage, two stages.  A row operand is read from LDS 16 bytes a lane; a col
+// operand with the transposing 64-bit read, so no operand is transposed in
+// memory.  Chunks are permuted within a stage (the permutation is made on the
+// global address, since the LDS side of the load is fixed) so that the lanes
+// that LDS serves together touch different banks.
+//
+// 512 threads, 8 waves, 2 a SIMD; a wave holds 128 x 64 (BN 256) or 64 x 64
+// (BN 128) accumulators in 32x32x16 matrix instructions.  The fragments of the
+// next 16 k are read while those of the present ones multiply, over the end of a
+// stage as well: the one barrier of a stage stands before its last quarter, when
+// all its reads are done, so that the stage's buffer can be refilled and the next
+// stage's first fragments fetched under that quarter's products.
+#pragma once
+
+#include "mrr_rows.hpp"
+
+namespace mrr {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kGemmThreads = 512;
+constexpr int kTileM = 256;  // also the unit that vocabulary shards are padded to
+constexpr int kTileK = 64;
+
+template <int T> __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
+  if constexpr (T == kF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// Lane l of a wave's accumulator tile: n is l % 32, element i's m is this.
+__device__ __forceinline__ int acc_row(int lane, int i) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
+
+// ---- addresses -----------------------------------------------------------------
+// Row operand: a stage is [rows][64 k], 128 bytes a row, 8 chunks of 16.  Load i
+// of thread t brings row 64 i + t / 8; chunk c of row r lies at position
+// c ^ f(r), f(r) = (r & 7) ^ (r >> 3 & 1): any 8 rows, and any 16 over 64 banks, differ.
+__device__ __forceinline__ uint32_t row_src_chunk(int tid) {
+  return (uint32_t)((tid & 7) ^ ((tid >> 3) & 7) ^ ((tid >> 6) & 1));
+}
+// Byte offset of lane's 8 k of quarter 0 in the row tile that starts at `row0`
+// (a multiple of 32); quarter kk flips bits of the chunk: offset ^ (kk * 32).
+__device__ __forceinline__ uint32_t row_frag(int row0, int lane) {
+  const int r = lane & 31;
+  return (uint32_t)((row0 + r) * 128 + (((lane >> 5) ^ (r & 7) ^ ((r >> 3) & 1)) << 4));
+}
+// Col operand: a stage is [64 k][256 m], 512 bytes a k.  Load i of thread t
+// brings k 16 i + t / 32; 64-byte units are at unit ^ (k & 7).
+__device__ __forceinline__ uint32_t col_src_chunk(int tid) {
+  return (uint32_t)((tid & 31) ^ (((tid >> 5) & 7) << 2));
+}
+// A transposing read serves 16 lanes with a block of 4 k x 16 m: lane j of the
+// 16 addresses k j / 4, m 4 (j % 4), and receives the 4 k of m j.  Byte offset
+// for the 32 m from m0 on, k 0..3 (+ 4 for r = 1) and 8..11; 16 k are 8192 bytes.
+__device__ __forceinline__ uint32_t col_frag(int m0, int r, int lane) {
+  const int k = 8 * (lane >> 5) + 4 * r + ((lane >> 2) & 3);
+  const int unit = (m0 >> 5) ^ (k & 7);
+  return (uint32_t)(k * 512 + unit * 64 + 32 * ((lane >> 4) & 1) + 8 * (lane & 3));
+}
+
+typedef __attribute__((address_space(3))) uint8_t lds8;
+typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+
+__device__ __forceinline__ u32x4 read_row(const lds8* p) { return *(const lds_u32x4*)p; }
+__device__ __forceinline__ u32x4 read_col(const lds8* lo, const lds8* hi) {
+  const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)lo));
+  const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)hi));
+  return u32x4{a.x, a.y, b.x, b.y};
+}
+
+// 16 bytes a lane from base + off to LDS, lane l's at lds + 16 l.  In assembly
+// because the compiler, given the builtin, waits for the loads in flight before it
+// reads the other stage's buffer; there is no output register, and sync() below
+// waits for them.
+__device__ __forceinline__ void load_lds(const uint8_t* base, uint32_t off, lds8* lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :: "s"((uint32_t)(uintptr_t)lds), "v"(off), "s"(base));
+}
+
+// The product over `steps` stages.  src(s, pa, pb, oa, ob) sets the (wave-uniform)
+// addresses and the lane offsets of stage s; it is called once for each s in order.
+template <int T, bool ACOL, bool BCOL, int BN> struct Tile {
+  static constexpr int WN = BN == 256 ? 4 : 2, WM = 8 / WN;       // waves along n and m
+  static constexpr int FM = kTileM / WM / 32, FN = BN / WN / 32;  // 32 x 32 tiles of a wave
+  static constexpr int SA = kTileM * kTileK * 2, SB = BN * kTileK * 2;  // bytes of a stage
+  static constexpr int LA = SA / 8192, LB = SB / 8192;                  // loads of a lane
+  static constexpr int kLds = 2 * (SA + SB);                            // A, A, B, B
+  f32x16 acc[FM][FN];
+
+  template <class Src> __device__ __forceinline__ void run(int steps, lds8* lds, Src&& src) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int m0 = wave / WN * (FM * 32), n0 = wave % WN * (FN * 32);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+    if (steps <= 0) return;
+    // offsets of this lane's fragments, and of its wave's loads, in the present stage
+    constexpr int NA = ACOL ? 2 * FM : 4, NB = BCOL ? 2 * FN : 4;
+    uint32_t fa[NA], fb[NB];
+    uint32_t wa = (uint32_t)wave * 1024, wb = 2 * SA + (uint32_t)wave * 1024;
+#pragma unroll
+    for (int i = 0; i < NA; ++i) fa[i] = ACOL ? col_frag(m0 + 32 * (i >> 1), i & 1, lane) : row_frag(m0, lane) ^ (i * 32);
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+      fb[i] = 2 * SA + (BCOL ? col_frag(n0 + 32 * (i >> 1), i & 1, lane) : row_frag(n0, lane) ^ (i * 32));
+    const uint8_t *pa, *pb;
+    uint32_t oa[LA], ob[LB];
+    u32x4 va[2][FM], vb[2][FN];
+
+    auto fetch = [&](int i) {
+      if (i < LA) load_lds(pa, oa[i < LA ? i : 0], lds + wa + i * 8192);
+      else load_lds(pb, ob[i < LA ? 0 : i - LA], lds + wb + (i - LA) * 8192);
+    };
+    auto read = [&](int f, int kk) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        if constexpr (BCOL) vb[f][j] = read_col(lds + fb[2 * j] + kk * 8192, lds + fb[2 * j + 1] + kk * 8192);
+        else vb[f][j] = read_row(lds + fb[kk] + j * 4096);
+      }
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        if constexpr (ACOL) va[f][i] = read_col(lds + fa[2 * i] + kk * 8192, lds + fa[2 * i + 1] + kk * 8192);
+        else va[f][i] = read_row(lds + fa[kk] + i * 4096);
+      }
+    };
+    auto product = [&](int f, int p) {
+      acc[p / FN][p % FN] = mfma<T>(va[f][p / FN], vb[f][p % FN], acc[p / FN][p % FN]);
+    };
+    constexpr int kProducts = FM * FN;
+    // fragments f multiply while the others are read from quarter kk
+    auto quarter = [&](int f, int kk) {
+      constexpr int reads = (ACOL ? 2 : 1) * FM + (BCOL ? 2 : 1) * FN;
+      constexpr int each = (reads + kProducts - 1) / kProducts;
+      read(f ^ 1, kk);
+#pragma unroll
+      for (int p = 0; p < kProducts; ++p) product(f, p);
+#pragma unroll
+      for (int p = 0; p < kProducts; ++p) {
+        __builtin_amdgcn_sched_group_barrier(0x100, each, 0);  // LDS reads
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);     // a matrix instruction
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // this wave's reads are done and its loads have arrived, then every wave's; the
+    // other buffer becomes the present one
+    auto turn = [&]() {
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < NA; ++i) fa[i] ^= SA;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) fb[i] ^= SB;
+    };
+    src(0, pa, pb, oa, ob);
+#pragma unroll
+    for (int i = 0; i < LA + LB; ++i) fetch(i);
+    wa ^= SA;
+    wb ^= SB;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (steps > 1) {
+      src(1, pa, pb, oa, ob);
+#pragma unroll
+      for (int i = 0; i < LA + LB; ++i) fetch(i);
+      wa ^= SA;
+      wb ^= SB;
+    }
+    read(0, 0);
+    int s = 0;
+    for (; s + 2 < steps; ++s) {
+      quarter(0, 1);
+      quarter(1, 2);
+      quarter(0, 3);
+      turn();
+      src(s + 2, pa, pb, oa, ob);
+      read(0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int p = 0; p < kProducts || p < LA + LB; ++p) {
+        if (p < kProducts) product(1, p);
+        if (p < LA + LB) fetch(p);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      wa ^= SA;
+      wb ^= SB;
+    }
+    for (; s + 1 < steps; ++s) {
+      quarter(0, 1);
+      quarter(1, 2);
+      quarter(0, 3);
+      turn();
+      quarter(1, 0);
+    }
+    quarter(0, 1);
+    quarter(1, 2);
+    quarter(0, 3);
+#pragma unroll
+    for (int p = 0; p < kProducts; ++p) product(1, p);
+  }
+};
+
+}  // namespace mrr

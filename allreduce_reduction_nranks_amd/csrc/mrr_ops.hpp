@@ -49,4 +49,89 @@ uint32_t norm_bwd_groups(uint64_t rows, uint32_t cols);
 hipError_t launch_norm_fwd(const NormFwdArgs& a, int t, hipStream_t stream);
 hipError_t launch_norm_bwd(NormBwdArgs a, int t, hipStream_t stream);
 
+// ---- cross entropy over a sharded vocabulary ---------------------------------------
+// The shards' rows, each shard padded to whole tiles of 256 rows.
+struct XentVocab {
+  const void* w[MRR_MAX_RANKS];
+  uint32_t first_tile[MRR_MAX_RANKS + 1];
+  uint32_t rows[MRR_MAX_RANKS];
+  uint32_t first_row[MRR_MAX_RANKS];  // of the whole vocabulary
+  int n;
+};
+
+// A counted token of a backward call.
+struct XentToken {
+  float lse, dl;
+  int32_t target, pad;
+};
+
+struct XentArgs {
+  XentVocab v;
+  const uint8_t* laid;  // weights of the piece laid out, null: read where they are
+  const uint8_t* h;     // hidden states laid out, [tpad][kpad]
+  uint64_t laid_plane, h_plane, dz_plane;
+  uint32_t ldw, ldh, lddz;      // bytes between rows
+  uint32_t tokens, tpad, cols, kpad;
+  uint32_t tile0, ntiles;       // the piece
+  // forward
+  float2* part;                 // [tiles x waves][tokens]: max and sum, base 2
+  float* zt;                    // [tokens]: the target's logit
+  const int64_t* targets;
+  int64_t ignore;
+  uint32_t part0;
+  // backward
+  uint8_t* dz;                  // [tpad][piece]
+  const XentToken* token;
+  const uint32_t* count;
+  const int32_t* place;
+  const float* unscale;
+  float* sum;                   // [splits][tpad][kpad]
+  uint32_t splits, add;
+  void* dhidden;
+  void* dw[MRR_MAX_RANKS];
+  uint64_t ld_dh, ld_dw;
+};
+
+struct XentJoinArgs {
+  const float2* part;
+  const float* zt;
+  const int64_t* targets;
+  int64_t ignore, vocab;
+  float* loss;
+  float* lse;
+  uint32_t parts, tokens;
+};
+
+// A call as the C ABI received it.
+struct XentCall {
+  const void* hidden;
+  const void* const* weights;
+  const size_t* rows;
+  int nranks;
+  const int64_t* targets;
+  int64_t ignore;
+  float* loss;         // forward
+  float* lse_out;      // forward
+  const float* lse;    // backward
+  const float* dloss;  // backward
+  size_t dloss_stride;
+  void* dhidden;
+  void* const* dweights;
+  uint32_t tokens, cols;
+  size_t ld_hidden, ld_weight;
+  void* workspace;
+};
+
+// Tiles, pieces and the workspace's parts (byte offsets) of a call.
+struct XentPlan {
+  uint32_t bn, tpad, kpad, tiles, piece, splits;
+  uint64_t h_plane, laid_plane, dz_plane;
+  uint64_t h, laid, dz, sum, token, idx, place, scalars, part, zt;
+  uint64_t bytes;
+};
+
+XentPlan xent_plan(uint32_t tokens, uint32_t cols, const size_t* rows, int nranks, int t, bool backward);
+hipError_t launch_xent_fwd(const XentCall& c, int t, hipStream_t stream);
+hipError_t launch_xent_bwd(const XentCall& c, int t, hipStream_t stream);
+
 }  // namespace mrr

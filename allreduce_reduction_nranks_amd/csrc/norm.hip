@@ -24,52 +24,10 @@
 #include "mrr_device.hpp"
 #include "mrr_internal.hpp"
 #include "mrr_ops.hpp"
+#include "mrr_rows.hpp"
 
 namespace mrr {
 namespace {
-
-typedef u32x4 u32x4_any __attribute__((aligned(2)));
-
-// V elements from `p` on, of which the first `n` exist; zeros after them.
-template <int T> __device__ __forceinline__ u32x4 load_raw(const void* p, int n) {
-  constexpr int V = Vec<T>::VW;
-  if (n >= V) return *reinterpret_cast<const u32x4_any*>(p);
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if constexpr (T == kF32) {
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (j < n) v[j] = reinterpret_cast<const uint32_t*>(p)[j];
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (j < n) v[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[j] << (16 * (j & 1));
-  }
-  return v;
-}
-
-template <int T> __device__ __forceinline__ void store_raw(void* p, int n, u32x4 v) {
-  constexpr int V = Vec<T>::VW;
-  if (n >= V) {
-    *reinterpret_cast<u32x4_any*>(p) = v;
-    return;
-  }
-  if constexpr (T == kF32) {
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (j < n) reinterpret_cast<uint32_t*>(p)[j] = v[j];
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (j < n) reinterpret_cast<uint16_t*>(p)[j] = (uint16_t)(v[j / 2] >> (16 * (j & 1)));
-  }
-}
-
-template <int T> __device__ __forceinline__ const uint8_t* at(const void* p, uint64_t i) {
-  return reinterpret_cast<const uint8_t*>(p) + i * Ty<T>::size;
-}
-template <int T> __device__ __forceinline__ uint8_t* at(void* p, uint64_t i) {
-  return reinterpret_cast<uint8_t*>(p) + i * Ty<T>::size;
-}
 
 // V weights from column c on, widened; `fill` where there is no weight.
 template <int T>

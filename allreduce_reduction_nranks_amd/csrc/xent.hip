@@ -1,0 +1,710 @@
+// xent.hip -- cross entropy of a linear layer whose vocabulary lies in N rank
+// shards, without the logits in memory, and its gradient.
+//
+//   z[t][v] = sum over c of h[t][c] w[v][c]
+//   lse[t]  = log(sum over v of exp(z[t][v])),  loss[t] = lse[t] - z[t][target[t]]
+//
+//   dz[t][v] = (exp(z[t][v] - lse[t]) - [v = target[t]]) dloss[t]
+//   dh[t][c] = sum over v of dz[t][v] w[v][c],  dw[v][c] = sum over t of dz[t][v] h[t][c]
+//
+// The forward is one product whose tile epilogue reduces 128 logits of each token
+// to (max, sum of exponentials); a join over those pairs gives lse.  Logits stay
+// f32 in accumulators.  The backward computes the logits again, a piece of the
+// vocabulary at a time, keeps that piece's dz in 16 bits and multiplies it with
+// the piece's weights and with the hidden states: 3 products of 2 T V C
+// operations, bound by the matrix units.
+//
+// Tokens without a loss are left out of the backward altogether: the others'
+// hidden states are gathered first, so nothing in an ignored token's row (not
+// even a NaN) reaches a gradient, and a batch pays for its counted tokens only.
+//
+// f32 operands are split into bf16 planes, x = x1 + x2 + x3 exactly (8 + 8 +
+// 8 bits), and a product is the sum of the 6 plane products x_i y_j with
+// i + j <= 4, smallest first; what is left out is below 2^-24 of |x y|, an f32
+// product's rounding.  An infinite x stays whole in x1, and the five smaller products
+// read a copy of x1 that has 0 in its place (else infinity would meet the zeros and
+// the signs of the other operand's smaller parts and give NaN): a row of -inf weights
+// keeps its probability of 0.
+#include "mrr_gemm.hpp"
+#include "mrr_internal.hpp"
+#include "mrr_ops.hpp"
+#include "mrr_rows.hpp"
+
+namespace mrr {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr int kPlanes = 4, kSegs = 6;  // x1, x2, x3, x1 without infinities
+
+// Plane of A and of B in segment s of an f32 product.
+__device__ __forceinline__ uint32_t seg_a(uint32_t s) { return (0x031132u >> (4 * s)) & 3u; }
+__device__ __forceinline__ uint32_t seg_b(uint32_t s) { return (0x013123u >> (4 * s)) & 3u; }
+
+// ---- layouts of operands ---------------------------------------------------------
+// A product reads rows of a multiple of 64 elements, 16-byte aligned, zeros past
+// the last column.  What does not lie so, and all f32, is laid out first.
+struct LayoutArgs {
+  XentVocab v;          // source of weights: padded row r is row r % 256 of tile tile0 + r / 256
+  const void* src;      // source of hidden states (null: weights)
+  const int32_t* idx;   // source row of each row, -1: zeros; null: row r itself
+  uint64_t ld, rows, src_rows;
+  uint8_t* dst;
+  uint64_t plane;       // bytes between planes
+  uint32_t cols, kpad, tile0, units_log2;
+};
+
+__device__ __forceinline__ void split(float x, uint32_t* p) {
+  float a = bf16_to_f32(f32_to_bf16(x));
+  const bool finite = (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u;
+  // the largest values round to infinity: cut those off instead
+  if (finite && (__float_as_uint(a) & 0x7F800000u) == 0x7F800000u) a = __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
+  const float r = finite ? x - a : 0.0f;
+  const float b = bf16_to_f32(f32_to_bf16(r));
+  p[0] = f32_to_bf16(a);
+  p[1] = f32_to_bf16(b);
+  p[2] = f32_to_bf16(r - b);
+  p[3] = finite ? p[0] : 0u;
+}
+
+template <int T> __global__ void __launch_bounds__(256) layout_k(LayoutArgs a) {
+  const uint32_t lanes = 1u << a.units_log2, units = a.kpad / 8;
+  const uint32_t u0 = threadIdx.x & (lanes - 1);
+  const uint32_t per = 256u >> a.units_log2;
+  for (uint64_t row = (uint64_t)blockIdx.x * per + (threadIdx.x >> a.units_log2); row < a.rows;
+       row += (uint64_t)gridDim.x * per) {
+    const uint8_t* src = nullptr;
+    if (a.src) {
+      const int64_t r = a.idx ? (int64_t)a.idx[row] : row < a.src_rows ? (int64_t)row : -1;
+      if (r >= 0) src = at<T>(a.src, (uint64_t)r * a.ld);
+    } else {
+      const uint32_t tile = a.tile0 + (uint32_t)(row / kTileM);
+      int sh = 0;
+      while (tile >= a.v.first_tile[sh + 1]) ++sh;
+      const uint32_t r = (tile - a.v.first_tile[sh]) * kTileM + (uint32_t)(row % kTileM);
+      if (r < a.v.rows[sh]) src = at<T>(a.v.w[sh], (uint64_t)r * a.ld);
+    }
+    for (uint32_t u = u0; u < units; u += lanes) {
+      const int n = src && 8 * u < a.cols ? (int)(a.cols - 8 * u) : 0;
+      uint8_t* d = a.dst + ((uint64_t)row * a.kpad + 8 * u) * 2;
+      if constexpr (T == kF32) {
+        float x[8];
+        decode16<kF32>(load_raw<kF32>(src + 32 * u, n), x);
+        decode16<kF32>(load_raw<kF32>(src + 32 * u + 16, n - 4), x + 4);
+        uint32_t p[kPlanes][8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint32_t q[kPlanes];
+          split(x[j], q);
+#pragma unroll
+          for (int k = 0; k < kPlanes; ++k) p[k][j] = q[k];
+        }
+#pragma unroll
+        for (int k = 0; k < kPlanes; ++k)
+          *reinterpret_cast<u32x4*>(d + k * a.plane) =
+              u32x4{p[k][0] | p[k][1] << 16, p[k][2] | p[k][3] << 16, p[k][4] | p[k][5] << 16, p[k][6] | p[k][7] << 16};
+      } else {
+        *reinterpret_cast<u32x4*>(d) = load_raw<T>(src + 16 * u, n);
+      }
+    }
+  }
+}
+
+// ---- tokens of a backward call ---------------------------------------------------
+// Counted tokens in order, what their gradient needs, and for each token its place.
+// One workgroup.  f16 gradients of logits are scaled so that the largest dloss is
+// 2^14: p dloss goes far below f16's smallest normal otherwise.  The scale is a
+// power of two and is taken out of the f32 sums of both gradients.
+struct TokensArgs {
+  const int64_t* targets;
+  const float* lse;
+  const float* dloss;
+  uint64_t dloss_stride;
+  int64_t ignore, vocab;
+  XentToken* token;  // [tpad]
+  int32_t* idx;      // [tpad]: source row, -1 past the counted ones
+  int32_t* place;    // [tokens]: place among the counted ones, -1: ignored
+  uint32_t* count;
+  float* unscale;
+  uint32_t tokens, tpad;
+  int scaled;
+};
+
+constexpr int kTokensThreads = 1024;
+
+__global__ void __launch_bounds__(kTokensThreads) tokens_k(TokensArgs a) {
+  __shared__ uint32_t sums[kTokensThreads / 64];
+  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  float scale = 1.0f;
+  if (a.scaled) {
+    uint32_t most = 0;  // bits of |dloss| order as the values do
+    for (uint32_t t = tid; t < a.tokens; t += kTokensThreads) {
+      const int64_t target = a.targets[t];
+      const uint32_t u = __float_as_uint(a.dloss[t * a.dloss_stride]) & 0x7FFFFFFFu;
+      if (target != a.ignore && target >= 0 && target < a.vocab && u < 0x7F800000u && u > most) most = u;
+    }
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) {
+      const uint32_t o = __shfl_xor(most, m);
+      most = o > most ? o : most;
+    }
+    if (lane == 0) sums[wave] = most;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kTokensThreads / 64; ++w) most = sums[w] > most ? sums[w] : most;
+    __syncthreads();
+    // the power of two at or above it, kept where scale and its inverse are normal
+    uint32_t e = (most >> 23) + ((most & 0x7FFFFFu) ? 1u : 0u);
+    e = e < 27 ? 27 : e > 254 ? 254 : e;
+    if (most == 0) e = 127;
+    scale = __uint_as_float((268u - e) << 23);  // 2^14 / 2^(e - 127)
+  }
+  uint32_t before = 0;
+  for (uint32_t t0 = 0; t0 < a.tokens; t0 += kTokensThreads) {
+    const uint32_t t = t0 + tid;
+    int64_t target = -1;
+    if (t < a.tokens) target = a.targets[t];
+    const bool counted = t < a.tokens && target != a.ignore && target >= 0 && target < a.vocab;
+    const uint64_t mask = __ballot(counted);
+    if (lane == 0) sums[wave] = (uint32_t)__popcll(mask);
+    __syncthreads();
+    uint32_t at = before, all = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < kTokensThreads / 64; ++w) {
+      if (w < wave) at += sums[w];
+      all += sums[w];
+    }
+    at += (uint32_t)__popcll(mask & ((1ull << lane) - 1));
+    if (counted) {
+      a.token[at] = {a.lse[t], a.dloss[t * a.dloss_stride] * scale, (int32_t)target, 0};
+      a.idx[at] = (int32_t)t;
+    }
+    if (t < a.tokens) a.place[t] = counted ? (int32_t)at : -1;
+    before += all;
+    __syncthreads();
+  }
+  for (uint32_t t = before + tid; t < a.tpad; t += kTokensThreads) {
+    a.token[t] = {0.0f, 0.0f, -1, 0};
+    a.idx[t] = -1;
+  }
+  if (tid == 0) {
+    *a.count = before;
+    *a.unscale = 1.0f / scale;
+  }
+}
+
+// ---- tiles -------------------------------------------------------------------------
+// Workgroup id to tile (m, n) of mt x nt.  Workgroups go to the 8 XCDs in turn; each
+// XCD gets one contiguous run of the tile order, which walks 8 m tiles by all n
+// tiles, so that the tiles an XCD works on together share operands in its L2.
+__device__ __forceinline__ bool tile_of(uint32_t id, uint32_t mt, uint32_t nt, uint32_t& m, uint32_t& n) {
+  const uint32_t total = mt * nt, per = total / 8, extra = total % 8, x = id & 7, j = id >> 3;
+  if (j >= per + (x < extra ? 1u : 0u)) return false;
+  const uint32_t t = x * per + (x < extra ? x : extra) + j;
+  constexpr uint32_t G = 8;
+  const uint32_t g = t / (G * nt), rem = t - g * (G * nt), gm = mt - g * G < G ? mt - g * G : G;
+  m = g * G + rem % gm;
+  n = rem / gm;
+  return true;
+}
+uint32_t tile_grid(uint64_t tiles) { return (uint32_t)((tiles + 7) / 8 * 8); }
+
+// Logits of one tile of 256 vocabulary rows by BN tokens.  Forward: reduced to a
+// (max, sum) pair in base 2 for each wave's rows, and the target's logit.
+// Backward: dz, vocabulary contiguous.
+template <int T, int BN, bool BWD, int SEG>
+__global__ void __launch_bounds__(kGemmThreads) logits_k(XentArgs a) {
+  typedef Tile<T, false, false, BN> Prod;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
+  uint32_t mt, nt;
+  if (!tile_of(blockIdx.x, a.ntiles, a.tpad / BN, mt, nt)) return;
+  const uint32_t tokens = BWD ? *a.count : a.tokens;
+  const uint32_t t0 = nt * BN, tile = a.tile0 + mt;
+  if (t0 >= tokens) return;
+  int sh = 0;
+  while (tile >= a.v.first_tile[sh + 1]) ++sh;
+  const uint32_t row0 = (tile - a.v.first_tile[sh]) * kTileM;  // of the shard
+  const uint32_t left = a.v.rows[sh] - row0 < (uint32_t)kTileM ? a.v.rows[sh] - row0 : (uint32_t)kTileM;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  const uint8_t* wa = a.laid ? a.laid + (uint64_t)mt * kTileM * a.ldw : (const uint8_t*)a.v.w[sh] + (uint64_t)row0 * a.ldw;
+  const uint8_t* hb = a.h + (uint64_t)t0 * a.ldh;
+  uint32_t k = 0, seg = 0;
+  const uint32_t kend = a.kpad * 2;
+  const uint32_t have = a.laid ? (uint32_t)kTileM : left;
+  auto src = [&](int s, const uint8_t*& pa, const uint8_t*& pb, uint32_t (&oa)[Prod::LA], uint32_t (&ob)[Prod::LB]) {
+    if (s == 0) {
+      const uint32_t c = row_src_chunk(tid) * 16;
+#pragma unroll
+      for (int i = 0; i < Prod::LA; ++i) {
+        const uint32_t r = 64 * i + (tid >> 3);
+        oa[i] = (r < have ? r : have - 1) * a.ldw + c;  // rows past the shard: any that exists
+      }
+#pragma unroll
+      for (int i = 0; i < Prod::LB; ++i) ob[i] = (64 * i + (tid >> 3)) * a.ldh + c;
+    }
+    pa = wa + k;
+    pb = hb + k;
+    if constexpr (SEG > 1) {
+      pa += seg_a(seg) * a.laid_plane;
+      pb += seg_b(seg) * a.h_plane;
+    }
+    k += kTileK * 2;
+    if (SEG > 1 && k == kend) k = 0, ++seg;
+  };
+  Prod p;
+  p.run((int)(a.kpad / kTileK) * SEG, (lds8*)lds, src);
+
+  const int wm = wave / Prod::WN, wn = wave % Prod::WN;
+  const uint32_t first = a.v.first_row[sh] + row0;  // of the whole vocabulary
+#pragma unroll
+  for (int j = 0; j < Prod::FN; ++j) {
+    const uint32_t t = t0 + (wn * Prod::FN + j) * 32 + (lane & 31);
+    if constexpr (!BWD) {
+      const int64_t target = t < tokens ? a.targets[t] : -1;
+      // the target's row in this tile, if it is there
+      const uint32_t hit = target >= first && target < (int64_t)first + left ? (uint32_t)(target - first) : ~0u;
+      float mx = -__builtin_inff();
+#pragma unroll
+      for (int i = 0; i < Prod::FM; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint32_t m = (wm * Prod::FM + i) * 32 + acc_row(lane, e);
+          const float z = p.acc[i][j][e];
+          if (m == hit) a.zt[t] = z;
+          const float x = m < left ? z : -__builtin_inff();
+          p.acc[i][j][e] = x;
+          mx = __builtin_fmaxf(mx, x);
+        }
+      mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32));
+      const float top = mx * kLog2e;
+      // a tile without a finite logit adds nothing (or, with +inf, NaN)
+      const float base = mx == -__builtin_inff() ? 0.0f : top;
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < Prod::FM; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(p.acc[i][j][e], kLog2e, -base));
+      s += __shfl_xor(s, 32);
+      if (lane < 32 && t < tokens) a.part[((uint64_t)(a.part0 + mt) * Prod::WM + wm) * a.tokens + t] = make_float2(top, s);
+    } else {
+      const XentToken tk = a.token[t];
+      const bool live = t < tokens;
+      const uint32_t hit = tk.target >= 0 && (uint32_t)tk.target - first < left ? (uint32_t)tk.target - first : ~0u;
+      uint8_t* row = a.dz + (uint64_t)t * a.lddz + (uint64_t)mt * kTileM * 2;
+#pragma unroll
+      for (int i = 0; i < Prod::FM; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t m = (wm * Prod::FM + i) * 32 + 8 * q + 4 * (lane >> 5);
+          uint32_t w[SEG > 1 ? kPlanes : 1][2] = {};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = p.acc[i][j][4 * q + e] - tk.lse;
+            float d = SEG > 1 ? __builtin_expf(x) : __builtin_amdgcn_exp2f(x * kLog2e);
+            d = (d - (m + e == hit ? 1.0f : 0.0f)) * tk.dl;
+            if (!live || m + e >= left) d = 0.0f;
+            if constexpr (SEG > 1) {
+              uint32_t part[kPlanes];
+              split(d, part);
+#pragma unroll
+              for (int b = 0; b < kPlanes; ++b) w[b][e >> 1] |= part[b] << (16 * (e & 1));
+            } else {
+              w[0][e >> 1] |= from_f32<T>(d) << (16 * (e & 1));
+            }
+          }
+#pragma unroll
+          for (int b = 0; b < (SEG > 1 ? kPlanes : 1); ++b)
+            *reinterpret_cast<u32x2*>(row + b * a.dz_plane + m * 2) = u32x2{w[b][0], w[b][1]};
+        }
+    }
+  }
+}
+
+// Gradient of the hidden states from one piece of the vocabulary: a tile of 256
+// columns by BN tokens over the split's share of the piece's rows, into (or, after
+// the first piece, added to) the split's f32 sums.
+template <int T, int BN, int SEG> __global__ void __launch_bounds__(kGemmThreads) dhidden_k(XentArgs a) {
+  typedef Tile<T, true, false, BN> Prod;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
+  uint32_t mt, nt;
+  if (!tile_of(blockIdx.x, (a.kpad + kTileM - 1) / kTileM, a.tpad / BN, mt, nt)) return;
+  const uint32_t t0 = nt * BN, c0 = mt * kTileM;
+  if (t0 >= *a.count) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint32_t blocks = a.ntiles * (kTileM / kTileK);  // of 64 rows
+  const uint32_t split = blockIdx.y;
+  const uint32_t k0 = (uint32_t)((uint64_t)blocks * split / a.splits), k1 = (uint32_t)((uint64_t)blocks * (split + 1) / a.splits);
+  uint32_t k = k0, seg = 0;
+  int sh = 0;
+  // a lane's column chunk; past the last column any that exists
+  uint32_t col = c0 + col_src_chunk(tid) * 8;
+  col = (col < a.kpad ? col : a.kpad - 8) * 2;
+  auto src = [&](int s, const uint8_t*& pa, const uint8_t*& pb, uint32_t (&oa)[Prod::LA], uint32_t (&ob)[Prod::LB]) {
+    if (s == 0) {
+      const uint32_t c = row_src_chunk(tid) * 16;
+#pragma unroll
+      for (int i = 0; i < Prod::LB; ++i) ob[i] = (64 * i + (tid >> 3)) * a.lddz + c;
+    }
+    uint32_t have = kTileK;
+    if (SEG > 1 || a.laid) {
+      pa = a.laid + (uint64_t)k * kTileK * a.ldw;
+    } else {
+      const uint32_t tile = a.tile0 + k / (kTileM / kTileK);
+      while (tile >= a.v.first_tile[sh + 1]) ++sh;
+      // rows past the shard meet zeros of dz: any that exists
+      const uint32_t row = (tile - a.v.first_tile[sh]) * kTileM + k % (kTileM / kTileK) * kTileK, rows = a.v.rows[sh];
+      const uint32_t at = row < rows ? row : rows - 1;
+      have = rows - at < (uint32_t)kTileK ? rows - at : (uint32_t)kTileK;
+      pa = (const uint8_t*)a.v.w[sh] + (uint64_t)at * a.ldw;
+    }
+    pb = a.dz + (uint64_t)t0 * a.lddz + (uint64_t)k * kTileK * 2;
+    if constexpr (SEG > 1) {
+      pa += seg_a(seg) * a.laid_plane;
+      pb += seg_b(seg) * a.dz_plane;
+    }
+#pragma unroll
+    for (int i = 0; i < Prod::LA; ++i) {
+      const uint32_t r = 16 * i + (tid >> 5);
+      oa[i] = (r < have ? r : have - 1) * a.ldw + col;
+    }
+    if (++k == k1) k = k0, ++seg;
+  };
+  Prod p;
+  p.run((int)(k1 - k0) * SEG, (lds8*)lds, src);
+
+  const int wm = wave / Prod::WN, wn = wave % Prod::WN;
+  float* sum = a.sum + (uint64_t)split * a.tpad * a.kpad;
+#pragma unroll
+  for (int j = 0; j < Prod::FN; ++j) {
+    const uint32_t t = t0 + (wn * Prod::FN + j) * 32 + (lane & 31);
+#pragma unroll
+    for (int i = 0; i < Prod::FM; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t c = c0 + (wm * Prod::FM + i) * 32 + 8 * q + 4 * (lane >> 5);
+        if (c >= a.kpad) continue;
+        f32x4* to = reinterpret_cast<f32x4*>(sum + (uint64_t)t * a.kpad + c);
+        f32x4 x = {p.acc[i][j][4 * q], p.acc[i][j][4 * q + 1], p.acc[i][j][4 * q + 2], p.acc[i][j][4 * q + 3]};
+        if (a.add) {
+          const f32x4 o = *to;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = o[e] + x[e];
+        }
+        *to = x;
+      }
+  }
+}
+
+// Weight gradients of one piece: a tile of 256 columns by 256 vocabulary rows over
+// the counted tokens, rounded once.
+template <int T, int OUT, int SEG> __global__ void __launch_bounds__(kGemmThreads) dweight_k(XentArgs a) {
+  typedef Tile<T, true, true, 256> Prod;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
+  uint32_t mt, nt;
+  if (!tile_of(blockIdx.x, (a.kpad + kTileM - 1) / kTileM, a.ntiles, mt, nt)) return;
+  const uint32_t c0 = mt * kTileM, tile = a.tile0 + nt;
+  int sh = 0;
+  while (tile >= a.v.first_tile[sh + 1]) ++sh;
+  if (!a.dw[sh]) return;
+  const uint32_t row0 = (tile - a.v.first_tile[sh]) * kTileM;
+  const uint32_t left = a.v.rows[sh] - row0 < (uint32_t)kTileM ? a.v.rows[sh] - row0 : (uint32_t)kTileM;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  uint32_t col = c0 + col_src_chunk(tid) * 8;
+  col = (col < a.kpad ? col : a.kpad - 8) * 2;
+  const uint32_t blocks = (*a.count + kTileK - 1) / kTileK;  // of 64 tokens; those past the last have dz 0
+  uint32_t k = 0, seg = 0;
+  auto src = [&](int s, const uint8_t*& pa, const uint8_t*& pb, uint32_t (&oa)[Prod::LA], uint32_t (&ob)[Prod::LB]) {
+    if (s == 0) {
+#pragma unroll
+      for (int i = 0; i < Prod::LA; ++i) {
+        oa[i] = (16 * i + (tid >> 5)) * a.ldh + col;
+        ob[i] = (16 * i + (tid >> 5)) * a.lddz + col_src_chunk(tid) * 16;
+      }
+    }
+    pa = a.h + (uint64_t)k * kTileK * a.ldh;
+    pb = a.dz + (uint64_t)k * kTileK * a.lddz + (uint64_t)nt * kTileM * 2;
+    if constexpr (SEG > 1) {
+      pa += seg_a(seg) * a.h_plane;
+      pb += seg_b(seg) * a.dz_plane;
+    }
+    if (++k == blocks) k = 0, ++seg;
+  };
+  Prod p;
+  p.run((int)blocks * SEG, (lds8*)lds, src);
+
+  const float unscale = *a.unscale;
+  const int wm = wave / Prod::WN, wn = wave % Prod::WN;
+#pragma unroll
+  for (int j = 0; j < Prod::FN; ++j) {
+    const uint32_t v = (wn * Prod::FN + j) * 32 + (lane & 31);
+    if (v >= left) continue;
+    uint8_t* row = at<OUT>(a.dw[sh], (uint64_t)(row0 + v) * a.ld_dw);
+#pragma unroll
+    for (int i = 0; i < Prod::FM; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t c = c0 + (wm * Prod::FM + i) * 32 + 8 * q + 4 * (lane >> 5);
+        if (c >= a.cols) continue;
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = p.acc[i][j][4 * q + e] * unscale;
+        store4<OUT>(at<OUT>(row, c), (int)(a.cols - c), x);
+      }
+  }
+}
+
+// ---- joins -------------------------------------------------------------------------
+// lse and loss of 16 tokens a workgroup: 64 chains of pairs, then those in order.
+constexpr int kJoinTokens = 16, kJoinLanes = 64;
+
+__device__ __forceinline__ float2 join2(float2 a, float2 b) {
+  const float top = __builtin_fmaxf(a.x, b.x);
+  if (top == -__builtin_inff()) return make_float2(top, a.y + b.y);
+  return make_float2(top, a.y * __builtin_amdgcn_exp2f(a.x - top) + b.y * __builtin_amdgcn_exp2f(b.x - top));
+}
+
+__global__ void __launch_bounds__(kJoinTokens * kJoinLanes) join_k(XentJoinArgs a) {
+  __shared__ float2 lds[kJoinLanes][kJoinTokens];
+  const uint32_t x = threadIdx.x % kJoinTokens, chain = threadIdx.x / kJoinTokens;
+  const uint32_t t = blockIdx.x * kJoinTokens + x;
+  float2 s = make_float2(-__builtin_inff(), 0.0f);
+  if (t < a.tokens) {
+#pragma unroll 4
+    for (uint32_t p = chain; p < a.parts; p += kJoinLanes) s = join2(s, a.part[(uint64_t)p * a.tokens + t]);
+  }
+  lds[chain][x] = s;
+  __syncthreads();
+  if (chain || t >= a.tokens) return;
+#pragma unroll 8
+  for (int k = 1; k < kJoinLanes; ++k) s = join2(s, lds[k][x]);
+  const float lse = (s.x + __builtin_log2f(s.y)) * kLn2;
+  if (a.lse) a.lse[t] = lse;
+  if (a.loss) {
+    const int64_t target = a.targets[t];
+    a.loss[t] = target == a.ignore ? 0.0f : target >= 0 && target < a.vocab ? lse - a.zt[t] : __builtin_nanf("");
+  }
+}
+
+// Gradient rows of the hidden states: the splits' sums in order, rounded once; zeros
+// for a token that has no loss.
+template <int T> __global__ void __launch_bounds__(256) dhidden_join_k(XentArgs a) {
+  const float unscale = *a.unscale;
+  for (uint32_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+    const int32_t from = a.place[t];
+    for (uint32_t c = 4 * (blockIdx.y * 256 + threadIdx.x); c < a.cols; c += 1024 * gridDim.y) {
+      float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (from >= 0) {
+        const float* p = a.sum + (uint64_t)from * a.kpad + c;
+        for (uint32_t s = 0; s < a.splits; ++s) {
+          const f32x4 y = *reinterpret_cast<const f32x4*>(p + (uint64_t)s * a.tpad * a.kpad);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] += y[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] *= unscale;
+      }
+      store4<T>(at<T>(a.dhidden, (uint64_t)t * a.ld_dh + c), (int)(a.cols - c), x);
+    }
+  }
+}
+
+// Weight gradients of a call without tokens.
+__global__ void __launch_bounds__(256) zero_rows_k(uint8_t* p, uint64_t rows, uint64_t pitch, uint32_t halves) {
+  for (uint64_t r = blockIdx.x; r < rows; r += gridDim.x)
+    for (uint32_t i = threadIdx.x; i < halves; i += 256) reinterpret_cast<uint16_t*>(p + r * pitch)[i] = 0;
+}
+
+// ---- plan --------------------------------------------------------------------------
+constexpr uint64_t kPieceBytes = 256ull << 20;  // of dz, and of weights laid out
+constexpr uint64_t kMaxTiles = 1ull << 22;       // workgroups of 512 threads in a launch
+uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
+
+}  // namespace
+
+XentPlan xent_plan(uint32_t tokens, uint32_t cols, const size_t* rows, int nranks, int t, bool backward) {
+  XentPlan p{};
+  const uint64_t planes = t == kF32 ? kPlanes : 1;
+  p.bn = tokens <= 128 ? 128 : 256;
+  p.tpad = (uint32_t)up(tokens, p.bn);
+  p.kpad = (uint32_t)up(cols, kTileK);
+  uint64_t tiles = 0;
+  for (int r = 0; r < nranks; ++r) tiles += up(rows[r], kTileM) / kTileM;
+  p.tiles = (uint32_t)tiles;
+  // tiles of a piece: dz of all tokens, and the weights, each within kPieceBytes
+  uint64_t most = kPieceBytes / ((uint64_t)kTileM * p.kpad * 2 * planes);
+  if (backward) {
+    const uint64_t d = kPieceBytes / ((uint64_t)kTileM * p.tpad * 2 * planes);
+    if (d < most) most = d;
+  }
+  const uint64_t grid = kMaxTiles / (p.tpad / p.bn);
+  if (grid < most) most = grid;
+  if (most < 1) most = 1;
+  const uint64_t pieces = tiles ? (tiles + most - 1) / most : 1;
+  p.piece = (uint32_t)((tiles + pieces - 1) / pieces);
+  uint64_t at = 0;
+  auto take = [&](uint64_t bytes) {
+    const uint64_t o = at;
+    at += up(bytes, 1024);
+    return o;
+  };
+  p.h_plane = (uint64_t)p.tpad * p.kpad * 2;
+  p.laid_plane = (uint64_t)p.piece * kTileM * p.kpad * 2;
+  p.h = take(p.h_plane * planes);
+  p.laid = take(p.laid_plane * planes);
+  if (backward) {
+    p.dz_plane = (uint64_t)p.tpad * p.piece * kTileM * 2;
+    p.dz = take(p.dz_plane * planes);
+    // enough splits of a piece's rows that a tile of every split has a CU
+    const uint64_t n = up(p.kpad, kTileM) / kTileM * (p.tpad / p.bn);
+    uint64_t s = n ? 256 / n : 1;
+    if (s > p.piece) s = p.piece;
+    p.splits = s < 1 ? 1 : (uint32_t)s;
+    p.sum = take((uint64_t)p.splits * p.tpad * p.kpad * 4);
+    p.token = take((uint64_t)p.tpad * sizeof(XentToken));
+    p.idx = take((uint64_t)p.tpad * 4);
+    p.place = take((uint64_t)tokens * 4);
+    p.scalars = take(8);
+  } else {
+    p.part = take(tiles * (p.bn == 256 ? 2 : 4) * tokens * sizeof(float2));
+    p.zt = take((uint64_t)tokens * 4);
+  }
+  p.bytes = at;
+  return p;
+}
+
+namespace {
+
+template <int T> void layout(LayoutArgs l, hipStream_t s) {
+  uint32_t log2 = 0;
+  while (log2 < 8 && (1u << log2) < l.kpad / 8) ++log2;
+  l.units_log2 = log2;
+  const uint64_t per = 256u >> log2, blocks = (l.rows + per - 1) / per;
+  hipLaunchKernelGGL(layout_k<T>, dim3((uint32_t)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, l);
+}
+
+// T: type of the caller's tensors.  M: type that multiplies.
+template <int T, int BN, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, hipStream_t s) {
+  constexpr int M = T == kF32 ? kBF16 : T, SEG = T == kF32 ? kSegs : 1;
+  uint8_t* ws = (uint8_t*)c.workspace;
+  XentArgs a{};
+  uint64_t vocab = 0;
+  bool direct = T != kF32 && c.cols % kTileK == 0 && c.ld_weight % 8 == 0 && c.ld_weight <= (1u << 22);
+  a.v.n = c.nranks;
+  for (int r = 0; r < c.nranks; ++r) {
+    a.v.w[r] = c.weights[r];
+    a.v.rows[r] = (uint32_t)c.rows[r];
+    a.v.first_row[r] = (uint32_t)vocab;
+    a.v.first_tile[r + 1] = a.v.first_tile[r] + (uint32_t)(up(c.rows[r], kTileM) / kTileM);
+    vocab += c.rows[r];
+    if (c.rows[r] && (uintptr_t)c.weights[r] % 16) direct = false;
+    if (c.dweights) a.dw[r] = c.dweights[r];
+  }
+  a.ldw = direct ? (uint32_t)c.ld_weight * 2 : p.kpad * 2;
+  a.laid_plane = p.laid_plane;
+  a.h = ws + p.h;
+  a.h_plane = p.h_plane;
+  a.ldh = p.kpad * 2;
+  a.tokens = c.tokens;
+  a.tpad = p.tpad;
+  a.cols = c.cols;
+  a.kpad = p.kpad;
+  a.targets = c.targets;
+  a.ignore = c.ignore;
+  LayoutArgs l{};
+  l.v = a.v;
+  l.cols = c.cols;
+  l.kpad = p.kpad;
+  if constexpr (BWD) {
+    a.dz = ws + p.dz;
+    a.dz_plane = p.dz_plane;
+    a.lddz = p.piece * kTileM * 2;
+    a.sum = (float*)(ws + p.sum);
+    a.splits = p.splits;
+    a.token = (XentToken*)(ws + p.token);
+    a.place = (int32_t*)(ws + p.place);
+    a.count = (uint32_t*)(ws + p.scalars);
+    a.unscale = (float*)(ws + p.scalars + 4);
+    a.dhidden = c.dhidden;
+    a.ld_dh = c.ld_hidden;
+    a.ld_dw = c.ld_weight;
+    const TokensArgs t{c.targets, c.lse, c.dloss, c.dloss_stride, c.ignore, (int64_t)vocab, (XentToken*)(ws + p.token),
+                       (int32_t*)(ws + p.idx), (int32_t*)(ws + p.place), (uint32_t*)(ws + p.scalars),
+                       (float*)(ws + p.scalars + 4), c.tokens, p.tpad, T == kF16};
+    hipLaunchKernelGGL(tokens_k, dim3(1), dim3(kTokensThreads), 0, s, t);
+    l.idx = (const int32_t*)(ws + p.idx);
+  } else {
+    a.part = (float2*)(ws + p.part);
+    a.zt = (float*)(ws + p.zt);
+  }
+  l.src = c.hidden;
+  l.ld = c.ld_hidden;
+  l.rows = p.tpad;
+  l.src_rows = c.tokens;
+  l.dst = ws + p.h;
+  l.plane = p.h_plane;
+  layout<T>(l, s);
+  l.src = nullptr;
+  l.ld = c.ld_weight;
+  l.dst = ws + p.laid;
+  l.plane = p.laid_plane;
+  const uint32_t nt = p.tpad / BN, ct = (uint32_t)(up(p.kpad, kTileM) / kTileM);
+  // a forward that reads the weights in place has nothing to divide but the grid
+  uint32_t piece = p.piece;
+  if (!BWD && direct) piece = nt <= kMaxTiles / p.tiles ? p.tiles : kMaxTiles / nt ? (uint32_t)(kMaxTiles / nt) : 1;
+  for (a.tile0 = 0; a.tile0 < p.tiles; a.tile0 += piece) {
+    a.ntiles = p.tiles - a.tile0 < piece ? p.tiles - a.tile0 : piece;
+    a.part0 = a.tile0;
+    if (!direct) {
+      l.tile0 = a.tile0;
+      l.rows = (uint64_t)a.ntiles * kTileM;
+      layout<T>(l, s);
+      a.laid = ws + p.laid;
+    }
+    hipLaunchKernelGGL((logits_k<M, BN, BWD, SEG>), dim3(tile_grid((uint64_t)a.ntiles * nt)), dim3(kGemmThreads), 0, s, a);
+    if constexpr (BWD) {
+      if (c.dhidden)
+        hipLaunchKernelGGL((dhidden_k<M, BN, SEG>), dim3(tile_grid((uint64_t)ct * nt), a.splits), dim3(kGemmThreads), 0, s, a);
+      a.add = 1;
+      if (c.dweights)
+        hipLaunchKernelGGL((dweight_k<M, T, SEG>), dim3(tile_grid((uint64_t)ct * a.ntiles)), dim3(kGemmThreads), 0, s, a);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if constexpr (BWD) {
+    if (c.dhidden) {
+      const uint32_t y = (c.cols + 1023) / 1024;
+      hipLaunchKernelGGL(dhidden_join_k<T>, dim3(c.tokens < 65536 ? c.tokens : 65536, y < 1024 ? y : 1024), dim3(256), 0, s, a);
+    }
+  } else {
+    const XentJoinArgs j{a.part, a.zt, c.targets, c.ignore, (int64_t)vocab, c.loss, c.lse_out,
+                         p.tiles * (uint32_t)(BN == 256 ? 2 : 4), c.tokens};
+    hipLaunchKernelGGL(join_k, dim3((c.tokens + kJoinTokens - 1) / kJoinTokens), dim3(kJoinTokens * kJoinLanes), 0, s, j);
+  }
+  return hipGetLastError();
+}
+
+template <bool BWD> hipError_t typed(const XentCall& c, int t, hipStream_t s) {
+  if (c.tokens == 0) {
+    const uint32_t e = t == kF32 ? 4 : 2;
+    for (int r = 0; c.dweights && r < c.nranks; ++r) {
+      if (!c.dweights[r] || !c.rows[r]) continue;
+      hipLaunchKernelGGL(zero_rows_k, dim3((uint32_t)(c.rows[r] < 65536 ? c.rows[r] : 65536)), dim3(256), 0, s,
+                         (uint8_t*)c.dweights[r], c.rows[r], c.ld_weight * e, c.cols * (e / 2));
+      const hipError_t err = hipGetLastError();
+      if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
+  }
+  const XentPlan p = xent_plan(c.tokens, c.cols, c.rows, c.nranks, t, BWD);
+  if (t == kF32) return p.bn == 128 ? run<kF32, 128, BWD>(c, p, s) : run<kF32, 256, BWD>(c, p, s);
+  if (t == kF16) return p.bn == 128 ? run<kF16, 128, BWD>(c, p, s) : run<kF16, 256, BWD>(c, p, s);
+  return p.bn == 128 ? run<kBF16, 128, BWD>(c, p, s) : run<kBF16, 256, BWD>(c, p, s);
+}
+
+}  // namespace
+
+hipError_t launch_xent_fwd(const XentCall& c, int t, hipStream_t stream) { return typed<false>(c, t, stream); }
+hipError_t launch_xent_bwd(const XentCall& c, int t, hipStream_t stream) { return typed<true>(c, t, stream); }
+
+}  // namespace mrr

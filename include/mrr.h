@@ -466,6 +466,79 @@ mrr_status mrr_layernorm_bwd(const void* dout, const void* sum, const void* weig
                              void* workspace, size_t workspace_bytes, void* stream);
 
 /* --------------------------------------------------------------------------
+ * Cross entropy of a linear layer whose vocabulary rows lie in nranks shards,
+ * without the logits in memory.
+ *
+ *   z[t][v]  = sum over c of hidden[t][c] * weight[v][c]       (f32, not rounded)
+ *   lse[t]   = log( sum over v of exp(z[t][v]) )
+ *   loss[t]  = lse[t] - z[t][targets[t]]
+ * v runs over the rows of shard 0, then of shard 1, and so on.
+ *
+ * hidden:  tokens x cols elements of dtype (F32 | F16 | BF16), rows ld_hidden
+ *          elements apart.
+ * weights: host array of nranks (1..32) device pointers; weights[r] is rows[r] x
+ *          cols elements of dtype, rows ld_weight elements apart.  rows: host
+ *          array; a shard may have no rows (its pointer is then not read).
+ * targets: tokens 64-bit indices into the whole vocabulary.  ignore_index: the
+ *          target of a token without a loss (its loss is 0, its lse is still
+ *          computed); it may be any value.  Any other target outside [0, vocabulary)
+ *          gives the loss NaN and counts as ignored in the gradient.
+ * loss, lse: receive tokens f32 values each; one of them may be NULL.
+ * f32 products are computed in the matrix units as sums of products of bf16 parts,
+ * exact to less than an f32 product's rounding; every sum is f32.
+ * workspace: device, 16-byte aligned, mrr_linear_xent_workspace_bytes(...,
+ * backward 0) bytes at least (else MRR_ESCRATCH), contents irrelevant before and
+ * after.  It may not overlap anything else.
+ * Pointers are aligned to their element (MRR_EALIGN).  16-bit weights whose shards
+ * are 16-byte aligned, with cols a multiple of 64 and ld_weight of 8, are read in
+ * place; others, and all f32, are first laid out in the workspace, 256 MiB of the
+ * vocabulary at a time.
+ * The same call gives the same bits.  tokens == 0 launches nothing.
+ * Errors: MRR_EUNSUPPORTED for another type or nranks outside [1, 32];
+ * MRR_EINVAL for null pointers, cols 0 or over 2^20, tokens over 2^24, a
+ * vocabulary of 0 or over 2^30 rows, or a row stride below cols or over 2^31;
+ * MRR_EOVERLAP for an output that overlaps anything.
+ * ------------------------------------------------------------------------ */
+size_t mrr_linear_xent_workspace_bytes(size_t tokens, size_t cols, const size_t* rows, int nranks,
+                                       mrr_dtype dtype, int backward);
+
+mrr_status mrr_linear_xent_fwd(const void* hidden, const void* const* weights, const size_t* rows,
+                               int nranks, const int64_t* targets, int64_t ignore_index,
+                               float* loss, float* lse, size_t tokens, size_t cols,
+                               size_t ld_hidden, size_t ld_weight, mrr_dtype dtype,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* --------------------------------------------------------------------------
+ * Gradient of mrr_linear_xent_fwd.
+ *
+ *   dz[t][v]       = (exp(z[t][v] - lse[t]) - [v == targets[t]]) * dloss[t]
+ *   dhidden[t][c]  = round( sum over v of dz[t][v] * weight[v][c] )
+ *   dweight[v][c]  = round( sum over t of dz[t][v] * hidden[t][c] )
+ * The logits are computed again, a piece of the vocabulary at a time; the piece's
+ * dz is held in dtype (f16: scaled so that the largest |dloss| is 2^14, f32: as
+ * bf16 parts that hold all its bits), which rounds each dz once; sums are f32.
+ * Ignored tokens are left out: their dhidden is zero and nothing in their rows,
+ * NaN included, reaches a gradient.
+ *
+ * hidden, weights, rows, targets, ignore_index: as in the forward.  lse: the
+ * forward's.
+ * dloss: gradient of token t's loss at dloss[t * dloss_stride]; stride 0 takes
+ * one value for all (that of a mean or a sum).
+ * dhidden: rows ld_hidden apart; NULL = not wanted.  It may be exactly hidden.
+ * dweights: host array of nranks device pointers, rows ld_weight apart; NULL, or
+ * an entry NULL = not wanted.  At least one output is wanted (else MRR_EINVAL).
+ * workspace: as in the forward, with backward 1.
+ * tokens == 0 sets the weight gradients to zero (no workspace needed).
+ * Errors as in the forward, and MRR_EINVAL for a dloss_stride over 2^31.
+ * ------------------------------------------------------------------------ */
+mrr_status mrr_linear_xent_bwd(const void* hidden, const void* const* weights, const size_t* rows,
+                               int nranks, const int64_t* targets, int64_t ignore_index,
+                               const float* lse, const float* dloss, size_t dloss_stride,
+                               void* dhidden, void* const* dweights, size_t tokens, size_t cols,
+                               size_t ld_hidden, size_t ld_weight, mrr_dtype dtype,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* --------------------------------------------------------------------------
  * Copy-kernel calibration (measurement aid, not part of the reduction).
  * Copies nbytes from src to dst with the launch scheme of the RS/AG kernels
  * (one single-wave workgroup per tile, residency capped through an unused
