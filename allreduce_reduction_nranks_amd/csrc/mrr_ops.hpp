@@ -71,6 +71,8 @@ struct XentArgs {
   const uint8_t* h;     // hidden states laid out, [tpad][kpad]
   uint64_t laid_plane, h_plane, dz_plane;
   uint32_t ldw, ldh, lddz;      // bytes between rows
+  const void* hidden;           // the caller's, rows ld_h elements apart; the shards' ld_w
+  uint64_t ld_h, ld_w;
   uint32_t tokens, tpad, cols, kpad;
   uint32_t tile0, ntiles;       // the piece
   // forward
@@ -84,6 +86,7 @@ struct XentArgs {
   const XentToken* token;
   const uint32_t* count;
   const int32_t* place;
+  const int32_t* idx;
   const float* unscale;
   float* sum;                   // [splits][tpad][kpad]
   uint32_t splits, add;
@@ -125,6 +128,8 @@ struct XentCall {
 // Tiles, pieces and the workspace's parts (byte offsets) of a call.
 struct XentPlan {
   uint32_t bn, tpad, kpad, tiles, piece, splits;
+  uint32_t few;    // 16-token groups of a few_k workgroup, 0: logits_k
+  uint32_t parts;  // (max, sum) pairs of a tile and token
   uint64_t h_plane, laid_plane, dz_plane;
   uint64_t h, laid, dz, sum, token, idx, place, scalars, part, zt;
   uint64_t bytes;

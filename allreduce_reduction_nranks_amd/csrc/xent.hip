@@ -208,6 +208,29 @@ __device__ __forceinline__ bool tile_of(uint32_t id, uint32_t mt, uint32_t nt, u
 }
 uint32_t tile_grid(uint64_t tiles) { return (uint32_t)((tiles + 7) / 8 * 8); }
 
+// dz of 4 vocabulary rows from m on, for one token; zeros from row `left` on.  T is
+// the caller's type.
+template <int T>
+__device__ __forceinline__ void store_dz(uint8_t* row, uint64_t plane, uint32_t m, const float* z, const XentToken& tk,
+                                         uint32_t hit, uint32_t left) {
+  constexpr int P = T == kF32 ? kPlanes : 1;
+  uint32_t w[P][2] = {};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float x = z[e] - tk.lse;
+    float d = T == kF32 ? __builtin_expf(x) : __builtin_amdgcn_exp2f(x * kLog2e);
+    d = (d - (m + e == hit ? 1.0f : 0.0f)) * tk.dl;
+    if (m + e >= left) d = 0.0f;
+    uint32_t part[kPlanes];
+    if constexpr (T == kF32) split(d, part);
+    else part[0] = from_f32<T>(d);
+#pragma unroll
+    for (int b = 0; b < P; ++b) w[b][e >> 1] |= part[b] << (16 * (e & 1));
+  }
+#pragma unroll
+  for (int b = 0; b < P; ++b) *reinterpret_cast<u32x2*>(row + b * plane + m * 2) = u32x2{w[b][0], w[b][1]};
+}
+
 // Logits of one tile of 256 vocabulary rows by BN tokens.  Forward: reduced to a
 // (max, sum) pair in base 2 for each wave's rows, and the target's logit.
 // Backward: dz, vocabulary contiguous.
@@ -296,26 +319,157 @@ __global__ void __launch_bounds__(kGemmThreads) logits_k(XentArgs a) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const uint32_t m = (wm * Prod::FM + i) * 32 + 8 * q + 4 * (lane >> 5);
-          uint32_t w[SEG > 1 ? kPlanes : 1][2] = {};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x = p.acc[i][j][4 * q + e] - tk.lse;
-            float d = SEG > 1 ? __builtin_expf(x) : __builtin_amdgcn_exp2f(x * kLog2e);
-            d = (d - (m + e == hit ? 1.0f : 0.0f)) * tk.dl;
-            if (!live || m + e >= left) d = 0.0f;
-            if constexpr (SEG > 1) {
-              uint32_t part[kPlanes];
-              split(d, part);
-#pragma unroll
-              for (int b = 0; b < kPlanes; ++b) w[b][e >> 1] |= part[b] << (16 * (e & 1));
-            } else {
-              w[0][e >> 1] |= from_f32<T>(d) << (16 * (e & 1));
-            }
-          }
-#pragma unroll
-          for (int b = 0; b < (SEG > 1 ? kPlanes : 1); ++b)
-            *reinterpret_cast<u32x2*>(row + b * a.dz_plane + m * 2) = u32x2{w[b][0], w[b][1]};
+          const float z[4] = {p.acc[i][j][4 * q], p.acc[i][j][4 * q + 1], p.acc[i][j][4 * q + 2], p.acc[i][j][4 * q + 3]};
+          store_dz<SEG == 1 ? T : (int)kF32>(row, a.dz_plane, m, z, tk, hit, live ? left : 0u);
         }
+    }
+  }
+}
+
+// ---- logits of few tokens ----------------------------------------------------------
+// The same without LDS tiles, for calls that are bound by reading the weights: a
+// workgroup takes 16 R vocabulary rows by 16 NT tokens, its 4 waves every fourth 128
+// bytes of the rows, and operands go from memory to the matrix instructions as they
+// are loaded (any address, no layout pass; f32 multiplies as f32).  A lane loads 32
+// bytes of its row, two loads that use up a line together; which k of the block a
+// lane's elements are is the same for both operands, so their order does not matter.
+typedef float f32x4v __attribute__((ext_vector_type(4)));
+template <int T> __device__ __forceinline__ f32x4v mfma16(u32x4 a, u32x4 b, f32x4v c) {
+  if constexpr (T == kF32) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[e]), __uint_as_float(b[e]), c, 0, 0, 0);
+    return c;
+  } else if constexpr (T == kF16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  } else {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+}
+
+template <int T, int NT, int R, bool BWD> __global__ void __launch_bounds__(256) few_k(XentArgs a) {
+  constexpr int V = Vec<T>::VW, B = 8 * V;  // elements of a load, and of a 128-byte block
+  constexpr int U = R * NT >= 8 ? 2 : 4;    // blocks in flight
+  __shared__ f32x4v red[4][R * NT][64];
+  const uint32_t tokens = BWD ? *a.count : a.tokens;
+  const uint32_t t0 = blockIdx.y * (16 * NT);
+  // dz of the last 64 tokens' places past the counted ones is zero
+  if (t0 >= (BWD ? (tokens + kTileK - 1) / kTileK * kTileK : tokens)) return;
+  constexpr uint32_t per = kTileM / (16 * R);
+  const uint32_t mt = blockIdx.x / per, tile = a.tile0 + mt, sub = blockIdx.x % per * (16 * R);
+  int sh = 0;
+  while (tile >= a.v.first_tile[sh + 1]) ++sh;
+  const uint32_t row0 = (tile - a.v.first_tile[sh]) * kTileM + sub, rows = a.v.rows[sh];
+  const uint32_t left = row0 < rows ? (rows - row0 < 16u * R ? rows - row0 : 16u * R) : 0u;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  f32x4v acc[R][NT];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[r][n] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+  if (left && tokens) {
+    const uint32_t lane0 = (lane >> 4) * 2 * V;  // a lane's first element of a block
+    const uint8_t *pw[R], *ph[NT];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint32_t m = 16 * r + (lane & 15);
+      pw[r] = at<T>(a.v.w[sh], (uint64_t)(row0 + (m < left ? m : left - 1)) * a.ld_w + lane0);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint32_t t = t0 + 16 * n + (lane & 15);
+      uint32_t from = t < tokens ? t : tokens - 1;
+      if constexpr (BWD) from = (uint32_t)a.idx[from];
+      ph[n] = at<T>(a.hidden, (uint64_t)from * a.ld_h + lane0);
+    }
+    const uint32_t blocks = a.cols / B;
+    uint32_t b = wave;
+    for (; b + 4 * (U - 1) < blocks; b += 4 * U) {
+      u32x4 vw[U][R][2], vh[U][NT][2];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) vw[u][r][x] = load_raw<T>(pw[r] + (uint64_t)(b + 4 * u) * 128 + 16 * x, V);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) vh[u][n][x] = load_raw<T>(ph[n] + (uint64_t)(b + 4 * u) * 128 + 16 * x, V);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) acc[r][n] = mfma16<T>(vw[u][r][x], vh[u][n][x], acc[r][n]);
+    }
+    for (; b * B < a.cols; b += 4) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t c = b * B + lane0 + x * V;
+        const int n_left = c < a.cols ? (int)(a.cols - c) : 0;
+        u32x4 vw[R], vh[NT];
+#pragma unroll
+        for (int r = 0; r < R; ++r) vw[r] = load_raw<T>(pw[r] + (uint64_t)b * 128 + 16 * x, n_left);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) vh[n] = load_raw<T>(ph[n] + (uint64_t)b * 128 + 16 * x, n_left);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) acc[r][n] = mfma16<T>(vw[r], vh[n], acc[r][n]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) red[wave][r * NT + n][lane] = acc[r][n];
+  __syncthreads();
+  if (wave >= NT) return;
+  // wave n joins the four parts of the n-th 16 tokens; a lane has token lane % 16
+  const uint32_t t = t0 + 16 * wave + (lane & 15), first = a.v.first_row[sh] + row0;
+  f32x4v z[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    z[r] = red[0][r * NT + wave][lane];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) z[r] += red[w][r * NT + wave][lane];
+  }
+  if constexpr (!BWD) {
+    const int64_t target = t < tokens ? a.targets[t] : -1;
+    const uint32_t hit = target >= first && target < (int64_t)first + left ? (uint32_t)(target - first) : ~0u;
+    float mx = -__builtin_inff();
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t m = 16 * r + 4 * (lane >> 4) + e;
+        if (m == hit) a.zt[t] = z[r][e];
+        if (m >= left) z[r][e] = -__builtin_inff();
+        mx = __builtin_fmaxf(mx, z[r][e]);
+      }
+    mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16));
+    mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32));
+    const float top = mx * kLog2e, base = mx == -__builtin_inff() ? 0.0f : top;
+    float s = 0.0f;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(z[r][e], kLog2e, -base));
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (lane < 16 && t < tokens) a.part[((uint64_t)a.part0 * per + blockIdx.x) * a.tokens + t] = make_float2(top, s);
+  } else {
+    const XentToken tk = a.token[t];
+    const uint32_t hit = tk.target >= 0 && (uint32_t)tk.target - first < left ? (uint32_t)tk.target - first : ~0u;
+    uint8_t* row = a.dz + (uint64_t)t * a.lddz + ((uint64_t)mt * kTileM + sub) * 2;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float x[4] = {z[r][0], z[r][1], z[r][2], z[r][3]};
+      store_dz<T>(row, a.dz_plane, 16 * r + 4 * (lane >> 4), x, tk, hit, t < tokens ? left : 0u);
     }
   }
 }
@@ -524,6 +678,7 @@ uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 XentPlan xent_plan(uint32_t tokens, uint32_t cols, const size_t* rows, int nranks, int t, bool backward) {
   XentPlan p{};
   const uint64_t planes = t == kF32 ? kPlanes : 1;
+  p.few = tokens <= 16 ? 1 : tokens <= 32 ? 2 : tokens <= 64 ? 4 : 0;
   p.bn = tokens <= 128 ? 128 : 256;
   p.tpad = (uint32_t)up(tokens, p.bn);
   p.kpad = (uint32_t)up(cols, kTileK);
@@ -565,7 +720,8 @@ XentPlan xent_plan(uint32_t tokens, uint32_t cols, const size_t* rows, int nrank
     p.place = take((uint64_t)tokens * 4);
     p.scalars = take(8);
   } else {
-    p.part = take(tiles * (p.bn == 256 ? 2 : 4) * tokens * sizeof(float2));
+    p.parts = p.few ? kTileM / (16 * p.few) : p.bn == 256 ? 2 : 4;  // of a tile
+    p.part = take(tiles * p.parts * tokens * sizeof(float2));
     p.zt = take((uint64_t)tokens * 4);
   }
   p.bytes = at;
@@ -580,6 +736,14 @@ template <int T> void layout(LayoutArgs l, hipStream_t s) {
   l.units_log2 = log2;
   const uint64_t per = 256u >> log2, blocks = (l.rows + per - 1) / per;
   hipLaunchKernelGGL(layout_k<T>, dim3((uint32_t)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, l);
+}
+
+template <int T, bool BWD> void few(const XentArgs& a, uint32_t few, hipStream_t s) {
+  const uint32_t tokens = BWD ? (uint32_t)up(a.tokens, kTileK) : a.tokens;
+  const dim3 grid(a.ntiles * (kTileM / (16 * few)), (tokens + 16 * few - 1) / (16 * few));
+  if (few == 1) hipLaunchKernelGGL((few_k<T, 1, 1, BWD>), grid, dim3(256), 0, s, a);
+  else if (few == 2) hipLaunchKernelGGL((few_k<T, 2, 2, BWD>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((few_k<T, 4, 4, BWD>), grid, dim3(256), 0, s, a);
 }
 
 // T: type of the caller's tensors.  M: type that multiplies.
@@ -610,6 +774,10 @@ template <int T, int BN, bool BWD> hipError_t run(const XentCall& c, const XentP
   a.kpad = p.kpad;
   a.targets = c.targets;
   a.ignore = c.ignore;
+  // few_k reads the operands where they are
+  a.hidden = c.hidden;
+  a.ld_h = c.ld_hidden;
+  a.ld_w = c.ld_weight;
   LayoutArgs l{};
   l.v = a.v;
   l.cols = c.cols;
@@ -622,6 +790,7 @@ template <int T, int BN, bool BWD> hipError_t run(const XentCall& c, const XentP
     a.splits = p.splits;
     a.token = (XentToken*)(ws + p.token);
     a.place = (int32_t*)(ws + p.place);
+    a.idx = (const int32_t*)(ws + p.idx);
     a.count = (uint32_t*)(ws + p.scalars);
     a.unscale = (float*)(ws + p.scalars + 4);
     a.dhidden = c.dhidden;
@@ -642,7 +811,7 @@ template <int T, int BN, bool BWD> hipError_t run(const XentCall& c, const XentP
   l.src_rows = c.tokens;
   l.dst = ws + p.h;
   l.plane = p.h_plane;
-  layout<T>(l, s);
+  if (BWD || !p.few) layout<T>(l, s);
   l.src = nullptr;
   l.ld = c.ld_weight;
   l.dst = ws + p.laid;
@@ -650,17 +819,19 @@ template <int T, int BN, bool BWD> hipError_t run(const XentCall& c, const XentP
   const uint32_t nt = p.tpad / BN, ct = (uint32_t)(up(p.kpad, kTileM) / kTileM);
   // a forward that reads the weights in place has nothing to divide but the grid
   uint32_t piece = p.piece;
-  if (!BWD && direct) piece = nt <= kMaxTiles / p.tiles ? p.tiles : kMaxTiles / nt ? (uint32_t)(kMaxTiles / nt) : 1;
+  if (!BWD && p.few) piece = p.tiles < kMaxTiles / 8 ? p.tiles : (uint32_t)(kMaxTiles / 8);
+  else if (!BWD && direct) piece = nt <= kMaxTiles / p.tiles ? p.tiles : kMaxTiles / nt ? (uint32_t)(kMaxTiles / nt) : 1;
   for (a.tile0 = 0; a.tile0 < p.tiles; a.tile0 += piece) {
     a.ntiles = p.tiles - a.tile0 < piece ? p.tiles - a.tile0 : piece;
     a.part0 = a.tile0;
-    if (!direct) {
+    if (!direct && (BWD || !p.few)) {
       l.tile0 = a.tile0;
       l.rows = (uint64_t)a.ntiles * kTileM;
       layout<T>(l, s);
       a.laid = ws + p.laid;
     }
-    hipLaunchKernelGGL((logits_k<M, BN, BWD, SEG>), dim3(tile_grid((uint64_t)a.ntiles * nt)), dim3(kGemmThreads), 0, s, a);
+    if (p.few) few<T, BWD>(a, p.few, s);
+    else hipLaunchKernelGGL((logits_k<M, BN, BWD, SEG>), dim3(tile_grid((uint64_t)a.ntiles * nt)), dim3(kGemmThreads), 0, s, a);
     if constexpr (BWD) {
       if (c.dhidden)
         hipLaunchKernelGGL((dhidden_k<M, BN, SEG>), dim3(tile_grid((uint64_t)ct * nt), a.splits), dim3(kGemmThreads), 0, s, a);
@@ -678,7 +849,7 @@ template <int T, int BN, bool BWD> hipError_t run(const XentCall& c, const XentP
     }
   } else {
     const XentJoinArgs j{a.part, a.zt, c.targets, c.ignore, (int64_t)vocab, c.loss, c.lse_out,
-                         p.tiles * (uint32_t)(BN == 256 ? 2 : 4), c.tokens};
+                         p.tiles * p.parts, c.tokens};
     hipLaunchKernelGGL(join_k, dim3((c.tokens + kJoinTokens - 1) / kJoinTokens), dim3(kJoinTokens * kJoinLanes), 0, s, j);
   }
   return hipGetLastError();
