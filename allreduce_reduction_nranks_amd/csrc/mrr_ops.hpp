@@ -76,11 +76,11 @@ struct XentArgs {
   uint32_t tokens, tpad, cols, kpad;
   uint32_t tile0, ntiles;       // the piece
   // forward
-  float2* part;                 // [tiles x waves][tokens]: max and sum, base 2
+  float2* part;                 // max and sum, base 2: logits_k [parts][tokens], few_k [tokens][parts]
   float* zt;                    // [tokens]: the target's logit
   const int64_t* targets;
   int64_t ignore;
-  uint32_t part0;
+  uint32_t parts;
   // backward
   uint8_t* dz;                  // [tpad][piece]
   const XentToken* token;
@@ -102,6 +102,7 @@ struct XentJoinArgs {
   int64_t ignore, vocab;
   float* loss;
   float* lse;
+  uint64_t part_stride, token_stride;
   uint32_t parts, tokens;
 };
 

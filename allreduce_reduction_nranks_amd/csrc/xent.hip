@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kGemmThreads) logits_k(XentArgs a) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(p.acc[i][j][e], kLog2e, -base));
       s += __shfl_xor(s, 32);
-      if (lane < 32 && t < tokens) a.part[((uint64_t)(a.part0 + mt) * Prod::WM + wm) * a.tokens + t] = make_float2(top, s);
+      if (lane < 32 && t < tokens) a.part[((uint64_t)(a.tile0 + mt) * Prod::WM + wm) * a.tokens + t] = make_float2(top, s);
     } else {
       const XentToken tk = a.token[t];
       const bool live = t < tokens;
@@ -461,7 +461,7 @@ template <int T, int NT, int R, bool BWD> __global__ void __launch_bounds__(256)
       for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(z[r][e], kLog2e, -base));
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
-    if (lane < 16 && t < tokens) a.part[((uint64_t)a.part0 * per + blockIdx.x) * a.tokens + t] = make_float2(top, s);
+    if (lane < 16 && t < tokens) a.part[(uint64_t)t * a.parts + (uint64_t)a.tile0 * per + blockIdx.x] = make_float2(top, s);
   } else {
     const XentToken tk = a.token[t];
     const uint32_t hit = tk.target >= 0 && (uint32_t)tk.target - first < left ? (uint32_t)tk.target - first : ~0u;
@@ -608,8 +608,9 @@ template <int T, int OUT, int SEG> __global__ void __launch_bounds__(kGemmThread
 }
 
 // ---- joins -------------------------------------------------------------------------
-// lse and loss of 16 tokens a workgroup: 64 chains of pairs, then those in order.
-constexpr int kJoinTokens = 16, kJoinLanes = 64;
+// lse and loss of JT tokens a workgroup: 1024 / JT chains of pairs, then those in order
+// (halves first, so that the last steps are few).
+constexpr int kJoinThreads = 1024;
 
 __device__ __forceinline__ float2 join2(float2 a, float2 b) {
   const float top = __builtin_fmaxf(a.x, b.x);
@@ -617,20 +618,25 @@ __device__ __forceinline__ float2 join2(float2 a, float2 b) {
   return make_float2(top, a.y * __builtin_amdgcn_exp2f(a.x - top) + b.y * __builtin_amdgcn_exp2f(b.x - top));
 }
 
-__global__ void __launch_bounds__(kJoinTokens * kJoinLanes) join_k(XentJoinArgs a) {
-  __shared__ float2 lds[kJoinLanes][kJoinTokens];
-  const uint32_t x = threadIdx.x % kJoinTokens, chain = threadIdx.x / kJoinTokens;
-  const uint32_t t = blockIdx.x * kJoinTokens + x;
+template <int JT> __global__ void __launch_bounds__(kJoinThreads) join_k(XentJoinArgs a) {
+  constexpr uint32_t chains = kJoinThreads / JT;
+  __shared__ float2 lds[kJoinThreads];
+  const uint32_t x = threadIdx.x % JT, chain = threadIdx.x / JT;
+  const uint32_t t = blockIdx.x * JT + x;
   float2 s = make_float2(-__builtin_inff(), 0.0f);
   if (t < a.tokens) {
+    const float2* part = a.part + t * a.token_stride;
 #pragma unroll 4
-    for (uint32_t p = chain; p < a.parts; p += kJoinLanes) s = join2(s, a.part[(uint64_t)p * a.tokens + t]);
+    for (uint32_t p = chain; p < a.parts; p += chains) s = join2(s, part[p * a.part_stride]);
   }
-  lds[chain][x] = s;
-  __syncthreads();
+  lds[threadIdx.x] = s;
+#pragma unroll
+  for (uint32_t n = chains / 2; n > 0; n /= 2) {
+    __syncthreads();
+    if (chain < n) lds[threadIdx.x] = join2(lds[threadIdx.x], lds[threadIdx.x + n * JT]);
+  }
   if (chain || t >= a.tokens) return;
-#pragma unroll 8
-  for (int k = 1; k < kJoinLanes; ++k) s = join2(s, lds[k][x]);
+  s = lds[threadIdx.x];
   const float lse = (s.x + __builtin_log2f(s.y)) * kLn2;
   if (a.lse) a.lse[t] = lse;
   if (a.loss) {
@@ -803,6 +809,7 @@ template <int T, int BN, bool BWD> hipError_t run(const XentCall& c, const XentP
     l.idx = (const int32_t*)(ws + p.idx);
   } else {
     a.part = (float2*)(ws + p.part);
+    a.parts = p.tiles * p.parts;
     a.zt = (float*)(ws + p.zt);
   }
   l.src = c.hidden;
@@ -823,7 +830,6 @@ template <int T, int BN, bool BWD> hipError_t run(const XentCall& c, const XentP
   else if (!BWD && direct) piece = nt <= kMaxTiles / p.tiles ? p.tiles : kMaxTiles / nt ? (uint32_t)(kMaxTiles / nt) : 1;
   for (a.tile0 = 0; a.tile0 < p.tiles; a.tile0 += piece) {
     a.ntiles = p.tiles - a.tile0 < piece ? p.tiles - a.tile0 : piece;
-    a.part0 = a.tile0;
     if (!direct && (BWD || !p.few)) {
       l.tile0 = a.tile0;
       l.rows = (uint64_t)a.ntiles * kTileM;
@@ -848,9 +854,15 @@ template <int T, int BN, bool BWD> hipError_t run(const XentCall& c, const XentP
       hipLaunchKernelGGL(dhidden_join_k<T>, dim3(c.tokens < 65536 ? c.tokens : 65536, y < 1024 ? y : 1024), dim3(256), 0, s, a);
     }
   } else {
+    const uint64_t parts = (uint64_t)p.tiles * p.parts;
     const XentJoinArgs j{a.part, a.zt, c.targets, c.ignore, (int64_t)vocab, c.loss, c.lse_out,
-                         p.tiles * p.parts, c.tokens};
-    hipLaunchKernelGGL(join_k, dim3((c.tokens + kJoinTokens - 1) / kJoinTokens), dim3(kJoinTokens * kJoinLanes), 0, s, j);
+                         p.few ? 1u : c.tokens, p.few ? parts : 1u, (uint32_t)parts, c.tokens};
+    // as many chains as leave every CU a workgroup
+    const uint32_t jt = p.few ? 1 : c.tokens <= 1024 ? 4 : 16;
+    const dim3 grid((c.tokens + jt - 1) / jt), block(kJoinThreads);
+    if (jt == 1) hipLaunchKernelGGL(join_k<1>, grid, block, 0, s, j);
+    else if (jt == 4) hipLaunchKernelGGL(join_k<4>, grid, block, 0, s, j);
+    else hipLaunchKernelGGL(join_k<16>, grid, block, 0, s, j);
   }
   return hipGetLastError();
 }
