@@ -65,8 +65,16 @@ struct XentToken {
   int32_t target, pad;
 };
 
+// What the kernels of a call leave for each other.
+struct XentScalars {
+  uint32_t count;                  // counted tokens
+  float unscale_dz;
+  float w, unscale_w, h, unscale_h;  // f32 operands
+};
+
 struct XentArgs {
   XentVocab v;
+  const XentScalars* scalars;
   const uint8_t* laid;  // weights of the piece laid out, null: read where they are
   const uint8_t* h;     // hidden states laid out, [tpad][kpad]
   uint64_t laid_plane, h_plane, dz_plane;
@@ -84,10 +92,8 @@ struct XentArgs {
   // backward
   uint8_t* dz;                  // [tpad][piece]
   const XentToken* token;
-  const uint32_t* count;
   const int32_t* place;
   const int32_t* idx;
-  const float* unscale;
   float* sum;                   // [splits][tpad][kpad]
   uint32_t splits, add;
   void* dhidden;
@@ -132,7 +138,7 @@ struct XentPlan {
   uint32_t few;    // 16-token groups of a few_k workgroup, 0: logits_k
   uint32_t parts;  // (max, sum) pairs of a tile and token
   uint64_t h_plane, laid_plane, dz_plane;
-  uint64_t h, laid, dz, sum, token, idx, place, scalars, part, zt;
+  uint64_t h, laid, dz, sum, token, idx, place, scalars, most, part, zt;
   uint64_t bytes;
 };
 

@@ -18,13 +18,15 @@
 // hidden states are gathered first, so nothing in an ignored token's row (not
 // even a NaN) reaches a gradient, and a batch pays for its counted tokens only.
 //
-// f32 operands are split into bf16 planes, x = x1 + x2 + x3 exactly (8 + 8 +
-// 8 bits), and a product is the sum of the 6 plane products x_i y_j with
-// i + j <= 4, smallest first; what is left out is below 2^-24 of |x y|, an f32
-// product's rounding.  An infinite x stays whole in x1, and the five smaller products
-// read a copy of x1 that has 0 in its place (else infinity would meet the zeros and
-// the signs of the other operand's smaller parts and give NaN): a row of -inf weights
-// keeps its probability of 0.
+// f32 operands are split into two f16 parts, x s = x1 + x2 to 22 bits, and a product
+// is x2 y1 + x1 y2 + x1 y1 in f32.  What is left out (x2 y2, and the bits below x2) is
+// at most 3 x 2^-22 of |x y| and on average below an f32 product's rounding, which a sum
+// of 64 such products already exceeds; three f16 products take a fifth of one f32
+// product's time in the matrix units.  s is a power of two for all of a tensor that
+// brings its largest value to 2^15, so an element's error is never above 2^-40 of the
+// largest.  An infinite x stays whole in x1, and the two smaller products read a copy
+// of x1 that has 0 in its place (else infinity would meet the zeros and the signs of
+// the other operand's x2 and give NaN): a row of -inf weights keeps its probability 0.
 #include "mrr_gemm.hpp"
 #include "mrr_internal.hpp"
 #include "mrr_ops.hpp"
@@ -34,11 +36,11 @@ namespace mrr {
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-constexpr int kPlanes = 4, kSegs = 6;  // x1, x2, x3, x1 without infinities
+constexpr int kPlanes = 3, kSegs = 3;  // x1, x2, x1 without infinities
 
 // Plane of A and of B in segment s of an f32 product.
-__device__ __forceinline__ uint32_t seg_a(uint32_t s) { return (0x031132u >> (4 * s)) & 3u; }
-__device__ __forceinline__ uint32_t seg_b(uint32_t s) { return (0x013123u >> (4 * s)) & 3u; }
+__device__ __forceinline__ uint32_t seg_a(uint32_t s) { return (0x021u >> (4 * s)) & 3u; }
+__device__ __forceinline__ uint32_t seg_b(uint32_t s) { return (0x012u >> (4 * s)) & 3u; }
 
 // ---- layouts of operands ---------------------------------------------------------
 // A product reads rows of a multiple of 64 elements, 16-byte aligned, zeros past
@@ -50,20 +52,81 @@ struct LayoutArgs {
   uint64_t ld, rows, src_rows;
   uint8_t* dst;
   uint64_t plane;       // bytes between planes
+  const XentScalars* scalars;
   uint32_t cols, kpad, tile0, units_log2;
 };
 
 __device__ __forceinline__ void split(float x, uint32_t* p) {
-  float a = bf16_to_f32(f32_to_bf16(x));
   const bool finite = (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u;
-  // the largest values round to infinity: cut those off instead
-  if (finite && (__float_as_uint(a) & 0x7F800000u) == 0x7F800000u) a = __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
-  const float r = finite ? x - a : 0.0f;
-  const float b = bf16_to_f32(f32_to_bf16(r));
-  p[0] = f32_to_bf16(a);
-  p[1] = f32_to_bf16(b);
-  p[2] = f32_to_bf16(r - b);
-  p[3] = finite ? p[0] : 0u;
+  p[0] = f32_to_f16(x);
+  p[1] = finite ? f32_to_f16(x - f16_to_f32(p[0])) : 0u;
+  p[2] = finite ? p[0] : 0u;
+}
+
+// The power of two that brings the largest of values with these bits (of |x|, finite)
+// to at most 2^n, kept where it and its inverse are normal.
+__device__ __forceinline__ float scale_to(uint32_t most, int n) {
+  uint32_t e = (most >> 23) + ((most & 0x7FFFFFu) ? 1u : 0u);
+  e = e < 32u ? 32u : e > 254u ? 254u : e;
+  return most == 0 ? 1.0f : __uint_as_float((254u + n - e) << 23);
+}
+
+// Largest finite |x| of the weights and of the hidden states, as bits (they order as
+// the values do): one part a workgroup, joined by scale_k.
+constexpr int kMostParts = 1024;
+struct MostArgs {
+  XentVocab v;
+  const void* src;
+  uint64_t ld_w, ld_src, src_rows;
+  uint32_t* parts;  // [2][kMostParts]: weights, hidden states
+  uint32_t cols, units_log2;
+};
+
+__device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* lds) {
+#pragma unroll
+  for (int x = 32; x > 0; x >>= 1) {
+    const uint32_t o = __shfl_xor(m, x);
+    m = o > m ? o : m;
+  }
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = m;
+  __syncthreads();
+  for (uint32_t w = 0; w < blockDim.x / 64; ++w) m = lds[w] > m ? lds[w] : m;
+  return m;
+}
+
+__global__ void __launch_bounds__(256) most_k(MostArgs a) {
+  __shared__ uint32_t lds[4];
+  const uint32_t lanes = 1u << a.units_log2, per = 256u >> a.units_log2;
+  const uint32_t u0 = threadIdx.x & (lanes - 1);
+  uint32_t most = 0;
+  auto rows_of = [&](const void* base, uint64_t rows, uint64_t ld) {
+    for (uint64_t row = (uint64_t)blockIdx.x * per + (threadIdx.x >> a.units_log2); row < rows; row += (uint64_t)gridDim.x * per) {
+      const uint8_t* p = at<kF32>(base, row * ld);
+#pragma unroll 4
+      for (uint32_t c = 4 * u0; c < a.cols; c += 4 * lanes) {
+        const u32x4 x = load_raw<kF32>(p + 4 * (uint64_t)c, (int)(a.cols - c));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t u = x[e] & 0x7FFFFFFFu;
+          if (u < 0x7F800000u && u > most) most = u;
+        }
+      }
+    }
+  };
+  if (blockIdx.y) rows_of(a.src, a.src_rows, a.ld_src);
+  else
+    for (int r = 0; r < a.v.n; ++r) rows_of(a.v.w[r], a.v.rows[r], a.ld_w);
+  most = block_max(most, lds);
+  if (threadIdx.x == 0) a.parts[blockIdx.y * kMostParts + blockIdx.x] = most;
+}
+
+__global__ void __launch_bounds__(kMostParts) scale_k(const uint32_t* parts, uint32_t n, XentScalars* to) {
+  __shared__ uint32_t lds[kMostParts / 64];
+  const uint32_t most = block_max(threadIdx.x < n ? parts[blockIdx.x * kMostParts + threadIdx.x] : 0u, lds);
+  if (threadIdx.x) return;
+  const float s = scale_to(most, 15);
+  (blockIdx.x ? to->h : to->w) = s;
+  (blockIdx.x ? to->unscale_h : to->unscale_w) = 1.0f / s;
 }
 
 template <int T> __global__ void __launch_bounds__(256) layout_k(LayoutArgs a) {
@@ -90,11 +153,12 @@ template <int T> __global__ void __launch_bounds__(256) layout_k(LayoutArgs a) {
         float x[8];
         decode16<kF32>(load_raw<kF32>(src + 32 * u, n), x);
         decode16<kF32>(load_raw<kF32>(src + 32 * u + 16, n - 4), x + 4);
+        const float scale = a.src ? a.scalars->h : a.scalars->w;
         uint32_t p[kPlanes][8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           uint32_t q[kPlanes];
-          split(x[j], q);
+          split(x[j] * scale, q);
 #pragma unroll
           for (int k = 0; k < kPlanes; ++k) p[k][j] = q[k];
         }
@@ -111,7 +175,7 @@ template <int T> __global__ void __launch_bounds__(256) layout_k(LayoutArgs a) {
 
 // ---- tokens of a backward call ---------------------------------------------------
 // Counted tokens in order, what their gradient needs, and for each token its place.
-// One workgroup.  f16 gradients of logits are scaled so that the largest dloss is
+// One workgroup.  Gradients of logits held in f16 are scaled so that the largest dloss is
 // 2^14: p dloss goes far below f16's smallest normal otherwise.  The scale is a
 // power of two and is taken out of the f32 sums of both gradients.
 struct TokensArgs {
@@ -123,8 +187,7 @@ struct TokensArgs {
   XentToken* token;  // [tpad]
   int32_t* idx;      // [tpad]: source row, -1 past the counted ones
   int32_t* place;    // [tokens]: place among the counted ones, -1: ignored
-  uint32_t* count;
-  float* unscale;
+  XentScalars* scalars;
   uint32_t tokens, tpad;
   int scaled;
 };
@@ -142,21 +205,8 @@ __global__ void __launch_bounds__(kTokensThreads) tokens_k(TokensArgs a) {
       const uint32_t u = __float_as_uint(a.dloss[t * a.dloss_stride]) & 0x7FFFFFFFu;
       if (target != a.ignore && target >= 0 && target < a.vocab && u < 0x7F800000u && u > most) most = u;
     }
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) {
-      const uint32_t o = __shfl_xor(most, m);
-      most = o > most ? o : most;
-    }
-    if (lane == 0) sums[wave] = most;
+    scale = scale_to(block_max(most, sums), 14);
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kTokensThreads / 64; ++w) most = sums[w] > most ? sums[w] : most;
-    __syncthreads();
-    // the power of two at or above it, kept where scale and its inverse are normal
-    uint32_t e = (most >> 23) + ((most & 0x7FFFFFu) ? 1u : 0u);
-    e = e < 27 ? 27 : e > 254 ? 254 : e;
-    if (most == 0) e = 127;
-    scale = __uint_as_float((268u - e) << 23);  // 2^14 / 2^(e - 127)
   }
   uint32_t before = 0;
   for (uint32_t t0 = 0; t0 < a.tokens; t0 += kTokensThreads) {
@@ -187,8 +237,8 @@ __global__ void __launch_bounds__(kTokensThreads) tokens_k(TokensArgs a) {
     a.idx[t] = -1;
   }
   if (tid == 0) {
-    *a.count = before;
-    *a.unscale = 1.0f / scale;
+    a.scalars->count = before;
+    a.scalars->unscale_dz = 1.0f / scale;
   }
 }
 
@@ -240,7 +290,7 @@ __global__ void __launch_bounds__(kGemmThreads) logits_k(XentArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
   uint32_t mt, nt;
   if (!tile_of(blockIdx.x, a.ntiles, a.tpad / BN, mt, nt)) return;
-  const uint32_t tokens = BWD ? *a.count : a.tokens;
+  const uint32_t tokens = BWD ? a.scalars->count : a.tokens;
   const uint32_t t0 = nt * BN, tile = a.tile0 + mt;
   if (t0 >= tokens) return;
   int sh = 0;
@@ -276,6 +326,7 @@ __global__ void __launch_bounds__(kGemmThreads) logits_k(XentArgs a) {
   };
   Prod p;
   p.run((int)(a.kpad / kTileK) * SEG, (lds8*)lds, src);
+  const float unscale = SEG > 1 ? a.scalars->unscale_w * a.scalars->unscale_h : 1.0f;
 
   const int wm = wave / Prod::WN, wn = wave % Prod::WN;
   const uint32_t first = a.v.first_row[sh] + row0;  // of the whole vocabulary
@@ -292,7 +343,7 @@ __global__ void __launch_bounds__(kGemmThreads) logits_k(XentArgs a) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const uint32_t m = (wm * Prod::FM + i) * 32 + acc_row(lane, e);
-          const float z = p.acc[i][j][e];
+          const float z = SEG > 1 ? p.acc[i][j][e] * unscale : p.acc[i][j][e];
           if (m == hit) a.zt[t] = z;
           const float x = m < left ? z : -__builtin_inff();
           p.acc[i][j][e] = x;
@@ -319,7 +370,9 @@ __global__ void __launch_bounds__(kGemmThreads) logits_k(XentArgs a) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const uint32_t m = (wm * Prod::FM + i) * 32 + 8 * q + 4 * (lane >> 5);
-          const float z[4] = {p.acc[i][j][4 * q], p.acc[i][j][4 * q + 1], p.acc[i][j][4 * q + 2], p.acc[i][j][4 * q + 3]};
+          float z[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[e] = SEG > 1 ? p.acc[i][j][4 * q + e] * unscale : p.acc[i][j][4 * q + e];
           store_dz<SEG == 1 ? T : (int)kF32>(row, a.dz_plane, m, z, tk, hit, live ? left : 0u);
         }
     }
@@ -351,7 +404,7 @@ template <int T, int NT, int R, bool BWD> __global__ void __launch_bounds__(256)
   constexpr int V = Vec<T>::VW, B = 8 * V;  // elements of a load, and of a 128-byte block
   constexpr int U = R * NT >= 8 ? 2 : 4;    // blocks in flight
   __shared__ f32x4v red[4][R * NT][64];
-  const uint32_t tokens = BWD ? *a.count : a.tokens;
+  const uint32_t tokens = BWD ? a.scalars->count : a.tokens;
   const uint32_t t0 = blockIdx.y * (16 * NT);
   // dz of the last 64 tokens' places past the counted ones is zero
   if (t0 >= (BWD ? (tokens + kTileK - 1) / kTileK * kTileK : tokens)) return;
@@ -483,7 +536,7 @@ template <int T, int BN, int SEG> __global__ void __launch_bounds__(kGemmThreads
   uint32_t mt, nt;
   if (!tile_of(blockIdx.x, (a.kpad + kTileM - 1) / kTileM, a.tpad / BN, mt, nt)) return;
   const uint32_t t0 = nt * BN, c0 = mt * kTileM;
-  if (t0 >= *a.count) return;
+  if (t0 >= a.scalars->count) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t blocks = a.ntiles * (kTileM / kTileK);  // of 64 rows
   const uint32_t split = blockIdx.y;
@@ -565,7 +618,7 @@ template <int T, int OUT, int SEG> __global__ void __launch_bounds__(kGemmThread
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   uint32_t col = c0 + col_src_chunk(tid) * 8;
   col = (col < a.kpad ? col : a.kpad - 8) * 2;
-  const uint32_t blocks = (*a.count + kTileK - 1) / kTileK;  // of 64 tokens; those past the last have dz 0
+  const uint32_t blocks = (a.scalars->count + kTileK - 1) / kTileK;  // of 64 tokens; those past the last have dz 0
   uint32_t k = 0, seg = 0;
   auto src = [&](int s, const uint8_t*& pa, const uint8_t*& pb, uint32_t (&oa)[Prod::LA], uint32_t (&ob)[Prod::LB]) {
     if (s == 0) {
@@ -586,7 +639,7 @@ template <int T, int OUT, int SEG> __global__ void __launch_bounds__(kGemmThread
   Prod p;
   p.run((int)blocks * SEG, (lds8*)lds, src);
 
-  const float unscale = *a.unscale;
+  const float unscale = a.scalars->unscale_dz * (SEG > 1 ? a.scalars->unscale_h : 1.0f);
   const int wm = wave / Prod::WN, wn = wave % Prod::WN;
 #pragma unroll
   for (int j = 0; j < Prod::FN; ++j) {
@@ -648,7 +701,7 @@ template <int JT> __global__ void __launch_bounds__(kJoinThreads) join_k(XentJoi
 // Gradient rows of the hidden states: the splits' sums in order, rounded once; zeros
 // for a token that has no loss.
 template <int T> __global__ void __launch_bounds__(256) dhidden_join_k(XentArgs a) {
-  const float unscale = *a.unscale;
+  const float unscale = a.scalars->unscale_dz * (T == kF32 ? a.scalars->unscale_w : 1.0f);
   for (uint32_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
     const int32_t from = a.place[t];
     for (uint32_t c = 4 * (blockIdx.y * 256 + threadIdx.x); c < a.cols; c += 1024 * gridDim.y) {
@@ -724,12 +777,13 @@ XentPlan xent_plan(uint32_t tokens, uint32_t cols, const size_t* rows, int nrank
     p.token = take((uint64_t)p.tpad * sizeof(XentToken));
     p.idx = take((uint64_t)p.tpad * 4);
     p.place = take((uint64_t)tokens * 4);
-    p.scalars = take(8);
   } else {
     p.parts = p.few ? kTileM / (16 * p.few) : p.bn == 256 ? 2 : 4;  // of a tile
     p.part = take(tiles * p.parts * tokens * sizeof(float2));
     p.zt = take((uint64_t)tokens * 4);
   }
+  p.scalars = take(sizeof(XentScalars));
+  p.most = take(t == kF32 ? 2 * kMostParts * 4 : 0);
   p.bytes = at;
   return p;
 }
@@ -754,7 +808,7 @@ template <int T, bool BWD> void few(const XentArgs& a, uint32_t few, hipStream_t
 
 // T: type of the caller's tensors.  M: type that multiplies.
 template <int T, int BN, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, hipStream_t s) {
-  constexpr int M = T == kF32 ? kBF16 : T, SEG = T == kF32 ? kSegs : 1;
+  constexpr int M = T == kF32 ? kF16 : T, SEG = T == kF32 ? kSegs : 1;
   uint8_t* ws = (uint8_t*)c.workspace;
   XentArgs a{};
   uint64_t vocab = 0;
@@ -784,7 +838,10 @@ template <int T, int BN, bool BWD> hipError_t run(const XentCall& c, const XentP
   a.hidden = c.hidden;
   a.ld_h = c.ld_hidden;
   a.ld_w = c.ld_weight;
+  XentScalars* scalars = (XentScalars*)(ws + p.scalars);
+  a.scalars = scalars;
   LayoutArgs l{};
+  l.scalars = scalars;
   l.v = a.v;
   l.cols = c.cols;
   l.kpad = p.kpad;
@@ -797,20 +854,28 @@ template <int T, int BN, bool BWD> hipError_t run(const XentCall& c, const XentP
     a.token = (XentToken*)(ws + p.token);
     a.place = (int32_t*)(ws + p.place);
     a.idx = (const int32_t*)(ws + p.idx);
-    a.count = (uint32_t*)(ws + p.scalars);
-    a.unscale = (float*)(ws + p.scalars + 4);
     a.dhidden = c.dhidden;
     a.ld_dh = c.ld_hidden;
     a.ld_dw = c.ld_weight;
     const TokensArgs t{c.targets, c.lse, c.dloss, c.dloss_stride, c.ignore, (int64_t)vocab, (XentToken*)(ws + p.token),
-                       (int32_t*)(ws + p.idx), (int32_t*)(ws + p.place), (uint32_t*)(ws + p.scalars),
-                       (float*)(ws + p.scalars + 4), c.tokens, p.tpad, T == kF16};
+                       (int32_t*)(ws + p.idx), (int32_t*)(ws + p.place), scalars, c.tokens, p.tpad, T != kBF16};
     hipLaunchKernelGGL(tokens_k, dim3(1), dim3(kTokensThreads), 0, s, t);
     l.idx = (const int32_t*)(ws + p.idx);
   } else {
     a.part = (float2*)(ws + p.part);
     a.parts = p.tiles * p.parts;
     a.zt = (float*)(ws + p.zt);
+  }
+  if constexpr (T == kF32) {
+    if (BWD || !p.few) {
+      MostArgs m{a.v, c.hidden, c.ld_weight, c.ld_hidden, c.tokens, (uint32_t*)(ws + p.most), c.cols, 0};
+      while (m.units_log2 < 8 && (4u << m.units_log2) < c.cols) ++m.units_log2;
+      // about 64 KiB a workgroup
+      const uint64_t n = (vocab * c.cols >> 14) + 1;
+      const uint32_t grid = n < (uint64_t)kMostParts ? (uint32_t)n : (uint32_t)kMostParts;
+      hipLaunchKernelGGL(most_k, dim3(grid, 2), dim3(256), 0, s, m);
+      hipLaunchKernelGGL(scale_k, dim3(2), dim3(kMostParts), 0, s, (const uint32_t*)m.parts, grid, scalars);
+    }
   }
   l.src = c.hidden;
   l.ld = c.ld_hidden;

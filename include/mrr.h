@@ -484,8 +484,9 @@ mrr_status mrr_layernorm_bwd(const void* dout, const void* sum, const void* weig
  *          computed); it may be any value.  Any other target outside [0, vocabulary)
  *          gives the loss NaN and counts as ignored in the gradient.
  * loss, lse: receive tokens f32 values each; one of them may be NULL.
- * f32 products are computed in the matrix units as sums of products of bf16 parts,
- * exact to less than an f32 product's rounding; every sum is f32.
+ * Every sum is f32.  Up to 64 tokens f32 multiplies as f32; above, as sums of
+ * products of two f16 parts of each operand (22 bits, to 2^-40 of a tensor's largest
+ * value), which is as exact as an f32 product and five times as fast.
  * workspace: device, 16-byte aligned, mrr_linear_xent_workspace_bytes(...,
  * backward 0) bytes at least (else MRR_ESCRATCH), contents irrelevant before and
  * after.  It may not overlap anything else.
@@ -515,8 +516,8 @@ mrr_status mrr_linear_xent_fwd(const void* hidden, const void* const* weights, c
  *   dhidden[t][c]  = round( sum over v of dz[t][v] * weight[v][c] )
  *   dweight[v][c]  = round( sum over t of dz[t][v] * hidden[t][c] )
  * The logits are computed again, a piece of the vocabulary at a time; the piece's
- * dz is held in dtype (f16: scaled so that the largest |dloss| is 2^14, f32: as
- * bf16 parts that hold all its bits), which rounds each dz once; sums are f32.
+ * dz is held in dtype (f16: scaled so that the largest |dloss| is 2^14; f32: so, in
+ * two f16 parts), which rounds each dz once; sums are f32.
  * Ignored tokens are left out: their dhidden is zero and nothing in their rows,
  * NaN included, reaches a gradient.
  *

@@ -2,9 +2,10 @@
 
 Tolerances, with u = 2^-24 (half a step of f32 relative to the value) and eps/2
 for half a step of the stored type:
-- a logit is a sum of C exact products (f32: of 6 C products of parts, which leave
-  out less than 2^-24 of each product), off by at most its count of terms times u
-  times the sum of their sizes;
+- a logit is a sum of C exact products, off by at most its count of terms times u
+  times the sum of their sizes.  f32: of 3 C products of f16 parts, which leave out
+  3 x 2^-22 of each product, and parts of an element no smaller than 2^-40 of the
+  tensor's largest;
 - exp is off by 2 u and by what its argument's rounding makes of it, u per unit of
   the argument on the way in (twice: the product with log2 e, its constant);
 - lse moves by the logits' errors weighted with p, by the chain of its sum (64 in a
@@ -62,9 +63,12 @@ class Case:
 
     def exact(self, lse=None, dloss=None):
         h, w = self.hidden.double(), torch.cat([x.double() for x in self.weights])
-        terms = self.cols * (6 if self.t == "f32" else 1) + (2 if self.t == "f32" else 0)
+        f32 = self.t == "f32"
+        terms = self.cols * 3 + 12 if f32 else self.cols
         z = h @ w.T
         ez = terms * U * (h.abs() @ w.abs().T)
+        if f32:
+            ez = ez + 2.0 ** -40 * (h.abs().sum(1)[:, None] * w.abs().max() + w.abs().sum(1)[None] * h.abs().max())
         self.lse = torch.logsumexp(z, 1)
         p = (z - self.lse[:, None]).exp()
         size = (p * z.abs()).sum(1) + z.abs().amax(1)
@@ -85,7 +89,9 @@ class Case:
         hit = torch.zeros_like(p).scatter_(1, at, 1.0) * counted[:, None]
         dz = (p - hit) * dl[:, None]
         rel, sub = half_step(self.t)
-        sub = sub * 2 ** -13 * float(dl.abs().max()) if self.t == "f16" else 0.0
+        if f32:
+            rel, sub = 2.0 ** -22, half_step("f16")[1]
+        sub = sub * 2 ** -13 * float(dl.abs().max()) if self.t != "bf16" else 0.0
         edz = (ep + 2 * U) * dl.abs()[:, None]
         edz = edz + rel * (dz.abs() + edz) + sub * counted[:, None]
         orel, osub = half_step(self.t)
@@ -93,11 +99,13 @@ class Case:
         def grad(want, e):
             return want, (e + orel * (want.abs() + e) + osub) * 1.01
 
-        n = 6 if self.t == "f32" else 1
-        # a gradient left to one piece at a time adds the pieces too: 64 covers them and the splits
-        self.dhidden = grad(dz @ w, edz @ w.abs() + U * (n * vocab + 256) * (dz.abs() @ w.abs()))
+        # f32: as for a logit; a gradient left to one piece at a time adds the pieces too
+        n, part = (3, 2.0 ** -40) if f32 else (1, 0.0)
+        self.dhidden = grad(dz @ w, edz @ w.abs() + U * (n * vocab + 256) * (dz.abs() @ w.abs())
+                            + part * w.abs().max() * dz.abs().sum(1)[:, None])
         dw, edw = grad(dz.T.contiguous() @ h, edz.T.contiguous() @ h.abs()
-                       + U * (n * self.tokens + 64) * (dz.abs().T.contiguous() @ h.abs()))
+                       + U * (n * self.tokens + 64) * (dz.abs().T.contiguous() @ h.abs())
+                       + part * h.abs().max() * dz.abs().sum(0)[:, None])
         self.dweights = list(zip(dw.split(self.rows), edw.split(self.rows)))
 
     def workspace(self, backward):
