@@ -1,6 +1,5 @@
 // mrr_gemm.hpp -- the tile product that the cross entropy kernels share: one
-// workgroup computes D[m][n] = sum over k of A[m][k] B[n][k] for a tile of
-// 256 m by BN n in f32, from 16-bit operands, and hands each wave its part.
+// workgroup computes D[m][n] = sum over k of A[m][k] B[n][k] for a tile of S m by S n in f32, from 16-bit operands, and hands each wave its part.
 //
 // An operand lies in memory either with k contiguous ("row": a row for each m)
 // or with m contiguous ("col": a row for each k).  Both reach LDS by loads that
@@ -11,8 +10,11 @@
 // global address, since the LDS side of the load is fixed) so that the lanes
 // that LDS serves together touch different banks.
 //
-// 512 threads, 8 waves, 2 a SIMD; a wave holds 128 x 64 (BN 256) or 64 x 64
-// (BN 128) accumulators in 32x32x16 matrix instructions.  The fragments of the
+// Two sizes of tile, S x S.  256: 8 waves, 2 a SIMD, each with 128 x 64 accumulators;
+// a stage's products take 2048 cycles of a CU's matrix units against 1536 of LDS reads.
+// 128: 4 waves with 64 x 64 each, two workgroups a CU; as many cycles of LDS reads as of
+// products, but four times the workgroups, for calls with too few large tiles.  Matrix
+// instructions are 32x32x16.  The fragments of the
 // next 16 k are read while those of the present ones multiply, over the end of a
 // stage as well: the one barrier of a stage stands before its last quarter, when
 // all its reads are done, so that the stage's buffer can be refilled and the next
@@ -28,9 +30,9 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kGemmThreads = 512;
-constexpr int kTileM = 256;  // also the unit that vocabulary shards are padded to
+constexpr int kTileV = 256;  // vocabulary shards are padded to multiples of this
 constexpr int kTileK = 64;
+constexpr int tile_threads(int s) { return s == 256 ? 512 : 256; }
 
 template <int T> __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
   if constexpr (T == kF16)
@@ -43,9 +45,12 @@ template <int T> __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16
 __device__ __forceinline__ int acc_row(int lane, int i) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
 
 // ---- addresses -----------------------------------------------------------------
-// Row operand: a stage is [rows][64 k], 128 bytes a row, 8 chunks of 16.  Load i
-// of thread t brings row 64 i + t / 8; chunk c of row r lies at position
+// Row operand: a stage is [S rows][64 k], 128 bytes a row, 8 chunks of 16.  Load i
+// of thread t brings row i threads / 8 + t / 8; chunk c of row r lies at position
 // c ^ f(r), f(r) = (r & 7) ^ (r >> 3 & 1): any 8 rows, and any 16 over 64 banks, differ.
+template <int S> __device__ __forceinline__ uint32_t row_src_row(int tid, int i) {
+  return (uint32_t)(i * (tile_threads(S) / 8) + (tid >> 3));
+}
 __device__ __forceinline__ uint32_t row_src_chunk(int tid) {
   return (uint32_t)((tid & 7) ^ ((tid >> 3) & 7) ^ ((tid >> 6) & 1));
 }
@@ -55,18 +60,19 @@ __device__ __forceinline__ uint32_t row_frag(int row0, int lane) {
   const int r = lane & 31;
   return (uint32_t)((row0 + r) * 128 + (((lane >> 5) ^ (r & 7) ^ ((r >> 3) & 1)) << 4));
 }
-// Col operand: a stage is [64 k][256 m], 512 bytes a k.  Load i of thread t
-// brings k 16 i + t / 32; 64-byte units are at unit ^ (k & 7).
-__device__ __forceinline__ uint32_t col_src_chunk(int tid) {
-  return (uint32_t)((tid & 31) ^ (((tid >> 5) & 7) << 2));
+// Col operand: a stage is [64 k][S m], 2 S bytes a k.  Load i of thread t brings k
+// 16 i + t / (S / 8); 64-byte units are at unit ^ (k modulo their count).
+template <int S> __device__ __forceinline__ uint32_t col_src_k(int tid, int i) { return (uint32_t)(16 * i + tid / (S / 8)); }
+template <int S> __device__ __forceinline__ uint32_t col_src_chunk(int tid) {
+  return (uint32_t)((tid % (S / 8)) ^ ((tid / (S / 8) % (S / 32)) << 2));
 }
 // A transposing read serves 16 lanes with a block of 4 k x 16 m: lane j of the
 // 16 addresses k j / 4, m 4 (j % 4), and receives the 4 k of m j.  Byte offset
-// for the 32 m from m0 on, k 0..3 (+ 4 for r = 1) and 8..11; 16 k are 8192 bytes.
-__device__ __forceinline__ uint32_t col_frag(int m0, int r, int lane) {
+// for the 32 m from m0 on, k 0..3 (+ 4 for r = 1) and 8..11.
+template <int S> __device__ __forceinline__ uint32_t col_frag(int m0, int r, int lane) {
   const int k = 8 * (lane >> 5) + 4 * r + ((lane >> 2) & 3);
-  const int unit = (m0 >> 5) ^ (k & 7);
-  return (uint32_t)(k * 512 + unit * 64 + 32 * ((lane >> 4) & 1) + 8 * (lane & 3));
+  const int unit = (m0 >> 5) ^ (k % (S / 32));
+  return (uint32_t)(k * (2 * S) + unit * 64 + 32 * ((lane >> 4) & 1) + 8 * (lane & 3));
 }
 
 typedef __attribute__((address_space(3))) uint8_t lds8;
@@ -91,12 +97,12 @@ __device__ __forceinline__ void load_lds(const uint8_t* base, uint32_t off, lds8
 
 // The product over `steps` stages.  src(s, pa, pb, oa, ob) sets the (wave-uniform)
 // addresses and the lane offsets of stage s; it is called once for each s in order.
-template <int T, bool ACOL, bool BCOL, int BN> struct Tile {
-  static constexpr int WN = BN == 256 ? 4 : 2, WM = 8 / WN;       // waves along n and m
-  static constexpr int FM = kTileM / WM / 32, FN = BN / WN / 32;  // 32 x 32 tiles of a wave
-  static constexpr int SA = kTileM * kTileK * 2, SB = BN * kTileK * 2;  // bytes of a stage
-  static constexpr int LA = SA / 8192, LB = SB / 8192;                  // loads of a lane
-  static constexpr int kLds = 2 * (SA + SB);                            // A, A, B, B
+template <int T, bool ACOL, bool BCOL, int S> struct Tile {
+  static constexpr int WN = S == 256 ? 4 : 2, WM = 2;        // waves along n and m
+  static constexpr int FM = S / WM / 32, FN = S / WN / 32;   // 32 x 32 tiles of a wave
+  static constexpr int kStage = S * kTileK * 2;              // bytes of an operand's stage
+  static constexpr int kLoad = tile_threads(S) * 16, L = kStage / kLoad;  // bytes of a load, loads of a lane
+  static constexpr int kLds = 4 * kStage;                    // A, A, B, B
   f32x16 acc[FM][FN];
 
   template <class Src> __device__ __forceinline__ void run(int steps, lds8* lds, Src&& src) {
@@ -113,29 +119,29 @@ template <int T, bool ACOL, bool BCOL, int BN> struct Tile {
     // offsets of this lane's fragments, and of its wave's loads, in the present stage
     constexpr int NA = ACOL ? 2 * FM : 4, NB = BCOL ? 2 * FN : 4;
     uint32_t fa[NA], fb[NB];
-    uint32_t wa = (uint32_t)wave * 1024, wb = 2 * SA + (uint32_t)wave * 1024;
+    uint32_t wa = (uint32_t)wave * 1024, wb = 2 * kStage + (uint32_t)wave * 1024;
 #pragma unroll
-    for (int i = 0; i < NA; ++i) fa[i] = ACOL ? col_frag(m0 + 32 * (i >> 1), i & 1, lane) : row_frag(m0, lane) ^ (i * 32);
+    for (int i = 0; i < NA; ++i) fa[i] = ACOL ? col_frag<S>(m0 + 32 * (i >> 1), i & 1, lane) : row_frag(m0, lane) ^ (i * 32);
 #pragma unroll
     for (int i = 0; i < NB; ++i)
-      fb[i] = 2 * SA + (BCOL ? col_frag(n0 + 32 * (i >> 1), i & 1, lane) : row_frag(n0, lane) ^ (i * 32));
+      fb[i] = 2 * kStage + (BCOL ? col_frag<S>(n0 + 32 * (i >> 1), i & 1, lane) : row_frag(n0, lane) ^ (i * 32));
     const uint8_t *pa, *pb;
-    uint32_t oa[LA], ob[LB];
+    uint32_t oa[L], ob[L];
     u32x4 va[2][FM], vb[2][FN];
 
     auto fetch = [&](int i) {
-      if (i < LA) load_lds(pa, oa[i < LA ? i : 0], lds + wa + i * 8192);
-      else load_lds(pb, ob[i < LA ? 0 : i - LA], lds + wb + (i - LA) * 8192);
+      if (i < L) load_lds(pa, oa[i % L], lds + wa + i * kLoad);
+      else load_lds(pb, ob[i % L], lds + wb + (i - L) * kLoad);
     };
     auto read = [&](int f, int kk) {
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
-        if constexpr (BCOL) vb[f][j] = read_col(lds + fb[2 * j] + kk * 8192, lds + fb[2 * j + 1] + kk * 8192);
+        if constexpr (BCOL) vb[f][j] = read_col(lds + fb[2 * j] + kk * (32 * S), lds + fb[2 * j + 1] + kk * (32 * S));
         else vb[f][j] = read_row(lds + fb[kk] + j * 4096);
       }
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
-        if constexpr (ACOL) va[f][i] = read_col(lds + fa[2 * i] + kk * 8192, lds + fa[2 * i + 1] + kk * 8192);
+        if constexpr (ACOL) va[f][i] = read_col(lds + fa[2 * i] + kk * (32 * S), lds + fa[2 * i + 1] + kk * (32 * S));
         else va[f][i] = read_row(lds + fa[kk] + i * 4096);
       }
     };
@@ -163,23 +169,23 @@ template <int T, bool ACOL, bool BCOL, int BN> struct Tile {
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < NA; ++i) fa[i] ^= SA;
+      for (int i = 0; i < NA; ++i) fa[i] ^= kStage;
 #pragma unroll
-      for (int i = 0; i < NB; ++i) fb[i] ^= SB;
+      for (int i = 0; i < NB; ++i) fb[i] ^= kStage;
     };
     src(0, pa, pb, oa, ob);
 #pragma unroll
-    for (int i = 0; i < LA + LB; ++i) fetch(i);
-    wa ^= SA;
-    wb ^= SB;
+    for (int i = 0; i < 2 * L; ++i) fetch(i);
+    wa ^= kStage;
+    wb ^= kStage;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (steps > 1) {
       src(1, pa, pb, oa, ob);
 #pragma unroll
-      for (int i = 0; i < LA + LB; ++i) fetch(i);
-      wa ^= SA;
-      wb ^= SB;
+      for (int i = 0; i < 2 * L; ++i) fetch(i);
+      wa ^= kStage;
+      wb ^= kStage;
     }
     read(0, 0);
     int s = 0;
@@ -192,13 +198,13 @@ template <int T, bool ACOL, bool BCOL, int BN> struct Tile {
       read(0, 0);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int p = 0; p < kProducts || p < LA + LB; ++p) {
+      for (int p = 0; p < kProducts || p < 2 * L; ++p) {
         if (p < kProducts) product(1, p);
-        if (p < LA + LB) fetch(p);
+        if (p < 2 * L) fetch(p);
         __builtin_amdgcn_sched_barrier(0);
       }
-      wa ^= SA;
-      wb ^= SB;
+      wa ^= kStage;
+      wb ^= kStage;
     }
     for (; s + 1 < steps; ++s) {
       quarter(0, 1);

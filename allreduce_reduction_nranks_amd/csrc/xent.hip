@@ -140,10 +140,10 @@ template <int T> __global__ void __launch_bounds__(256) layout_k(LayoutArgs a) {
       const int64_t r = a.idx ? (int64_t)a.idx[row] : row < a.src_rows ? (int64_t)row : -1;
       if (r >= 0) src = at<T>(a.src, (uint64_t)r * a.ld);
     } else {
-      const uint32_t tile = a.tile0 + (uint32_t)(row / kTileM);
+      const uint32_t tile = a.tile0 + (uint32_t)(row / kTileV);
       int sh = 0;
       while (tile >= a.v.first_tile[sh + 1]) ++sh;
-      const uint32_t r = (tile - a.v.first_tile[sh]) * kTileM + (uint32_t)(row % kTileM);
+      const uint32_t r = (tile - a.v.first_tile[sh]) * kTileV + (uint32_t)(row % kTileV);
       if (r < a.v.rows[sh]) src = at<T>(a.v.w[sh], (uint64_t)r * a.ld);
     }
     for (uint32_t u = u0; u < units; u += lanes) {
@@ -281,39 +281,40 @@ __device__ __forceinline__ void store_dz(uint8_t* row, uint64_t plane, uint32_t 
   for (int b = 0; b < P; ++b) *reinterpret_cast<u32x2*>(row + b * plane + m * 2) = u32x2{w[b][0], w[b][1]};
 }
 
-// Logits of one tile of 256 vocabulary rows by BN tokens.  Forward: reduced to a
+// Logits of one tile of S vocabulary rows by S tokens.  Forward: reduced to a
 // (max, sum) pair in base 2 for each wave's rows, and the target's logit.
 // Backward: dz, vocabulary contiguous.
-template <int T, int BN, bool BWD, int SEG>
-__global__ void __launch_bounds__(kGemmThreads) logits_k(XentArgs a) {
-  typedef Tile<T, false, false, BN> Prod;
+template <int T, int S, bool BWD, int SEG>
+__global__ void __launch_bounds__(tile_threads(S)) logits_k(XentArgs a) {
+  typedef Tile<T, false, false, S> Prod;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
   uint32_t mt, nt;
-  if (!tile_of(blockIdx.x, a.ntiles, a.tpad / BN, mt, nt)) return;
+  constexpr uint32_t per = kTileV / S;  // of a vocabulary tile
+  if (!tile_of(blockIdx.x, a.ntiles * per, a.tpad / S, mt, nt)) return;
   const uint32_t tokens = BWD ? a.scalars->count : a.tokens;
-  const uint32_t t0 = nt * BN, tile = a.tile0 + mt;
+  const uint32_t t0 = nt * S, tile = a.tile0 + mt / per;
   if (t0 >= tokens) return;
   int sh = 0;
   while (tile >= a.v.first_tile[sh + 1]) ++sh;
-  const uint32_t row0 = (tile - a.v.first_tile[sh]) * kTileM;  // of the shard
-  const uint32_t left = a.v.rows[sh] - row0 < (uint32_t)kTileM ? a.v.rows[sh] - row0 : (uint32_t)kTileM;
+  const uint32_t row0 = (tile - a.v.first_tile[sh]) * kTileV + mt % per * S, rows = a.v.rows[sh];  // of the shard
+  const uint32_t left = row0 < rows ? (rows - row0 < (uint32_t)S ? rows - row0 : (uint32_t)S) : 0u;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-  const uint8_t* wa = a.laid ? a.laid + (uint64_t)mt * kTileM * a.ldw : (const uint8_t*)a.v.w[sh] + (uint64_t)row0 * a.ldw;
+  // rows past the shard: any that exists
+  const uint32_t at0 = row0 < rows ? row0 : rows - 1, have = a.laid ? (uint32_t)S : left ? left : 1u;
+  const uint8_t* wa = a.laid ? a.laid + (uint64_t)mt * S * a.ldw : (const uint8_t*)a.v.w[sh] + (uint64_t)at0 * a.ldw;
   const uint8_t* hb = a.h + (uint64_t)t0 * a.ldh;
   uint32_t k = 0, seg = 0;
   const uint32_t kend = a.kpad * 2;
-  const uint32_t have = a.laid ? (uint32_t)kTileM : left;
-  auto src = [&](int s, const uint8_t*& pa, const uint8_t*& pb, uint32_t (&oa)[Prod::LA], uint32_t (&ob)[Prod::LB]) {
+  auto src = [&](int s, const uint8_t*& pa, const uint8_t*& pb, uint32_t (&oa)[Prod::L], uint32_t (&ob)[Prod::L]) {
     if (s == 0) {
       const uint32_t c = row_src_chunk(tid) * 16;
 #pragma unroll
-      for (int i = 0; i < Prod::LA; ++i) {
-        const uint32_t r = 64 * i + (tid >> 3);
-        oa[i] = (r < have ? r : have - 1) * a.ldw + c;  // rows past the shard: any that exists
+      for (int i = 0; i < Prod::L; ++i) {
+        const uint32_t r = row_src_row<S>(tid, i);
+        oa[i] = (r < have ? r : have - 1) * a.ldw + c;
+        ob[i] = r * a.ldh + c;
       }
-#pragma unroll
-      for (int i = 0; i < Prod::LB; ++i) ob[i] = (64 * i + (tid >> 3)) * a.ldh + c;
     }
     pa = wa + k;
     pb = hb + k;
@@ -359,12 +360,12 @@ __global__ void __launch_bounds__(kGemmThreads) logits_k(XentArgs a) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(p.acc[i][j][e], kLog2e, -base));
       s += __shfl_xor(s, 32);
-      if (lane < 32 && t < tokens) a.part[((uint64_t)(a.tile0 + mt) * Prod::WM + wm) * a.tokens + t] = make_float2(top, s);
+      if (lane < 32 && t < tokens) a.part[(((uint64_t)a.tile0 * per + mt) * Prod::WM + wm) * a.tokens + t] = make_float2(top, s);
     } else {
       const XentToken tk = a.token[t];
       const bool live = t < tokens;
       const uint32_t hit = tk.target >= 0 && (uint32_t)tk.target - first < left ? (uint32_t)tk.target - first : ~0u;
-      uint8_t* row = a.dz + (uint64_t)t * a.lddz + (uint64_t)mt * kTileM * 2;
+      uint8_t* row = a.dz + (uint64_t)t * a.lddz + (uint64_t)mt * S * 2;
 #pragma unroll
       for (int i = 0; i < Prod::FM; ++i)
 #pragma unroll
@@ -408,11 +409,11 @@ template <int T, int NT, int R, bool BWD> __global__ void __launch_bounds__(256)
   const uint32_t t0 = blockIdx.y * (16 * NT);
   // dz of the last 64 tokens' places past the counted ones is zero
   if (t0 >= (BWD ? (tokens + kTileK - 1) / kTileK * kTileK : tokens)) return;
-  constexpr uint32_t per = kTileM / (16 * R);
+  constexpr uint32_t per = kTileV / (16 * R);
   const uint32_t mt = blockIdx.x / per, tile = a.tile0 + mt, sub = blockIdx.x % per * (16 * R);
   int sh = 0;
   while (tile >= a.v.first_tile[sh + 1]) ++sh;
-  const uint32_t row0 = (tile - a.v.first_tile[sh]) * kTileM + sub, rows = a.v.rows[sh];
+  const uint32_t row0 = (tile - a.v.first_tile[sh]) * kTileV + sub, rows = a.v.rows[sh];
   const uint32_t left = row0 < rows ? (rows - row0 < 16u * R ? rows - row0 : 16u * R) : 0u;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   f32x4v acc[R][NT];
@@ -518,7 +519,7 @@ template <int T, int NT, int R, bool BWD> __global__ void __launch_bounds__(256)
   } else {
     const XentToken tk = a.token[t];
     const uint32_t hit = tk.target >= 0 && (uint32_t)tk.target - first < left ? (uint32_t)tk.target - first : ~0u;
-    uint8_t* row = a.dz + (uint64_t)t * a.lddz + ((uint64_t)mt * kTileM + sub) * 2;
+    uint8_t* row = a.dz + (uint64_t)t * a.lddz + ((uint64_t)mt * kTileV + sub) * 2;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const float x[4] = {z[r][0], z[r][1], z[r][2], z[r][3]};
@@ -527,39 +528,39 @@ template <int T, int NT, int R, bool BWD> __global__ void __launch_bounds__(256)
   }
 }
 
-// Gradient of the hidden states from one piece of the vocabulary: a tile of 256
-// columns by BN tokens over the split's share of the piece's rows, into (or, after
-// the first piece, added to) the split's f32 sums.
-template <int T, int BN, int SEG> __global__ void __launch_bounds__(kGemmThreads) dhidden_k(XentArgs a) {
-  typedef Tile<T, true, false, BN> Prod;
+// Gradient of the hidden states from one piece of the vocabulary: a tile of S columns
+// by S tokens over the split's share of the piece's rows, into (or, after the first
+// piece, added to) the split's f32 sums.
+template <int T, int S, int SEG> __global__ void __launch_bounds__(tile_threads(S)) dhidden_k(XentArgs a) {
+  typedef Tile<T, true, false, S> Prod;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
   uint32_t mt, nt;
-  if (!tile_of(blockIdx.x, (a.kpad + kTileM - 1) / kTileM, a.tpad / BN, mt, nt)) return;
-  const uint32_t t0 = nt * BN, c0 = mt * kTileM;
+  if (!tile_of(blockIdx.x, (a.kpad + S - 1) / S, a.tpad / S, mt, nt)) return;
+  const uint32_t t0 = nt * S, c0 = mt * S;
   if (t0 >= a.scalars->count) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const uint32_t blocks = a.ntiles * (kTileM / kTileK);  // of 64 rows
+  const uint32_t blocks = a.ntiles * (kTileV / kTileK);  // of 64 rows
   const uint32_t split = blockIdx.y;
   const uint32_t k0 = (uint32_t)((uint64_t)blocks * split / a.splits), k1 = (uint32_t)((uint64_t)blocks * (split + 1) / a.splits);
   uint32_t k = k0, seg = 0;
   int sh = 0;
   // a lane's column chunk; past the last column any that exists
-  uint32_t col = c0 + col_src_chunk(tid) * 8;
+  uint32_t col = c0 + col_src_chunk<S>(tid) * 8;
   col = (col < a.kpad ? col : a.kpad - 8) * 2;
-  auto src = [&](int s, const uint8_t*& pa, const uint8_t*& pb, uint32_t (&oa)[Prod::LA], uint32_t (&ob)[Prod::LB]) {
+  auto src = [&](int s, const uint8_t*& pa, const uint8_t*& pb, uint32_t (&oa)[Prod::L], uint32_t (&ob)[Prod::L]) {
     if (s == 0) {
       const uint32_t c = row_src_chunk(tid) * 16;
 #pragma unroll
-      for (int i = 0; i < Prod::LB; ++i) ob[i] = (64 * i + (tid >> 3)) * a.lddz + c;
+      for (int i = 0; i < Prod::L; ++i) ob[i] = row_src_row<S>(tid, i) * a.lddz + c;
     }
     uint32_t have = kTileK;
     if (SEG > 1 || a.laid) {
       pa = a.laid + (uint64_t)k * kTileK * a.ldw;
     } else {
-      const uint32_t tile = a.tile0 + k / (kTileM / kTileK);
+      const uint32_t tile = a.tile0 + k / (kTileV / kTileK);
       while (tile >= a.v.first_tile[sh + 1]) ++sh;
       // rows past the shard meet zeros of dz: any that exists
-      const uint32_t row = (tile - a.v.first_tile[sh]) * kTileM + k % (kTileM / kTileK) * kTileK, rows = a.v.rows[sh];
+      const uint32_t row = (tile - a.v.first_tile[sh]) * kTileV + k % (kTileV / kTileK) * kTileK, rows = a.v.rows[sh];
       const uint32_t at = row < rows ? row : rows - 1;
       have = rows - at < (uint32_t)kTileK ? rows - at : (uint32_t)kTileK;
       pa = (const uint8_t*)a.v.w[sh] + (uint64_t)at * a.ldw;
@@ -570,8 +571,8 @@ template <int T, int BN, int SEG> __global__ void __launch_bounds__(kGemmThreads
       pb += seg_b(seg) * a.dz_plane;
     }
 #pragma unroll
-    for (int i = 0; i < Prod::LA; ++i) {
-      const uint32_t r = 16 * i + (tid >> 5);
+    for (int i = 0; i < Prod::L; ++i) {
+      const uint32_t r = col_src_k<S>(tid, i);
       oa[i] = (r < have ? r : have - 1) * a.ldw + col;
     }
     if (++k == k1) k = k0, ++seg;
@@ -602,34 +603,35 @@ template <int T, int BN, int SEG> __global__ void __launch_bounds__(kGemmThreads
   }
 }
 
-// Weight gradients of one piece: a tile of 256 columns by 256 vocabulary rows over
-// the counted tokens, rounded once.
-template <int T, int OUT, int SEG> __global__ void __launch_bounds__(kGemmThreads) dweight_k(XentArgs a) {
-  typedef Tile<T, true, true, 256> Prod;
+// Weight gradients of one piece: a tile of S columns by S vocabulary rows over the
+// counted tokens, rounded once.
+template <int T, int OUT, int S, int SEG> __global__ void __launch_bounds__(tile_threads(S)) dweight_k(XentArgs a) {
+  typedef Tile<T, true, true, S> Prod;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
   uint32_t mt, nt;
-  if (!tile_of(blockIdx.x, (a.kpad + kTileM - 1) / kTileM, a.ntiles, mt, nt)) return;
-  const uint32_t c0 = mt * kTileM, tile = a.tile0 + nt;
+  constexpr uint32_t per = kTileV / S;  // of a vocabulary tile
+  if (!tile_of(blockIdx.x, (a.kpad + S - 1) / S, a.ntiles * per, mt, nt)) return;
+  const uint32_t c0 = mt * S, tile = a.tile0 + nt / per;
   int sh = 0;
   while (tile >= a.v.first_tile[sh + 1]) ++sh;
-  if (!a.dw[sh]) return;
-  const uint32_t row0 = (tile - a.v.first_tile[sh]) * kTileM;
-  const uint32_t left = a.v.rows[sh] - row0 < (uint32_t)kTileM ? a.v.rows[sh] - row0 : (uint32_t)kTileM;
+  const uint32_t row0 = (tile - a.v.first_tile[sh]) * kTileV + nt % per * S, rows = a.v.rows[sh];
+  if (!a.dw[sh] || row0 >= rows) return;
+  const uint32_t left = rows - row0 < (uint32_t)S ? rows - row0 : (uint32_t)S;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  uint32_t col = c0 + col_src_chunk(tid) * 8;
+  uint32_t col = c0 + col_src_chunk<S>(tid) * 8;
   col = (col < a.kpad ? col : a.kpad - 8) * 2;
   const uint32_t blocks = (a.scalars->count + kTileK - 1) / kTileK;  // of 64 tokens; those past the last have dz 0
   uint32_t k = 0, seg = 0;
-  auto src = [&](int s, const uint8_t*& pa, const uint8_t*& pb, uint32_t (&oa)[Prod::LA], uint32_t (&ob)[Prod::LB]) {
+  auto src = [&](int s, const uint8_t*& pa, const uint8_t*& pb, uint32_t (&oa)[Prod::L], uint32_t (&ob)[Prod::L]) {
     if (s == 0) {
 #pragma unroll
-      for (int i = 0; i < Prod::LA; ++i) {
-        oa[i] = (16 * i + (tid >> 5)) * a.ldh + col;
-        ob[i] = (16 * i + (tid >> 5)) * a.lddz + col_src_chunk(tid) * 16;
+      for (int i = 0; i < Prod::L; ++i) {
+        oa[i] = col_src_k<S>(tid, i) * a.ldh + col;
+        ob[i] = col_src_k<S>(tid, i) * a.lddz + col_src_chunk<S>(tid) * 16;
       }
     }
     pa = a.h + (uint64_t)k * kTileK * a.ldh;
-    pb = a.dz + (uint64_t)k * kTileK * a.lddz + (uint64_t)nt * kTileM * 2;
+    pb = a.dz + (uint64_t)k * kTileK * a.lddz + (uint64_t)nt * S * 2;
     if constexpr (SEG > 1) {
       pa += seg_a(seg) * a.h_plane;
       pb += seg_b(seg) * a.dz_plane;
@@ -732,25 +734,38 @@ constexpr uint64_t kPieceBytes = 256ull << 20;  // of dz, and of weights laid ou
 constexpr uint64_t kMaxTiles = 1ull << 22;       // workgroups of 512 threads in a launch
 uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 
+uint64_t tiles_of(uint64_t m, uint64_t n, uint64_t s) { return (m + s - 1) / s * ((n + s - 1) / s); }
+
+// Size of tile for an m x n product.  In rounds over the 256 CUs, from the times of a
+// 64-k stage measured on large products: 0.95 us for a round of 256 x 256 tiles, 0.55 us
+// for one of 128 x 128 (two a CU), 0.35 us when a CU has one of those.
+int pick_tile(uint64_t m, uint64_t n) {
+  const uint64_t big = tiles_of(m, n, 256), small = tiles_of(m, n, 128);
+  const uint64_t c256 = (big + 255) / 256 * 95, c128 = small <= 256 ? 35 : (small + 511) / 512 * 55;
+  return n <= 128 || c128 < c256 ? 128 : 256;
+}
+
 }  // namespace
 
 XentPlan xent_plan(uint32_t tokens, uint32_t cols, const size_t* rows, int nranks, int t, bool backward) {
   XentPlan p{};
   const uint64_t planes = t == kF32 ? kPlanes : 1;
   p.few = tokens <= 16 ? 1 : tokens <= 32 ? 2 : tokens <= 64 ? 4 : 0;
-  p.bn = tokens <= 128 ? 128 : 256;
-  p.tpad = (uint32_t)up(tokens, p.bn);
+  p.tpad = (uint32_t)up(tokens, tokens <= 128 ? 128 : 256);
   p.kpad = (uint32_t)up(cols, kTileK);
   uint64_t tiles = 0;
-  for (int r = 0; r < nranks; ++r) tiles += up(rows[r], kTileM) / kTileM;
+  for (int r = 0; r < nranks; ++r) tiles += up(rows[r], kTileV) / kTileV;
   p.tiles = (uint32_t)tiles;
   // tiles of a piece: dz of all tokens, and the weights, each within kPieceBytes
-  uint64_t most = kPieceBytes / ((uint64_t)kTileM * p.kpad * 2 * planes);
+  uint64_t most = kPieceBytes / ((uint64_t)kTileV * p.kpad * 2 * planes);
   if (backward) {
-    const uint64_t d = kPieceBytes / ((uint64_t)kTileM * p.tpad * 2 * planes);
+    const uint64_t d = kPieceBytes / ((uint64_t)kTileV * p.tpad * 2 * planes);
     if (d < most) most = d;
   }
-  const uint64_t grid = kMaxTiles / (p.tpad / p.bn);
+  // at least two rounds of small tiles over the CUs, however many bytes that is up to 1 GiB
+  const uint64_t fill = 4 * kPieceBytes / ((uint64_t)kTileV * p.kpad * 2 * planes), want = (1024 + p.tpad / 64) / (p.tpad / 64);
+  if (most < want) most = want < fill ? want : fill;
+  const uint64_t grid = kMaxTiles / (p.tpad / 128 * 2);
   if (grid < most) most = grid;
   if (most < 1) most = 1;
   const uint64_t pieces = tiles ? (tiles + most - 1) / most : 1;
@@ -762,15 +777,16 @@ XentPlan xent_plan(uint32_t tokens, uint32_t cols, const size_t* rows, int nrank
     return o;
   };
   p.h_plane = (uint64_t)p.tpad * p.kpad * 2;
-  p.laid_plane = (uint64_t)p.piece * kTileM * p.kpad * 2;
+  p.laid_plane = (uint64_t)p.piece * kTileV * p.kpad * 2;
   p.h = take(p.h_plane * planes);
   p.laid = take(p.laid_plane * planes);
   if (backward) {
-    p.dz_plane = (uint64_t)p.tpad * p.piece * kTileM * 2;
+    p.dz_plane = (uint64_t)p.tpad * p.piece * kTileV * 2;
     p.dz = take(p.dz_plane * planes);
-    // enough splits of a piece's rows that a tile of every split has a CU
-    const uint64_t n = up(p.kpad, kTileM) / kTileM * (p.tpad / p.bn);
-    uint64_t s = n ? 256 / n : 1;
+    // enough splits of a piece's rows that every CU has a tile of 256 (small calls: two of 128)
+    const uint64_t big = tiles_of(p.kpad, p.tpad, 256);
+    p.dh_tile = p.tpad > 128 && big >= 32 ? 256 : 128;
+    uint64_t s = p.dh_tile == 256 ? 256 / big : 512 / tiles_of(p.kpad, p.tpad, 128);
     if (s > p.piece) s = p.piece;
     p.splits = s < 1 ? 1 : (uint32_t)s;
     p.sum = take((uint64_t)p.splits * p.tpad * p.kpad * 4);
@@ -778,8 +794,8 @@ XentPlan xent_plan(uint32_t tokens, uint32_t cols, const size_t* rows, int nrank
     p.idx = take((uint64_t)p.tpad * 4);
     p.place = take((uint64_t)tokens * 4);
   } else {
-    p.parts = p.few ? kTileM / (16 * p.few) : p.bn == 256 ? 2 : 4;  // of a tile
-    p.part = take(tiles * p.parts * tokens * sizeof(float2));
+    // pairs of a tile and token: of 128 x 128 tiles, or of few_k's
+    p.part = take(tiles * (p.few ? kTileV / (16 * p.few) : 4) * tokens * sizeof(float2));
     p.zt = take((uint64_t)tokens * 4);
   }
   p.scalars = take(sizeof(XentScalars));
@@ -800,14 +816,27 @@ template <int T> void layout(LayoutArgs l, hipStream_t s) {
 
 template <int T, bool BWD> void few(const XentArgs& a, uint32_t few, hipStream_t s) {
   const uint32_t tokens = BWD ? (uint32_t)up(a.tokens, kTileK) : a.tokens;
-  const dim3 grid(a.ntiles * (kTileM / (16 * few)), (tokens + 16 * few - 1) / (16 * few));
+  const dim3 grid(a.ntiles * (kTileV / (16 * few)), (tokens + 16 * few - 1) / (16 * few));
   if (few == 1) hipLaunchKernelGGL((few_k<T, 1, 1, BWD>), grid, dim3(256), 0, s, a);
   else if (few == 2) hipLaunchKernelGGL((few_k<T, 2, 2, BWD>), grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((few_k<T, 4, 4, BWD>), grid, dim3(256), 0, s, a);
 }
 
+template <int M, int S, bool BWD, int SEG> void logits(const XentArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((logits_k<M, S, BWD, SEG>), dim3(tile_grid(tiles_of(a.ntiles * kTileV, a.tpad, S))), dim3(tile_threads(S)),
+                     0, s, a);
+}
+template <int M, int S, int SEG> void dhidden(const XentArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((dhidden_k<M, S, SEG>), dim3(tile_grid(tiles_of(a.kpad, a.tpad, S)), a.splits), dim3(tile_threads(S)), 0, s,
+                     a);
+}
+template <int M, int T, int S, int SEG> void dweight(const XentArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((dweight_k<M, T, S, SEG>), dim3(tile_grid(tiles_of(a.kpad, a.ntiles * kTileV, S))), dim3(tile_threads(S)), 0,
+                     s, a);
+}
+
 // T: type of the caller's tensors.  M: type that multiplies.
-template <int T, int BN, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, hipStream_t s) {
+template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, hipStream_t s) {
   constexpr int M = T == kF32 ? kF16 : T, SEG = T == kF32 ? kSegs : 1;
   uint8_t* ws = (uint8_t*)c.workspace;
   XentArgs a{};
@@ -818,7 +847,7 @@ template <int T, int BN, bool BWD> hipError_t run(const XentCall& c, const XentP
     a.v.w[r] = c.weights[r];
     a.v.rows[r] = (uint32_t)c.rows[r];
     a.v.first_row[r] = (uint32_t)vocab;
-    a.v.first_tile[r + 1] = a.v.first_tile[r] + (uint32_t)(up(c.rows[r], kTileM) / kTileM);
+    a.v.first_tile[r + 1] = a.v.first_tile[r] + (uint32_t)(up(c.rows[r], kTileV) / kTileV);
     vocab += c.rows[r];
     if (c.rows[r] && (uintptr_t)c.weights[r] % 16) direct = false;
     if (c.dweights) a.dw[r] = c.dweights[r];
@@ -848,7 +877,7 @@ template <int T, int BN, bool BWD> hipError_t run(const XentCall& c, const XentP
   if constexpr (BWD) {
     a.dz = ws + p.dz;
     a.dz_plane = p.dz_plane;
-    a.lddz = p.piece * kTileM * 2;
+    a.lddz = p.piece * kTileV * 2;
     a.sum = (float*)(ws + p.sum);
     a.splits = p.splits;
     a.token = (XentToken*)(ws + p.token);
@@ -863,7 +892,6 @@ template <int T, int BN, bool BWD> hipError_t run(const XentCall& c, const XentP
     l.idx = (const int32_t*)(ws + p.idx);
   } else {
     a.part = (float2*)(ws + p.part);
-    a.parts = p.tiles * p.parts;
     a.zt = (float*)(ws + p.zt);
   }
   if constexpr (T == kF32) {
@@ -888,27 +916,35 @@ template <int T, int BN, bool BWD> hipError_t run(const XentCall& c, const XentP
   l.ld = c.ld_weight;
   l.dst = ws + p.laid;
   l.plane = p.laid_plane;
-  const uint32_t nt = p.tpad / BN, ct = (uint32_t)(up(p.kpad, kTileM) / kTileM);
+  const uint32_t nt = p.tpad / 128 * 2;  // of the smaller tiles, in halves of a vocabulary tile
+  const int tile = pick_tile((uint64_t)(BWD || !direct ? p.piece : p.tiles) * kTileV, p.tpad);
   // a forward that reads the weights in place has nothing to divide but the grid
   uint32_t piece = p.piece;
   if (!BWD && p.few) piece = p.tiles < kMaxTiles / 8 ? p.tiles : (uint32_t)(kMaxTiles / 8);
   else if (!BWD && direct) piece = nt <= kMaxTiles / p.tiles ? p.tiles : kMaxTiles / nt ? (uint32_t)(kMaxTiles / nt) : 1;
+  if (!BWD) a.parts = p.tiles * (p.few ? kTileV / (16 * p.few) : tile == 256 ? 2 : 4);
   for (a.tile0 = 0; a.tile0 < p.tiles; a.tile0 += piece) {
     a.ntiles = p.tiles - a.tile0 < piece ? p.tiles - a.tile0 : piece;
     if (!direct && (BWD || !p.few)) {
       l.tile0 = a.tile0;
-      l.rows = (uint64_t)a.ntiles * kTileM;
+      l.rows = (uint64_t)a.ntiles * kTileV;
       layout<T>(l, s);
       a.laid = ws + p.laid;
     }
+    const uint64_t rows = (uint64_t)a.ntiles * kTileV;
     if (p.few) few<T, BWD>(a, p.few, s);
-    else hipLaunchKernelGGL((logits_k<M, BN, BWD, SEG>), dim3(tile_grid((uint64_t)a.ntiles * nt)), dim3(kGemmThreads), 0, s, a);
+    else if (tile == 256) logits<M, 256, BWD, SEG>(a, s);
+    else logits<M, 128, BWD, SEG>(a, s);
     if constexpr (BWD) {
-      if (c.dhidden)
-        hipLaunchKernelGGL((dhidden_k<M, BN, SEG>), dim3(tile_grid((uint64_t)ct * nt), a.splits), dim3(kGemmThreads), 0, s, a);
+      if (c.dhidden) {
+        if (p.dh_tile == 256) dhidden<M, 256, SEG>(a, s);
+        else dhidden<M, 128, SEG>(a, s);
+      }
       a.add = 1;
-      if (c.dweights)
-        hipLaunchKernelGGL((dweight_k<M, T, SEG>), dim3(tile_grid((uint64_t)ct * a.ntiles)), dim3(kGemmThreads), 0, s, a);
+      if (c.dweights) {
+        if (pick_tile(p.kpad, rows) == 256) dweight<M, T, 256, SEG>(a, s);
+        else dweight<M, T, 128, SEG>(a, s);
+      }
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -919,7 +955,7 @@ template <int T, int BN, bool BWD> hipError_t run(const XentCall& c, const XentP
       hipLaunchKernelGGL(dhidden_join_k<T>, dim3(c.tokens < 65536 ? c.tokens : 65536, y < 1024 ? y : 1024), dim3(256), 0, s, a);
     }
   } else {
-    const uint64_t parts = (uint64_t)p.tiles * p.parts;
+    const uint64_t parts = a.parts;
     const XentJoinArgs j{a.part, a.zt, c.targets, c.ignore, (int64_t)vocab, c.loss, c.lse_out,
                          p.few ? 1u : c.tokens, p.few ? parts : 1u, (uint32_t)parts, c.tokens};
     // as many chains as leave every CU a workgroup
@@ -945,9 +981,9 @@ template <bool BWD> hipError_t typed(const XentCall& c, int t, hipStream_t s) {
     return hipSuccess;
   }
   const XentPlan p = xent_plan(c.tokens, c.cols, c.rows, c.nranks, t, BWD);
-  if (t == kF32) return p.bn == 128 ? run<kF32, 128, BWD>(c, p, s) : run<kF32, 256, BWD>(c, p, s);
-  if (t == kF16) return p.bn == 128 ? run<kF16, 128, BWD>(c, p, s) : run<kF16, 256, BWD>(c, p, s);
-  return p.bn == 128 ? run<kBF16, 128, BWD>(c, p, s) : run<kBF16, 256, BWD>(c, p, s);
+  if (t == kF32) return run<kF32, BWD>(c, p, s);
+  if (t == kF16) return run<kF16, BWD>(c, p, s);
+  return run<kBF16, BWD>(c, p, s);
 }
 
 }  // namespace
