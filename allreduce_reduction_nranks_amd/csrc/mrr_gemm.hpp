@@ -21,6 +21,8 @@
 // stage's first fragments fetched under that quarter's products.
 #pragma once
 
+#include <type_traits>
+
 #include "mrr_rows.hpp"
 
 namespace mrr {
@@ -45,9 +47,9 @@ template <int T> __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16
 __device__ __forceinline__ int acc_row(int lane, int i) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
 
 // ---- addresses -----------------------------------------------------------------
-// Row operand: a stage is [S rows][64 k], 128 bytes a row, 8 chunks of 16.  Load i
-// of thread t brings row i threads / 8 + t / 8; chunk c of row r lies at position
-// c ^ f(r), f(r) = (r & 7) ^ (r >> 3 & 1): any 8 rows, and any 16 over 64 banks, differ.
+// Row operand: a stage is [S rows][64 k], 128 bytes a row in chunks of 16.  Load i of
+// thread t brings row i threads / 8 + t / 8; chunk c of row r lies at position c ^ f(r),
+// f(r) = (r & 7) ^ (r >> 3 & 1): any 8 rows, and any 16 over 64 banks, differ.
 template <int S> __device__ __forceinline__ uint32_t row_src_row(int tid, int i) {
   return (uint32_t)(i * (tile_threads(S) / 8) + (tid >> 3));
 }
@@ -55,14 +57,16 @@ __device__ __forceinline__ uint32_t row_src_chunk(int tid) {
   return (uint32_t)((tid & 7) ^ ((tid >> 3) & 7) ^ ((tid >> 6) & 1));
 }
 // Byte offset of lane's 8 k of quarter 0 in the row tile that starts at `row0`
-// (a multiple of 32); quarter kk flips bits of the chunk: offset ^ (kk * 32).
+// (a multiple of 32); quarter kk is at offset ^ (kk * 32).
 __device__ __forceinline__ uint32_t row_frag(int row0, int lane) {
   const int r = lane & 31;
   return (uint32_t)((row0 + r) * 128 + (((lane >> 5) ^ (r & 7) ^ ((r >> 3) & 1)) << 4));
 }
 // Col operand: a stage is [64 k][S m], 2 S bytes a k.  Load i of thread t brings k
-// 16 i + t / (S / 8); 64-byte units are at unit ^ (k modulo their count).
-template <int S> __device__ __forceinline__ uint32_t col_src_k(int tid, int i) { return (uint32_t)(16 * i + tid / (S / 8)); }
+// i threads 8 / S + t 8 / S; 64-byte units are at unit ^ (k modulo their count).
+template <int S> __device__ __forceinline__ uint32_t col_src_k(int tid, int i) {
+  return (uint32_t)(i * (tile_threads(S) / (S / 8)) + tid / (S / 8));
+}
 template <int S> __device__ __forceinline__ uint32_t col_src_chunk(int tid) {
   return (uint32_t)((tid % (S / 8)) ^ ((tid / (S / 8) % (S / 32)) << 2));
 }
@@ -95,14 +99,16 @@ __device__ __forceinline__ void load_lds(const uint8_t* base, uint32_t off, lds8
                :: "s"((uint32_t)(uintptr_t)lds), "v"(off), "s"(base));
 }
 
-// The product over `steps` stages.  src(s, pa, pb, oa, ob) sets the (wave-uniform)
-// addresses and the lane offsets of stage s; it is called once for each s in order.
-template <int T, bool ACOL, bool BCOL, int S> struct Tile {
+// The product over `steps` stages of 64 k, NS of them in LDS.  src(s, pa, pb, oa, ob) sets
+// the (wave-uniform) addresses and the lane offsets of stage s; it is called once for
+// each s in order.
+template <int T, bool ACOL, bool BCOL, int S, int NS> struct Tile {
   static constexpr int WN = S == 256 ? 4 : 2, WM = 2;        // waves along n and m
   static constexpr int FM = S / WM / 32, FN = S / WN / 32;   // 32 x 32 tiles of a wave
-  static constexpr int kStage = S * kTileK * 2;              // bytes of an operand's stage
+  static constexpr int kStage = S * kTileK * 2;                 // bytes of an operand's stage
   static constexpr int kLoad = tile_threads(S) * 16, L = kStage / kLoad;  // bytes of a load, loads of a lane
-  static constexpr int kLds = 4 * kStage;                    // A, A, B, B
+  static constexpr int kLds = 2 * NS * kStage;               // A's stages, then B's
+  static constexpr int Q = kTileK / 16;                      // quarters of a stage, which multiply together
   f32x16 acc[FM][FN];
 
   template <class Src> __device__ __forceinline__ void run(int steps, lds8* lds, Src&& src) {
@@ -116,23 +122,26 @@ template <int T, bool ACOL, bool BCOL, int S> struct Tile {
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
     if (steps <= 0) return;
-    // offsets of this lane's fragments, and of its wave's loads, in the present stage
-    constexpr int NA = ACOL ? 2 * FM : 4, NB = BCOL ? 2 * FN : 4;
+    // offsets of this lane's fragments in the present stage, and of its wave's loads in
+    // the one that is filled next
+    constexpr int NA = ACOL ? 2 * FM : Q, NB = BCOL ? 2 * FN : Q;
     uint32_t fa[NA], fb[NB];
-    uint32_t wa = (uint32_t)wave * 1024, wb = 2 * kStage + (uint32_t)wave * 1024;
+    uint32_t at = 0, fill = 0;
 #pragma unroll
     for (int i = 0; i < NA; ++i) fa[i] = ACOL ? col_frag<S>(m0 + 32 * (i >> 1), i & 1, lane) : row_frag(m0, lane) ^ (i * 32);
 #pragma unroll
     for (int i = 0; i < NB; ++i)
-      fb[i] = 2 * kStage + (BCOL ? col_frag<S>(n0 + 32 * (i >> 1), i & 1, lane) : row_frag(n0, lane) ^ (i * 32));
+      fb[i] = NS * kStage + (BCOL ? col_frag<S>(n0 + 32 * (i >> 1), i & 1, lane) : row_frag(n0, lane) ^ (i * 32));
+    lds8* const wave_lds = lds + wave * 1024;
     const uint8_t *pa, *pb;
     uint32_t oa[L], ob[L];
     u32x4 va[2][FM], vb[2][FN];
 
     auto fetch = [&](int i) {
-      if (i < L) load_lds(pa, oa[i % L], lds + wa + i * kLoad);
-      else load_lds(pb, ob[i % L], lds + wb + (i - L) * kLoad);
+      if (i < L) load_lds(pa, oa[i % L], wave_lds + fill + i * kLoad);
+      else load_lds(pb, ob[i % L], wave_lds + fill + NS * kStage + (i - L) * kLoad);
     };
+    auto filled = [&]() { fill = fill == (NS - 1) * kStage ? 0 : fill + kStage; };
     auto read = [&](int f, int kk) {
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
@@ -163,59 +172,59 @@ template <int T, bool ACOL, bool BCOL, int S> struct Tile {
       }
       __builtin_amdgcn_sched_barrier(0);
     };
-    // this wave's reads are done and its loads have arrived, then every wave's; the
-    // other buffer becomes the present one
-    auto turn = [&]() {
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    // this wave's reads of the present stage are done and its loads of the next have
+    // arrived, then every wave's; all but the last stages have NS - 2 more in flight
+    auto turn = [&](auto more) {
+      if constexpr (more) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" :: "n"((NS - 2) * 2 * L) : "memory");
+      else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       __syncthreads();
+      const uint32_t next = at == (NS - 1) * kStage ? 0u : at + kStage, d = next - at;
+      at = next;
 #pragma unroll
-      for (int i = 0; i < NA; ++i) fa[i] ^= kStage;
+      for (int i = 0; i < NA; ++i) fa[i] += d;
 #pragma unroll
-      for (int i = 0; i < NB; ++i) fb[i] ^= kStage;
+      for (int i = 0; i < NB; ++i) fb[i] += d;
     };
-    src(0, pa, pb, oa, ob);
 #pragma unroll
-    for (int i = 0; i < 2 * L; ++i) fetch(i);
-    wa ^= kStage;
-    wb ^= kStage;
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (steps > 1) {
-      src(1, pa, pb, oa, ob);
+    for (int s = 0; s < NS; ++s) {
+      if (s < steps) {
+        src(s, pa, pb, oa, ob);
 #pragma unroll
-      for (int i = 0; i < 2 * L; ++i) fetch(i);
-      wa ^= kStage;
-      wb ^= kStage;
+        for (int i = 0; i < 2 * L; ++i) fetch(i);
+        filled();
+      }
     }
+    if (steps >= NS) asm volatile("s_waitcnt vmcnt(%0)" :: "n"((NS - 1) * 2 * L) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
     read(0, 0);
     int s = 0;
-    for (; s + 2 < steps; ++s) {
-      quarter(0, 1);
-      quarter(1, 2);
-      quarter(0, 3);
-      turn();
-      src(s + 2, pa, pb, oa, ob);
+    for (; s + NS < steps; ++s) {
+#pragma unroll
+      for (int q = 0; q < Q - 1; ++q) quarter(q & 1, q + 1);
+      turn(std::true_type{});
+      src(s + NS, pa, pb, oa, ob);
       read(0, 0);
       __builtin_amdgcn_sched_barrier(0);
+      // a wave that is past the barrier goes first: 1.3 % on large products
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int p = 0; p < kProducts || p < 2 * L; ++p) {
         if (p < kProducts) product(1, p);
         if (p < 2 * L) fetch(p);
         __builtin_amdgcn_sched_barrier(0);
       }
-      wa ^= kStage;
-      wb ^= kStage;
+      __builtin_amdgcn_s_setprio(0);
+      filled();
     }
     for (; s + 1 < steps; ++s) {
-      quarter(0, 1);
-      quarter(1, 2);
-      quarter(0, 3);
-      turn();
+#pragma unroll
+      for (int q = 0; q < Q - 1; ++q) quarter(q & 1, q + 1);
+      turn(std::false_type{});
       quarter(1, 0);
     }
-    quarter(0, 1);
-    quarter(1, 2);
-    quarter(0, 3);
+#pragma unroll
+    for (int q = 0; q < Q - 1; ++q) quarter(q & 1, q + 1);
 #pragma unroll
     for (int p = 0; p < kProducts; ++p) product(1, p);
   }

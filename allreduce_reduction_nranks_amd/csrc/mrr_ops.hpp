@@ -135,7 +135,6 @@ struct XentCall {
 // Tiles, pieces and the workspace's parts (byte offsets) of a call.
 struct XentPlan {
   uint32_t tpad, kpad, tiles, piece, splits, dh_tile;
-  uint32_t few;    // 16-token groups of a few_k workgroup, 0: logits_k
   uint64_t h_plane, laid_plane, dz_plane;
   uint64_t h, laid, dz, sum, token, idx, place, scalars, most, part, zt;
   uint64_t bytes;

@@ -284,9 +284,9 @@ __device__ __forceinline__ void store_dz(uint8_t* row, uint64_t plane, uint32_t 
 // Logits of one tile of S vocabulary rows by S tokens.  Forward: reduced to a
 // (max, sum) pair in base 2 for each wave's rows, and the target's logit.
 // Backward: dz, vocabulary contiguous.
-template <int T, int S, bool BWD, int SEG>
+template <int T, int S, int NS, bool BWD, int SEG>
 __global__ void __launch_bounds__(tile_threads(S)) logits_k(XentArgs a) {
-  typedef Tile<T, false, false, S> Prod;
+  typedef Tile<T, false, false, S, NS> Prod;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
   uint32_t mt, nt;
   constexpr uint32_t per = kTileV / S;  // of a vocabulary tile
@@ -421,7 +421,7 @@ template <int T, int NT, int R, bool BWD> __global__ void __launch_bounds__(256)
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[r][n] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
-  if (left && tokens) {
+  if (left && t0 < tokens) {
     const uint32_t lane0 = (lane >> 4) * 2 * V;  // a lane's first element of a block
     const uint8_t *pw[R], *ph[NT];
 #pragma unroll
@@ -531,8 +531,8 @@ template <int T, int NT, int R, bool BWD> __global__ void __launch_bounds__(256)
 // Gradient of the hidden states from one piece of the vocabulary: a tile of S columns
 // by S tokens over the split's share of the piece's rows, into (or, after the first
 // piece, added to) the split's f32 sums.
-template <int T, int S, int SEG> __global__ void __launch_bounds__(tile_threads(S)) dhidden_k(XentArgs a) {
-  typedef Tile<T, true, false, S> Prod;
+template <int T, int S, int NS, int SEG> __global__ void __launch_bounds__(tile_threads(S)) dhidden_k(XentArgs a) {
+  typedef Tile<T, true, false, S, NS> Prod;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
   uint32_t mt, nt;
   if (!tile_of(blockIdx.x, (a.kpad + S - 1) / S, a.tpad / S, mt, nt)) return;
@@ -605,8 +605,8 @@ template <int T, int S, int SEG> __global__ void __launch_bounds__(tile_threads(
 
 // Weight gradients of one piece: a tile of S columns by S vocabulary rows over the
 // counted tokens, rounded once.
-template <int T, int OUT, int S, int SEG> __global__ void __launch_bounds__(tile_threads(S)) dweight_k(XentArgs a) {
-  typedef Tile<T, true, true, S> Prod;
+template <int T, int OUT, int S, int NS, int SEG> __global__ void __launch_bounds__(tile_threads(S)) dweight_k(XentArgs a) {
+  typedef Tile<T, true, true, S, NS> Prod;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
   uint32_t mt, nt;
   constexpr uint32_t per = kTileV / S;  // of a vocabulary tile
@@ -750,7 +750,6 @@ int pick_tile(uint64_t m, uint64_t n) {
 XentPlan xent_plan(uint32_t tokens, uint32_t cols, const size_t* rows, int nranks, int t, bool backward) {
   XentPlan p{};
   const uint64_t planes = t == kF32 ? kPlanes : 1;
-  p.few = tokens <= 16 ? 1 : tokens <= 32 ? 2 : tokens <= 64 ? 4 : 0;
   p.tpad = (uint32_t)up(tokens, tokens <= 128 ? 128 : 256);
   p.kpad = (uint32_t)up(cols, kTileK);
   uint64_t tiles = 0;
@@ -785,7 +784,7 @@ XentPlan xent_plan(uint32_t tokens, uint32_t cols, const size_t* rows, int nrank
     p.dz = take(p.dz_plane * planes);
     // enough splits of a piece's rows that every CU has a tile of 256 (small calls: two of 128)
     const uint64_t big = tiles_of(p.kpad, p.tpad, 256);
-    p.dh_tile = p.tpad > 128 && big >= 32 ? 256 : 128;
+    p.dh_tile = p.tpad > 128 && big >= 8 ? 256 : 128;
     uint64_t s = p.dh_tile == 256 ? 256 / big : 512 / tiles_of(p.kpad, p.tpad, 128);
     if (s > p.piece) s = p.piece;
     p.splits = s < 1 ? 1 : (uint32_t)s;
@@ -794,8 +793,8 @@ XentPlan xent_plan(uint32_t tokens, uint32_t cols, const size_t* rows, int nrank
     p.idx = take((uint64_t)p.tpad * 4);
     p.place = take((uint64_t)tokens * 4);
   } else {
-    // pairs of a tile and token: of 128 x 128 tiles, or of few_k's
-    p.part = take(tiles * (p.few ? kTileV / (16 * p.few) : 4) * tokens * sizeof(float2));
+    // pairs of a tile and token: at most few_k's, else those of 128 x 128 tiles
+    p.part = take(tiles * (tokens <= 16 ? 16 : tokens <= 32 ? 8 : 4) * tokens * sizeof(float2));
     p.zt = take((uint64_t)tokens * 4);
   }
   p.scalars = take(sizeof(XentScalars));
@@ -814,25 +813,53 @@ template <int T> void layout(LayoutArgs l, hipStream_t s) {
   hipLaunchKernelGGL(layout_k<T>, dim3((uint32_t)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, l);
 }
 
+// 16-token groups of a few_k workgroup, 0: logits_k.  16 bits: up to 4 tokens (of 32000 x
+// 4096, 1 / 4 / 8 / 16 tokens: 49 / 50 / 55 / 63 us against 51 for all of them; the
+// hidden states then take as much of the L1s as the weights; unaligned, 50257 x 1023: 60
+// us for 1 and 98 for 16 against 68).  f32: up to 128 tokens, as the other way has to lay
+// out the weights first (of 32000 x 4096, 64 / 128: 220 / 440 us against 540).
+uint32_t few_groups(int t, uint32_t tokens) {
+  if (t == kF32) return tokens <= 16 ? 1 : tokens <= 32 ? 2 : tokens <= 128 ? 4 : 0;
+  return tokens <= 4 ? 1 : 0;
+}
+
 template <int T, bool BWD> void few(const XentArgs& a, uint32_t few, hipStream_t s) {
   const uint32_t tokens = BWD ? (uint32_t)up(a.tokens, kTileK) : a.tokens;
   const dim3 grid(a.ntiles * (kTileV / (16 * few)), (tokens + 16 * few - 1) / (16 * few));
   if (few == 1) hipLaunchKernelGGL((few_k<T, 1, 1, BWD>), grid, dim3(256), 0, s, a);
-  else if (few == 2) hipLaunchKernelGGL((few_k<T, 2, 2, BWD>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((few_k<T, 4, 4, BWD>), grid, dim3(256), 0, s, a);
+  if constexpr (T == kF32) {
+    if (few == 2) hipLaunchKernelGGL((few_k<T, 2, 2, BWD>), grid, dim3(256), 0, s, a);
+    if (few == 4) hipLaunchKernelGGL((few_k<T, 4, 4, BWD>), grid, dim3(256), 0, s, a);
+  }
 }
 
-template <int M, int S, bool BWD, int SEG> void logits(const XentArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((logits_k<M, S, BWD, SEG>), dim3(tile_grid(tiles_of(a.ntiles * kTileV, a.tpad, S))), dim3(tile_threads(S)),
-                     0, s, a);
+// 128 x 128 tiles go two a CU with 2 stages, or with 4 when there is one a CU anyway.
+template <int M, int S, int NS, bool BWD, int SEG> void logits_of(const XentArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((logits_k<M, S, NS, BWD, SEG>), dim3(tile_grid(tiles_of(a.ntiles * kTileV, a.tpad, S))),
+                     dim3(tile_threads(S)), 0, s, a);
 }
-template <int M, int S, int SEG> void dhidden(const XentArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((dhidden_k<M, S, SEG>), dim3(tile_grid(tiles_of(a.kpad, a.tpad, S)), a.splits), dim3(tile_threads(S)), 0, s,
-                     a);
+template <int M, bool BWD, int SEG> void logits(const XentArgs& a, int tile, hipStream_t s) {
+  if (tile == 256) logits_of<M, 256, 2, BWD, SEG>(a, s);
+  else if (tiles_of(a.ntiles * kTileV, a.tpad, 128) > 256) logits_of<M, 128, 2, BWD, SEG>(a, s);
+  else logits_of<M, 128, 4, BWD, SEG>(a, s);
 }
-template <int M, int T, int S, int SEG> void dweight(const XentArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((dweight_k<M, T, S, SEG>), dim3(tile_grid(tiles_of(a.kpad, a.ntiles * kTileV, S))), dim3(tile_threads(S)), 0,
-                     s, a);
+template <int M, int S, int NS, int SEG> void dhidden_of(const XentArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((dhidden_k<M, S, NS, SEG>), dim3(tile_grid(tiles_of(a.kpad, a.tpad, S)), a.splits),
+                     dim3(tile_threads(S)), 0, s, a);
+}
+template <int M, int SEG> void dhidden(const XentArgs& a, int tile, hipStream_t s) {
+  if (tile == 256) dhidden_of<M, 256, 2, SEG>(a, s);
+  else if (tiles_of(a.kpad, a.tpad, 128) * a.splits > 256) dhidden_of<M, 128, 2, SEG>(a, s);
+  else dhidden_of<M, 128, 4, SEG>(a, s);
+}
+template <int M, int T, int S, int NS, int SEG> void dweight_of(const XentArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((dweight_k<M, T, S, NS, SEG>), dim3(tile_grid(tiles_of(a.kpad, a.ntiles * kTileV, S))),
+                     dim3(tile_threads(S)), 0, s, a);
+}
+template <int M, int T, int SEG> void dweight(const XentArgs& a, int tile, hipStream_t s) {
+  if (tile == 256) dweight_of<M, T, 256, 2, SEG>(a, s);
+  else if (tiles_of(a.kpad, a.ntiles * kTileV, 128) > 256) dweight_of<M, T, 128, 2, SEG>(a, s);
+  else dweight_of<M, T, 128, 4, SEG>(a, s);
 }
 
 // T: type of the caller's tensors.  M: type that multiplies.
@@ -852,6 +879,7 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
     if (c.rows[r] && (uintptr_t)c.weights[r] % 16) direct = false;
     if (c.dweights) a.dw[r] = c.dweights[r];
   }
+  const uint32_t groups = few_groups(T, c.tokens);
   a.ldw = direct ? (uint32_t)c.ld_weight * 2 : p.kpad * 2;
   a.laid_plane = p.laid_plane;
   a.h = ws + p.h;
@@ -895,11 +923,11 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
     a.zt = (float*)(ws + p.zt);
   }
   if constexpr (T == kF32) {
-    if (BWD || !p.few) {
+    if (BWD || !groups) {
       MostArgs m{a.v, c.hidden, c.ld_weight, c.ld_hidden, c.tokens, (uint32_t*)(ws + p.most), c.cols, 0};
       while (m.units_log2 < 8 && (4u << m.units_log2) < c.cols) ++m.units_log2;
-      // about 64 KiB a workgroup
-      const uint64_t n = (vocab * c.cols >> 14) + 1;
+      // from 8 KiB a workgroup
+      const uint64_t n = (vocab * c.cols >> 11) + 1;
       const uint32_t grid = n < (uint64_t)kMostParts ? (uint32_t)n : (uint32_t)kMostParts;
       hipLaunchKernelGGL(most_k, dim3(grid, 2), dim3(256), 0, s, m);
       hipLaunchKernelGGL(scale_k, dim3(2), dim3(kMostParts), 0, s, (const uint32_t*)m.parts, grid, scalars);
@@ -911,7 +939,7 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
   l.src_rows = c.tokens;
   l.dst = ws + p.h;
   l.plane = p.h_plane;
-  if (BWD || !p.few) layout<T>(l, s);
+  if (BWD || !groups) layout<T>(l, s);
   l.src = nullptr;
   l.ld = c.ld_weight;
   l.dst = ws + p.laid;
@@ -920,31 +948,24 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
   const int tile = pick_tile((uint64_t)(BWD || !direct ? p.piece : p.tiles) * kTileV, p.tpad);
   // a forward that reads the weights in place has nothing to divide but the grid
   uint32_t piece = p.piece;
-  if (!BWD && p.few) piece = p.tiles < kMaxTiles / 8 ? p.tiles : (uint32_t)(kMaxTiles / 8);
+  if (!BWD && groups) piece = p.tiles < kMaxTiles / 8 ? p.tiles : (uint32_t)(kMaxTiles / 8);
   else if (!BWD && direct) piece = nt <= kMaxTiles / p.tiles ? p.tiles : kMaxTiles / nt ? (uint32_t)(kMaxTiles / nt) : 1;
-  if (!BWD) a.parts = p.tiles * (p.few ? kTileV / (16 * p.few) : tile == 256 ? 2 : 4);
+  if (!BWD) a.parts = p.tiles * (groups ? kTileV / (16 * groups) : tile == 256 ? 2 : 4);
   for (a.tile0 = 0; a.tile0 < p.tiles; a.tile0 += piece) {
     a.ntiles = p.tiles - a.tile0 < piece ? p.tiles - a.tile0 : piece;
-    if (!direct && (BWD || !p.few)) {
+    if (!direct && (BWD || !groups)) {
       l.tile0 = a.tile0;
       l.rows = (uint64_t)a.ntiles * kTileV;
       layout<T>(l, s);
       a.laid = ws + p.laid;
     }
     const uint64_t rows = (uint64_t)a.ntiles * kTileV;
-    if (p.few) few<T, BWD>(a, p.few, s);
-    else if (tile == 256) logits<M, 256, BWD, SEG>(a, s);
-    else logits<M, 128, BWD, SEG>(a, s);
+    if (groups) few<T, BWD>(a, groups, s);
+    else logits<M, BWD, SEG>(a, tile, s);
     if constexpr (BWD) {
-      if (c.dhidden) {
-        if (p.dh_tile == 256) dhidden<M, 256, SEG>(a, s);
-        else dhidden<M, 128, SEG>(a, s);
-      }
+      if (c.dhidden) dhidden<M, SEG>(a, p.dh_tile, s);
       a.add = 1;
-      if (c.dweights) {
-        if (pick_tile(p.kpad, rows) == 256) dweight<M, T, 256, SEG>(a, s);
-        else dweight<M, T, 128, SEG>(a, s);
-      }
+      if (c.dweights) dweight<M, T, SEG>(a, pick_tile(p.kpad, rows), s);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -957,9 +978,9 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
   } else {
     const uint64_t parts = a.parts;
     const XentJoinArgs j{a.part, a.zt, c.targets, c.ignore, (int64_t)vocab, c.loss, c.lse_out,
-                         p.few ? 1u : c.tokens, p.few ? parts : 1u, (uint32_t)parts, c.tokens};
+                         groups ? 1u : c.tokens, groups ? parts : 1u, (uint32_t)parts, c.tokens};
     // as many chains as leave every CU a workgroup
-    const uint32_t jt = p.few ? 1 : c.tokens <= 1024 ? 4 : 16;
+    const uint32_t jt = groups ? 1 : c.tokens <= 1024 ? 4 : 16;
     const dim3 grid((c.tokens + jt - 1) / jt), block(kJoinThreads);
     if (jt == 1) hipLaunchKernelGGL(join_k<1>, grid, block, 0, s, j);
     else if (jt == 4) hipLaunchKernelGGL(join_k<4>, grid, block, 0, s, j);
