@@ -82,6 +82,7 @@ template <int S> __device__ __forceinline__ uint32_t col_frag(int m0, int r, int
 typedef __attribute__((address_space(3))) uint8_t lds8;
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
 
 __device__ __forceinline__ u32x4 read_row(const lds8* p) { return *(const lds_u32x4*)p; }
 __device__ __forceinline__ u32x4 read_col(const lds8* lo, const lds8* hi) {
@@ -227,6 +228,53 @@ template <int T, bool ACOL, bool BCOL, int S, int NS> struct Tile {
     for (int q = 0; q < Q - 1; ++q) quarter(q & 1, q + 1);
 #pragma unroll
     for (int p = 0; p < kProducts; ++p) product(1, p);
+  }
+
+  // Hands out the accumulators of the wave's j-th 32 columns by rows of n, through LDS so
+  // that neighbouring lanes hold neighbouring m: put(n, m, x) for W consecutive m from m
+  // on, n and m within the tile.  Before that fix(add) may add to rows: add(r, m, x) to 4
+  // values of the wave's r-th row, m from its first.  The caller has a barrier between
+  // run() and the first call.
+  template <int W, class Fix, class Put> __device__ __forceinline__ void rows_out(lds8* lds, int j, Fix&& fix, Put&& put) const {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int kRow = FM * 128, kUnits = FM * 32 / W;  // bytes of a row of m, units of W in it
+    lds8* mine = lds + wave * (32 * kRow);
+    const int n = lane & 31;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int chunk = (i * 8 + 2 * q + (lane >> 5)) ^ (n & 15);
+        const f32x16& v = acc[i][j];
+        *(lds_f32x4*)(mine + n * kRow + chunk * 16) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+      }
+    auto settle = [] {
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    };
+    settle();
+    fix([&](int r, int m, const float (&x)[4]) {
+      lds_f32x4* at = (lds_f32x4*)(mine + r * kRow + (((m >> 2) ^ (r & 15)) << 4));
+      f32x4 v = *at;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += x[e];
+      *at = v;
+      settle();
+    });
+#pragma unroll 4
+    for (int r = 0; r < 32 * kUnits / 64; ++r) {
+      const int at = r * 64 + lane, row = at / kUnits, unit = at % kUnits;
+      float x[W];
+#pragma unroll
+      for (int b = 0; b < W / 4; ++b) {
+        const f32x4 v = *(const lds_f32x4*)(mine + row * kRow + (((unit * (W / 4) + b) ^ (row & 15)) << 4));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[4 * b + e] = v[e];
+      }
+      put((wave % WN * FN + j) * 32 + row, wave / WN * (FM * 32) + unit * W, x);
+    }
+    __builtin_amdgcn_wave_barrier();
   }
 };
 

@@ -94,6 +94,9 @@ struct XentArgs {
   const XentToken* token;
   const int32_t* place;
   const int32_t* idx;
+  float* residue;               // [tpad]: what rounding took from the target's dz
+  uint32_t* hits;               // counted tokens by their target's tile, null: not sorted
+  uint32_t* hits_first;         // [tiles + 1]: a tile's first
   float* sum;                   // [splits][tpad][kpad]
   uint32_t splits, add;
   void* dhidden;
@@ -136,7 +139,7 @@ struct XentCall {
 struct XentPlan {
   uint32_t tpad, kpad, tiles, piece, splits, dh_tile;
   uint64_t h_plane, laid_plane, dz_plane;
-  uint64_t h, laid, dz, sum, token, idx, place, scalars, most, part, zt;
+  uint64_t h, laid, dz, sum, token, idx, place, residue, hits, hits_first, scalars, most, part, zt;
   uint64_t bytes;
 };
 

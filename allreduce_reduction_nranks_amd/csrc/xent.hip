@@ -258,27 +258,37 @@ __device__ __forceinline__ bool tile_of(uint32_t id, uint32_t mt, uint32_t nt, u
 }
 uint32_t tile_grid(uint64_t tiles) { return (uint32_t)((tiles + 7) / 8 * 8); }
 
-// dz of 4 vocabulary rows from m on, for one token; zeros from row `left` on.  T is
-// the caller's type.
-template <int T>
-__device__ __forceinline__ void store_dz(uint8_t* row, uint64_t plane, uint32_t m, const float* z, const XentToken& tk,
-                                         uint32_t hit, uint32_t left) {
+// dz of a logit.
+template <bool F32> __device__ __forceinline__ float dz_of(float z, const XentToken& tk, bool hit) {
+  const float x = z - tk.lse;
+  return ((F32 ? __builtin_expf(x) : __builtin_amdgcn_exp2f(x * kLog2e)) - (hit ? 1.0f : 0.0f)) * tk.dl;
+}
+
+// What 16 bits lose of a target's dz, nearly all of most rows' gradient: kept in f32
+// and added to the sums of both gradients, so that the rounding of dz does not show
+// in them.  (An f32 call's dz keeps 22 bits.)
+template <int T> __device__ __forceinline__ float residue_of(float d) {
+  const float r = d - to_f32<T>(from_f32<T>(d));
+  return (__float_as_uint(r) & 0x7F800000u) != 0x7F800000u ? r : 0.0f;
+}
+
+// N values of dz stored in T (f32: as planes).
+template <int T, int N> __device__ __forceinline__ void store_dz(uint8_t* to, uint64_t plane, const float* d) {
   constexpr int P = T == kF32 ? kPlanes : 1;
-  uint32_t w[P][2] = {};
+  uint32_t w[P][N / 2] = {};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float x = z[e] - tk.lse;
-    float d = T == kF32 ? __builtin_expf(x) : __builtin_amdgcn_exp2f(x * kLog2e);
-    d = (d - (m + e == hit ? 1.0f : 0.0f)) * tk.dl;
-    if (m + e >= left) d = 0.0f;
+  for (int e = 0; e < N; ++e) {
     uint32_t part[kPlanes];
-    if constexpr (T == kF32) split(d, part);
-    else part[0] = from_f32<T>(d);
+    if constexpr (T == kF32) split(d[e], part);
+    else part[0] = from_f32<T>(d[e]);
 #pragma unroll
     for (int b = 0; b < P; ++b) w[b][e >> 1] |= part[b] << (16 * (e & 1));
   }
 #pragma unroll
-  for (int b = 0; b < P; ++b) *reinterpret_cast<u32x2*>(row + b * plane + m * 2) = u32x2{w[b][0], w[b][1]};
+  for (int b = 0; b < P; ++b) {
+    if constexpr (N == 8) *reinterpret_cast<u32x4*>(to + b * plane) = u32x4{w[b][0], w[b][1], w[b][2], w[b][3]};
+    else *reinterpret_cast<u32x2*>(to + b * plane) = u32x2{w[b][0], w[b][1]};
+  }
 }
 
 // Logits of one tile of S vocabulary rows by S tokens.  Forward: reduced to a
@@ -364,18 +374,21 @@ __global__ void __launch_bounds__(tile_threads(S)) logits_k(XentArgs a) {
     } else {
       const XentToken tk = a.token[t];
       const bool live = t < tokens;
-      const uint32_t hit = tk.target >= 0 && (uint32_t)tk.target - first < left ? (uint32_t)tk.target - first : ~0u;
-      uint8_t* row = a.dz + (uint64_t)t * a.lddz + (uint64_t)mt * S * 2;
+      const uint32_t hit = live && (uint32_t)tk.target - first < left ? (uint32_t)tk.target - first : ~0u;
 #pragma unroll
       for (int i = 0; i < Prod::FM; ++i)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t m = (wm * Prod::FM + i) * 32 + 8 * q + 4 * (lane >> 5);
-          float z[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) z[e] = SEG > 1 ? p.acc[i][j][4 * q + e] * unscale : p.acc[i][j][4 * q + e];
-          store_dz<SEG == 1 ? T : (int)kF32>(row, a.dz_plane, m, z, tk, hit, live ? left : 0u);
+        for (int e = 0; e < 16; ++e) {
+          const uint32_t m = (wm * Prod::FM + i) * 32 + acc_row(lane, e);
+          const float z = SEG > 1 ? p.acc[i][j][e] * unscale : p.acc[i][j][e];
+          const float d = live && m < left ? dz_of<(SEG > 1)>(z, tk, m == hit) : 0.0f;
+          if (SEG == 1 && m == hit) a.residue[t] = residue_of<T>(d);
+          p.acc[i][j][e] = d;
         }
+      if (j == 0) __syncthreads();
+      p.template rows_out<8>((lds8*)lds, j, [](auto) {}, [&](int n, int m, const float (&d)[8]) {
+        store_dz<SEG == 1 ? T : (int)kF32, 8>(a.dz + (uint64_t)(t0 + n) * a.lddz + ((uint64_t)mt * S + m) * 2, a.dz_plane, d);
+      });
     }
   }
 }
@@ -518,12 +531,20 @@ template <int T, int NT, int R, bool BWD> __global__ void __launch_bounds__(256)
     if (lane < 16 && t < tokens) a.part[(uint64_t)t * a.parts + (uint64_t)a.tile0 * per + blockIdx.x] = make_float2(top, s);
   } else {
     const XentToken tk = a.token[t];
-    const uint32_t hit = tk.target >= 0 && (uint32_t)tk.target - first < left ? (uint32_t)tk.target - first : ~0u;
+    const bool live = t < tokens;
+    const uint32_t hit = live && (uint32_t)tk.target - first < left ? (uint32_t)tk.target - first : ~0u;
     uint8_t* row = a.dz + (uint64_t)t * a.lddz + ((uint64_t)mt * kTileV + sub) * 2;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float x[4] = {z[r][0], z[r][1], z[r][2], z[r][3]};
-      store_dz<T>(row, a.dz_plane, 16 * r + 4 * (lane >> 4), x, tk, hit, t < tokens ? left : 0u);
+      float d[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t m = 16 * r + 4 * (lane >> 4) + e;
+        d[e] = live && m < left ? dz_of<T == kF32>(z[r][e], tk, m == hit) : 0.0f;
+        if constexpr (T != kF32)
+          if (m == hit) a.residue[t] = residue_of<T>(d[e]);
+      }
+      store_dz<T, 4>(row + (16 * r + 4 * (lane >> 4)) * 2, a.dz_plane, d);
     }
   }
 }
@@ -538,7 +559,7 @@ template <int T, int S, int NS, int SEG> __global__ void __launch_bounds__(tile_
   if (!tile_of(blockIdx.x, (a.kpad + S - 1) / S, a.tpad / S, mt, nt)) return;
   const uint32_t t0 = nt * S, c0 = mt * S;
   if (t0 >= a.scalars->count) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x;
   const uint32_t blocks = a.ntiles * (kTileV / kTileK);  // of 64 rows
   const uint32_t split = blockIdx.y;
   const uint32_t k0 = (uint32_t)((uint64_t)blocks * split / a.splits), k1 = (uint32_t)((uint64_t)blocks * (split + 1) / a.splits);
@@ -580,26 +601,57 @@ template <int T, int S, int NS, int SEG> __global__ void __launch_bounds__(tile_
   Prod p;
   p.run((int)(k1 - k0) * SEG, (lds8*)lds, src);
 
-  const int wm = wave / Prod::WN, wn = wave % Prod::WN;
   float* sum = a.sum + (uint64_t)split * a.tpad * a.kpad;
+  __syncthreads();
 #pragma unroll
-  for (int j = 0; j < Prod::FN; ++j) {
-    const uint32_t t = t0 + (wn * Prod::FN + j) * 32 + (lane & 31);
+  for (int j = 0; j < Prod::FN; ++j)
+    p.template rows_out<4>((lds8*)lds, j, [](auto) {}, [&](int n, int m, const float (&x)[4]) {
+      if (c0 + m >= a.kpad) return;
+      f32x4* to = reinterpret_cast<f32x4*>(sum + (uint64_t)(t0 + n) * a.kpad + c0 + m);
+      f32x4 y = {x[0], x[1], x[2], x[3]};
+      if (a.add) {
+        const f32x4 o = *to;
 #pragma unroll
-    for (int i = 0; i < Prod::FM; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t c = c0 + (wm * Prod::FM + i) * 32 + 8 * q + 4 * (lane >> 5);
-        if (c >= a.kpad) continue;
-        f32x4* to = reinterpret_cast<f32x4*>(sum + (uint64_t)t * a.kpad + c);
-        f32x4 x = {p.acc[i][j][4 * q], p.acc[i][j][4 * q + 1], p.acc[i][j][4 * q + 2], p.acc[i][j][4 * q + 3]};
-        if (a.add) {
-          const f32x4 o = *to;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = o[e] + x[e];
-        }
-        *to = x;
+        for (int e = 0; e < 4; ++e) y[e] = o[e] + y[e];
       }
+      *to = y;
+    });
+}
+
+// Counted tokens in the order of their targets' 256-row tiles, tokens of a tile in
+// order: a workgroup a tile finds its own and counts those of the tiles before.
+__global__ void __launch_bounds__(256) hits_k(XentArgs a) {
+  __shared__ uint32_t before[4], mine[4];
+  const uint32_t tile = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int sh = 0;
+  while (tile >= a.v.first_tile[sh + 1]) ++sh;
+  const uint32_t row0 = (tile - a.v.first_tile[sh]) * kTileV, first = a.v.first_row[sh] + row0;
+  const uint32_t rows = a.v.rows[sh] - row0 < (uint32_t)kTileV ? a.v.rows[sh] - row0 : (uint32_t)kTileV;
+  const uint32_t count = a.scalars->count;
+  uint32_t less = 0;
+  for (uint32_t t = tid; t < count; t += 256) less += (uint32_t)a.token[t].target < first;
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) less += __shfl_xor(less, m);
+  if (lane == 0) before[wave] = less;
+  __syncthreads();
+  uint32_t at = before[0] + before[1] + before[2] + before[3];
+  if (tid == 0) {
+    a.hits_first[tile] = at;
+    if (tile + 1 == gridDim.x) a.hits_first[tile + 1] = count;
+  }
+  for (uint32_t t0 = 0; t0 < count; t0 += 256) {
+    const uint32_t t = t0 + tid;
+    const bool in = t < count && (uint32_t)a.token[t].target - first < rows;
+    const uint64_t mask = __ballot(in);
+    if (lane == 0) mine[wave] = (uint32_t)__popcll(mask);
+    __syncthreads();
+    uint32_t to = at + (uint32_t)__popcll(mask & ((1ull << lane) - 1));
+    for (uint32_t w = 0; w < 4; ++w) {
+      if (w < wave) to += mine[w];
+      at += mine[w];
+    }
+    if (in) a.hits[to] = t;
+    __syncthreads();
   }
 }
 
@@ -642,23 +694,58 @@ template <int T, int OUT, int S, int NS, int SEG> __global__ void __launch_bound
   p.run((int)blocks * SEG, (lds8*)lds, src);
 
   const float unscale = a.scalars->unscale_dz * (SEG > 1 ? a.scalars->unscale_h : 1.0f);
-  const int wm = wave / Prod::WN, wn = wave % Prod::WN;
+  constexpr int W = OUT == kF32 ? 4 : 8;
+  const uint32_t first = a.v.first_row[sh] + row0;
+  // tokens whose target may lie in this tile: its list, or of a short call all
+  uint32_t h0 = 0, h1 = 0;
+  if constexpr (SEG == 1) {
+    h0 = a.hits ? a.hits_first[tile] : 0u;
+    h1 = a.hits ? a.hits_first[tile + 1] : a.scalars->count;
+  }
+  // a lane's token of the list's k-th 64, and its target's row in the tile
+  auto entry = [&](uint32_t k, uint32_t& t) {
+    t = k < h1 ? (a.hits ? a.hits[k] : k) : 0u;
+    return k < h1 ? (uint32_t)a.token[t].target - first : ~0u;
+  };
+  uint32_t t0 = 0, r0 = ~0u;
+  if (h0 < h1) r0 = entry(h0 + lane, t0);
+  const int wm0 = wave / Prod::WN * (Prod::FM * 32);  // the wave's first column of the tile
+  const uint32_t hc = c0 + wm0 + 4 * lane;
+  __syncthreads();
 #pragma unroll
   for (int j = 0; j < Prod::FN; ++j) {
-    const uint32_t v = (wn * Prod::FN + j) * 32 + (lane & 31);
-    if (v >= left) continue;
-    uint8_t* row = at<OUT>(a.dw[sh], (uint64_t)(row0 + v) * a.ld_dw);
-#pragma unroll
-    for (int i = 0; i < Prod::FM; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t c = c0 + (wm * Prod::FM + i) * 32 + 8 * q + 4 * (lane >> 5);
-        if (c >= a.cols) continue;
-        float x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = p.acc[i][j][4 * q + e] * unscale;
-        store4<OUT>(at<OUT>(row, c), (int)(a.cols - c), x);
+    const uint32_t n0 = (wave % Prod::WN * Prod::FN + j) * 32;
+    auto residues = [&](auto add) {
+      for (uint32_t k = h0; k < h1; k += 64) {
+        uint32_t t = t0, r = r0;
+        if (k != h0) r = entry(k + lane, t);
+        uint64_t mask = __ballot(r - n0 < 32u);
+        while (mask) {
+          const int l = __builtin_ctzll(mask);
+          mask &= mask - 1;
+          const uint32_t token = __builtin_amdgcn_readlane(t, l), row = __builtin_amdgcn_readlane(r, l) - n0;
+          if (lane < Prod::FM * 8 && hc < a.kpad) {
+            const u32x2 raw = *reinterpret_cast<const u32x2*>(a.h + (uint64_t)token * a.ldh + (uint64_t)hc * 2);
+            const float e = a.residue[token];
+            const float x[4] = {e * to_f32<T>(raw.x & 0xFFFFu), e * to_f32<T>(raw.x >> 16), e * to_f32<T>(raw.y & 0xFFFFu),
+                                e * to_f32<T>(raw.y >> 16)};
+            add((int)row, 4 * lane, x);
+          }
+        }
       }
+    };
+    p.template rows_out<W>(
+        (lds8*)lds, j,
+        [&](auto add) {
+          if constexpr (SEG == 1) residues(add);
+        },
+        [&](int n, int m, float (&x)[W]) {
+          const uint32_t c = c0 + m;
+          if ((uint32_t)n >= left || c >= a.cols) return;
+#pragma unroll
+          for (int i = 0; i < W; ++i) x[i] *= unscale;
+          store_raw<OUT>(at<OUT>(a.dw[sh], (uint64_t)(row0 + n) * a.ld_dw + c), (int)(a.cols - c), encode16<OUT>(x));
+        });
   }
 }
 
@@ -706,6 +793,17 @@ template <int T> __global__ void __launch_bounds__(256) dhidden_join_k(XentArgs 
   const float unscale = a.scalars->unscale_dz * (T == kF32 ? a.scalars->unscale_w : 1.0f);
   for (uint32_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
     const int32_t from = a.place[t];
+    const uint8_t* w = nullptr;  // the target's row
+    float residue = 0.0f;
+    if constexpr (T != kF32) {
+      if (from >= 0) {
+        const uint32_t target = (uint32_t)a.token[from].target;
+        int sh = 0;
+        while (target - a.v.first_row[sh] >= a.v.rows[sh]) ++sh;
+        w = at<T>(a.v.w[sh], (uint64_t)(target - a.v.first_row[sh]) * a.ld_w);
+        residue = a.residue[from];
+      }
+    }
     for (uint32_t c = 4 * (blockIdx.y * 256 + threadIdx.x); c < a.cols; c += 1024 * gridDim.y) {
       float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       if (from >= 0) {
@@ -716,7 +814,10 @@ template <int T> __global__ void __launch_bounds__(256) dhidden_join_k(XentArgs 
           for (int e = 0; e < 4; ++e) x[e] += y[e];
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] *= unscale;
+        for (int e = 0; e < 4; ++e) {
+          if (T != kF32 && c + e < a.cols) x[e] = __builtin_fmaf(residue, load_elem<T>(w, c + e), x[e]);
+          x[e] *= unscale;
+        }
       }
       store4<T>(at<T>(a.dhidden, (uint64_t)t * a.ld_dh + c), (int)(a.cols - c), x);
     }
@@ -792,6 +893,9 @@ XentPlan xent_plan(uint32_t tokens, uint32_t cols, const size_t* rows, int nrank
     p.token = take((uint64_t)p.tpad * sizeof(XentToken));
     p.idx = take((uint64_t)p.tpad * 4);
     p.place = take((uint64_t)tokens * 4);
+    p.residue = take((uint64_t)p.tpad * 4);
+    p.hits = take((uint64_t)p.tpad * 4);
+    p.hits_first = take((tiles + 1) * 4);
   } else {
     // pairs of a tile and token: at most few_k's, else those of 128 x 128 tiles
     p.part = take(tiles * (tokens <= 16 ? 16 : tokens <= 32 ? 8 : 4) * tokens * sizeof(float2));
@@ -911,6 +1015,7 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
     a.token = (XentToken*)(ws + p.token);
     a.place = (int32_t*)(ws + p.place);
     a.idx = (const int32_t*)(ws + p.idx);
+    a.residue = (float*)(ws + p.residue);
     a.dhidden = c.dhidden;
     a.ld_dh = c.ld_hidden;
     a.ld_dw = c.ld_weight;
@@ -918,6 +1023,12 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
                        (int32_t*)(ws + p.idx), (int32_t*)(ws + p.place), scalars, c.tokens, p.tpad, T != kBF16};
     hipLaunchKernelGGL(tokens_k, dim3(1), dim3(kTokensThreads), 0, s, t);
     l.idx = (const int32_t*)(ws + p.idx);
+    // up to 64 tokens a tile's workgroup looks through them all
+    if (T != kF32 && c.dweights && c.tokens > 64) {
+      a.hits = (uint32_t*)(ws + p.hits);
+      a.hits_first = (uint32_t*)(ws + p.hits_first);
+      hipLaunchKernelGGL(hits_k, dim3(p.tiles), dim3(256), 0, s, a);
+    }
   } else {
     a.part = (float2*)(ws + p.part);
     a.zt = (float*)(ws + p.zt);
