@@ -15,6 +15,7 @@ from __future__ import annotations
 import builtins
 import ctypes
 import os
+import struct
 import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -59,7 +60,7 @@ def load_library() -> ctypes.CDLL:
             raise RuntimeError("libmrr.so is not built (%s); run __graft_entry__.build()" % LIB_PATH)
         L = ctypes.CDLL(LIB_PATH)
         vp, sz, i, u32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_uint32
-        f32, i64, psz = ctypes.c_float, ctypes.c_int64, ctypes.POINTER(sz)
+        f32, i64 = ctypes.c_float, ctypes.c_int64
         pp = ctypes.POINTER(vp)
         sigs = {
             "mrr_allreduce_rsag": ([pp, pp, sz, i, i, vp], i),
@@ -82,12 +83,12 @@ def load_library() -> ctypes.CDLL:
             "mrr_fp8b15_to_f32": ([vp, vp, sz, vp], i),
             "mrr_f16_to_fp8b15": ([vp, vp, sz, vp], i),
             "mrr_f32_to_fp8b15": ([vp, vp, sz, vp], i),
-            "mrr_layernorm_fwd": ([pp, i, vp, vp, vp, vp, vp, vp, vp, sz, sz, sz, sz, f32, i, i, vp], i),
+            "mrr_layernorm_fwd": ([vp, i, vp, vp, vp, vp, vp, vp, vp, sz, sz, sz, sz, f32, i, i, vp], i),
             "mrr_layernorm_bwd_workspace_bytes": ([sz, sz], sz),
             "mrr_layernorm_bwd": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, sz, sz, sz, i, i, vp, sz, vp], i),
-            "mrr_linear_xent_workspace_bytes": ([sz, sz, psz, i, i, i], sz),
-            "mrr_linear_xent_fwd": ([vp, pp, psz, i, vp, i64, vp, vp, sz, sz, sz, sz, i, vp, sz, vp], i),
-            "mrr_linear_xent_bwd": ([vp, pp, psz, i, vp, i64, vp, vp, sz, vp, pp, sz, sz, sz, sz, i, vp, sz, vp], i),
+            "mrr_linear_xent_workspace_bytes": ([sz, sz, vp, i, i, i], sz),
+            "mrr_linear_xent_fwd": ([vp, vp, vp, i, vp, i64, vp, vp, sz, sz, sz, sz, i, vp, sz, vp], i),
+            "mrr_linear_xent_bwd": ([vp, vp, vp, i, vp, i64, vp, vp, sz, vp, vp, sz, sz, sz, sz, i, vp, sz, vp], i),
             "mrr_stream_copy": ([vp, vp, sz, vp], i),
             "mrr_rank_buffer_pitch": ([sz, i], sz),
             "mrr_status_string": ([i], ctypes.c_char_p),
@@ -401,23 +402,59 @@ def _span(x) -> int:
     return (1 + builtins.sum((n - 1) * s for n, s in zip(x.shape, x.stride()))) * x.element_size()
 
 
-def _rows_room(x, nbytes: int, what: str) -> None:
-    """_room() for an argument whose rows may lie apart: a view of a wider tensor
-    counts with its strides."""
-    if x is not None and not isinstance(x, int) and x.nbytes < nbytes and _span(x) < nbytes:
+def _rows_arg(x, nbytes: int, what: str) -> int:
+    """Address of an argument whose rows may lie apart: a tensor must hold nbytes
+    bytes, a view of a wider one counting with its strides.  (Checks and addresses
+    in one step, and packed pointer arrays below: they halve an eager call's host
+    cost, which is what a small call takes.)"""
+    if x is None:
+        return 0
+    if isinstance(x, int):
+        return x
+    if x.nbytes < nbytes and _span(x) < nbytes:
         raise ValueError("%s spans %d bytes, the call needs %d" % (what, _span(x), nbytes))
+    return x.data_ptr()
 
 
-def _rows_ptrs(xs, n: int, nbytes, what: str):
-    """_rank_ptrs() for per-rank matrices; nbytes[r] is what entry r has to span."""
+def _flat_arg(x, nbytes: int, what: str) -> int:
+    """_rows_arg() for an argument without a row stride."""
+    if x is None:
+        return 0
+    if isinstance(x, int):
+        return x
+    if x.nbytes < nbytes:
+        raise ValueError("%s holds %d bytes, the call needs %d" % (what, x.nbytes, nbytes))
+    return x.data_ptr()
+
+
+_words: dict = {}
+
+
+def _pack(values) -> bytes:
+    """Host array of 64-bit words for the C ABI (it lives as long as the call's arguments)."""
+    n = len(values)
+    p = _words.get(n)
+    if p is None:
+        p = _words[n] = struct.Struct("%dQ" % n).pack
+    return p(*values)
+
+
+def _rows_args(xs, n: int, nbytes, what: str):
+    """Packed addresses of per-rank matrices; nbytes[r] is what entry r has to span
+    (one number: all of them)."""
     if xs is None:
         return None
     if len(xs) < n:
         raise ValueError("%s has %d entries, nranks is %d" % (what, len(xs), n))
-    for r in range(n):
-        if xs[r] is not None and type(xs[r]) is not int and xs[r].nbytes < nbytes[r]:
-            _rows_room(xs[r], nbytes[r], "%s[%d]" % (what, r))
-    return (_VP * len(xs))(*[_ptr(x) for x in xs])
+    one = type(nbytes) is int
+    ptrs = []
+    for r, x in enumerate(xs):
+        if x is None or type(x) is int:
+            ptrs.append(x or 0)
+            continue
+        need = 0 if r >= n else nbytes if one else nbytes[r]
+        ptrs.append(x.data_ptr() if x.nbytes >= need else _rows_arg(x, need, "%s[%d]" % (what, r)))
+    return _pack(ptrs)
 
 
 def _wtype(dtype, wdtype) -> int:
@@ -428,19 +465,15 @@ def _wtype(dtype, wdtype) -> int:
 def mrr_layernorm_fwd(inputs, nranks, residual, weight, bias, sum, out, mean, rstd, rows, cols,
                       ld_in, ld_out, eps, dtype, wdtype="auto", stream=None) -> int:
     t, tw = _dt(dtype), _wtype(dtype, wdtype)
-    nin, nout = (_matrix_bytes(rows, cols, ld, _ESIZE.get(t, 0)) for ld in (ld_in, ld_out))
+    nin = nout = _matrix_bytes(rows, cols, ld_in, _ESIZE.get(t, 0))
+    if ld_out != ld_in:
+        nout = _matrix_bytes(rows, cols, ld_out, _ESIZE.get(t, 0))
     wb = cols * _ESIZE.get(tw, 0)
-    _rows_room(residual, nin, "residual")
-    _room(weight, wb, "weight")
-    _room(bias, wb, "bias")
-    _rows_room(sum, nout, "sum")
-    _rows_room(out, nout, "out")
-    _room(mean, 4 * rows, "mean")
-    _room(rstd, 4 * rows, "rstd")
     return load_library().mrr_layernorm_fwd(
-        _rows_ptrs(inputs, nranks, [nin] * max(0, nranks), "inputs"), nranks, _ptr(residual), _ptr(weight), _ptr(bias),
-        _ptr(sum), _ptr(out), _ptr(mean), _ptr(rstd), rows, cols, ld_in, ld_out, eps, t, tw,
-        _stream(stream))
+        _rows_args(inputs, nranks, nin, "inputs"), nranks, _rows_arg(residual, nin, "residual"),
+        _flat_arg(weight, wb, "weight"), _flat_arg(bias, wb, "bias"), _rows_arg(sum, nout, "sum"),
+        _rows_arg(out, nout, "out"), _flat_arg(mean, 4 * rows, "mean"), _flat_arg(rstd, 4 * rows, "rstd"),
+        rows, cols, ld_in, ld_out, eps, t, tw, _stream(stream))
 
 
 def mrr_layernorm_bwd_workspace_bytes(rows, cols) -> int:
@@ -451,22 +484,16 @@ def mrr_layernorm_bwd(dout, sum, weight, mean, rstd, dresidual, dsum, dweight, d
                       ld_in, ld_out, dtype, wdtype="auto", workspace=None, workspace_bytes=0,
                       stream=None) -> int:
     t, tw = _dt(dtype), _wtype(dtype, wdtype)
-    nin, nout = (_matrix_bytes(rows, cols, ld, _ESIZE.get(t, 0)) for ld in (ld_in, ld_out))
+    nin = nout = _matrix_bytes(rows, cols, ld_in, _ESIZE.get(t, 0))
+    if ld_out != ld_in:
+        nout = _matrix_bytes(rows, cols, ld_out, _ESIZE.get(t, 0))
     wb = cols * _ESIZE.get(tw, 0)
-    _rows_room(dout, nin, "dout")
-    _rows_room(sum, nin, "sum")
-    _room(weight, wb, "weight")
-    _room(mean, 4 * rows, "mean")
-    _room(rstd, 4 * rows, "rstd")
-    _rows_room(dresidual, nin, "dresidual")
-    _rows_room(dsum, nout, "dsum")
-    _room(dweight, wb, "dweight")
-    _room(dbias, wb, "dbias")
-    _room(workspace, workspace_bytes, "workspace")
     return load_library().mrr_layernorm_bwd(
-        _ptr(dout), _ptr(sum), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dresidual), _ptr(dsum),
-        _ptr(dweight), _ptr(dbias), rows, cols, ld_in, ld_out, t, tw, _ptr(workspace),
-        workspace_bytes, _stream(stream))
+        _rows_arg(dout, nin, "dout"), _rows_arg(sum, nin, "sum"), _flat_arg(weight, wb, "weight"),
+        _flat_arg(mean, 4 * rows, "mean"), _flat_arg(rstd, 4 * rows, "rstd"),
+        _rows_arg(dresidual, nin, "dresidual"), _rows_arg(dsum, nout, "dsum"), _flat_arg(dweight, wb, "dweight"),
+        _flat_arg(dbias, wb, "dbias"), rows, cols, ld_in, ld_out, t, tw,
+        _flat_arg(workspace, workspace_bytes, "workspace"), workspace_bytes, _stream(stream))
 
 
 def _sizes(rows, n: int):
@@ -474,7 +501,7 @@ def _sizes(rows, n: int):
         return None
     if len(rows) < n:
         raise ValueError("rows has %d entries, nranks is %d" % (len(rows), n))
-    return (ctypes.c_size_t * max(1, len(rows)))(*rows)
+    return _pack(rows) if len(rows) else _pack((0,))
 
 
 def mrr_linear_xent_workspace_bytes(tokens, cols, rows, nranks, dtype, backward) -> int:
@@ -484,36 +511,31 @@ def mrr_linear_xent_workspace_bytes(tokens, cols, rows, nranks, dtype, backward)
 
 def mrr_linear_xent_fwd(hidden, weights, rows, nranks, targets, ignore_index, loss, lse, tokens, cols,
                         ld_hidden, ld_weight, dtype, workspace=None, workspace_bytes=0, stream=None) -> int:
-    t, e = _dt(dtype), _ESIZE.get(_dt(dtype), 0)
+    t = _dt(dtype)
+    e = _ESIZE.get(t, 0)
     sizes = _sizes(rows, nranks)
-    _rows_room(hidden, _matrix_bytes(tokens, cols, ld_hidden, e), "hidden")
-    _room(targets, 8 * tokens, "targets")
-    _room(loss, 4 * tokens, "loss")
-    _room(lse, 4 * tokens, "lse")
-    _room(workspace, workspace_bytes, "workspace")
     need = [_matrix_bytes(n, cols, ld_weight, e) for n in rows[:max(0, nranks)]] if rows is not None else []
     return load_library().mrr_linear_xent_fwd(
-        _ptr(hidden), _rows_ptrs(weights, len(need), need, "weights"), sizes, nranks, _ptr(targets), ignore_index,
-        _ptr(loss), _ptr(lse), tokens, cols, ld_hidden, ld_weight, t, _ptr(workspace), workspace_bytes, _stream(stream))
+        _rows_arg(hidden, _matrix_bytes(tokens, cols, ld_hidden, e), "hidden"),
+        _rows_args(weights, len(need), need, "weights"), sizes, nranks, _flat_arg(targets, 8 * tokens, "targets"),
+        ignore_index, _flat_arg(loss, 4 * tokens, "loss"), _flat_arg(lse, 4 * tokens, "lse"), tokens, cols, ld_hidden,
+        ld_weight, t, _flat_arg(workspace, workspace_bytes, "workspace"), workspace_bytes, _stream(stream))
 
 
 def mrr_linear_xent_bwd(hidden, weights, rows, nranks, targets, ignore_index, lse, dloss, dloss_stride, dhidden,
                         dweights, tokens, cols, ld_hidden, ld_weight, dtype, workspace=None, workspace_bytes=0,
                         stream=None) -> int:
-    t, e = _dt(dtype), _ESIZE.get(_dt(dtype), 0)
+    t = _dt(dtype)
+    e = _ESIZE.get(t, 0)
     sizes = _sizes(rows, nranks)
     nh = _matrix_bytes(tokens, cols, ld_hidden, e)
-    _rows_room(hidden, nh, "hidden")
-    _room(targets, 8 * tokens, "targets")
-    _room(lse, 4 * tokens, "lse")
-    _rows_room(dloss, 4 * ((tokens - 1) * dloss_stride + 1) if tokens > 0 else 0, "dloss")
-    _rows_room(dhidden, nh, "dhidden")
-    _room(workspace, workspace_bytes, "workspace")
     need = [_matrix_bytes(n, cols, ld_weight, e) for n in rows[:max(0, nranks)]] if rows is not None else []
     return load_library().mrr_linear_xent_bwd(
-        _ptr(hidden), _rows_ptrs(weights, len(need), need, "weights"), sizes, nranks, _ptr(targets), ignore_index,
-        _ptr(lse), _ptr(dloss), dloss_stride, _ptr(dhidden), _rows_ptrs(dweights, len(need), need, "dweights"), tokens,
-        cols, ld_hidden, ld_weight, t, _ptr(workspace), workspace_bytes, _stream(stream))
+        _rows_arg(hidden, nh, "hidden"), _rows_args(weights, len(need), need, "weights"), sizes, nranks,
+        _flat_arg(targets, 8 * tokens, "targets"), ignore_index, _flat_arg(lse, 4 * tokens, "lse"),
+        _rows_arg(dloss, 4 * ((tokens - 1) * dloss_stride + 1) if tokens > 0 else 0, "dloss"), dloss_stride,
+        _rows_arg(dhidden, nh, "dhidden"), _rows_args(dweights, len(need), need, "dweights"), tokens, cols, ld_hidden,
+        ld_weight, t, _flat_arg(workspace, workspace_bytes, "workspace"), workspace_bytes, _stream(stream))
 
 
 def mrr_stream_copy(src, dst, nbytes, stream=None) -> int:
