@@ -29,6 +29,16 @@
 namespace mrr {
 namespace {
 
+// The same past the caches (NT) or through them.
+template <int T, bool NT> __device__ __forceinline__ u32x4 load_in(const void* p, int n) {
+  if (NT && n >= Vec<T>::VW) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
+  return load_raw<T>(p, n);
+}
+template <int T, bool NT> __device__ __forceinline__ void store_out(void* p, int n, u32x4 v) {
+  if (NT && n >= Vec<T>::VW) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(p));
+  else store_raw<T>(p, n, v);
+}
+
 // V weights from column c on, widened; `fill` where there is no weight.
 template <int T>
 __device__ __forceinline__ void load_weights(const void* w, int wf32, uint32_t c, int n, float fill,
@@ -76,7 +86,7 @@ constexpr int block_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
 // Elements of a lane's unit at column c that exist.
 __device__ __forceinline__ int unit_left(uint32_t cols, uint32_t c) { return c < cols ? (int)(cols - c) : 0; }
 
-template <int T, int TPR, int E>
+template <int T, int TPR, int E, bool NTL, bool NTS>
 __global__ void __launch_bounds__(block_threads(TPR)) norm_fwd_k(NormFwdArgs a) {
   constexpr int V = Vec<T>::VW, U = E / V, RPB = block_threads(TPR) / TPR;
   // ranks whose loads are in flight together
@@ -99,7 +109,7 @@ __global__ void __launch_bounds__(block_threads(TPR)) norm_fwd_k(NormFwdArgs a) 
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             const uint32_t c = (u * TPR + lane) * V;
-            raw[g][u] = load_raw<T>(p + (uint64_t)c * Ty<T>::size, live ? unit_left(a.cols, c) : 0);
+            raw[g][u] = load_in<T, NTL>(p + (uint64_t)c * Ty<T>::size, live ? unit_left(a.cols, c) : 0);
           }
         }
       }
@@ -121,7 +131,7 @@ __global__ void __launch_bounds__(block_threads(TPR)) norm_fwd_k(NormFwdArgs a) 
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const uint32_t c = (u * TPR + lane) * V;
-        raw[0][u] = load_raw<T>(p + (uint64_t)c * Ty<T>::size, live ? unit_left(a.cols, c) : 0);
+        raw[0][u] = load_in<T, NTL>(p + (uint64_t)c * Ty<T>::size, live ? unit_left(a.cols, c) : 0);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -137,7 +147,7 @@ __global__ void __launch_bounds__(block_threads(TPR)) norm_fwd_k(NormFwdArgs a) 
       const u32x4 h = encode16<T>(x + u * V);
       if (a.sum) {
         const uint32_t c = (u * TPR + lane) * V;
-        store_raw<T>(at<T>(a.sum, row * a.ld_out + c), live ? unit_left(a.cols, c) : 0, h);
+        store_out<T, NTS>(at<T>(a.sum, row * a.ld_out + c), live ? unit_left(a.cols, c) : 0, h);
       }
       decode16<T>(h, x + u * V);
 #pragma unroll
@@ -170,7 +180,7 @@ __global__ void __launch_bounds__(block_threads(TPR)) norm_fwd_k(NormFwdArgs a) 
       load_weights<T>(a.bias, a.wf32, c, n, 0.0f, b);
 #pragma unroll
       for (int j = 0; j < V; ++j) b[j] = __builtin_fmaf(x[u * V + j] * rstd, w[j], b[j]);
-      store_raw<T>(at<T>(a.out, row * a.ld_out + c), n, encode16<T>(b));
+      store_out<T, NTS>(at<T>(a.out, row * a.ld_out + c), n, encode16<T>(b));
     }
   }
 }
@@ -216,15 +226,14 @@ template <int T> __global__ void __launch_bounds__(kWideThreads) norm_fwd_wide_k
   }
 }
 
-// One group of TPR lanes walks the rows group, group + groups, ...; its lanes
-// keep the weight and bias gradients of their columns in registers over all of
-// them and write them once, so the sums over rows take a fixed order.
-template <int T, int TPR, int E>
-__global__ void __launch_bounds__(block_threads(TPR)) norm_bwd_k(NormBwdArgs a) {
-  constexpr int V = Vec<T>::VW, U = E / V, RPB = block_threads(TPR) / TPR;
-  __shared__ float2 lds[2][block_threads(TPR) / 64];
-  const uint32_t lane = threadIdx.x % TPR;
-  const uint32_t group = blockIdx.x * RPB + threadIdx.x / TPR;
+// A workgroup of BT lanes takes BT / TPR rows at a time, every gridDim-th such set; its
+// lanes keep the weight and bias gradients of their columns in registers over all of
+// them.  At the end the workgroup's rows are joined in LDS, in order, and written
+// once: the sums over rows take a fixed order.
+template <int T, int TPR, int E, int BT, bool AHEAD, bool NT> __global__ void __launch_bounds__(BT) norm_bwd_k(NormBwdArgs a) {
+  constexpr int V = Vec<T>::VW, U = E / V, RPB = BT / TPR;
+  __shared__ float2 lds[2][BT / 64];
+  const uint32_t lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   const float inv = 1.0f / (float)a.cols;
   float dw[E], db[E], w[E];
 #pragma unroll
@@ -234,27 +243,45 @@ __global__ void __launch_bounds__(block_threads(TPR)) norm_bwd_k(NormBwdArgs a) 
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) dw[e] = db[e] = 0.0f;
-  int flip = 0;
-  for (uint64_t row0 = (uint64_t)blockIdx.x * RPB; row0 < a.rows; row0 += a.groups, flip ^= 1) {
-    const uint64_t row = row0 + threadIdx.x / TPR;
-    const bool live = group < a.groups && row < a.rows;
-    u32x4 rdy[U], rh[U], rres[U];
+  struct Row {
+    u32x4 dy[U], h[U], res[U];
+    float mean, rstd;
+  };
+  auto fetch = [&](uint64_t row0, Row& x) {
+    const uint64_t row = row0 + sub;
+    const bool live = row < a.rows;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint32_t c = (u * TPR + lane) * V;
       const int n = live ? unit_left(a.cols, c) : 0;
-      rdy[u] = load_raw<T>(at<T>(a.dout, row * a.ld_in + c), n);
-      rh[u] = load_raw<T>(at<T>(a.sum, row * a.ld_in + c), n);
-      if (a.dresidual && a.dsum) rres[u] = load_raw<T>(at<T>(a.dresidual, row * a.ld_in + c), n);
+      x.dy[u] = load_in<T, NT>(at<T>(a.dout, row * a.ld_in + c), n);
+      x.h[u] = load_in<T, NT>(at<T>(a.sum, row * a.ld_in + c), n);
+      if (a.dresidual && a.dsum) x.res[u] = load_in<T, NT>(at<T>(a.dresidual, row * a.ld_in + c), n);
     }
-    const float mean = live ? a.mean[row] : 0.0f, rstd = live ? a.rstd[row] : 0.0f;
+    x.mean = live ? a.mean[row] : 0.0f;
+    x.rstd = live ? a.rstd[row] : 0.0f;
+  };
+  int flip = 0;
+  const uint64_t step = (uint64_t)gridDim.x * RPB;
+  Row now, next;
+  if (AHEAD) fetch((uint64_t)blockIdx.x * RPB, next);
+  for (uint64_t row0 = (uint64_t)blockIdx.x * RPB; row0 < a.rows; row0 += step, flip ^= 1) {
+    const uint64_t row = row0 + sub;
+    const bool live = row < a.rows;
+    if (AHEAD) {
+      now = next;
+      if (row0 + step < a.rows) fetch(row0 + step, next);
+    } else {
+      fetch(row0, now);
+    }
+    const float mean = now.mean, rstd = now.rstd;
     float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int n = live ? unit_left(a.cols, (u * TPR + lane) * V) : 0;
       float dy[V], h[V];
-      decode16<T>(rdy[u], dy);
-      decode16<T>(rh[u], h);
+      decode16<T>(now.dy[u], dy);
+      decode16<T>(now.h[u], h);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         if (j < n) {
@@ -274,23 +301,40 @@ __global__ void __launch_bounds__(block_threads(TPR)) norm_bwd_k(NormBwdArgs a) 
       const uint32_t c = (u * TPR + lane) * V;
       const int n = live ? unit_left(a.cols, c) : 0;
       float dy[V], h[V], d[V];
-      decode16<T>(rdy[u], dy);
-      decode16<T>(rh[u], h);
+      decode16<T>(now.dy[u], dy);
+      decode16<T>(now.h[u], h);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const float xhat = (h[j] - mean) * rstd;
         d[j] = (dy[j] * w[u * V + j] - c1 - xhat * c2) * rstd;
       }
       if (a.dresidual) {
-        decode16<T>(rres[u], h);
+        decode16<T>(now.res[u], h);
 #pragma unroll
         for (int j = 0; j < V; ++j) d[j] += h[j];
       }
-      store_raw<T>(at<T>(a.dsum, row * a.ld_out + c), n, encode16<T>(d));
+      store_out<T, NT>(at<T>(a.dsum, row * a.ld_out + c), n, encode16<T>(d));
     }
   }
-  if ((a.dweight || a.dbias) && group < a.groups) {
-    float* p = a.partial + (uint64_t)group * 2 * a.cols;
+  if (!a.dweight && !a.dbias) return;
+  if constexpr (RPB > 1) {
+    __shared__ float sums[RPB / 2][2 * E][TPR];
+#pragma unroll
+    for (uint32_t half = RPB / 2; half > 0; half /= 2) {
+      if (sub >= half && sub < 2 * half) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) sums[sub - half][e][lane] = dw[e], sums[sub - half][E + e][lane] = db[e];
+      }
+      __syncthreads();
+      if (sub < half) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) dw[e] += sums[sub][e][lane], db[e] += sums[sub][E + e][lane];
+      }
+      __syncthreads();
+    }
+  }
+  if (sub == 0) {
+    float* p = a.partial + (uint64_t)blockIdx.x * 2 * a.cols;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint32_t c = (u * TPR + lane) * V;
@@ -392,11 +436,22 @@ RowShape row_shape(uint32_t cols) {
 
 constexpr uint32_t kMaxGrid = 1u << 20;  // rows past it are walked in strides
 
+// Calls that move more than the 256 MiB of the Infinity Cache store past the caches,
+// and from 2 ranks on load past them: 16384 x 4096 bf16, 1 rank with residual, 103 us
+// plain, 89 with such stores, 100 with both; 4096 x 8192, 4 ranks with residual, 97 /
+// 90 / 87; 8192 x 4096, 8 ranks, 125 / 121 / 111.  Smaller calls may find their inputs
+// in that cache (the gradient of 16384 x 1024: 38 us plain, 44 past it).
+constexpr uint64_t kCacheBytes = 256ull << 20;
+
 template <int T, int TPR, int E> hipError_t fwd(const NormFwdArgs& a, hipStream_t s) {
   constexpr uint64_t rpb = block_threads(TPR) / TPR;
   const uint64_t blocks = (a.rows + rpb - 1) / rpb;
-  hipLaunchKernelGGL((norm_fwd_k<T, TPR, E>), dim3((uint32_t)(blocks < kMaxGrid ? blocks : kMaxGrid)),
-                     dim3(block_threads(TPR)), 0, s, a);
+  const dim3 grid((uint32_t)(blocks < kMaxGrid ? blocks : kMaxGrid)), block(block_threads(TPR));
+  const uint64_t tensors = a.nranks + (a.residual ? 1 : 0) + (a.sum ? 1 : 0) + 1;
+  const bool stream = a.rows * a.cols * Ty<T>::size * tensors > kCacheBytes;
+  if (stream && a.nranks >= 2) hipLaunchKernelGGL((norm_fwd_k<T, TPR, E, true, true>), grid, block, 0, s, a);
+  else if (stream) hipLaunchKernelGGL((norm_fwd_k<T, TPR, E, false, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((norm_fwd_k<T, TPR, E, false, false>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
@@ -412,9 +467,27 @@ template <int T> hipError_t fwd_typed(const NormFwdArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Workgroup of norm_bwd_k: 1024 lanes, one a CU, which leaves 128 registers a lane and
+// few parts to join (16384 x 4096 bf16 with residual: 99 us, 113 with 512 lanes).  Rows
+// of 512 lanes would go two a workgroup, in step at each barrier: those take 512 lanes
+// and load the next row ahead (8192 x 8192: 105 us with 1024 lanes, 100 with 512, 87
+// loading ahead; 93 with two such a CU).  f32: 512 lanes, two a CU.
+constexpr int bwd_threads(int t, int tpr) { return t == kF32 || tpr == 512 ? 512 : 1024; }
+constexpr bool bwd_ahead(int t, int tpr) { return t != kF32 && tpr == 512; }
+uint32_t bwd_blocks(uint64_t rows, uint32_t cols, int t) {
+  const RowShape r = row_shape(cols);
+  if (r.tpr == 0 || (t == kF32 && r.tpr > 512)) return rows < 256 ? (uint32_t)rows : 256;  // the kernels of long rows
+  const uint32_t bt = bwd_threads(t, r.tpr), rpb = bt / r.tpr, most = t == kF32 ? 512 : 256;
+  const uint64_t blocks = (rows + rpb - 1) / rpb;
+  return blocks < most ? (uint32_t)blocks : most;
+}
+
 template <int T, int TPR, int E> void bwd(const NormBwdArgs& a, hipStream_t s) {
-  constexpr uint32_t rpb = block_threads(TPR) / TPR;
-  hipLaunchKernelGGL((norm_bwd_k<T, TPR, E>), dim3((a.groups + rpb - 1) / rpb), dim3(block_threads(TPR)), 0, s, a);
+  constexpr int BT = bwd_threads(T, TPR);
+  const uint64_t tensors = 2 + (a.dsum ? 1 : 0) + (a.dsum && a.dresidual ? 1 : 0);
+  if (a.rows * a.cols * Ty<T>::size * tensors > kCacheBytes)
+    hipLaunchKernelGGL((norm_bwd_k<T, TPR, E, BT, bwd_ahead(T, TPR), true>), dim3(a.groups), dim3(BT), 0, s, a);
+  else hipLaunchKernelGGL((norm_bwd_k<T, TPR, E, BT, bwd_ahead(T, TPR), false>), dim3(a.groups), dim3(BT), 0, s, a);
 }
 
 template <int T> void bwd_1024(const NormBwdArgs& a, hipStream_t s) {
@@ -451,13 +524,10 @@ template <int T> hipError_t bwd_typed(const NormBwdArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// About two workgroups a CU, a multiple of the rows that share a workgroup.
+// Parts that the weight gradients' sums take, whatever the type.
 uint32_t norm_bwd_groups(uint64_t rows, uint32_t cols) {
-  const RowShape r = row_shape(cols);
-  const uint32_t most = r.tpr == 0 ? 256 : r.tpr <= 128 ? 1024 : r.tpr <= 512 ? 512 : 256;
-  const uint32_t rpb = r.tpr ? block_threads(r.tpr) / r.tpr : 1;
-  if (rows >= most) return most;
-  return (uint32_t)((rows + rpb - 1) / rpb * rpb);
+  const uint32_t a = bwd_blocks(rows, cols, kF32), b = bwd_blocks(rows, cols, kBF16);
+  return a > b ? a : b;
 }
 
 hipError_t launch_norm_fwd(const NormFwdArgs& a, int t, hipStream_t stream) {
@@ -467,7 +537,7 @@ hipError_t launch_norm_fwd(const NormFwdArgs& a, int t, hipStream_t stream) {
 }
 
 hipError_t launch_norm_bwd(NormBwdArgs a, int t, hipStream_t stream) {
-  a.groups = norm_bwd_groups(a.rows, a.cols);
+  a.groups = bwd_blocks(a.rows, a.cols, t);
   if (t == kF32) return bwd_typed<kF32>(a, stream);
   if (t == kF16) return bwd_typed<kF16>(a, stream);
   return bwd_typed<kBF16>(a, stream);
