@@ -291,6 +291,99 @@ template <int T, int N> __device__ __forceinline__ void store_dz(uint8_t* to, ui
   }
 }
 
+// What becomes of a tile's logits.  FULL: all its rows and tokens exist.  The rare
+// lanes whose target lies in the wave's rows are looked for once for 32 tokens, not at
+// each logit: what is left is an fma, an exponential (a quarter of the rate) and an
+// add or two.
+template <int T, int S, bool BWD, int SEG, bool FULL, class Prod>
+__device__ __forceinline__ void logits_out(const XentArgs& a, Prod& p, lds8* lds, float unscale, int wm, int wn, int lane,
+                                           uint32_t mt, uint32_t t0, uint32_t tokens, uint32_t first, uint32_t left) {
+  constexpr uint32_t per = kTileV / S;
+  const uint32_t m0 = wm * Prod::FM * 32;
+#pragma unroll
+  for (int j = 0; j < Prod::FN; ++j) {
+    const uint32_t t = t0 + (wn * Prod::FN + j) * 32 + (lane & 31);
+    const bool live = FULL || t < tokens;
+    // the target's row of the wave's, if it is there
+    uint32_t hit = ~0u;
+    XentToken tk;
+    if constexpr (BWD) {
+      tk = a.token[t];
+      if (live && (uint32_t)tk.target - first < left) hit = (uint32_t)tk.target - first - m0;
+    } else {
+      const int64_t target = live ? a.targets[t] : -1;
+      if (target >= first && target < (int64_t)first + left) hit = (uint32_t)(target - first) - m0;
+    }
+    if constexpr (SEG > 1) {
+#pragma unroll
+      for (int i = 0; i < Prod::FM; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) p.acc[i][j][e] *= unscale;
+    }
+    const bool hits = __any(hit < Prod::FM * 32u);
+    if constexpr (!BWD) {
+      if (hits) {
+        float z = 0.0f;
+        bool mine = false;
+#pragma unroll
+        for (int i = 0; i < Prod::FM; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const bool is = (uint32_t)(32 * i + acc_row(lane, e)) == hit;
+            z = is ? p.acc[i][j][e] : z;
+            mine |= is;
+          }
+        if (mine) a.zt[t] = z;
+      }
+      float mx = -__builtin_inff();
+#pragma unroll
+      for (int i = 0; i < Prod::FM; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (!FULL && m0 + 32 * i + acc_row(lane, e) >= left) p.acc[i][j][e] = -__builtin_inff();
+          mx = __builtin_fmaxf(mx, p.acc[i][j][e]);
+        }
+      mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32));
+      const float top = mx * kLog2e;
+      // a tile without a finite logit adds nothing (or, with +inf, NaN)
+      const float base = mx == -__builtin_inff() ? 0.0f : top;
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < Prod::FM; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(p.acc[i][j][e], kLog2e, -base));
+      s += __shfl_xor(s, 32);
+      if (lane < 32 && live) a.part[(((uint64_t)a.tile0 * per + mt) * Prod::WM + wm) * a.tokens + t] = make_float2(top, s);
+    } else {
+#pragma unroll
+      for (int i = 0; i < Prod::FM; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float d = dz_of<(SEG > 1)>(p.acc[i][j][e], tk, false);
+          p.acc[i][j][e] = FULL || (live && m0 + 32 * i + acc_row(lane, e) < left) ? d : 0.0f;
+        }
+      if (hits) {
+        float d = 0.0f;
+        bool mine = false;
+#pragma unroll
+        for (int i = 0; i < Prod::FM; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const bool is = (uint32_t)(32 * i + acc_row(lane, e)) == hit;
+            p.acc[i][j][e] -= is ? tk.dl : 0.0f;
+            d = is ? p.acc[i][j][e] : d;
+            mine |= is;
+          }
+        if (SEG == 1 && mine) a.residue[t] = residue_of<T>(d);
+      }
+      if (j == 0) __syncthreads();
+      p.template rows_out<8>(lds, j, [](auto) {}, [&](int n, int m, const float (&d)[8]) {
+        store_dz<SEG == 1 ? T : (int)kF32, 8>(a.dz + (uint64_t)(t0 + n) * a.lddz + ((uint64_t)mt * S + m) * 2, a.dz_plane, d);
+      });
+    }
+  }
+}
+
 // Logits of one tile of S vocabulary rows by S tokens.  Forward: reduced to a
 // (max, sum) pair in base 2 for each wave's rows, and the target's logit.
 // Backward: dz, vocabulary contiguous.
@@ -341,56 +434,8 @@ __global__ void __launch_bounds__(tile_threads(S)) logits_k(XentArgs a) {
 
   const int wm = wave / Prod::WN, wn = wave % Prod::WN;
   const uint32_t first = a.v.first_row[sh] + row0;  // of the whole vocabulary
-#pragma unroll
-  for (int j = 0; j < Prod::FN; ++j) {
-    const uint32_t t = t0 + (wn * Prod::FN + j) * 32 + (lane & 31);
-    if constexpr (!BWD) {
-      const int64_t target = t < tokens ? a.targets[t] : -1;
-      // the target's row in this tile, if it is there
-      const uint32_t hit = target >= first && target < (int64_t)first + left ? (uint32_t)(target - first) : ~0u;
-      float mx = -__builtin_inff();
-#pragma unroll
-      for (int i = 0; i < Prod::FM; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const uint32_t m = (wm * Prod::FM + i) * 32 + acc_row(lane, e);
-          const float z = SEG > 1 ? p.acc[i][j][e] * unscale : p.acc[i][j][e];
-          if (m == hit) a.zt[t] = z;
-          const float x = m < left ? z : -__builtin_inff();
-          p.acc[i][j][e] = x;
-          mx = __builtin_fmaxf(mx, x);
-        }
-      mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32));
-      const float top = mx * kLog2e;
-      // a tile without a finite logit adds nothing (or, with +inf, NaN)
-      const float base = mx == -__builtin_inff() ? 0.0f : top;
-      float s = 0.0f;
-#pragma unroll
-      for (int i = 0; i < Prod::FM; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(p.acc[i][j][e], kLog2e, -base));
-      s += __shfl_xor(s, 32);
-      if (lane < 32 && t < tokens) a.part[(((uint64_t)a.tile0 * per + mt) * Prod::WM + wm) * a.tokens + t] = make_float2(top, s);
-    } else {
-      const XentToken tk = a.token[t];
-      const bool live = t < tokens;
-      const uint32_t hit = live && (uint32_t)tk.target - first < left ? (uint32_t)tk.target - first : ~0u;
-#pragma unroll
-      for (int i = 0; i < Prod::FM; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const uint32_t m = (wm * Prod::FM + i) * 32 + acc_row(lane, e);
-          const float z = SEG > 1 ? p.acc[i][j][e] * unscale : p.acc[i][j][e];
-          const float d = live && m < left ? dz_of<(SEG > 1)>(z, tk, m == hit) : 0.0f;
-          if (SEG == 1 && m == hit) a.residue[t] = residue_of<T>(d);
-          p.acc[i][j][e] = d;
-        }
-      if (j == 0) __syncthreads();
-      p.template rows_out<8>((lds8*)lds, j, [](auto) {}, [&](int n, int m, const float (&d)[8]) {
-        store_dz<SEG == 1 ? T : (int)kF32, 8>(a.dz + (uint64_t)(t0 + n) * a.lddz + ((uint64_t)mt * S + m) * 2, a.dz_plane, d);
-      });
-    }
-  }
+  if (left == (uint32_t)S && t0 + S <= tokens) logits_out<T, S, BWD, SEG, true>(a, p, (lds8*)lds, unscale, wm, wn, lane, mt, t0, tokens, first, left);
+  else logits_out<T, S, BWD, SEG, false>(a, p, (lds8*)lds, unscale, wm, wn, lane, mt, t0, tokens, first, left);
 }
 
 // ---- logits of few tokens ----------------------------------------------------------
