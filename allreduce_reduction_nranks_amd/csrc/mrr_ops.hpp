@@ -83,12 +83,14 @@ struct XentArgs {
   uint64_t ld_h, ld_w;
   uint32_t tokens, tpad, cols, kpad;
   uint32_t tile0, ntiles;       // the piece
+  uint32_t sub0, sub;           // tiles of the piece that a launch takes: from sub0 on, sub of them
   // forward
   float2* part;                 // max and sum, base 2: logits_k [parts][tokens], few_k [tokens][parts]
   float* zt;                    // [tokens]: the target's logit
   const int64_t* targets;
   int64_t ignore;
-  uint32_t parts;
+  uint64_t part0;               // logits_k: pairs of the launches before
+  uint32_t parts;               // few_k: pairs of a token
   // backward
   uint8_t* dz;                  // [tpad][piece]
   const XentToken* token;

@@ -77,6 +77,8 @@ constexpr int kMostParts = 1024;
 struct MostArgs {
   XentVocab v;
   const void* src;
+  const int32_t* idx;           // rows of src that count, scalars->count of them; null: all
+  const XentScalars* scalars;
   uint64_t ld_w, ld_src, src_rows;
   uint32_t* parts;  // [2][kMostParts]: weights, hidden states
   uint32_t cols, units_log2;
@@ -99,9 +101,9 @@ __global__ void __launch_bounds__(256) most_k(MostArgs a) {
   const uint32_t lanes = 1u << a.units_log2, per = 256u >> a.units_log2;
   const uint32_t u0 = threadIdx.x & (lanes - 1);
   uint32_t most = 0;
-  auto rows_of = [&](const void* base, uint64_t rows, uint64_t ld) {
+  auto rows_of = [&](const void* base, const int32_t* idx, uint64_t rows, uint64_t ld) {
     for (uint64_t row = (uint64_t)blockIdx.x * per + (threadIdx.x >> a.units_log2); row < rows; row += (uint64_t)gridDim.x * per) {
-      const uint8_t* p = at<kF32>(base, row * ld);
+      const uint8_t* p = at<kF32>(base, (idx ? (uint64_t)idx[row] : row) * ld);
 #pragma unroll 4
       for (uint32_t c = 4 * u0; c < a.cols; c += 4 * lanes) {
         const u32x4 x = load_raw<kF32>(p + 4 * (uint64_t)c, (int)(a.cols - c));
@@ -113,9 +115,9 @@ __global__ void __launch_bounds__(256) most_k(MostArgs a) {
       }
     }
   };
-  if (blockIdx.y) rows_of(a.src, a.src_rows, a.ld_src);
+  if (blockIdx.y) rows_of(a.src, a.idx, a.idx ? a.scalars->count : a.src_rows, a.ld_src);
   else
-    for (int r = 0; r < a.v.n; ++r) rows_of(a.v.w[r], a.v.rows[r], a.ld_w);
+    for (int r = 0; r < a.v.n; ++r) rows_of(a.v.w[r], nullptr, a.v.rows[r], a.ld_w);
   most = block_max(most, lds);
   if (threadIdx.x == 0) a.parts[blockIdx.y * kMostParts + blockIdx.x] = most;
 }
@@ -297,8 +299,8 @@ template <int T, int N> __device__ __forceinline__ void store_dz(uint8_t* to, ui
 // add or two.
 template <int T, int S, bool BWD, int SEG, bool FULL, class Prod>
 __device__ __forceinline__ void logits_out(const XentArgs& a, Prod& p, lds8* lds, float unscale, int wm, int wn, int lane,
-                                           uint32_t mt, uint32_t t0, uint32_t tokens, uint32_t first, uint32_t left) {
-  constexpr uint32_t per = kTileV / S;
+                                           uint32_t mt, uint32_t part, uint32_t t0, uint32_t tokens, uint32_t first,
+                                           uint32_t left) {
   const uint32_t m0 = wm * Prod::FM * 32;
 #pragma unroll
   for (int j = 0; j < Prod::FN; ++j) {
@@ -353,7 +355,7 @@ __device__ __forceinline__ void logits_out(const XentArgs& a, Prod& p, lds8* lds
 #pragma unroll
         for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(p.acc[i][j][e], kLog2e, -base));
       s += __shfl_xor(s, 32);
-      if (lane < 32 && live) a.part[(((uint64_t)a.tile0 * per + mt) * Prod::WM + wm) * a.tokens + t] = make_float2(top, s);
+      if (lane < 32 && live) a.part[(a.part0 + (uint64_t)part * Prod::WM + wm) * a.tokens + t] = make_float2(top, s);
     } else {
 #pragma unroll
       for (int i = 0; i < Prod::FM; ++i)
@@ -393,7 +395,9 @@ __global__ void __launch_bounds__(tile_threads(S)) logits_k(XentArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
   uint32_t mt, nt;
   constexpr uint32_t per = kTileV / S;  // of a vocabulary tile
-  if (!tile_of(blockIdx.x, a.ntiles * per, a.tpad / S, mt, nt)) return;
+  if (!tile_of(blockIdx.x, a.sub * per, a.tpad / S, mt, nt)) return;
+  const uint32_t part = mt;
+  mt += a.sub0 * per;
   const uint32_t tokens = BWD ? a.scalars->count : a.tokens;
   const uint32_t t0 = nt * S, tile = a.tile0 + mt / per;
   if (t0 >= tokens) return;
@@ -434,8 +438,8 @@ __global__ void __launch_bounds__(tile_threads(S)) logits_k(XentArgs a) {
 
   const int wm = wave / Prod::WN, wn = wave % Prod::WN;
   const uint32_t first = a.v.first_row[sh] + row0;  // of the whole vocabulary
-  if (left == (uint32_t)S && t0 + S <= tokens) logits_out<T, S, BWD, SEG, true>(a, p, (lds8*)lds, unscale, wm, wn, lane, mt, t0, tokens, first, left);
-  else logits_out<T, S, BWD, SEG, false>(a, p, (lds8*)lds, unscale, wm, wn, lane, mt, t0, tokens, first, left);
+  if (left == (uint32_t)S && t0 + S <= tokens) logits_out<T, S, BWD, SEG, true>(a, p, (lds8*)lds, unscale, wm, wn, lane, mt, part, t0, tokens, first, left);
+  else logits_out<T, S, BWD, SEG, false>(a, p, (lds8*)lds, unscale, wm, wn, lane, mt, part, t0, tokens, first, left);
 }
 
 // ---- logits of few tokens ----------------------------------------------------------
@@ -707,7 +711,8 @@ template <int T, int OUT, int S, int NS, int SEG> __global__ void __launch_bound
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
   uint32_t mt, nt;
   constexpr uint32_t per = kTileV / S;  // of a vocabulary tile
-  if (!tile_of(blockIdx.x, (a.kpad + S - 1) / S, a.ntiles * per, mt, nt)) return;
+  if (!tile_of(blockIdx.x, (a.kpad + S - 1) / S, a.sub * per, mt, nt)) return;
+  nt += a.sub0 * per;
   const uint32_t c0 = mt * S, tile = a.tile0 + nt / per;
   int sh = 0;
   while (tile >= a.v.first_tile[sh + 1]) ++sh;
@@ -882,13 +887,25 @@ uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 
 uint64_t tiles_of(uint64_t m, uint64_t n, uint64_t s) { return (m + s - 1) / s * ((n + s - 1) / s); }
 
-// Size of tile for an m x n product.  In rounds over the 256 CUs, from the times of a
-// 64-k stage measured on large products: 0.95 us for a round of 256 x 256 tiles, 0.55 us
-// for one of 128 x 128 (two a CU), 0.35 us when a CU has one of those.
-int pick_tile(uint64_t m, uint64_t n) {
-  const uint64_t big = tiles_of(m, n, 256), small = tiles_of(m, n, 128);
-  const uint64_t c256 = (big + 255) / 256 * 95, c128 = small <= 256 ? 35 : (small + 511) / 512 * 55;
-  return n <= 128 || c128 < c256 ? 128 : 256;
+// A product of `rows` 256-row tiles by q256 tiles of 256 (q128 of 128): how many of the
+// rows go in 256 x 256 tiles, the rest in 128 x 128.  Large tiles are the faster ones,
+// but the last of their rounds over the 256 CUs may be nearly empty: then the rows past
+// the full rounds go in small ones.  Times in 10 ns, measured: a round of large tiles
+// 1.43 us for each 64 k and 9 us; of small ones, two a CU, 0.85 and 6, one a CU 0.75 and
+// 6.  (700 tokens x 50257 x 1600, 25 stages: 138 us in large tiles, 136 in small ones,
+// 119 in both.)
+uint32_t large_rows(uint32_t rows, uint64_t q256, uint64_t q128, uint64_t stages) {
+  const uint64_t large = 143 * stages + 900;
+  auto small = [&](uint64_t n) {
+    return n == 0 ? 0 : n <= 256 ? 75 * stages + 600 : (n + 511) / 512 * (85 * stages + 600);
+  };
+  if (q128 == 1) return 0;
+  uint64_t best = small(2 * rows * q128);
+  uint32_t r = 0;
+  if (const uint64_t c = (rows * q256 + 255) / 256 * large; c < best) best = c, r = rows;
+  const uint64_t full = rows * q256 / 256, most = full * 256 / q256;
+  if (most && most < rows && full * large + small(2 * (rows - most) * q128) + 200 < best) r = (uint32_t)most;
+  return r;
 }
 
 }  // namespace
@@ -984,13 +1001,21 @@ template <int T, bool BWD> void few(const XentArgs& a, uint32_t few, hipStream_t
 
 // 128 x 128 tiles go two a CU with 2 stages, or with 4 when there is one a CU anyway.
 template <int M, int S, int NS, bool BWD, int SEG> void logits_of(const XentArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((logits_k<M, S, NS, BWD, SEG>), dim3(tile_grid(tiles_of(a.ntiles * kTileV, a.tpad, S))),
+  hipLaunchKernelGGL((logits_k<M, S, NS, BWD, SEG>), dim3(tile_grid(tiles_of(a.sub * kTileV, a.tpad, S))),
                      dim3(tile_threads(S)), 0, s, a);
 }
-template <int M, bool BWD, int SEG> void logits(const XentArgs& a, int tile, hipStream_t s) {
-  if (tile == 256) logits_of<M, 256, 2, BWD, SEG>(a, s);
-  else if (tiles_of(a.ntiles * kTileV, a.tpad, 128) > 256) logits_of<M, 128, 2, BWD, SEG>(a, s);
-  else logits_of<M, 128, 4, BWD, SEG>(a, s);
+// Of a forward, part0 moves past the pairs it writes.
+template <int M, bool BWD, int SEG> void logits(XentArgs& a, hipStream_t s) {
+  const uint32_t large = large_rows(a.ntiles, (a.tpad + 255) / 256, a.tpad / 128, a.kpad / kTileK * SEG);
+  a.sub0 = 0;
+  a.sub = large;
+  if (a.sub) logits_of<M, 256, 2, BWD, SEG>(a, s);
+  a.part0 += 2 * a.sub;
+  a.sub0 = large;
+  a.sub = a.ntiles - large;
+  if (a.sub && tiles_of(a.sub * kTileV, a.tpad, 128) > 256) logits_of<M, 128, 2, BWD, SEG>(a, s);
+  else if (a.sub) logits_of<M, 128, 4, BWD, SEG>(a, s);
+  a.part0 += 4 * a.sub;
 }
 template <int M, int S, int NS, int SEG> void dhidden_of(const XentArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((dhidden_k<M, S, NS, SEG>), dim3(tile_grid(tiles_of(a.kpad, a.tpad, S)), a.splits),
@@ -1002,13 +1027,18 @@ template <int M, int SEG> void dhidden(const XentArgs& a, int tile, hipStream_t 
   else dhidden_of<M, 128, 4, SEG>(a, s);
 }
 template <int M, int T, int S, int NS, int SEG> void dweight_of(const XentArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((dweight_k<M, T, S, NS, SEG>), dim3(tile_grid(tiles_of(a.kpad, a.ntiles * kTileV, S))),
-                     dim3(tile_threads(S)), 0, s, a);
+  hipLaunchKernelGGL((dweight_k<M, T, S, NS, SEG>), dim3(tile_grid(tiles_of(a.kpad, a.sub * kTileV, S))), dim3(tile_threads(S)),
+                     0, s, a);
 }
-template <int M, int T, int SEG> void dweight(const XentArgs& a, int tile, hipStream_t s) {
-  if (tile == 256) dweight_of<M, T, 256, 2, SEG>(a, s);
-  else if (tiles_of(a.kpad, a.ntiles * kTileV, 128) > 256) dweight_of<M, T, 128, 2, SEG>(a, s);
-  else dweight_of<M, T, 128, 4, SEG>(a, s);
+template <int M, int T, int SEG> void dweight(XentArgs& a, hipStream_t s) {
+  const uint32_t large = large_rows(a.ntiles, (a.kpad + 255) / 256, (a.kpad + 127) / 128, a.tpad / kTileK * SEG);
+  a.sub0 = 0;
+  a.sub = large;
+  if (a.sub) dweight_of<M, T, 256, 2, SEG>(a, s);
+  a.sub0 = large;
+  a.sub = a.ntiles - large;
+  if (a.sub && tiles_of(a.kpad, a.sub * kTileV, 128) > 256) dweight_of<M, T, 128, 2, SEG>(a, s);
+  else if (a.sub) dweight_of<M, T, 128, 4, SEG>(a, s);
 }
 
 // T: type of the caller's tensors.  M: type that multiplies.
@@ -1080,7 +1110,7 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
   }
   if constexpr (T == kF32) {
     if (BWD || !groups) {
-      MostArgs m{a.v, c.hidden, c.ld_weight, c.ld_hidden, c.tokens, (uint32_t*)(ws + p.most), c.cols, 0};
+      MostArgs m{a.v, c.hidden, l.idx, scalars, c.ld_weight, c.ld_hidden, c.tokens, (uint32_t*)(ws + p.most), c.cols, 0};
       while (m.units_log2 < 8 && (4u << m.units_log2) < c.cols) ++m.units_log2;
       // from 8 KiB a workgroup
       const uint64_t n = (vocab * c.cols >> 11) + 1;
@@ -1101,12 +1131,11 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
   l.dst = ws + p.laid;
   l.plane = p.laid_plane;
   const uint32_t nt = p.tpad / 128 * 2;  // of the smaller tiles, in halves of a vocabulary tile
-  const int tile = pick_tile((uint64_t)(BWD || !direct ? p.piece : p.tiles) * kTileV, p.tpad);
   // a forward that reads the weights in place has nothing to divide but the grid
   uint32_t piece = p.piece;
   if (!BWD && groups) piece = p.tiles < kMaxTiles / 8 ? p.tiles : (uint32_t)(kMaxTiles / 8);
   else if (!BWD && direct) piece = nt <= kMaxTiles / p.tiles ? p.tiles : kMaxTiles / nt ? (uint32_t)(kMaxTiles / nt) : 1;
-  if (!BWD) a.parts = p.tiles * (groups ? kTileV / (16 * groups) : tile == 256 ? 2 : 4);
+  if (groups) a.parts = p.tiles * (kTileV / (16 * groups));
   for (a.tile0 = 0; a.tile0 < p.tiles; a.tile0 += piece) {
     a.ntiles = p.tiles - a.tile0 < piece ? p.tiles - a.tile0 : piece;
     if (!direct && (BWD || !groups)) {
@@ -1115,13 +1144,12 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
       layout<T>(l, s);
       a.laid = ws + p.laid;
     }
-    const uint64_t rows = (uint64_t)a.ntiles * kTileV;
     if (groups) few<T, BWD>(a, groups, s);
-    else logits<M, BWD, SEG>(a, tile, s);
+    else logits<M, BWD, SEG>(a, s);
     if constexpr (BWD) {
       if (c.dhidden) dhidden<M, SEG>(a, p.dh_tile, s);
       a.add = 1;
-      if (c.dweights) dweight<M, T, SEG>(a, pick_tile(p.kpad, rows), s);
+      if (c.dweights) dweight<M, T, SEG>(a, s);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -1132,7 +1160,7 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
       hipLaunchKernelGGL(dhidden_join_k<T>, dim3(c.tokens < 65536 ? c.tokens : 65536, y < 1024 ? y : 1024), dim3(256), 0, s, a);
     }
   } else {
-    const uint64_t parts = a.parts;
+    const uint64_t parts = groups ? a.parts : a.part0;
     const XentJoinArgs j{a.part, a.zt, c.targets, c.ignore, (int64_t)vocab, c.loss, c.lse_out,
                          groups ? 1u : c.tokens, groups ? parts : 1u, (uint32_t)parts, c.tokens};
     // as many chains as leave every CU a workgroup

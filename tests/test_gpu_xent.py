@@ -246,6 +246,37 @@ def test_tokens_without_a_loss(tokens):
     assert not bool(c.got_dh[0].any()) and not bool(c.got_dh[tokens - 1].any())
 
 
+@pytest.mark.parametrize("tokens", [5, 140])
+def test_an_ignored_token_does_not_set_the_scale_of_f32_parts(tokens):
+    announce("xent f32 scale", tokens)
+    c = Case(tokens, [300, 41], 72, "f32", 30, ignored=0.0)
+    c.targets[1] = IGNORE
+    c.hidden[1] = 0.0
+    c.exact()
+    lse = c.lse.float()
+    c.exact(lse, c.dloss)
+    c.hidden[1] = 3e30
+    c.backward(lse, c.dloss)
+    torch.cuda.synchronize()
+    c.check_backward()
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_rows_in_both_sizes_of_tile(t):
+    """Full rounds of large tiles and the rest in small ones, in each product."""
+    tokens, rows, cols = (700, [30000, 10257], 128) if t == "bf16" else (700, [23000], 128)
+    announce("xent both tiles", t)
+    c = Case(tokens, rows, cols, t, 31)
+    c.forward()
+    torch.cuda.synchronize()
+    c.check_forward()
+    lse = c.lse.float()
+    c.backward(lse, c.dloss)
+    torch.cuda.synchronize()
+    c.exact(lse, c.dloss)
+    c.check_backward()
+
+
 @pytest.mark.parametrize("tokens", [3, 50, 200])
 @pytest.mark.parametrize("t", ["bf16", "f32"])
 def test_logits_that_are_large_or_not_finite(tokens, t):
