@@ -245,13 +245,18 @@ __global__ void __launch_bounds__(kTokensThreads) tokens_k(TokensArgs a) {
 }
 
 // ---- tiles -------------------------------------------------------------------------
-// Workgroup id to tile (m, n) of mt x nt.  Workgroups go to the 8 XCDs in turn; each
-// XCD gets one contiguous run of the tile order, which walks 8 m tiles by all n
-// tiles, so that the tiles an XCD works on together share operands in its L2.
-__device__ __forceinline__ bool tile_of(uint32_t id, uint32_t mt, uint32_t nt, uint32_t& m, uint32_t& n) {
-  const uint32_t total = mt * nt, per = total / 8, extra = total % 8, x = id & 7, j = id >> 3;
+// Workgroup id to tile (m, n) of mt x nt, and to one of `splits` parts of k.  Workgroups
+// go to the 8 XCDs in turn; each XCD gets one contiguous run of the order, which walks 8
+// m tiles by all n tiles of a split, so that the tiles an XCD works on together share
+// operands in its L2.  (Splits dealt out over the XCDs instead: 231 us against 134 for
+// the hidden states' gradient of 700 x 50257 x 1600 f16.)
+__device__ __forceinline__ bool tile_of(uint32_t id, uint32_t mt, uint32_t nt, uint32_t splits, uint32_t& m, uint32_t& n,
+                                        uint32_t& split) {
+  const uint32_t tiles = mt * nt, total = tiles * splits, per = total / 8, extra = total % 8, x = id & 7, j = id >> 3;
   if (j >= per + (x < extra ? 1u : 0u)) return false;
-  const uint32_t t = x * per + (x < extra ? x : extra) + j;
+  uint32_t t = x * per + (x < extra ? x : extra) + j;
+  split = t / tiles;
+  t -= split * tiles;
   constexpr uint32_t G = 8;
   const uint32_t g = t / (G * nt), rem = t - g * (G * nt), gm = mt - g * G < G ? mt - g * G : G;
   m = g * G + rem % gm;
@@ -393,9 +398,9 @@ template <int T, int S, int NS, bool BWD, int SEG>
 __global__ void __launch_bounds__(tile_threads(S)) logits_k(XentArgs a) {
   typedef Tile<T, false, false, S, NS> Prod;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
-  uint32_t mt, nt;
+  uint32_t mt, nt, split;
   constexpr uint32_t per = kTileV / S;  // of a vocabulary tile
-  if (!tile_of(blockIdx.x, a.sub * per, a.tpad / S, mt, nt)) return;
+  if (!tile_of(blockIdx.x, a.sub * per, a.tpad / S, 1, mt, nt, split)) return;
   const uint32_t part = mt;
   mt += a.sub0 * per;
   const uint32_t tokens = BWD ? a.scalars->count : a.tokens;
@@ -604,13 +609,12 @@ template <int T, int NT, int R, bool BWD> __global__ void __launch_bounds__(256)
 template <int T, int S, int NS, int SEG> __global__ void __launch_bounds__(tile_threads(S)) dhidden_k(XentArgs a) {
   typedef Tile<T, true, false, S, NS> Prod;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
-  uint32_t mt, nt;
-  if (!tile_of(blockIdx.x, (a.kpad + S - 1) / S, a.tpad / S, mt, nt)) return;
+  uint32_t mt, nt, split;
+  if (!tile_of(blockIdx.x, (a.kpad + S - 1) / S, a.tpad / S, a.splits, mt, nt, split)) return;
   const uint32_t t0 = nt * S, c0 = mt * S;
   if (t0 >= a.scalars->count) return;
   const int tid = threadIdx.x;
   const uint32_t blocks = a.ntiles * (kTileV / kTileK);  // of 64 rows
-  const uint32_t split = blockIdx.y;
   const uint32_t k0 = (uint32_t)((uint64_t)blocks * split / a.splits), k1 = (uint32_t)((uint64_t)blocks * (split + 1) / a.splits);
   uint32_t k = k0, seg = 0;
   int sh = 0;
@@ -709,9 +713,9 @@ __global__ void __launch_bounds__(256) hits_k(XentArgs a) {
 template <int T, int OUT, int S, int NS, int SEG> __global__ void __launch_bounds__(tile_threads(S)) dweight_k(XentArgs a) {
   typedef Tile<T, true, true, S, NS> Prod;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
-  uint32_t mt, nt;
+  uint32_t mt, nt, split;
   constexpr uint32_t per = kTileV / S;  // of a vocabulary tile
-  if (!tile_of(blockIdx.x, (a.kpad + S - 1) / S, a.sub * per, mt, nt)) return;
+  if (!tile_of(blockIdx.x, (a.kpad + S - 1) / S, a.sub * per, 1, mt, nt, split)) return;
   nt += a.sub0 * per;
   const uint32_t c0 = mt * S, tile = a.tile0 + nt / per;
   int sh = 0;
@@ -794,7 +798,10 @@ template <int T, int OUT, int S, int NS, int SEG> __global__ void __launch_bound
           if ((uint32_t)n >= left || c >= a.cols) return;
 #pragma unroll
           for (int i = 0; i < W; ++i) x[i] *= unscale;
-          store_raw<OUT>(at<OUT>(a.dw[sh], (uint64_t)(row0 + n) * a.ld_dw + c), (int)(a.cols - c), encode16<OUT>(x));
+          // past the caches: the weights' next reader finds them there (1 token x 32000 x 4096: 212 to 177 us)
+          void* to = at<OUT>(a.dw[sh], (uint64_t)(row0 + n) * a.ld_dw + c);
+          if (a.cols - c >= W) __builtin_nontemporal_store(encode16<OUT>(x), reinterpret_cast<u32x4_any*>(to));
+          else store_raw<OUT>(to, (int)(a.cols - c), encode16<OUT>(x));
         });
   }
 }
@@ -858,6 +865,7 @@ template <int T> __global__ void __launch_bounds__(256) dhidden_join_k(XentArgs 
       float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       if (from >= 0) {
         const float* p = a.sum + (uint64_t)from * a.kpad + c;
+#pragma unroll 8
         for (uint32_t s = 0; s < a.splits; ++s) {
           const f32x4 y = *reinterpret_cast<const f32x4*>(p + (uint64_t)s * a.tpad * a.kpad);
 #pragma unroll
@@ -982,11 +990,22 @@ template <int T> void layout(LayoutArgs l, hipStream_t s) {
 // 16-token groups of a few_k workgroup, 0: logits_k.  16 bits: up to 4 tokens (of 32000 x
 // 4096, 1 / 4 / 8 / 16 tokens: 49 / 50 / 55 / 63 us against 51 for all of them; the
 // hidden states then take as much of the L1s as the weights; unaligned, 50257 x 1023: 60
-// us for 1 and 98 for 16 against 68).  f32: up to 128 tokens, as the other way has to lay
-// out the weights first (of 32000 x 4096, 64 / 128: 220 / 440 us against 540).
-uint32_t few_groups(int t, uint32_t tokens) {
-  if (t == kF32) return tokens <= 16 ? 1 : tokens <= 32 ? 2 : tokens <= 128 ? 4 : 0;
-  return tokens <= 4 ? 1 : 0;
+// us for 1 and 98 for 16 against 68).  f32: where it takes less than the other way, for
+// which a forward lays out the weights first.  In us: 5 and, for each weight, what its 4
+// bytes take at 4.4 TB/s or the products of 64 tokens at 75 TFLOP/s (64 x 32000 x 4096:
+// 220; 128: 440, against 540); against a stage's time in large_rows() and 14 bytes of
+// each weight moved at 5 TB/s.
+uint32_t few_groups(int t, uint32_t tokens, uint32_t rows, uint32_t tpad, uint32_t kpad, bool backward) {
+  if (t != kF32) return tokens <= 4 ? 1 : 0;
+  const uint32_t groups = tokens <= 16 ? 1 : tokens <= 32 ? 2 : 4;
+  const double weights = (double)rows * kTileV * kpad * 1e-6;  // millions
+  const double flops = 2.0 * (double)up(tokens, 16 * groups) / 75.0;
+  const double few = 5 + weights * (flops > 4 / 4.4 ? flops : 4 / 4.4);
+  const uint64_t stages = kpad / kTileK * kSegs, big = rows * (uint64_t)((tpad + 255) / 256), small = 2 * rows * (uint64_t)(tpad / 128);
+  const uint64_t c256 = (big + 255) / 256 * (143 * stages + 900);
+  const uint64_t c128 = small <= 256 ? 75 * stages + 600 : (small + 511) / 512 * (85 * stages + 600);
+  const double other = 0.01 * (double)(c256 < c128 ? c256 : c128) + (backward ? 0 : 8 + weights * 14 / 5);
+  return few < other ? groups : 0;
 }
 
 template <int T, bool BWD> void few(const XentArgs& a, uint32_t few, hipStream_t s) {
@@ -1018,7 +1037,7 @@ template <int M, bool BWD, int SEG> void logits(XentArgs& a, hipStream_t s) {
   a.part0 += 4 * a.sub;
 }
 template <int M, int S, int NS, int SEG> void dhidden_of(const XentArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((dhidden_k<M, S, NS, SEG>), dim3(tile_grid(tiles_of(a.kpad, a.tpad, S)), a.splits),
+  hipLaunchKernelGGL((dhidden_k<M, S, NS, SEG>), dim3(tile_grid(tiles_of(a.kpad, a.tpad, S) * a.splits)),
                      dim3(tile_threads(S)), 0, s, a);
 }
 template <int M, int SEG> void dhidden(const XentArgs& a, int tile, hipStream_t s) {
@@ -1058,7 +1077,7 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
     if (c.rows[r] && (uintptr_t)c.weights[r] % 16) direct = false;
     if (c.dweights) a.dw[r] = c.dweights[r];
   }
-  const uint32_t groups = few_groups(T, c.tokens);
+  const uint32_t groups = few_groups(T, c.tokens, p.tiles, p.tpad, p.kpad, BWD);
   a.ldw = direct ? (uint32_t)c.ld_weight * 2 : p.kpad * 2;
   a.laid_plane = p.laid_plane;
   a.h = ws + p.h;
