@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import builtins
 import ctypes
+import operator
 import os
 import struct
 import threading
@@ -402,29 +403,52 @@ def _span(x) -> int:
     return (1 + builtins.sum((n - 1) * s for n, s in zip(x.shape, x.stride()))) * x.element_size()
 
 
+_bytes_of = operator.attrgetter("nbytes")
+_is_whole = operator.methodcaller("is_contiguous")
+_address = operator.methodcaller("data_ptr")
+
+
 def _rows_arg(x, nbytes: int, what: str) -> int:
     """Address of an argument whose rows may lie apart: a tensor must hold nbytes
-    bytes, a view of a wider one counting with its strides.  (Checks and addresses
-    in one step, and packed pointer arrays below: they halve an eager call's host
-    cost, which is what a small call takes.)"""
+    bytes, a view of a wider one counting with its strides, and the elements of a row
+    must lie side by side.  (Checks and address in one step, and below lists taken
+    whole: marshalling is half of an eager call's host cost, which is what a small
+    call takes.)"""
     if x is None:
         return 0
-    if isinstance(x, int):
+    try:
+        if x.nbytes >= nbytes and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
         return x
+    if x.dim() and x.size(-1) > 1 and x.stride(-1) != 1:
+        raise ValueError("%s has its rows' elements %d apart" % (what, x.stride(-1)))
+    if _span(x) < nbytes:
+        raise ValueError("%s spans %d bytes, the call needs %d" % (what, _span(x), nbytes))
+    return x.data_ptr()
+
+
+def _spaced_arg(x, nbytes: int, what: str) -> int:
+    """_rows_arg() for single values that a call takes at a stride of its own."""
+    if x is None or isinstance(x, int):
+        return x or 0
     if x.nbytes < nbytes and _span(x) < nbytes:
         raise ValueError("%s spans %d bytes, the call needs %d" % (what, _span(x), nbytes))
     return x.data_ptr()
 
 
 def _flat_arg(x, nbytes: int, what: str) -> int:
-    """_rows_arg() for an argument without a row stride."""
+    """_rows_arg() for an argument without a row stride: its elements lie side by side."""
     if x is None:
         return 0
-    if isinstance(x, int):
+    try:
+        if x.nbytes >= nbytes and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
         return x
     if x.nbytes < nbytes:
         raise ValueError("%s holds %d bytes, the call needs %d" % (what, x.nbytes, nbytes))
-    return x.data_ptr()
+    raise ValueError("%s is not contiguous" % what)
 
 
 _words: dict = {}
@@ -447,32 +471,36 @@ def _rows_args(xs, n: int, nbytes, what: str):
     if len(xs) < n:
         raise ValueError("%s has %d entries, nranks is %d" % (what, len(xs), n))
     one = type(nbytes) is int
+    if 0 < n == len(xs):
+        try:
+            fits = builtins.min(map(_bytes_of, xs)) >= nbytes if one else all(map(operator.ge, map(_bytes_of, xs), nbytes))
+            if fits and all(map(_is_whole, xs)):
+                return _pack(list(map(_address, xs)))
+        except AttributeError:
+            pass  # addresses among them, or no shard
     ptrs = []
     for r, x in enumerate(xs):
-        if x is None or type(x) is int:
-            ptrs.append(x or 0)
-            continue
         need = 0 if r >= n else nbytes if one else nbytes[r]
-        ptrs.append(x.data_ptr() if x.nbytes >= need else _rows_arg(x, need, "%s[%d]" % (what, r)))
+        ptrs.append(_rows_arg(x, need, "%s[%d]" % (what, r)))
     return _pack(ptrs)
 
 
-def _wtype(dtype, wdtype) -> int:
-    w = _dt(wdtype)
-    return _dt(dtype) if w == MRR_AUTO else w
+def _wtype(t: int, wdtype) -> int:
+    return _dt(wdtype) or t  # MRR_AUTO is 0
 
 
 def mrr_layernorm_fwd(inputs, nranks, residual, weight, bias, sum, out, mean, rstd, rows, cols,
                       ld_in, ld_out, eps, dtype, wdtype="auto", stream=None) -> int:
-    t, tw = _dt(dtype), _wtype(dtype, wdtype)
-    nin = nout = _matrix_bytes(rows, cols, ld_in, _ESIZE.get(t, 0))
+    t = _dt(dtype)
+    tw = _wtype(t, wdtype)
+    e, wb, rb = _ESIZE.get(t, 0), cols * _ESIZE.get(tw, 0), 4 * rows
+    nin = nout = _matrix_bytes(rows, cols, ld_in, e)
     if ld_out != ld_in:
-        nout = _matrix_bytes(rows, cols, ld_out, _ESIZE.get(t, 0))
-    wb = cols * _ESIZE.get(tw, 0)
+        nout = _matrix_bytes(rows, cols, ld_out, e)
     return load_library().mrr_layernorm_fwd(
         _rows_args(inputs, nranks, nin, "inputs"), nranks, _rows_arg(residual, nin, "residual"),
         _flat_arg(weight, wb, "weight"), _flat_arg(bias, wb, "bias"), _rows_arg(sum, nout, "sum"),
-        _rows_arg(out, nout, "out"), _flat_arg(mean, 4 * rows, "mean"), _flat_arg(rstd, 4 * rows, "rstd"),
+        _rows_arg(out, nout, "out"), _flat_arg(mean, rb, "mean"), _flat_arg(rstd, rb, "rstd"),
         rows, cols, ld_in, ld_out, eps, t, tw, _stream(stream))
 
 
@@ -483,14 +511,15 @@ def mrr_layernorm_bwd_workspace_bytes(rows, cols) -> int:
 def mrr_layernorm_bwd(dout, sum, weight, mean, rstd, dresidual, dsum, dweight, dbias, rows, cols,
                       ld_in, ld_out, dtype, wdtype="auto", workspace=None, workspace_bytes=0,
                       stream=None) -> int:
-    t, tw = _dt(dtype), _wtype(dtype, wdtype)
-    nin = nout = _matrix_bytes(rows, cols, ld_in, _ESIZE.get(t, 0))
+    t = _dt(dtype)
+    tw = _wtype(t, wdtype)
+    e, wb, rb = _ESIZE.get(t, 0), cols * _ESIZE.get(tw, 0), 4 * rows
+    nin = nout = _matrix_bytes(rows, cols, ld_in, e)
     if ld_out != ld_in:
-        nout = _matrix_bytes(rows, cols, ld_out, _ESIZE.get(t, 0))
-    wb = cols * _ESIZE.get(tw, 0)
+        nout = _matrix_bytes(rows, cols, ld_out, e)
     return load_library().mrr_layernorm_bwd(
         _rows_arg(dout, nin, "dout"), _rows_arg(sum, nin, "sum"), _flat_arg(weight, wb, "weight"),
-        _flat_arg(mean, 4 * rows, "mean"), _flat_arg(rstd, 4 * rows, "rstd"),
+        _flat_arg(mean, rb, "mean"), _flat_arg(rstd, rb, "rstd"),
         _rows_arg(dresidual, nin, "dresidual"), _rows_arg(dsum, nout, "dsum"), _flat_arg(dweight, wb, "dweight"),
         _flat_arg(dbias, wb, "dbias"), rows, cols, ld_in, ld_out, t, tw,
         _flat_arg(workspace, workspace_bytes, "workspace"), workspace_bytes, _stream(stream))
@@ -533,7 +562,7 @@ def mrr_linear_xent_bwd(hidden, weights, rows, nranks, targets, ignore_index, ls
     return load_library().mrr_linear_xent_bwd(
         _rows_arg(hidden, nh, "hidden"), _rows_args(weights, len(need), need, "weights"), sizes, nranks,
         _flat_arg(targets, 8 * tokens, "targets"), ignore_index, _flat_arg(lse, 4 * tokens, "lse"),
-        _rows_arg(dloss, 4 * ((tokens - 1) * dloss_stride + 1) if tokens > 0 else 0, "dloss"), dloss_stride,
+        _spaced_arg(dloss, 4 * ((tokens - 1) * dloss_stride + 1) if tokens > 0 else 0, "dloss"), dloss_stride,
         _rows_arg(dhidden, nh, "dhidden"), _rows_args(dweights, len(need), need, "dweights"), tokens, cols, ld_hidden,
         ld_weight, t, _flat_arg(workspace, workspace_bytes, "workspace"), workspace_bytes, _stream(stream))
 

@@ -851,6 +851,7 @@ mrr_status mrr_layernorm_fwd(const void* const* inputs, int nranks, const void* 
       !aligned(bias, ew) || !aligned(mean, 4) || !aligned(rstd, 4))
     return refuse(MRR_EALIGN, fn, "element alignment");
   if (bad_overlap(ins, nin, in_place, outs, 4)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
+  for (int i = 0; sum && i < in_place; ++i) a.in_place |= ins[i].p == sum;
   a.residual = residual;
   a.weight = weight;
   a.bias = bias;

@@ -25,6 +25,7 @@ struct NormFwdArgs {
   int nranks;
   float eps;
   int wf32;              // weight and bias are f32 (otherwise the data type)
+  int in_place;          // sum is one of the inputs or the residual
 };
 
 struct NormBwdArgs {

@@ -19,8 +19,13 @@
 //
 // A lane's elements come in units of 16 bytes, unit u of a lane being unit
 // u * TPR + lane of the row: a wave's loads are contiguous.  Rows need no
-// alignment beyond their element's: gfx950 loads 16 bytes from any address, and
-// only the row's last, partial unit goes element by element.
+// alignment beyond their element's: gfx950 loads 16 bytes from any address.  Where
+// the row ends inside a unit, the unit is moved back to end with the row.  Its first
+// `over` elements are then the neighbour's too: they are left out of sums along the row,
+// and both lanes store the same value.  No access goes element by element, which keeps
+// the code a third of its size: a call of few rows runs it once, out of a cold cache.
+#include <type_traits>
+
 #include "mrr_device.hpp"
 #include "mrr_internal.hpp"
 #include "mrr_ops.hpp"
@@ -29,31 +34,52 @@
 namespace mrr {
 namespace {
 
-// The same past the caches (NT) or through them.
-template <int T, bool NT> __device__ __forceinline__ u32x4 load_in(const void* p, int n) {
-  if (NT && n >= Vec<T>::VW) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
-  return load_raw<T>(p, n);
+// The unit of a row of `cols` elements (a unit's worth at least) that begins at column c.
+template <int T> struct Unit {
+  uint32_t at, over;
+  __device__ __forceinline__ Unit(uint32_t cols, uint32_t c) {
+    at = c < cols - Vec<T>::VW ? c : cols - Vec<T>::VW;
+    over = c - at;
+  }
+  __device__ __forceinline__ bool any() const { return over < (uint32_t)Vec<T>::VW; }
+};
+
+// 16 bytes, past the caches (NT) or through them.
+template <bool NT> __device__ __forceinline__ u32x4 load_unit(const void* p) {
+  if (NT) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
+  return *reinterpret_cast<const u32x4_any*>(p);
 }
-template <int T, bool NT> __device__ __forceinline__ void store_out(void* p, int n, u32x4 v) {
-  if (NT && n >= Vec<T>::VW) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(p));
-  else store_raw<T>(p, n, v);
+template <bool NT> __device__ __forceinline__ void store_unit(void* p, u32x4 v) {
+  if (NT) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(p));
+  else *reinterpret_cast<u32x4_any*>(p) = v;
 }
 
-// V weights from column c on, widened; `fill` where there is no weight.
-template <int T>
-__device__ __forceinline__ void load_weights(const void* w, int wf32, uint32_t c, int n, float fill,
-                                             float* x) {
-  constexpr int V = Vec<T>::VW;
-  if (!w) {
+// V weights from column `at` on as they lie in memory, and widened; `fill` where there
+// are none.
+template <int T> struct RawWeights {
+  static constexpr int N = T == kF32 ? 1 : 2;  // f32 weights beside 16-bit data take two loads
+  u32x4 v[N];
+  __device__ __forceinline__ void load(const void* w, int wf32, uint32_t c) {
+    if (!w) return;
+    if (T == kF32 || wf32) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) x[j] = fill;
-  } else if (T == kF32 || wf32) {
-#pragma unroll
-    for (int h = 0; h < V / 4; ++h) decode16<kF32>(load_raw<kF32>(at<kF32>(w, c + 4 * h), n - 4 * h), x + 4 * h);
-  } else {
-    decode16<T>(load_raw<T>(at<T>(w, c), n), x);
+      for (int h = 0; h < N; ++h) v[h] = load_unit<false>(at<kF32>(w, c + 4 * h));
+    } else {
+      v[0] = load_unit<false>(at<T>(w, c));
+    }
   }
-}
+  __device__ __forceinline__ void get(const void* w, int wf32, float fill, float* x) const {
+    if (!w) {
+#pragma unroll
+      for (int j = 0; j < Vec<T>::VW; ++j) x[j] = fill;
+    } else if (T == kF32 || wf32) {
+#pragma unroll
+      for (int h = 0; h < N; ++h) decode16<kF32>(v[h], x + 4 * h);
+    } else {
+      decode16<T>(v[0], x);
+    }
+  }
+};
 
 // Sum of one value, or of two, over the TPR lanes of a row.  Rows of more than a
 // wave join through LDS, in wave order; `lds` holds 2 values a wave, and the
@@ -83,34 +109,49 @@ template <int TPR> __device__ __forceinline__ float2 row_sum(float2 v, float2* l
 // Lanes of a workgroup: rows of up to 256 lanes share one of 256.
 constexpr int block_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
 
-// Elements of a lane's unit at column c that exist.
-__device__ __forceinline__ int unit_left(uint32_t cols, uint32_t c) { return c < cols ? (int)(cols - c) : 0; }
-
-template <int T, int TPR, int E, bool NTL, bool NTS>
+// ONE: the workgroup has one set of rows, and all it reads is asked for at once (1 x 4096,
+// 8 ranks: 5.6 us a call in a graph, of which 4.5 are a call of any size).  TAIL:
+// rows may end inside a unit; without it, a unit is whole or not there.
+template <int T, int TPR, int E, bool NTL, bool NTS, bool ONE, bool TAIL>
 __global__ void __launch_bounds__(block_threads(TPR)) norm_fwd_k(NormFwdArgs a) {
   constexpr int V = Vec<T>::VW, U = E / V, RPB = block_threads(TPR) / TPR;
   // ranks whose loads are in flight together
-  constexpr int G = U >= 4 ? 2 : 4;
+  constexpr int G = ONE ? (U >= 4 ? 4 : 8) : U >= 4 || TPR == 1024 ? 2 : 4;
   __shared__ float2 lds[2][block_threads(TPR) / 64];
   const uint32_t lane = threadIdx.x % TPR;
   const uint32_t sub = threadIdx.x / TPR;
   const float inv = 1.0f / (float)a.cols;
   // every lane of a workgroup walks the same number of rows, as they share barriers
   for (uint64_t row0 = (uint64_t)blockIdx.x * RPB; row0 < a.rows; row0 += (uint64_t)gridDim.x * RPB) {
-    const uint64_t row = row0 + sub;
-    const bool live = row < a.rows;
+    const bool live = row0 + sub < a.rows;
+    const uint64_t row = live ? row0 + sub : a.rows - 1;  // a lane without a row reads the last one
     float x[E];
-    u32x4 raw[G][U];
+    u32x4 raw[G + (ONE ? 1 : 0)][U];  // ONE: the residual has a place of its own
+    u32x4(&res)[U] = raw[ONE ? G : 0];
+    RawWeights<T> w[U], b[U];
+    auto load_residual = [&]() {
+#pragma unroll
+      for (int u = 0; u < U; ++u) res[u] = load_unit<NTL>(at<T>(a.residual, row * a.ld_in + Unit<T>(a.cols, (u * TPR + lane) * V).at));
+    };
+    auto load_weights = [&](int u) {
+      const uint32_t c = Unit<T>(a.cols, (u * TPR + lane) * V).at;
+      w[u].load(a.weight, a.wf32, c);
+      b[u].load(a.bias, a.wf32, c);
+    };
+    if constexpr (ONE) {
+      if (a.residual) load_residual();
+#pragma unroll
+      for (int u = 0; u < U; ++u) load_weights(u);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = -0.0f;  // (the first sum is then exactly x_0)
     for (int r0 = 0; r0 < a.nranks; r0 += G) {
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         if (r0 + g < a.nranks) {
-          const uint8_t* p = at<T>(a.in[r0 + g], row * a.ld_in);
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const uint32_t c = (u * TPR + lane) * V;
-            raw[g][u] = load_in<T, NTL>(p + (uint64_t)c * Ty<T>::size, live ? unit_left(a.cols, c) : 0);
-          }
+          for (int u = 0; u < U; ++u)
+            raw[g][u] = load_unit<NTL>(at<T>(a.in[r0 + g], row * a.ld_in + Unit<T>(a.cols, (u * TPR + lane) * V).at));
         }
       }
 #pragma unroll
@@ -121,22 +162,17 @@ __global__ void __launch_bounds__(block_threads(TPR)) norm_fwd_k(NormFwdArgs a) 
             float d[V];
             decode16<T>(raw[g][u], d);
 #pragma unroll
-            for (int j = 0; j < V; ++j) x[u * V + j] = r0 + g == 0 ? d[j] : x[u * V + j] + d[j];
+            for (int j = 0; j < V; ++j) x[u * V + j] += d[j];
           }
         }
       }
     }
     if (a.residual) {
-      const uint8_t* p = at<T>(a.residual, row * a.ld_in);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const uint32_t c = (u * TPR + lane) * V;
-        raw[0][u] = load_in<T, NTL>(p + (uint64_t)c * Ty<T>::size, live ? unit_left(a.cols, c) : 0);
-      }
+      if constexpr (!ONE) load_residual();
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         float d[V];
-        decode16<T>(raw[0][u], d);
+        decode16<T>(res[u], d);
 #pragma unroll
         for (int j = 0; j < V; ++j) x[u * V + j] += d[j];
       }
@@ -144,26 +180,45 @@ __global__ void __launch_bounds__(block_threads(TPR)) norm_fwd_k(NormFwdArgs a) 
     float s = 0.0f;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const u32x4 h = encode16<T>(x + u * V);
-      if (a.sum) {
-        const uint32_t c = (u * TPR + lane) * V;
-        store_out<T, NTS>(at<T>(a.sum, row * a.ld_out + c), live ? unit_left(a.cols, c) : 0, h);
-      }
-      decode16<T>(h, x + u * V);
+      decode16<T>(encode16<T>(x + u * V), x + u * V);
+      const uint32_t over = Unit<T>(a.cols, (u * TPR + lane) * V).over;
+      float su = 0.0f;
+      if (over == 0) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) s += x[u * V + j];  // elements past the row are zeros
+        for (int j = 0; j < V; ++j) su += x[u * V + j];
+      } else if (TAIL) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) su += (uint32_t)j >= over ? x[u * V + j] : 0.0f;
+      }
+      s += su;
     }
+    auto store_sum = [&]() {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const Unit<T> unit(a.cols, (u * TPR + lane) * V);
+        if (live && unit.any()) store_unit<NTS>(at<T>(a.sum, row * a.ld_out + unit.at), encode16<T>(x + u * V));
+      }
+    };
+    // in an input's place, when every wave has read its units (else early: f32 rows of
+    // 1024 lanes are 5 % faster)
+    if (a.sum && !a.in_place) store_sum();
     const float mean = row_sum<TPR>(make_float2(s, 0.0f), lds[0]).x * inv;
+    if (a.sum && a.in_place) store_sum();
     float q = 0.0f;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int n = unit_left(a.cols, (u * TPR + lane) * V);
+      const Unit<T> unit(a.cols, (u * TPR + lane) * V);
+      float qu = 0.0f;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float d = x[u * V + j] - mean;
-        x[u * V + j] = d;
-        if (j < n) q = __builtin_fmaf(d, d, q);
+      for (int j = 0; j < V; ++j) x[u * V + j] -= mean;
+      if (unit.over == 0) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) qu = __builtin_fmaf(x[u * V + j], x[u * V + j], qu);
+      } else if (TAIL) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) qu = __builtin_fmaf(x[u * V + j], (uint32_t)j >= unit.over ? x[u * V + j] : 0.0f, qu);
       }
+      q += qu;
     }
     const float var = row_sum<TPR>(make_float2(q, 0.0f), lds[1]).x * inv;
     const float rstd = 1.0f / __builtin_sqrtf(var + a.eps);
@@ -173,19 +228,19 @@ __global__ void __launch_bounds__(block_threads(TPR)) norm_fwd_k(NormFwdArgs a) 
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t c = (u * TPR + lane) * V;
-      const int n = live ? unit_left(a.cols, c) : 0;
-      float w[V], b[V];
-      load_weights<T>(a.weight, a.wf32, c, n, 1.0f, w);
-      load_weights<T>(a.bias, a.wf32, c, n, 0.0f, b);
+      const Unit<T> unit(a.cols, (u * TPR + lane) * V);
+      float wx[V], y[V];
+      if constexpr (!ONE) load_weights(u);
+      w[u].get(a.weight, a.wf32, 1.0f, wx);
+      b[u].get(a.bias, a.wf32, 0.0f, y);
 #pragma unroll
-      for (int j = 0; j < V; ++j) b[j] = __builtin_fmaf(x[u * V + j] * rstd, w[j], b[j]);
-      store_out<T, NTS>(at<T>(a.out, row * a.ld_out + c), n, encode16<T>(b));
+      for (int j = 0; j < V; ++j) y[j] = __builtin_fmaf(x[u * V + j] * rstd, wx[j], y[j]);
+      if (live && unit.any()) store_unit<NTS>(at<T>(a.out, row * a.ld_out + unit.at), encode16<T>(y));
     }
   }
 }
 
-// Rows too long for registers: the same three passes with the sum computed
+// Rows too long for registers (or shorter than a unit): the same three passes with the sum computed
 // again in each.  Element by element; a lane reads what it overwrites, so the
 // outputs may take an input's place here too.
 constexpr int kWideThreads = 1024;
@@ -230,7 +285,11 @@ template <int T> __global__ void __launch_bounds__(kWideThreads) norm_fwd_wide_k
 // lanes keep the weight and bias gradients of their columns in registers over all of
 // them.  At the end the workgroup's rows are joined in LDS, in order, and written
 // once: the sums over rows take a fixed order.
-template <int T, int TPR, int E, int BT, bool AHEAD, bool NT> __global__ void __launch_bounds__(BT) norm_bwd_k(NormBwdArgs a) {
+// DX: the gradient of h is wanted.  What is in flight at the end of a turn is known to
+// the compiler (a branch around some of the stores would make it wait for all of them
+// before the next turn's loads: 4 %, and 14 % of a call that loads ahead).
+template <int T, int TPR, int E, int BT, bool AHEAD, bool NT, bool TAIL, bool DX>
+__global__ void __launch_bounds__(BT) norm_bwd_k(NormBwdArgs a) {
   constexpr int V = Vec<T>::VW, U = E / V, RPB = BT / TPR;
   __shared__ float2 lds[2][BT / 64];
   const uint32_t lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
@@ -238,8 +297,9 @@ template <int T, int TPR, int E, int BT, bool AHEAD, bool NT> __global__ void __
   float dw[E], db[E], w[E];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const uint32_t c = (u * TPR + lane) * V;
-    load_weights<T>(a.weight, a.wf32, c, unit_left(a.cols, c), 1.0f, w + u * V);
+    RawWeights<T> raw;
+    raw.load(a.weight, a.wf32, Unit<T>(a.cols, (u * TPR + lane) * V).at);
+    raw.get(a.weight, a.wf32, 1.0f, w + u * V);
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) dw[e] = db[e] = 0.0f;
@@ -248,18 +308,20 @@ template <int T, int TPR, int E, int BT, bool AHEAD, bool NT> __global__ void __
     float mean, rstd;
   };
   auto fetch = [&](uint64_t row0, Row& x) {
-    const uint64_t row = row0 + sub;
-    const bool live = row < a.rows;
+    const uint64_t row = row0 + sub < a.rows ? row0 + sub : a.rows - 1;
+    const uint64_t from = row * a.ld_in;
+    x.mean = a.mean[row];
+    x.rstd = a.rstd[row];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t c = (u * TPR + lane) * V;
-      const int n = live ? unit_left(a.cols, c) : 0;
-      x.dy[u] = load_in<T, NT>(at<T>(a.dout, row * a.ld_in + c), n);
-      x.h[u] = load_in<T, NT>(at<T>(a.sum, row * a.ld_in + c), n);
-      if (a.dresidual && a.dsum) x.res[u] = load_in<T, NT>(at<T>(a.dresidual, row * a.ld_in + c), n);
+      const uint32_t c = Unit<T>(a.cols, (u * TPR + lane) * V).at;
+      x.dy[u] = load_unit<NT>(at<T>(a.dout, from + c));
+      x.h[u] = load_unit<NT>(at<T>(a.sum, from + c));
     }
-    x.mean = live ? a.mean[row] : 0.0f;
-    x.rstd = live ? a.rstd[row] : 0.0f;
+    if (DX && a.dresidual) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) x.res[u] = load_unit<NT>(at<T>(a.dresidual, from + Unit<T>(a.cols, (u * TPR + lane) * V).at));
+    }
   };
   int flip = 0;
   const uint64_t step = (uint64_t)gridDim.x * RPB;
@@ -276,16 +338,18 @@ template <int T, int TPR, int E, int BT, bool AHEAD, bool NT> __global__ void __
     }
     const float mean = now.mean, rstd = now.rstd;
     float2 s = make_float2(0.0f, 0.0f);
+    if (live) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int n = live ? unit_left(a.cols, (u * TPR + lane) * V) : 0;
-      float dy[V], h[V];
-      decode16<T>(now.dy[u], dy);
-      decode16<T>(now.h[u], h);
+      for (int u = 0; u < U; ++u) {
+        const uint32_t over = Unit<T>(a.cols, (u * TPR + lane) * V).over;
+        if (over >= (TAIL ? (uint32_t)V : 1u)) continue;
+        float dy[V], h[V];
+        decode16<T>(now.dy[u], dy);
+        decode16<T>(now.h[u], h);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        if (j < n) {
-          const float xhat = (h[j] - mean) * rstd, g = dy[j] * w[u * V + j];
+        for (int j = 0; j < V; ++j) {
+          const float xhat = (h[j] - mean) * rstd;
+          const float g = !TAIL || (uint32_t)j >= over ? dy[j] * w[u * V + j] : 0.0f;
           s.x += g;
           s.y = __builtin_fmaf(g, xhat, s.y);
           dw[u * V + j] = __builtin_fmaf(dy[j], xhat, dw[u * V + j]);
@@ -293,14 +357,18 @@ template <int T, int TPR, int E, int BT, bool AHEAD, bool NT> __global__ void __
         }
       }
     }
-    if (!a.dsum) continue;
-    s = row_sum<TPR>(s, lds[flip]);
+    if (!DX) continue;
+    s = row_sum<TPR>(s, lds[flip]);  // (with its barrier, dsum may lie in an input's place)
     const float c1 = s.x * inv, c2 = s.y * inv;
+    if (!AHEAD) __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the loads of this turn
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t c = (u * TPR + lane) * V;
-      const int n = live ? unit_left(a.cols, c) : 0;
+      const Unit<T> unit(a.cols, (u * TPR + lane) * V);
+      // (loading ahead, lanes past the row's end have its last unit and store it again)
+      if (!AHEAD && (!live || !unit.any())) continue;
       float dy[V], h[V], d[V];
+      // widened again: kept from above, the values would take twice the registers
+      if (TAIL || TPR == 1024) asm volatile("" : "+v"(now.dy[u]), "+v"(now.h[u]));
       decode16<T>(now.dy[u], dy);
       decode16<T>(now.h[u], h);
 #pragma unroll
@@ -313,7 +381,7 @@ template <int T, int TPR, int E, int BT, bool AHEAD, bool NT> __global__ void __
 #pragma unroll
         for (int j = 0; j < V; ++j) d[j] += h[j];
       }
-      store_out<T, NT>(at<T>(a.dsum, row * a.ld_out + c), n, encode16<T>(d));
+      store_unit<NT>(at<T>(a.dsum, row * a.ld_out + unit.at), encode16<T>(d));
     }
   }
   if (!a.dweight && !a.dbias) return;
@@ -337,18 +405,124 @@ template <int T, int TPR, int E, int BT, bool AHEAD, bool NT> __global__ void __
     float* p = a.partial + (uint64_t)blockIdx.x * 2 * a.cols;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t c = (u * TPR + lane) * V;
-      const int n = unit_left(a.cols, c);
+      const Unit<T> unit(a.cols, (u * TPR + lane) * V);
+      if (!unit.any()) continue;
 #pragma unroll
       for (int h = 0; h < V / 4; ++h) {
-        store_raw<kF32>(p + c + 4 * h, n - 4 * h, encode16<kF32>(dw + u * V + 4 * h));
-        store_raw<kF32>(p + a.cols + c + 4 * h, n - 4 * h, encode16<kF32>(db + u * V + 4 * h));
+        store_unit<false>(p + unit.at + 4 * h, encode16<kF32>(dw + u * V + 4 * h));
+        store_unit<false>(p + a.cols + unit.at + 4 * h, encode16<kF32>(db + u * V + 4 * h));
       }
     }
   }
 }
 
-// Long rows: the gradient of h, one workgroup a row.
+// Both gradients of few rows in one launch: the first `row_blocks` workgroups take rows
+// as above, without sums over them; the others take 16 V columns each and read all rows
+// again, 64 at a time, so that nothing has to be joined in another launch.  (Where dsum
+// lies in the place of what they read, they go first, in a launch of their own.)
+// One launch against two: 8 x 16384 bf16 5.2 us against 9.3 in a graph, 513 x 1600 f32 5.7
+// against 9.4; at its border (below, 4 MiB a tensor and 1024 rows) 10 against 10 to 12.
+constexpr int kSmallThreads = 1024, kSmallLanes = 16, kSmallRows = kSmallThreads / kSmallLanes;
+
+template <int T, int TPR, int E>
+__device__ __forceinline__ void small_rows(const NormBwdArgs& a, float2 (*lds)[kSmallThreads / 64]) {
+  constexpr int V = Vec<T>::VW, U = E / V, RPB = kSmallThreads / TPR;
+  const uint32_t lane = threadIdx.x % TPR;
+  const uint64_t mine = (uint64_t)blockIdx.x * RPB + threadIdx.x / TPR, row = mine < a.rows ? mine : a.rows - 1;
+  const float inv = 1.0f / (float)a.cols;
+  u32x4 rdy[U], rh[U], res[U];
+  RawWeights<T> rw[U];
+  const float mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const Unit<T> unit(a.cols, (u * TPR + lane) * V);
+    rdy[u] = load_unit<false>(at<T>(a.dout, row * a.ld_in + unit.at));
+    rh[u] = load_unit<false>(at<T>(a.sum, row * a.ld_in + unit.at));
+    rw[u].load(a.weight, a.wf32, unit.at);
+    if (a.dresidual) res[u] = load_unit<false>(at<T>(a.dresidual, row * a.ld_in + unit.at));
+  }
+  float g[E], xhat[E];
+  float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t over = Unit<T>(a.cols, (u * TPR + lane) * V).over;
+    float w[V];
+    rw[u].get(a.weight, a.wf32, 1.0f, w);
+    decode16<T>(rdy[u], g + u * V);
+    decode16<T>(rh[u], xhat + u * V);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int e = u * V + j;
+      xhat[e] = (xhat[e] - mean) * rstd;
+      g[e] *= w[j];
+      if ((uint32_t)j >= over) s.x += g[e], s.y = __builtin_fmaf(g[e], xhat[e], s.y);
+    }
+  }
+  s = row_sum<TPR>(s, lds[0]);
+  if (mine >= a.rows) return;
+  const float c1 = s.x * inv, c2 = s.y * inv;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const Unit<T> unit(a.cols, (u * TPR + lane) * V);
+    float d[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) d[j] = (g[u * V + j] - c1 - xhat[u * V + j] * c2) * rstd;
+    if (a.dresidual) {
+      float r[V];
+      decode16<T>(res[u], r);
+#pragma unroll
+      for (int j = 0; j < V; ++j) d[j] += r[j];
+    }
+    if (unit.any()) store_unit<false>(at<T>(a.dsum, row * a.ld_out + unit.at), encode16<T>(d));
+  }
+}
+
+template <int T, int TPR, int E> __global__ void __launch_bounds__(kSmallThreads) norm_bwd_small_k(NormBwdArgs a, uint32_t row_blocks) {
+  constexpr int V = Vec<T>::VW, kWaves = kSmallThreads / 64;
+  __shared__ union {
+    float2 rows[1][kWaves];
+    float cols[kWaves][2 * V][kSmallLanes];
+  } lds;
+  if (blockIdx.x < row_blocks) return small_rows<T, TPR, E>(a, lds.rows);
+  const uint32_t x = threadIdx.x % kSmallLanes, wave = threadIdx.x >> 6;
+  const Unit<T> unit(a.cols, ((blockIdx.x - row_blocks) * kSmallLanes + x) * V);
+  float dw[V], db[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) dw[j] = db[j] = 0.0f;
+#pragma unroll 4
+  for (uint32_t row = threadIdx.x / kSmallLanes; row < (uint32_t)a.rows; row += kSmallRows) {
+    float dy[V], h[V];
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    decode16<T>(load_unit<false>(at<T>(a.dout, row * a.ld_in + unit.at)), dy);
+    decode16<T>(load_unit<false>(at<T>(a.sum, row * a.ld_in + unit.at)), h);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      dw[j] = __builtin_fmaf(dy[j], (h[j] - mean) * rstd, dw[j]);
+      db[j] += dy[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+#pragma unroll
+    for (int m = kSmallLanes; m < 64; m *= 2) {
+      dw[j] += __shfl_xor(dw[j], m);
+      db[j] += __shfl_xor(db[j], m);
+    }
+    if ((threadIdx.x & 63) < kSmallLanes) lds.cols[wave][j][x] = dw[j], lds.cols[wave][V + j][x] = db[j];
+  }
+  __syncthreads();
+  const uint32_t j = threadIdx.x / kSmallLanes, col = unit.at + j % V;
+  if (j >= 2 * V || !unit.any()) return;
+  float s = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kWaves; ++k) s += lds.cols[k][j][x];
+  void* to = j < V ? a.dweight : a.dbias;
+  if (!to) return;
+  if (a.wf32) store_elem<kF32>(to, col, s);
+  else store_elem<T>(to, col, s);
+}
+
+// Such rows: the gradient of h, one workgroup a row.
 template <int T> __global__ void __launch_bounds__(kWideThreads) norm_bwd_wide_k(NormBwdArgs a) {
   __shared__ float2 lds[2][kWideThreads / 64];
   const float inv = 1.0f / (float)a.cols;
@@ -375,7 +549,7 @@ template <int T> __global__ void __launch_bounds__(kWideThreads) norm_bwd_wide_k
   }
 }
 
-// Long rows: the weight gradients of row group blockIdx.y, a column a lane.
+// Such rows: the weight gradients of row group blockIdx.y, a column a lane.
 template <int T> __global__ void __launch_bounds__(256) norm_bwd_cols_k(NormBwdArgs a) {
   const uint32_t c = blockIdx.x * 256 + threadIdx.x;
   if (c >= a.cols) return;
@@ -420,11 +594,13 @@ template <int T> __global__ void __launch_bounds__(kJoinCols * kJoinChains) norm
 
 // Lanes a row and elements a lane: the fewest lanes that hold the row at 16
 // elements each (8 for rows that one wave holds so), up to 1024 lanes.  0: the
-// row does not fit; 32 elements a lane of 1024 would not leave registers enough.
+// row does not fit; 32 elements a lane of 1024 would not leave registers enough.  Nor
+// does one that is shorter than a unit.
 struct RowShape {
   int tpr, e;
 };
 RowShape row_shape(uint32_t cols) {
+  if (cols < 8) return {0, 0};
   if (cols <= 512) return {64, 8};
   if (cols <= 1024) return {64, 16};
   if (cols <= 2048) return {128, 16};
@@ -449,9 +625,16 @@ template <int T, int TPR, int E> hipError_t fwd(const NormFwdArgs& a, hipStream_
   const dim3 grid((uint32_t)(blocks < kMaxGrid ? blocks : kMaxGrid)), block(block_threads(TPR));
   const uint64_t tensors = a.nranks + (a.residual ? 1 : 0) + (a.sum ? 1 : 0) + 1;
   const bool stream = a.rows * a.cols * Ty<T>::size * tensors > kCacheBytes;
-  if (stream && a.nranks >= 2) hipLaunchKernelGGL((norm_fwd_k<T, TPR, E, true, true>), grid, block, 0, s, a);
-  else if (stream) hipLaunchKernelGGL((norm_fwd_k<T, TPR, E, false, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((norm_fwd_k<T, TPR, E, false, false>), grid, block, 0, s, a);
+  auto go = [&](auto ntl, auto nts, auto one, auto tail) {
+    hipLaunchKernelGGL((norm_fwd_k<T, TPR, E, ntl, nts, one, tail>), grid, block, 0, s, a);
+  };
+  constexpr std::true_type yes;
+  constexpr std::false_type no;
+  const bool tail = a.cols % Vec<T>::VW != 0;
+  if (TPR < 1024 && blocks <= 256 && !stream) go(no, no, std::bool_constant<(TPR < 1024)>(), yes);
+  else if (stream && a.nranks >= 2) tail ? go(yes, yes, no, yes) : go(yes, yes, no, no);
+  else if (stream) tail ? go(no, yes, no, yes) : go(no, yes, no, no);
+  else tail ? go(no, no, no, yes) : go(no, no, no, no);
   return hipGetLastError();
 }
 
@@ -476,33 +659,61 @@ constexpr int bwd_threads(int t, int tpr) { return t == kF32 || tpr == 512 ? 512
 constexpr bool bwd_ahead(int t, int tpr) { return t != kF32 && tpr == 512; }
 uint32_t bwd_blocks(uint64_t rows, uint32_t cols, int t) {
   const RowShape r = row_shape(cols);
-  if (r.tpr == 0 || (t == kF32 && r.tpr > 512)) return rows < 256 ? (uint32_t)rows : 256;  // the kernels of long rows
+  if (r.tpr == 0 || (t == kF32 && r.tpr > 512)) return rows < 256 ? (uint32_t)rows : 256;  // the kernels of such rows
   const uint32_t bt = bwd_threads(t, r.tpr), rpb = bt / r.tpr, most = t == kF32 ? 512 : 256;
   const uint64_t blocks = (rows + rpb - 1) / rpb;
   return blocks < most ? (uint32_t)blocks : most;
 }
 
-template <int T, int TPR, int E> void bwd(const NormBwdArgs& a, hipStream_t s) {
-  constexpr int BT = bwd_threads(T, TPR);
-  const uint64_t tensors = 2 + (a.dsum ? 1 : 0) + (a.dsum && a.dresidual ? 1 : 0);
-  if (a.rows * a.cols * Ty<T>::size * tensors > kCacheBytes)
-    hipLaunchKernelGGL((norm_bwd_k<T, TPR, E, BT, bwd_ahead(T, TPR), true>), dim3(a.groups), dim3(BT), 0, s, a);
-  else hipLaunchKernelGGL((norm_bwd_k<T, TPR, E, BT, bwd_ahead(T, TPR), false>), dim3(a.groups), dim3(BT), 0, s, a);
+// Whether norm_bwd_small_k takes the call.
+template <int T> bool bwd_small(const NormBwdArgs& a) {
+  return (a.dweight || a.dbias) && a.rows <= 1024 && a.rows * a.cols * Ty<T>::size <= (4u << 20);
 }
 
-template <int T> void bwd_1024(const NormBwdArgs& a, hipStream_t s) {
-  if constexpr (T != kF32) bwd<T, 1024, 16>(a, s);
+// True: the weight gradients' parts are left to join.
+template <int T, int TPR, int E> bool bwd(const NormBwdArgs& a, hipStream_t s) {
+  if (bwd_small<T>(a)) {
+    constexpr uint32_t rpb = kSmallThreads / TPR, cpb = kSmallLanes * Vec<T>::VW;
+    const uint32_t rows = a.dsum ? (uint32_t)(a.rows + rpb - 1) / rpb : 0u;
+    const uint32_t cols = (a.cols + cpb - 1) / cpb;
+    if (a.dsum == a.dout || a.dsum == a.sum) {
+      hipLaunchKernelGGL((norm_bwd_small_k<T, TPR, E>), dim3(cols), dim3(kSmallThreads), 0, s, a, 0u);
+      hipLaunchKernelGGL((norm_bwd_small_k<T, TPR, E>), dim3(rows), dim3(kSmallThreads), 0, s, a, rows);
+    } else {
+      hipLaunchKernelGGL((norm_bwd_small_k<T, TPR, E>), dim3(rows + cols), dim3(kSmallThreads), 0, s, a, rows);
+    }
+    return false;
+  }
+  constexpr int BT = bwd_threads(T, TPR);
+  const uint64_t tensors = 2 + (a.dsum ? 1 : 0) + (a.dsum && a.dresidual ? 1 : 0);
+  auto go = [&](auto ahead, auto nt, auto tail, auto dx) {
+    hipLaunchKernelGGL((norm_bwd_k<T, TPR, E, BT, ahead, nt, tail, dx>), dim3(a.groups), dim3(BT), 0, s, a);
+  };
+  constexpr std::true_type yes;
+  constexpr std::false_type no;
+  constexpr std::bool_constant<bwd_ahead(T, TPR)> ahead;
+  const bool tail = a.cols % Vec<T>::VW != 0;
+  if (!a.dsum) go(no, no, yes, no);
+  else if (a.rows * a.cols * Ty<T>::size * tensors > kCacheBytes) tail ? go(ahead, yes, yes, yes) : go(ahead, yes, no, yes);
+  else tail ? go(ahead, no, yes, yes) : go(ahead, no, no, yes);
+  return a.dweight || a.dbias;
+}
+
+template <int T> bool bwd_1024(const NormBwdArgs& a, hipStream_t s) {
+  if constexpr (T != kF32) return bwd<T, 1024, 16>(a, s);
+  return false;
 }
 
 template <int T> hipError_t bwd_typed(const NormBwdArgs& a, hipStream_t s) {
+  bool join = a.dweight || a.dbias;
   if (a.rows > 0) {
     const RowShape r = row_shape(a.cols);
-    if (r.tpr == 64 && r.e == 8) bwd<T, 64, 8>(a, s);
-    else if (r.tpr == 64) bwd<T, 64, 16>(a, s);
-    else if (r.tpr == 128) bwd<T, 128, 16>(a, s);
-    else if (r.tpr == 256) bwd<T, 256, 16>(a, s);
-    else if (r.tpr == 512) bwd<T, 512, 16>(a, s);
-    else if (r.tpr == 1024 && T != kF32) bwd_1024<T>(a, s);
+    if (r.tpr == 64 && r.e == 8) join = bwd<T, 64, 8>(a, s);
+    else if (r.tpr == 64) join = bwd<T, 64, 16>(a, s);
+    else if (r.tpr == 128) join = bwd<T, 128, 16>(a, s);
+    else if (r.tpr == 256) join = bwd<T, 256, 16>(a, s);
+    else if (r.tpr == 512) join = bwd<T, 512, 16>(a, s);
+    else if (r.tpr == 1024 && T != kF32) join = bwd_1024<T>(a, s);
     else {  // f32 rows of 1024 lanes as well: the raw data alone would take half of a lane's 128 registers
       // the column sums first: the gradient of h may take the place of what they read
       if (a.dweight || a.dbias)
@@ -514,7 +725,7 @@ template <int T> hipError_t bwd_typed(const NormBwdArgs& a, hipStream_t s) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (a.dweight || a.dbias) {
+  if (join) {
     hipLaunchKernelGGL(norm_bwd_join_k<T>, dim3((a.cols + kJoinCols - 1) / kJoinCols, 2),
                        dim3(kJoinCols * kJoinChains), 0, s, a);
     return hipGetLastError();

@@ -317,3 +317,46 @@ def test_another_stream_and_replays_of_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, (h, y, mean, rstd, dsum, dw, db))), k
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(1500, 1000), (1030, 1003), (1200, 4100), (1100, 4096), (1025, 8200), (1025, 8192), (40, 33000),
+                                       (1024, 1600), (1024, 77), (700, 3001), (1025, 7)])
+def test_backward_on_both_sides_of_the_one_launch_rule(rows, cols, t):
+    """Rows that end inside a unit and whole ones, each through both ways to the weight
+    gradients; with outputs in an input's place as without."""
+    announce("norm_bwd ways", t, rows, cols)
+    g = seeded(rows + cols)
+    dout, h, dres = (randn(g, rows, cols, t=t, shift=0.1) for _ in range(3))
+    weight = randn(g, cols, t="f32", shift=1.0)
+    mean = h.float().mean(1)
+    rstd = torch.rsqrt(h.float().var(1, unbiased=False) + EPS) if cols > 1 else torch.ones(rows, device="cuda")
+    n = mrr.mrr_layernorm_bwd_workspace_bytes(rows, cols)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    first = None
+    for place in (None, 0, 1, 2):
+        src = [x.clone() for x in (dout, h, dres)]
+        dsum = torch.full_like(h, 7.0) if place is None else src[place]
+        dw, db = torch.full((cols,), 7.0, device="cuda"), torch.full((cols,), 7.0, device="cuda")
+        mrr.check(mrr.mrr_layernorm_bwd(src[0], src[1], weight, mean, rstd, src[2], dsum, dw, db, rows, cols, cols, cols, t,
+                                        "f32", ws, n))
+        if first is None:
+            first = (dsum, dw, db)
+            check_backward(dout, h, weight, mean, rstd, dres, dsum, dw, db, t, "f32", rows, cols)
+        assert all(torch.equal(a, b) for a, b in zip(first, (dsum, dw, db))), place
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(3, 1001), (2, 2050), (3, 4099), (2, 8197), (300, 515), (300, 2052), (40, 7)])
+def test_sums_in_the_place_of_inputs_where_rows_end_inside_a_unit(rows, cols, t):
+    announce("norm_fwd in place", t, rows, cols)
+    g = seeded(rows + cols)
+    inputs = [randn(g, rows, cols, t=t) for _ in range(3)]
+    residual = randn(g, rows, cols, t=t)
+    h, y = torch.empty_like(residual), torch.empty_like(residual)
+    mrr.check(forward(inputs, residual, None, None, h, y, None, None, rows, cols, t, "auto"))
+    for k in range(4):
+        src = [x.clone() for x in inputs + [residual]]
+        out = src[(k + 1) % 4]
+        mrr.check(forward(src[:3], src[3], None, None, src[k], out, None, None, rows, cols, t, "auto"))
+        assert torch.equal(src[k], h) and torch.equal(out, y), k

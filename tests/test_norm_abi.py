@@ -91,3 +91,16 @@ def test_workspace_size():
     one = mrr.mrr_layernorm_bwd_workspace_bytes(1, 4096)
     assert one >= 2 * 4096 * 4
     assert mrr.mrr_layernorm_bwd_workspace_bytes(1 << 30, 4096) <= 1024 * 2 * 4096 * 4
+
+
+def test_tensors_whose_elements_lie_apart_are_refused():
+    import torch
+    apart = torch.empty(2 * C, dtype=torch.bfloat16)[::2]
+    turned = torch.empty(C, R, dtype=torch.bfloat16).t()
+    for kw in (dict(weight=apart), dict(bias=apart), dict(mean=torch.empty(2 * R)[::2]), dict(out=turned),
+               dict(inputs=[turned, fake(1)]), dict(inputs=[turned, turned])):
+        with pytest.raises(ValueError):
+            fwd(**kw)
+    for kw in (dict(rstd=torch.empty(2 * R)[::2]), dict(dout=turned), dict(dsum=turned)):
+        with pytest.raises(ValueError):
+            bwd(**kw)

@@ -107,3 +107,16 @@ def test_workspace_size():
     # the logits of this call would take 2 GiB in 32 bits: neither direction keeps them
     big = [bytes_of(4096, 4096, [16032] * 8, 8, "bf16", b) for b in (False, True)]
     assert 0 < big[0] < big[1] < (3 << 29)
+
+
+def test_tensors_whose_elements_lie_apart_are_refused():
+    import torch
+    turned = torch.empty(C, T, dtype=torch.bfloat16).t()
+    wide = torch.empty(C, 200, dtype=torch.bfloat16).t()
+    for kw in (dict(hidden=turned), dict(weights=[wide, fake(2)]), dict(loss=torch.empty(2 * T)[::2]),
+               dict(targets=torch.empty(2 * T, dtype=torch.int64)[::2])):
+        with pytest.raises(ValueError):
+            fwd(**kw)
+    for kw in (dict(dh=turned), dict(dw=[wide, fake(10)]), dict(lse=torch.empty(2 * T)[::2])):
+        with pytest.raises(ValueError):
+            bwd(**kw)
