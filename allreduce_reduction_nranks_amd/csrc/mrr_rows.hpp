@@ -28,6 +28,23 @@ template <int T> __device__ __forceinline__ u32x4 load_raw(const void* p, int n)
   return v;
 }
 
+// V elements from column c on of a row of `cols`; zeros after its last.  One load, of the
+// row's last V where it ends before c + V.
+template <int T> __device__ __forceinline__ u32x4 load_cols(const uint8_t* row, uint32_t c, uint32_t cols) {
+  constexpr uint32_t V = Vec<T>::VW, size = Ty<T>::size;
+  if (cols < V) return load_raw<T>(row + (uint64_t)c * size, c < cols ? (int)(cols - c) : 0);
+  const uint32_t at = c < cols - V ? c : cols - V, over = c - at;
+  u32x4 v = *reinterpret_cast<const u32x4_any*>(row + (uint64_t)at * size);
+  if (over) {
+    const uint32_t bits = over * size * 8;
+    uint64_t lo = (uint64_t)v.y << 32 | v.x, hi = (uint64_t)v.w << 32 | v.z;
+    if (bits < 64) lo = lo >> bits | hi << (64 - bits), hi >>= bits;
+    else lo = bits < 128 ? hi >> (bits - 64) : 0, hi = 0;
+    v = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+  }
+  return v;
+}
+
 template <int T> __device__ __forceinline__ void store_raw(void* p, int n, u32x4 v) {
   constexpr int V = Vec<T>::VW;
   if (n >= V) {

@@ -46,14 +46,16 @@ __device__ __forceinline__ uint32_t seg_b(uint32_t s) { return (0x012u >> (4 * s
 // A product reads rows of a multiple of 64 elements, 16-byte aligned, zeros past
 // the last column.  What does not lie so, and all f32, is laid out first.
 struct LayoutArgs {
-  XentVocab v;          // source of weights: padded row r is row r % 256 of tile tile0 + r / 256
-  const void* src;      // source of hidden states (null: weights)
-  const int32_t* idx;   // source row of each row, -1: zeros; null: row r itself
-  uint64_t ld, rows, src_rows;
-  uint8_t* dst;
-  uint64_t plane;       // bytes between planes
-  const XentScalars* scalars;
-  uint32_t cols, kpad, tile0, units_log2;
+  XentVocab v;            // weights: padded row r is row r % 256 of tile tile0 + r / 256
+  const void* hidden;     // [tokens], rows ld_hidden elements apart
+  const int32_t* idx;     // source row of each row, -1: zeros; null: row r itself
+  uint64_t ld_weight, ld_hidden, hidden_plane, weight_plane;  // bytes between planes
+  uint64_t hidden_rows, weight_rows;
+  uint8_t *hidden_dst, *weight_dst;
+  XentScalars* scalars;
+  const uint32_t* parts;  // f32: of find_most, 2 grid of them; null: scalars holds the scales
+  uint32_t parts_grid, tokens, cols, kpad, tile0, units_log2;
+  uint32_t hidden_blocks, weight_blocks;  // workgroups of each
 };
 
 __device__ __forceinline__ void split(float x, uint32_t* p) {
@@ -71,17 +73,17 @@ __device__ __forceinline__ float scale_to(uint32_t most, int n) {
   return most == 0 ? 1.0f : __uint_as_float((254u + n - e) << 23);
 }
 
-// Largest finite |x| of the weights and of the hidden states, as bits (they order as
-// the values do): one part a workgroup, joined by scale_k.
-constexpr int kMostParts = 1024;
+// Largest finite |x| of the weights and of the counted tokens' hidden states, as bits
+// (they order as the values do): one part a workgroup, joined by whoever needs the scale.
+constexpr uint32_t kMostParts = 1024;
 struct MostArgs {
   XentVocab v;
   const void* src;
-  const int32_t* idx;           // rows of src that count, scalars->count of them; null: all
-  const XentScalars* scalars;
+  const int64_t* targets;  // null: every row of src counts
+  int64_t ignore, vocab;
   uint64_t ld_w, ld_src, src_rows;
-  uint32_t* parts;  // [2][kMostParts]: weights, hidden states
-  uint32_t cols, units_log2;
+  uint32_t* parts;  // [2][grid]: weights, hidden states
+  uint32_t grid, cols, units_log2;
 };
 
 __device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* lds) {
@@ -96,17 +98,22 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* lds) {
   return m;
 }
 
-__global__ void __launch_bounds__(256) most_k(MostArgs a) {
-  __shared__ uint32_t lds[4];
-  const uint32_t lanes = 1u << a.units_log2, per = 256u >> a.units_log2;
-  const uint32_t u0 = threadIdx.x & (lanes - 1);
+__device__ __forceinline__ bool is_counted(int64_t target, int64_t ignore, int64_t vocab) {
+  return target != ignore && target >= 0 && target < vocab;
+}
+
+// Workgroup `id` of the 2 grid.
+__device__ __forceinline__ void find_most(const MostArgs& a, uint32_t id, uint32_t* lds) {
+  const uint32_t lanes = 1u << a.units_log2, per = blockDim.x >> a.units_log2, hidden = id >= a.grid;
+  const uint32_t u0 = threadIdx.x & (lanes - 1), block = hidden ? id - a.grid : id;
   uint32_t most = 0;
-  auto rows_of = [&](const void* base, const int32_t* idx, uint64_t rows, uint64_t ld) {
-    for (uint64_t row = (uint64_t)blockIdx.x * per + (threadIdx.x >> a.units_log2); row < rows; row += (uint64_t)gridDim.x * per) {
-      const uint8_t* p = at<kF32>(base, (idx ? (uint64_t)idx[row] : row) * ld);
+  auto rows_of = [&](const void* base, uint64_t rows, uint64_t ld) {
+    for (uint64_t row = (uint64_t)block * per + (threadIdx.x >> a.units_log2); row < rows; row += (uint64_t)a.grid * per) {
+      if (hidden && a.targets && !is_counted(a.targets[row], a.ignore, a.vocab)) continue;
+      const uint8_t* p = at<kF32>(base, row * ld);
 #pragma unroll 4
       for (uint32_t c = 4 * u0; c < a.cols; c += 4 * lanes) {
-        const u32x4 x = load_raw<kF32>(p + 4 * (uint64_t)c, (int)(a.cols - c));
+        const u32x4 x = load_cols<kF32>(p, c, a.cols);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t u = x[e] & 0x7FFFFFFFu;
@@ -115,64 +122,11 @@ __global__ void __launch_bounds__(256) most_k(MostArgs a) {
       }
     }
   };
-  if (blockIdx.y) rows_of(a.src, a.idx, a.idx ? a.scalars->count : a.src_rows, a.ld_src);
+  if (hidden) rows_of(a.src, a.src_rows, a.ld_src);
   else
-    for (int r = 0; r < a.v.n; ++r) rows_of(a.v.w[r], nullptr, a.v.rows[r], a.ld_w);
+    for (int r = 0; r < a.v.n; ++r) rows_of(a.v.w[r], a.v.rows[r], a.ld_w);
   most = block_max(most, lds);
-  if (threadIdx.x == 0) a.parts[blockIdx.y * kMostParts + blockIdx.x] = most;
-}
-
-__global__ void __launch_bounds__(kMostParts) scale_k(const uint32_t* parts, uint32_t n, XentScalars* to) {
-  __shared__ uint32_t lds[kMostParts / 64];
-  const uint32_t most = block_max(threadIdx.x < n ? parts[blockIdx.x * kMostParts + threadIdx.x] : 0u, lds);
-  if (threadIdx.x) return;
-  const float s = scale_to(most, 15);
-  (blockIdx.x ? to->h : to->w) = s;
-  (blockIdx.x ? to->unscale_h : to->unscale_w) = 1.0f / s;
-}
-
-template <int T> __global__ void __launch_bounds__(256) layout_k(LayoutArgs a) {
-  const uint32_t lanes = 1u << a.units_log2, units = a.kpad / 8;
-  const uint32_t u0 = threadIdx.x & (lanes - 1);
-  const uint32_t per = 256u >> a.units_log2;
-  for (uint64_t row = (uint64_t)blockIdx.x * per + (threadIdx.x >> a.units_log2); row < a.rows;
-       row += (uint64_t)gridDim.x * per) {
-    const uint8_t* src = nullptr;
-    if (a.src) {
-      const int64_t r = a.idx ? (int64_t)a.idx[row] : row < a.src_rows ? (int64_t)row : -1;
-      if (r >= 0) src = at<T>(a.src, (uint64_t)r * a.ld);
-    } else {
-      const uint32_t tile = a.tile0 + (uint32_t)(row / kTileV);
-      int sh = 0;
-      while (tile >= a.v.first_tile[sh + 1]) ++sh;
-      const uint32_t r = (tile - a.v.first_tile[sh]) * kTileV + (uint32_t)(row % kTileV);
-      if (r < a.v.rows[sh]) src = at<T>(a.v.w[sh], (uint64_t)r * a.ld);
-    }
-    for (uint32_t u = u0; u < units; u += lanes) {
-      const int n = src && 8 * u < a.cols ? (int)(a.cols - 8 * u) : 0;
-      uint8_t* d = a.dst + ((uint64_t)row * a.kpad + 8 * u) * 2;
-      if constexpr (T == kF32) {
-        float x[8];
-        decode16<kF32>(load_raw<kF32>(src + 32 * u, n), x);
-        decode16<kF32>(load_raw<kF32>(src + 32 * u + 16, n - 4), x + 4);
-        const float scale = a.src ? a.scalars->h : a.scalars->w;
-        uint32_t p[kPlanes][8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint32_t q[kPlanes];
-          split(x[j] * scale, q);
-#pragma unroll
-          for (int k = 0; k < kPlanes; ++k) p[k][j] = q[k];
-        }
-#pragma unroll
-        for (int k = 0; k < kPlanes; ++k)
-          *reinterpret_cast<u32x4*>(d + k * a.plane) =
-              u32x4{p[k][0] | p[k][1] << 16, p[k][2] | p[k][3] << 16, p[k][4] | p[k][5] << 16, p[k][6] | p[k][7] << 16};
-      } else {
-        *reinterpret_cast<u32x4*>(d) = load_raw<T>(src + 16 * u, n);
-      }
-    }
-  }
+  if (threadIdx.x == 0) a.parts[id] = most;
 }
 
 // ---- tokens of a backward call ---------------------------------------------------
@@ -196,8 +150,7 @@ struct TokensArgs {
 
 constexpr int kTokensThreads = 1024;
 
-__global__ void __launch_bounds__(kTokensThreads) tokens_k(TokensArgs a) {
-  __shared__ uint32_t sums[kTokensThreads / 64];
+__device__ __forceinline__ void sort_tokens(const TokensArgs& a, uint32_t* sums) {
   const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   float scale = 1.0f;
   if (a.scaled) {
@@ -205,7 +158,7 @@ __global__ void __launch_bounds__(kTokensThreads) tokens_k(TokensArgs a) {
     for (uint32_t t = tid; t < a.tokens; t += kTokensThreads) {
       const int64_t target = a.targets[t];
       const uint32_t u = __float_as_uint(a.dloss[t * a.dloss_stride]) & 0x7FFFFFFFu;
-      if (target != a.ignore && target >= 0 && target < a.vocab && u < 0x7F800000u && u > most) most = u;
+      if (is_counted(target, a.ignore, a.vocab) && u < 0x7F800000u && u > most) most = u;
     }
     scale = scale_to(block_max(most, sums), 14);
     __syncthreads();
@@ -215,7 +168,7 @@ __global__ void __launch_bounds__(kTokensThreads) tokens_k(TokensArgs a) {
     const uint32_t t = t0 + tid;
     int64_t target = -1;
     if (t < a.tokens) target = a.targets[t];
-    const bool counted = t < a.tokens && target != a.ignore && target >= 0 && target < a.vocab;
+    const bool counted = t < a.tokens && is_counted(target, a.ignore, a.vocab);
     const uint64_t mask = __ballot(counted);
     if (lane == 0) sums[wave] = (uint32_t)__popcll(mask);
     __syncthreads();
@@ -241,6 +194,133 @@ __global__ void __launch_bounds__(kTokensThreads) tokens_k(TokensArgs a) {
   if (tid == 0) {
     a.scalars->count = before;
     a.scalars->unscale_dz = 1.0f / scale;
+  }
+}
+
+// What a call finds out first: the tokens (its workgroup is the first) and, of f32
+// operands, the largest values.
+__global__ void __launch_bounds__(kTokensThreads) first_k(TokensArgs t, MostArgs m) {
+  __shared__ uint32_t lds[kTokensThreads / 64];
+  uint32_t id = blockIdx.x;
+  if (t.token) {
+    if (id == 0) return sort_tokens(t, lds);
+    --id;
+  }
+  find_most(m, id, lds);
+}
+
+// Counted tokens in the order of their targets' 256-row tiles, tokens of a tile in
+// order: a workgroup a tile finds its own and counts those of the tiles before.
+struct HitsArgs {
+  XentVocab v;
+  const XentToken* token;
+  const XentScalars* scalars;
+  uint32_t *hits, *first;
+  uint32_t tiles;  // 0: not wanted
+};
+__device__ __forceinline__ void sort_hits(const HitsArgs& a, uint32_t tile, uint32_t* before, uint32_t* mine) {
+  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int sh = 0;
+  while (tile >= a.v.first_tile[sh + 1]) ++sh;
+  const uint32_t row0 = (tile - a.v.first_tile[sh]) * kTileV, first = a.v.first_row[sh] + row0;
+  const uint32_t rows = a.v.rows[sh] - row0 < (uint32_t)kTileV ? a.v.rows[sh] - row0 : (uint32_t)kTileV;
+  const uint32_t count = a.scalars->count;
+  uint32_t less = 0;
+  for (uint32_t t = tid; t < count; t += 256) less += (uint32_t)a.token[t].target < first;
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) less += __shfl_xor(less, m);
+  if (lane == 0) before[wave] = less;
+  __syncthreads();
+  uint32_t at = before[0] + before[1] + before[2] + before[3];
+  if (tid == 0) {
+    a.first[tile] = at;
+    if (tile + 1 == a.tiles) a.first[tile + 1] = count;
+  }
+  for (uint32_t t0 = 0; t0 < count; t0 += 256) {
+    const uint32_t t = t0 + tid;
+    const bool in = t < count && (uint32_t)a.token[t].target - first < rows;
+    const uint64_t mask = __ballot(in);
+    if (lane == 0) mine[wave] = (uint32_t)__popcll(mask);
+    __syncthreads();
+    uint32_t to = at + (uint32_t)__popcll(mask & ((1ull << lane) - 1));
+    for (uint32_t w = 0; w < 4; ++w) {
+      if (w < wave) to += mine[w];
+      at += mine[w];
+    }
+    if (in) a.hits[to] = t;
+    __syncthreads();
+  }
+}
+
+template <int T> __device__ __forceinline__ void lay_row(const LayoutArgs& a, const uint8_t* src, uint8_t* dst, uint64_t plane, float scale, uint32_t u0) {
+  const uint32_t lanes = 1u << a.units_log2, units = a.kpad / 8;
+  for (uint32_t u = u0; u < units; u += lanes) {
+    uint8_t* d = dst + 16 * (uint64_t)u;
+    if constexpr (T == kF32) {
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = 0.0f;
+      if (src) {
+        decode16<kF32>(load_cols<kF32>(src, 8 * u, a.cols), x);
+        decode16<kF32>(load_cols<kF32>(src, 8 * u + 4, a.cols), x + 4);
+      }
+      uint32_t p[kPlanes][8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t q[kPlanes];
+        split(x[j] * scale, q);
+#pragma unroll
+        for (int k = 0; k < kPlanes; ++k) p[k][j] = q[k];
+      }
+#pragma unroll
+      for (int k = 0; k < kPlanes; ++k)
+        *reinterpret_cast<u32x4*>(d + k * plane) =
+            u32x4{p[k][0] | p[k][1] << 16, p[k][2] | p[k][3] << 16, p[k][4] | p[k][5] << 16, p[k][6] | p[k][7] << 16};
+    } else {
+      *reinterpret_cast<u32x4*>(d) = src ? load_cols<T>(src, 8 * u, a.cols) : u32x4{0u, 0u, 0u, 0u};
+    }
+  }
+}
+
+// What the products need laid out, in one launch: hidden states, weights of a piece, and
+// the tokens by their targets.
+template <int T> __global__ void __launch_bounds__(256) layout_k(LayoutArgs a, HitsArgs h) {
+  __shared__ uint32_t lds[8];
+  uint32_t id = blockIdx.x;
+  const bool hidden = id < a.hidden_blocks;
+  if (!hidden) id -= a.hidden_blocks;
+  if (!hidden && id >= a.weight_blocks) return sort_hits(h, id - a.weight_blocks, lds, lds + 4);
+  const uint32_t per = 256u >> a.units_log2, sub = threadIdx.x >> a.units_log2, u0 = threadIdx.x & ((1u << a.units_log2) - 1);
+  float scale = 1.0f;
+  if constexpr (T == kF32) {
+    if (a.parts) {
+      uint32_t most = 0;
+      for (uint32_t k = threadIdx.x; k < a.parts_grid; k += 256) {
+        const uint32_t m = a.parts[(hidden ? a.parts_grid : 0) + k];
+        most = m > most ? m : most;
+      }
+      scale = scale_to(block_max(most, lds), 15);
+      if (id == 0 && threadIdx.x == 0) {
+        (hidden ? a.scalars->h : a.scalars->w) = scale;
+        (hidden ? a.scalars->unscale_h : a.scalars->unscale_w) = 1.0f / scale;
+      }
+    } else {
+      scale = hidden ? a.scalars->h : a.scalars->w;
+    }
+  }
+  if (hidden) {
+    for (uint64_t row = (uint64_t)id * per + sub; row < a.hidden_rows; row += (uint64_t)a.hidden_blocks * per) {
+      const int64_t r = a.idx ? (int64_t)a.idx[row] : row < a.tokens ? (int64_t)row : -1;
+      lay_row<T>(a, r >= 0 ? at<T>(a.hidden, (uint64_t)r * a.ld_hidden) : nullptr, a.hidden_dst + row * a.kpad * 2, a.hidden_plane, scale, u0);
+    }
+  } else {
+    for (uint64_t row = (uint64_t)id * per + sub; row < a.weight_rows; row += (uint64_t)a.weight_blocks * per) {
+      const uint32_t tile = a.tile0 + (uint32_t)(row / kTileV);
+      int sh = 0;
+      while (tile >= a.v.first_tile[sh + 1]) ++sh;
+      const uint32_t r = (tile - a.v.first_tile[sh]) * kTileV + (uint32_t)(row % kTileV);
+      lay_row<T>(a, r < a.v.rows[sh] ? at<T>(a.v.w[sh], (uint64_t)r * a.ld_weight) : nullptr, a.weight_dst + row * a.kpad * 2, a.weight_plane, scale, u0);
+    }
   }
 }
 
@@ -416,6 +496,7 @@ __global__ void __launch_bounds__(tile_threads(S)) logits_k(XentArgs a) {
   const uint32_t at0 = row0 < rows ? row0 : rows - 1, have = a.laid ? (uint32_t)S : left ? left : 1u;
   const uint8_t* wa = a.laid ? a.laid + (uint64_t)mt * S * a.ldw : (const uint8_t*)a.v.w[sh] + (uint64_t)at0 * a.ldw;
   const uint8_t* hb = a.h + (uint64_t)t0 * a.ldh;
+  const uint32_t t_have = tokens - t0;  // of a forward: hidden states may be read in place
   uint32_t k = 0, seg = 0;
   const uint32_t kend = a.kpad * 2;
   auto src = [&](int s, const uint8_t*& pa, const uint8_t*& pb, uint32_t (&oa)[Prod::L], uint32_t (&ob)[Prod::L]) {
@@ -425,7 +506,7 @@ __global__ void __launch_bounds__(tile_threads(S)) logits_k(XentArgs a) {
       for (int i = 0; i < Prod::L; ++i) {
         const uint32_t r = row_src_row<S>(tid, i);
         oa[i] = (r < have ? r : have - 1) * a.ldw + c;
-        ob[i] = r * a.ldh + c;
+        ob[i] = (BWD || r < t_have ? r : t_have - 1) * a.ldh + c;
       }
     }
     pa = wa + k;
@@ -531,12 +612,11 @@ template <int T, int NT, int R, bool BWD> __global__ void __launch_bounds__(256)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const uint32_t c = b * B + lane0 + x * V;
-        const int n_left = c < a.cols ? (int)(a.cols - c) : 0;
         u32x4 vw[R], vh[NT];
 #pragma unroll
-        for (int r = 0; r < R; ++r) vw[r] = load_raw<T>(pw[r] + (uint64_t)b * 128 + 16 * x, n_left);
+        for (int r = 0; r < R; ++r) vw[r] = load_cols<T>(pw[r] - (uint64_t)lane0 * Ty<T>::size, c, a.cols);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) vh[n] = load_raw<T>(ph[n] + (uint64_t)b * 128 + 16 * x, n_left);
+        for (int n = 0; n < NT; ++n) vh[n] = load_cols<T>(ph[n] - (uint64_t)lane0 * Ty<T>::size, c, a.cols);
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -669,43 +749,6 @@ template <int T, int S, int NS, int SEG> __global__ void __launch_bounds__(tile_
       }
       *to = y;
     });
-}
-
-// Counted tokens in the order of their targets' 256-row tiles, tokens of a tile in
-// order: a workgroup a tile finds its own and counts those of the tiles before.
-__global__ void __launch_bounds__(256) hits_k(XentArgs a) {
-  __shared__ uint32_t before[4], mine[4];
-  const uint32_t tile = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int sh = 0;
-  while (tile >= a.v.first_tile[sh + 1]) ++sh;
-  const uint32_t row0 = (tile - a.v.first_tile[sh]) * kTileV, first = a.v.first_row[sh] + row0;
-  const uint32_t rows = a.v.rows[sh] - row0 < (uint32_t)kTileV ? a.v.rows[sh] - row0 : (uint32_t)kTileV;
-  const uint32_t count = a.scalars->count;
-  uint32_t less = 0;
-  for (uint32_t t = tid; t < count; t += 256) less += (uint32_t)a.token[t].target < first;
-#pragma unroll
-  for (int m = 32; m > 0; m >>= 1) less += __shfl_xor(less, m);
-  if (lane == 0) before[wave] = less;
-  __syncthreads();
-  uint32_t at = before[0] + before[1] + before[2] + before[3];
-  if (tid == 0) {
-    a.hits_first[tile] = at;
-    if (tile + 1 == gridDim.x) a.hits_first[tile + 1] = count;
-  }
-  for (uint32_t t0 = 0; t0 < count; t0 += 256) {
-    const uint32_t t = t0 + tid;
-    const bool in = t < count && (uint32_t)a.token[t].target - first < rows;
-    const uint64_t mask = __ballot(in);
-    if (lane == 0) mine[wave] = (uint32_t)__popcll(mask);
-    __syncthreads();
-    uint32_t to = at + (uint32_t)__popcll(mask & ((1ull << lane) - 1));
-    for (uint32_t w = 0; w < 4; ++w) {
-      if (w < wave) to += mine[w];
-      at += mine[w];
-    }
-    if (in) a.hits[to] = t;
-    __syncthreads();
-  }
 }
 
 // Weight gradients of one piece: a tile of S columns by S vocabulary rows over the
@@ -968,7 +1011,7 @@ XentPlan xent_plan(uint32_t tokens, uint32_t cols, const size_t* rows, int nrank
     p.hits_first = take((tiles + 1) * 4);
   } else {
     // pairs of a tile and token: at most few_k's, else those of 128 x 128 tiles
-    p.part = take(tiles * (tokens <= 16 ? 16 : tokens <= 32 ? 8 : 4) * tokens * sizeof(float2));
+    p.part = take(tiles * (tokens <= 16 ? 16 : t == kF32 ? 8 : 4) * tokens * sizeof(float2));
     p.zt = take((uint64_t)tokens * 4);
   }
   p.scalars = take(sizeof(XentScalars));
@@ -979,12 +1022,19 @@ XentPlan xent_plan(uint32_t tokens, uint32_t cols, const size_t* rows, int nrank
 
 namespace {
 
-template <int T> void layout(LayoutArgs l, hipStream_t s) {
+// h.tiles workgroups past those of the rows sort tokens by their targets.
+template <int T> void layout(LayoutArgs l, const HitsArgs& h, hipStream_t s) {
   uint32_t log2 = 0;
   while (log2 < 8 && (1u << log2) < l.kpad / 8) ++log2;
   l.units_log2 = log2;
-  const uint64_t per = 256u >> log2, blocks = (l.rows + per - 1) / per;
-  hipLaunchKernelGGL(layout_k<T>, dim3((uint32_t)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, l);
+  auto blocks = [&](uint64_t rows) {
+    const uint64_t per = 256u >> log2, n = (rows + per - 1) / per;
+    return (uint32_t)(n < 65536 ? n : 65536);
+  };
+  l.hidden_blocks = blocks(l.hidden_rows);
+  l.weight_blocks = blocks(l.weight_rows);
+  if (const uint32_t grid = l.hidden_blocks + l.weight_blocks + h.tiles)
+    hipLaunchKernelGGL(layout_k<T>, dim3(grid), dim3(256), 0, s, l, h);
 }
 
 // 16-token groups of a few_k workgroup, 0: logits_k.  16 bits: up to 4 tokens (of 32000 x
@@ -997,7 +1047,8 @@ template <int T> void layout(LayoutArgs l, hipStream_t s) {
 // each weight moved at 5 TB/s.
 uint32_t few_groups(int t, uint32_t tokens, uint32_t rows, uint32_t tpad, uint32_t kpad, bool backward) {
   if (t != kF32) return tokens <= 4 ? 1 : 0;
-  const uint32_t groups = tokens <= 16 ? 1 : tokens <= 32 ? 2 : 4;
+  // (4 groups load less, 2 fill the CUs: 130 x 3003 x 520)
+  const uint32_t groups = tokens <= 16 ? 1 : tokens <= 32 || rows * 4 * ((tokens + 63) / 64) < 256 ? 2 : 4;
   const double weights = (double)rows * kTileV * kpad * 1e-6;  // millions
   const double flops = 2.0 * (double)up(tokens, 16 * groups) / 75.0;
   const double few = 5 + weights * (flops > 4 / 4.4 ? flops : 4 / 4.4);
@@ -1095,11 +1146,8 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
   a.ld_w = c.ld_weight;
   XentScalars* scalars = (XentScalars*)(ws + p.scalars);
   a.scalars = scalars;
-  LayoutArgs l{};
-  l.scalars = scalars;
-  l.v = a.v;
-  l.cols = c.cols;
-  l.kpad = p.kpad;
+  HitsArgs hits{};
+  TokensArgs tk{};
   if constexpr (BWD) {
     a.dz = ws + p.dz;
     a.dz_plane = p.dz_plane;
@@ -1113,42 +1161,52 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
     a.dhidden = c.dhidden;
     a.ld_dh = c.ld_hidden;
     a.ld_dw = c.ld_weight;
-    const TokensArgs t{c.targets, c.lse, c.dloss, c.dloss_stride, c.ignore, (int64_t)vocab, (XentToken*)(ws + p.token),
-                       (int32_t*)(ws + p.idx), (int32_t*)(ws + p.place), scalars, c.tokens, p.tpad, T != kBF16};
-    hipLaunchKernelGGL(tokens_k, dim3(1), dim3(kTokensThreads), 0, s, t);
-    l.idx = (const int32_t*)(ws + p.idx);
+    tk = TokensArgs{c.targets, c.lse, c.dloss, c.dloss_stride, c.ignore, (int64_t)vocab, (XentToken*)(ws + p.token),
+                    (int32_t*)(ws + p.idx), (int32_t*)(ws + p.place), scalars, c.tokens, p.tpad, T != kBF16};
     // up to 64 tokens a tile's workgroup looks through them all
     if (T != kF32 && c.dweights && c.tokens > 64) {
       a.hits = (uint32_t*)(ws + p.hits);
       a.hits_first = (uint32_t*)(ws + p.hits_first);
-      hipLaunchKernelGGL(hits_k, dim3(p.tiles), dim3(256), 0, s, a);
+      hits = HitsArgs{a.v, a.token, scalars, a.hits, a.hits_first, p.tiles};
     }
   } else {
     a.part = (float2*)(ws + p.part);
     a.zt = (float*)(ws + p.zt);
   }
-  if constexpr (T == kF32) {
-    if (BWD || !groups) {
-      MostArgs m{a.v, c.hidden, l.idx, scalars, c.ld_weight, c.ld_hidden, c.tokens, (uint32_t*)(ws + p.most), c.cols, 0};
-      while (m.units_log2 < 8 && (4u << m.units_log2) < c.cols) ++m.units_log2;
-      // from 8 KiB a workgroup
-      const uint64_t n = (vocab * c.cols >> 11) + 1;
-      const uint32_t grid = n < (uint64_t)kMostParts ? (uint32_t)n : (uint32_t)kMostParts;
-      hipLaunchKernelGGL(most_k, dim3(grid, 2), dim3(256), 0, s, m);
-      hipLaunchKernelGGL(scale_k, dim3(2), dim3(kMostParts), 0, s, (const uint32_t*)m.parts, grid, scalars);
-    }
+  const bool lay = BWD || !groups;  // few_k reads the operands where they are
+  LayoutArgs l{};
+  MostArgs m{};
+  if (T == kF32 && lay) {
+    // from 8 KiB a workgroup
+    const uint64_t n = (vocab * c.cols >> 11) + 1;
+    m = MostArgs{a.v, c.hidden, BWD ? c.targets : nullptr, c.ignore, (int64_t)vocab, c.ld_weight, c.ld_hidden, c.tokens,
+                 (uint32_t*)(ws + p.most), n < kMostParts ? (uint32_t)n : kMostParts, c.cols, 0};
+    while (m.units_log2 < 8 && (4u << m.units_log2) < c.cols) ++m.units_log2;
+    l.parts = m.parts;
+    l.parts_grid = m.grid;
   }
-  l.src = c.hidden;
-  l.ld = c.ld_hidden;
-  l.rows = p.tpad;
-  l.src_rows = c.tokens;
-  l.dst = ws + p.h;
-  l.plane = p.h_plane;
-  if (BWD || !groups) layout<T>(l, s);
-  l.src = nullptr;
-  l.ld = c.ld_weight;
-  l.dst = ws + p.laid;
-  l.plane = p.laid_plane;
+  if (const uint32_t grid = (BWD ? 1 : 0) + 2 * m.grid)
+    hipLaunchKernelGGL(first_k, dim3(grid), dim3(kTokensThreads), 0, s, tk, m);
+  l.v = a.v;
+  l.scalars = scalars;
+  l.hidden = c.hidden;
+  l.idx = a.idx;
+  l.tokens = c.tokens;
+  l.cols = c.cols;
+  l.kpad = p.kpad;
+  l.ld_hidden = c.ld_hidden;
+  l.ld_weight = c.ld_weight;
+  l.hidden_dst = ws + p.h;
+  l.weight_dst = ws + p.laid;
+  l.hidden_plane = p.h_plane;
+  l.weight_plane = p.laid_plane;
+  // a forward reads hidden states in place where it can
+  if (!BWD && T != kF32 && c.cols % kTileK == 0 && c.ld_hidden % 8 == 0 && c.ld_hidden <= (1u << 22) && (uintptr_t)c.hidden % 16 == 0) {
+    a.h = (const uint8_t*)c.hidden;
+    a.ldh = (uint32_t)c.ld_hidden * 2;
+  } else if (lay) {
+    l.hidden_rows = p.tpad;
+  }
   const uint32_t nt = p.tpad / 128 * 2;  // of the smaller tiles, in halves of a vocabulary tile
   // a forward that reads the weights in place has nothing to divide but the grid
   uint32_t piece = p.piece;
@@ -1157,12 +1215,15 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
   if (groups) a.parts = p.tiles * (kTileV / (16 * groups));
   for (a.tile0 = 0; a.tile0 < p.tiles; a.tile0 += piece) {
     a.ntiles = p.tiles - a.tile0 < piece ? p.tiles - a.tile0 : piece;
-    if (!direct && (BWD || !groups)) {
+    if (!direct && lay) {
       l.tile0 = a.tile0;
-      l.rows = (uint64_t)a.ntiles * kTileV;
-      layout<T>(l, s);
+      l.weight_rows = (uint64_t)a.ntiles * kTileV;
       a.laid = ws + p.laid;
     }
+    layout<T>(l, hits, s);
+    // once for the call
+    l.hidden_rows = hits.tiles = 0;
+    l.parts = nullptr;
     if (groups) few<T, BWD>(a, groups, s);
     else logits<M, BWD, SEG>(a, s);
     if constexpr (BWD) {
