@@ -686,11 +686,10 @@ template <int T, int NT, int R, bool BWD> __global__ void __launch_bounds__(256)
 // Gradient of the hidden states from one piece of the vocabulary: a tile of S columns
 // by S tokens over the split's share of the piece's rows, into (or, after the first
 // piece, added to) the split's f32 sums.
-template <int T, int S, int NS, int SEG> __global__ void __launch_bounds__(tile_threads(S)) dhidden_k(XentArgs a) {
+template <int T, int S, int NS, int SEG> __device__ __forceinline__ void dhidden_tile(const XentArgs& a, uint32_t id, lds8* lds) {
   typedef Tile<T, true, false, S, NS> Prod;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
   uint32_t mt, nt, split;
-  if (!tile_of(blockIdx.x, (a.kpad + S - 1) / S, a.tpad / S, a.splits, mt, nt, split)) return;
+  if (!tile_of(id, (a.kpad + S - 1) / S, a.tpad / S, a.splits, mt, nt, split)) return;
   const uint32_t t0 = nt * S, c0 = mt * S;
   if (t0 >= a.scalars->count) return;
   const int tid = threadIdx.x;
@@ -732,13 +731,13 @@ template <int T, int S, int NS, int SEG> __global__ void __launch_bounds__(tile_
     if (++k == k1) k = k0, ++seg;
   };
   Prod p;
-  p.run((int)(k1 - k0) * SEG, (lds8*)lds, src);
+  p.run((int)(k1 - k0) * SEG, lds, src);
 
   float* sum = a.sum + (uint64_t)split * a.tpad * a.kpad;
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < Prod::FN; ++j)
-    p.template rows_out<4>((lds8*)lds, j, [](auto) {}, [&](int n, int m, const float (&x)[4]) {
+    p.template rows_out<4>(lds, j, [](auto) {}, [&](int n, int m, const float (&x)[4]) {
       if (c0 + m >= a.kpad) return;
       f32x4* to = reinterpret_cast<f32x4*>(sum + (uint64_t)(t0 + n) * a.kpad + c0 + m);
       f32x4 y = {x[0], x[1], x[2], x[3]};
@@ -753,12 +752,11 @@ template <int T, int S, int NS, int SEG> __global__ void __launch_bounds__(tile_
 
 // Weight gradients of one piece: a tile of S columns by S vocabulary rows over the
 // counted tokens, rounded once.
-template <int T, int OUT, int S, int NS, int SEG> __global__ void __launch_bounds__(tile_threads(S)) dweight_k(XentArgs a) {
+template <int T, int OUT, int S, int NS, int SEG> __device__ __forceinline__ void dweight_tile(const XentArgs& a, uint32_t id, lds8* lds) {
   typedef Tile<T, true, true, S, NS> Prod;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
   uint32_t mt, nt, split;
   constexpr uint32_t per = kTileV / S;  // of a vocabulary tile
-  if (!tile_of(blockIdx.x, (a.kpad + S - 1) / S, a.sub * per, 1, mt, nt, split)) return;
+  if (!tile_of(id, (a.kpad + S - 1) / S, a.sub * per, 1, mt, nt, split)) return;
   nt += a.sub0 * per;
   const uint32_t c0 = mt * S, tile = a.tile0 + nt / per;
   int sh = 0;
@@ -788,7 +786,7 @@ template <int T, int OUT, int S, int NS, int SEG> __global__ void __launch_bound
     if (++k == blocks) k = 0, ++seg;
   };
   Prod p;
-  p.run((int)blocks * SEG, (lds8*)lds, src);
+  p.run((int)blocks * SEG, lds, src);
 
   const float unscale = a.scalars->unscale_dz * (SEG > 1 ? a.scalars->unscale_h : 1.0f);
   constexpr int W = OUT == kF32 ? 4 : 8;
@@ -832,7 +830,7 @@ template <int T, int OUT, int S, int NS, int SEG> __global__ void __launch_bound
       }
     };
     p.template rows_out<W>(
-        (lds8*)lds, j,
+        lds, j,
         [&](auto add) {
           if constexpr (SEG == 1) residues(add);
         },
@@ -847,6 +845,14 @@ template <int T, int OUT, int S, int NS, int SEG> __global__ void __launch_bound
           else store_raw<OUT>(to, (int)(a.cols - c), encode16<OUT>(x));
         });
   }
+}
+
+// Both gradients of a piece: the first `dh_grid` workgroups (none: 0) take tiles of the
+// hidden states', the others of the weights'.
+template <int T, int OUT, int S, int NS, int SEG> __global__ void __launch_bounds__(tile_threads(S)) grads_k(XentArgs a, uint32_t dh_grid) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile<T, true, true, S, NS>::kLds];
+  if (blockIdx.x < dh_grid) dhidden_tile<T, S, NS, SEG>(a, blockIdx.x, (lds8*)lds);
+  else dweight_tile<T, OUT, S, NS, SEG>(a, blockIdx.x - dh_grid, (lds8*)lds);
 }
 
 // ---- joins -------------------------------------------------------------------------
@@ -1011,7 +1017,7 @@ XentPlan xent_plan(uint32_t tokens, uint32_t cols, const size_t* rows, int nrank
     p.hits_first = take((tiles + 1) * 4);
   } else {
     // pairs of a tile and token: at most few_k's, else those of 128 x 128 tiles
-    p.part = take(tiles * (tokens <= 16 ? 16 : t == kF32 ? 8 : 4) * tokens * sizeof(float2));
+    p.part = take(tiles * (tokens <= 64 ? 16 : t == kF32 ? 8 : 4) * tokens * sizeof(float2));
     p.zt = take((uint64_t)tokens * 4);
   }
   p.scalars = take(sizeof(XentScalars));
@@ -1037,25 +1043,30 @@ template <int T> void layout(LayoutArgs l, const HitsArgs& h, hipStream_t s) {
     hipLaunchKernelGGL(layout_k<T>, dim3(grid), dim3(256), 0, s, l, h);
 }
 
-// 16-token groups of a few_k workgroup, 0: logits_k.  16 bits: up to 4 tokens (of 32000 x
-// 4096, 1 / 4 / 8 / 16 tokens: 49 / 50 / 55 / 63 us against 51 for all of them; the
-// hidden states then take as much of the L1s as the weights; unaligned, 50257 x 1023: 60
-// us for 1 and 98 for 16 against 68).  f32: where it takes less than the other way, for
-// which a forward lays out the weights first.  In us: 5 and, for each weight, what its 4
-// bytes take at 4.4 TB/s or the products of 64 tokens at 75 TFLOP/s (64 x 32000 x 4096:
-// 220; 128: 440, against 540); against a stage's time in large_rows() and 14 bytes of
-// each weight moved at 5 TB/s.
-uint32_t few_groups(int t, uint32_t tokens, uint32_t rows, uint32_t tpad, uint32_t kpad, bool backward) {
-  if (t != kF32) return tokens <= 4 ? 1 : 0;
-  // (4 groups load less, 2 fill the CUs: 130 x 3003 x 520)
-  const uint32_t groups = tokens <= 16 ? 1 : tokens <= 32 || rows * 4 * ((tokens + 63) / 64) < 256 ? 2 : 4;
+// 16-token groups of a few_k workgroup, 0: logits_k.  Up to 64 tokens, where it takes less
+// than the other way (times in us):
+// - the other way: the stages' time in large_rows(), and for a forward that lays the
+//   weights out first (f32) 14 bytes of each moved at 5 TB/s;
+// - 16 bits: 5 and all that its workgroups load, 32 rows each, at 9 TB/s, as each 16 tokens
+//   read the weights again from the L2s.  (32000 x 4096, 1 / 4 / 8 / 16 tokens: 49 / 50 /
+//   55 / 63 against 51; 35 x 512 x 2560: 8 against 24.)  Rows that are not aligned take
+//   longer, so that there it is left to up to 4 tokens (50257 x 1023: 60 for 1 and 98 for
+//   16 against 68), which it takes in any case;
+// - f32: 5 and, for each weight, what its 4 bytes take at 4.4 TB/s or the products of 64
+//   tokens at 75 TFLOP/s (64 x 32000 x 4096: 220; 128: 440, against 540).
+uint32_t few_groups(int t, uint32_t tokens, uint32_t rows, uint32_t tpad, uint32_t kpad, bool backward, bool direct) {
+  if (t != kF32 && tokens <= 4) return 1;
+  if (t != kF32 && (tokens > 64 || !direct)) return 0;
+  const uint32_t wg16 = rows * (kTileV / 16) * ((tokens + 15) / 16);
+  // (f32: 4 groups load less, 2 fill the CUs: 130 x 3003 x 520)
+  const uint32_t groups = t != kF32 || tokens <= 16 ? 1 : tokens <= 32 || wg16 < 16 * 256 ? 2 : 4;
   const double weights = (double)rows * kTileV * kpad * 1e-6;  // millions
   const double flops = 2.0 * (double)up(tokens, 16 * groups) / 75.0;
-  const double few = 5 + weights * (flops > 4 / 4.4 ? flops : 4 / 4.4);
-  const uint64_t stages = kpad / kTileK * kSegs, big = rows * (uint64_t)((tpad + 255) / 256), small = 2 * rows * (uint64_t)(tpad / 128);
+  const double few = t == kF32 ? 5 + weights * (flops > 4 / 4.4 ? flops : 4 / 4.4) : 5 + wg16 * (64.0 * kpad) / 9e6;
+  const uint64_t stages = kpad / kTileK * (t == kF32 ? kSegs : 1), big = rows * (uint64_t)((tpad + 255) / 256), small = 2 * rows * (uint64_t)(tpad / 128);
   const uint64_t c256 = (big + 255) / 256 * (143 * stages + 900);
   const uint64_t c128 = small <= 256 ? 75 * stages + 600 : (small + 511) / 512 * (85 * stages + 600);
-  const double other = 0.01 * (double)(c256 < c128 ? c256 : c128) + (backward ? 0 : 8 + weights * 14 / 5);
+  const double other = 0.01 * (double)(c256 < c128 ? c256 : c128) + (backward || t != kF32 ? 0 : 8 + weights * 14 / 5);
   return few < other ? groups : 0;
 }
 
@@ -1087,28 +1098,27 @@ template <int M, bool BWD, int SEG> void logits(XentArgs& a, hipStream_t s) {
   else if (a.sub) logits_of<M, 128, 4, BWD, SEG>(a, s);
   a.part0 += 4 * a.sub;
 }
-template <int M, int S, int NS, int SEG> void dhidden_of(const XentArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((dhidden_k<M, S, NS, SEG>), dim3(tile_grid(tiles_of(a.kpad, a.tpad, S) * a.splits)),
-                     dim3(tile_threads(S)), 0, s, a);
+template <int M, int T, int S, int SEG> void grads_of(const XentArgs& a, bool dh, bool dw, hipStream_t s) {
+  const uint64_t h = dh ? tiles_of(a.kpad, a.tpad, S) * a.splits : 0, w = dw ? tiles_of(a.kpad, a.sub * kTileV, S) : 0;
+  const uint32_t hg = tile_grid(h), grid = hg + tile_grid(w);
+  if (S == 256) hipLaunchKernelGGL((grads_k<M, T, 256, 2, SEG>), dim3(grid), dim3(512), 0, s, a, hg);
+  else if (h + w > 256) hipLaunchKernelGGL((grads_k<M, T, 128, 2, SEG>), dim3(grid), dim3(256), 0, s, a, hg);
+  else hipLaunchKernelGGL((grads_k<M, T, 128, 4, SEG>), dim3(grid), dim3(256), 0, s, a, hg);
 }
-template <int M, int SEG> void dhidden(const XentArgs& a, int tile, hipStream_t s) {
-  if (tile == 256) dhidden_of<M, 256, 2, SEG>(a, s);
-  else if (tiles_of(a.kpad, a.tpad, 128) * a.splits > 256) dhidden_of<M, 128, 2, SEG>(a, s);
-  else dhidden_of<M, 128, 4, SEG>(a, s);
-}
-template <int M, int T, int S, int NS, int SEG> void dweight_of(const XentArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((dweight_k<M, T, S, NS, SEG>), dim3(tile_grid(tiles_of(a.kpad, a.sub * kTileV, S))), dim3(tile_threads(S)),
-                     0, s, a);
-}
-template <int M, int T, int SEG> void dweight(XentArgs& a, hipStream_t s) {
-  const uint32_t large = large_rows(a.ntiles, (a.kpad + 255) / 256, (a.kpad + 127) / 128, a.tpad / kTileK * SEG);
+// The hidden states' tiles go with the weights' of their size where both together are few
+// rounds over the CUs (1001 x 32003 x 1023 f16: 252 to 235 us; 4096 x 128256 x 4096, 9
+// rounds, 9.90 to 9.97 ms), or alone.
+template <int M, int T, int SEG> void grads(XentArgs& a, int dh_tile, bool dh, bool dw, hipStream_t s) {
+  const uint32_t large = dw ? large_rows(a.ntiles, (a.kpad + 255) / 256, (a.kpad + 127) / 128, a.tpad / kTileK * SEG) : 0u;
+  const bool dh256 = dh && dh_tile == 256, dh128 = dh && !dh256;
   a.sub0 = 0;
   a.sub = large;
-  if (a.sub) dweight_of<M, T, 256, 2, SEG>(a, s);
+  const bool apart = dh256 && a.sub && tiles_of(a.kpad, a.tpad, 256) * a.splits + tiles_of(a.kpad, a.sub * kTileV, 256) > 4 * 256;
+  if (apart) grads_of<M, T, 256, SEG>(a, true, false, s);
+  if (dh256 || a.sub) grads_of<M, T, 256, SEG>(a, dh256 && !apart, a.sub != 0, s);
   a.sub0 = large;
-  a.sub = a.ntiles - large;
-  if (a.sub && tiles_of(a.kpad, a.sub * kTileV, 128) > 256) dweight_of<M, T, 128, 2, SEG>(a, s);
-  else if (a.sub) dweight_of<M, T, 128, 4, SEG>(a, s);
+  a.sub = dw ? a.ntiles - large : 0;
+  if (dh128 || a.sub) grads_of<M, T, 128, SEG>(a, dh128, a.sub != 0, s);
 }
 
 // T: type of the caller's tensors.  M: type that multiplies.
@@ -1128,7 +1138,8 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
     if (c.rows[r] && (uintptr_t)c.weights[r] % 16) direct = false;
     if (c.dweights) a.dw[r] = c.dweights[r];
   }
-  const uint32_t groups = few_groups(T, c.tokens, p.tiles, p.tpad, p.kpad, BWD);
+  const bool hidden_direct = T != kF32 && c.cols % kTileK == 0 && c.ld_hidden % 8 == 0 && c.ld_hidden <= (1u << 22) && (uintptr_t)c.hidden % 16 == 0;
+  const uint32_t groups = few_groups(T, c.tokens, p.tiles, p.tpad, p.kpad, BWD, direct && hidden_direct);
   a.ldw = direct ? (uint32_t)c.ld_weight * 2 : p.kpad * 2;
   a.laid_plane = p.laid_plane;
   a.h = ws + p.h;
@@ -1201,7 +1212,7 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
   l.hidden_plane = p.h_plane;
   l.weight_plane = p.laid_plane;
   // a forward reads hidden states in place where it can
-  if (!BWD && T != kF32 && c.cols % kTileK == 0 && c.ld_hidden % 8 == 0 && c.ld_hidden <= (1u << 22) && (uintptr_t)c.hidden % 16 == 0) {
+  if (!BWD && hidden_direct) {
     a.h = (const uint8_t*)c.hidden;
     a.ldh = (uint32_t)c.ld_hidden * 2;
   } else if (lay) {
@@ -1227,9 +1238,8 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
     if (groups) few<T, BWD>(a, groups, s);
     else logits<M, BWD, SEG>(a, s);
     if constexpr (BWD) {
-      if (c.dhidden) dhidden<M, SEG>(a, p.dh_tile, s);
+      grads<M, T, SEG>(a, p.dh_tile, c.dhidden != nullptr, c.dweights != nullptr, s);
       a.add = 1;
-      if (c.dweights) dweight<M, T, SEG>(a, s);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
