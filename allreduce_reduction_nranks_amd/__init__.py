@@ -525,6 +525,14 @@ def mrr_layernorm_bwd(dout, sum, weight, mean, rstd, dresidual, dsum, dweight, d
         _flat_arg(workspace, workspace_bytes, "workspace"), workspace_bytes, _stream(stream))
 
 
+def _shard_bytes(rows, n: int, cols, ld, esize):
+    """_matrix_bytes() of each shard."""
+    if rows is None:
+        return []
+    pitch, last = ld * esize, (cols - ld) * esize
+    return [r * pitch + last if r > 0 and cols > 0 else 0 for r in rows[:n if n > 0 else 0]]
+
+
 def _sizes(rows, n: int):
     if rows is None:
         return None
@@ -543,7 +551,7 @@ def mrr_linear_xent_fwd(hidden, weights, rows, nranks, targets, ignore_index, lo
     t = _dt(dtype)
     e = _ESIZE.get(t, 0)
     sizes = _sizes(rows, nranks)
-    need = [_matrix_bytes(n, cols, ld_weight, e) for n in rows[:max(0, nranks)]] if rows is not None else []
+    need = _shard_bytes(rows, nranks, cols, ld_weight, e)
     return load_library().mrr_linear_xent_fwd(
         _rows_arg(hidden, _matrix_bytes(tokens, cols, ld_hidden, e), "hidden"),
         _rows_args(weights, len(need), need, "weights"), sizes, nranks, _flat_arg(targets, 8 * tokens, "targets"),
@@ -558,7 +566,7 @@ def mrr_linear_xent_bwd(hidden, weights, rows, nranks, targets, ignore_index, ls
     e = _ESIZE.get(t, 0)
     sizes = _sizes(rows, nranks)
     nh = _matrix_bytes(tokens, cols, ld_hidden, e)
-    need = [_matrix_bytes(n, cols, ld_weight, e) for n in rows[:max(0, nranks)]] if rows is not None else []
+    need = _shard_bytes(rows, nranks, cols, ld_weight, e)
     return load_library().mrr_linear_xent_bwd(
         _rows_arg(hidden, nh, "hidden"), _rows_args(weights, len(need), need, "weights"), sizes, nranks,
         _flat_arg(targets, 8 * tokens, "targets"), ignore_index, _flat_arg(lse, 4 * tokens, "lse"),

@@ -1188,8 +1188,8 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
   LayoutArgs l{};
   MostArgs m{};
   if (T == kF32 && lay) {
-    // from 8 KiB a workgroup
-    const uint64_t n = (vocab * c.cols >> 11) + 1;
+    // from 32 KiB a workgroup
+    const uint64_t n = (vocab * c.cols >> 13) + 1;
     m = MostArgs{a.v, c.hidden, BWD ? c.targets : nullptr, c.ignore, (int64_t)vocab, c.ld_weight, c.ld_hidden, c.tokens,
                  (uint32_t*)(ws + p.most), n < kMostParts ? (uint32_t)n : kMostParts, c.cols, 0};
     while (m.units_log2 < 8 && (4u << m.units_log2) < c.cols) ++m.units_log2;
