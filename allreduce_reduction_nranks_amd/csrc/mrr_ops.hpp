@@ -86,7 +86,7 @@ struct XentArgs {
   uint32_t tile0, ntiles;       // the piece
   uint32_t sub0, sub;           // tiles of the piece that a launch takes: from sub0 on, sub of them
   // forward
-  float2* part;                 // max and sum, base 2: logits_k [parts][tokens], few_k [tokens][parts]
+  float2* part;                 // max and sum of exponentials: logits_k [parts][tokens], few_k [tokens][parts]
   float* zt;                    // [tokens]: the target's logit
   const int64_t* targets;
   int64_t ignore;

@@ -345,6 +345,16 @@ __device__ __forceinline__ bool tile_of(uint32_t id, uint32_t mt, uint32_t nt, u
 }
 uint32_t tile_grid(uint64_t tiles) { return (uint32_t)((tiles + 7) / 8 * 8); }
 
+// A pair of a forward: the largest logit z of some rows, and the sum of exp(z' - z) over
+// them.  The terms are exp2(fma(z', log2 e, -base)), base = z log2 e as rounded; what that
+// rounding takes is given back to the sum, so that the pair is as exact as its parts.
+// Rows without a finite logit add nothing (or, with +inf, NaN).
+__device__ __forceinline__ float base_of(float mx) { return mx == -__builtin_inff() ? 0.0f : mx * kLog2e; }
+__device__ __forceinline__ float2 part_of(float mx, float s, float base) {
+  const float lost = mx == -__builtin_inff() ? 0.0f : __builtin_fmaf(mx, kLog2e, -base);
+  return make_float2(mx, s * __builtin_amdgcn_exp2f(-lost));
+}
+
 // dz of a logit.
 template <bool F32> __device__ __forceinline__ float dz_of(float z, const XentToken& tk, bool hit) {
   const float x = z - tk.lse;
@@ -431,16 +441,14 @@ __device__ __forceinline__ void logits_out(const XentArgs& a, Prod& p, lds8* lds
           mx = __builtin_fmaxf(mx, p.acc[i][j][e]);
         }
       mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32));
-      const float top = mx * kLog2e;
-      // a tile without a finite logit adds nothing (or, with +inf, NaN)
-      const float base = mx == -__builtin_inff() ? 0.0f : top;
+      const float base = base_of(mx);
       float s = 0.0f;
 #pragma unroll
       for (int i = 0; i < Prod::FM; ++i)
 #pragma unroll
         for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(p.acc[i][j][e], kLog2e, -base));
       s += __shfl_xor(s, 32);
-      if (lane < 32 && live) a.part[(a.part0 + (uint64_t)part * Prod::WM + wm) * a.tokens + t] = make_float2(top, s);
+      if (lane < 32 && live) a.part[(a.part0 + (uint64_t)part * Prod::WM + wm) * a.tokens + t] = part_of(mx, s, base);
     } else {
 #pragma unroll
       for (int i = 0; i < Prod::FM; ++i)
@@ -472,7 +480,7 @@ __device__ __forceinline__ void logits_out(const XentArgs& a, Prod& p, lds8* lds
 }
 
 // Logits of one tile of S vocabulary rows by S tokens.  Forward: reduced to a
-// (max, sum) pair in base 2 for each wave's rows, and the target's logit.
+// (max, sum) pair for each wave's rows, and the target's logit.
 // Backward: dz, vocabulary contiguous.
 template <int T, int S, int NS, bool BWD, int SEG>
 __global__ void __launch_bounds__(tile_threads(S)) logits_k(XentArgs a) {
@@ -654,7 +662,7 @@ template <int T, int NT, int R, bool BWD> __global__ void __launch_bounds__(256)
       }
     mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16));
     mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32));
-    const float top = mx * kLog2e, base = mx == -__builtin_inff() ? 0.0f : top;
+    const float base = base_of(mx);
     float s = 0.0f;
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -662,7 +670,7 @@ template <int T, int NT, int R, bool BWD> __global__ void __launch_bounds__(256)
       for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(z[r][e], kLog2e, -base));
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
-    if (lane < 16 && t < tokens) a.part[(uint64_t)t * a.parts + (uint64_t)a.tile0 * per + blockIdx.x] = make_float2(top, s);
+    if (lane < 16 && t < tokens) a.part[(uint64_t)t * a.parts + (uint64_t)a.tile0 * per + blockIdx.x] = part_of(mx, s, base);
   } else {
     const XentToken tk = a.token[t];
     const bool live = t < tokens;
@@ -856,14 +864,15 @@ template <int T, int OUT, int S, int NS, int SEG> __global__ void __launch_bound
 }
 
 // ---- joins -------------------------------------------------------------------------
-// lse and loss of JT tokens a workgroup: 1024 / JT chains of pairs, then those in order
+// lse and loss of JT tokens a workgroup (the loss as the largest logit less the target's, 0
+// where they are one, and the log of the sum: a sure token's small loss keeps its digits): 1024 / JT chains of pairs, then those in order
 // (halves first, so that the last steps are few).
 constexpr int kJoinThreads = 1024;
 
 __device__ __forceinline__ float2 join2(float2 a, float2 b) {
   const float top = __builtin_fmaxf(a.x, b.x);
   if (top == -__builtin_inff()) return make_float2(top, a.y + b.y);
-  return make_float2(top, a.y * __builtin_amdgcn_exp2f(a.x - top) + b.y * __builtin_amdgcn_exp2f(b.x - top));
+  return make_float2(top, a.y * __builtin_amdgcn_exp2f((a.x - top) * kLog2e) + b.y * __builtin_amdgcn_exp2f((b.x - top) * kLog2e));
 }
 
 template <int JT> __global__ void __launch_bounds__(kJoinThreads) join_k(XentJoinArgs a) {
@@ -885,11 +894,11 @@ template <int JT> __global__ void __launch_bounds__(kJoinThreads) join_k(XentJoi
   }
   if (chain || t >= a.tokens) return;
   s = lds[threadIdx.x];
-  const float lse = (s.x + __builtin_log2f(s.y)) * kLn2;
-  if (a.lse) a.lse[t] = lse;
+  const float rest = __builtin_log2f(s.y) * kLn2;
+  if (a.lse) a.lse[t] = s.x + rest;
   if (a.loss) {
     const int64_t target = a.targets[t];
-    a.loss[t] = target == a.ignore ? 0.0f : target >= 0 && target < a.vocab ? lse - a.zt[t] : __builtin_nanf("");
+    a.loss[t] = target == a.ignore ? 0.0f : target >= 0 && target < a.vocab ? (s.x - a.zt[t]) + rest : __builtin_nanf("");
   }
 }
 

@@ -426,3 +426,26 @@ def test_another_stream_and_replays_of_a_graph(tokens):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, outs)), k
+
+
+@pytest.mark.parametrize("tokens", [2, 50, 300])
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_the_small_loss_of_a_sure_token_keeps_its_digits(tokens, t):
+    """A target's logit of 25 above all others, which are 0 (rows of zeros): the loss is
+    log(1 + (V - 1) exp(-25)), and only its sum's rounding (2 u of 1, twice for the pieces
+    it is joined from) and log's are between.  lse is off by its own rounding as well."""
+    announce("xent sure", tokens, t)
+    vocab, cols = 3000, 64
+    w = torch.zeros(vocab, cols, dtype=TYPES[t], device="cuda")
+    w[1234, 0] = 5.0
+    h = torch.zeros(tokens, cols, dtype=TYPES[t], device="cuda")
+    h[:, 0] = 5.0
+    targets = torch.full((tokens,), 1234, dtype=torch.int64, device="cuda")
+    loss, lse = torch.empty(tokens, device="cuda"), torch.empty(tokens, device="cuda")
+    n = mrr.mrr_linear_xent_workspace_bytes(tokens, cols, [1000, 2000], 2, t, False)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    mrr.check(mrr.mrr_linear_xent_fwd(h, [w[:1000], w[1000:]], [1000, 2000], 2, targets, IGNORE, loss, lse, tokens, cols, cols,
+                                      cols, t, ws, n))
+    want = float(torch.log1p(2999 * torch.exp(torch.tensor(-25.0, dtype=torch.float64))))
+    assert float((loss.double() - want).abs().max()) <= 4 * U + 2 * U * want
+    assert float((lse.double() - 25 - want).abs().max()) <= 4 * U + U * 26
