@@ -1,5 +1,6 @@
-// mrr_gemm.hpp -- the tile product that the cross entropy kernels share: one
-// workgroup computes D[m][n] = sum over k of A[m][k] B[n][k] for a tile of S m by S n in f32, from 16-bit operands, and hands each wave its part.
+// mrr_gemm.hpp -- the tile product that the cross entropy kernels share: one workgroup
+// computes D[m][n] = sum over k of A[m][k] B[n][k] for a tile of S m by S n in f32, from
+// 16-bit operands, and hands each wave its part.
 //
 // An operand lies in memory either with k contiguous ("row": a row for each m)
 // or with m contiguous ("col": a row for each k).  Both reach LDS by loads that

@@ -1052,8 +1052,8 @@ template <int T> void layout(LayoutArgs l, const HitsArgs& h, hipStream_t s) {
     hipLaunchKernelGGL(layout_k<T>, dim3(grid), dim3(256), 0, s, l, h);
 }
 
-// 16-token groups of a few_k workgroup, 0: logits_k.  Up to 64 tokens, where it takes less
-// than the other way (times in us):
+// 16-token groups of a few_k workgroup, 0: logits_k.  Up to 64 tokens (f32: 4096), where it
+// takes less than the other way (times in us):
 // - the other way: the stages' time in large_rows(), and for a forward that lays the
 //   weights out first (f32) 14 bytes of each moved at 5 TB/s;
 // - 16 bits: 5 and all that its workgroups load, 32 rows each, at 9 TB/s, as each 16 tokens
@@ -1065,8 +1065,8 @@ template <int T> void layout(LayoutArgs l, const HitsArgs& h, hipStream_t s) {
 //   tokens at 75 TFLOP/s (64 x 32000 x 4096: 220; 128: 440, against 540).
 uint32_t few_groups(int t, uint32_t tokens, uint32_t rows, uint32_t tpad, uint32_t kpad, bool backward, bool direct) {
   if (t != kF32 && tokens <= 4) return 1;
-  if (t != kF32 && (tokens > 64 || !direct)) return 0;
-  const uint32_t wg16 = rows * (kTileV / 16) * ((tokens + 15) / 16);
+  if (t != kF32 ? tokens > 64 || !direct : tokens > 4096) return 0;
+  const uint64_t wg16 = rows * (kTileV / 16) * ((tokens + 15) / 16);
   // (f32: 4 groups load less, 2 fill the CUs: 130 x 3003 x 520)
   const uint32_t groups = t != kF32 || tokens <= 16 ? 1 : tokens <= 32 || wg16 < 16 * 256 ? 2 : 4;
   const double weights = (double)rows * kTileV * kpad * 1e-6;  // millions

@@ -484,16 +484,18 @@ mrr_status mrr_layernorm_bwd(const void* dout, const void* sum, const void* weig
  *          computed); it may be any value.  Any other target outside [0, vocabulary)
  *          gives the loss NaN and counts as ignored in the gradient.
  * loss, lse: receive tokens f32 values each; one of them may be NULL.
- * Every sum is f32.  Up to 64 tokens f32 multiplies as f32; above, as sums of
- * products of two f16 parts of each operand (22 bits, to 2^-40 of a tensor's largest
- * value), which is as exact as an f32 product and five times as fast.
+ * The loss of a token that is sure of its target keeps its digits: it is the largest
+ * logit less the target's, plus the log of a sum that is relative to the largest.
+ * Every sum is f32.  f32 calls of few products (up to 4096 tokens; by time) multiply as
+ * f32; others as sums of products of two f16 parts of each operand (22 bits, to 2^-40 of
+ * a tensor's largest value), which is as exact as an f32 product and five times as fast.
  * workspace: device, 16-byte aligned, mrr_linear_xent_workspace_bytes(...,
  * backward 0) bytes at least (else MRR_ESCRATCH), contents irrelevant before and
  * after.  It may not overlap anything else.
  * Pointers are aligned to their element (MRR_EALIGN).  16-bit weights whose shards
  * are 16-byte aligned, with cols a multiple of 64 and ld_weight of 8, are read in
- * place; others, and all f32, are first laid out in the workspace, 256 MiB of the
- * vocabulary at a time.
+ * place, and so are hidden states in the forward; others, and f32 in calls of many
+ * products, are first laid out in the workspace, 256 MiB of the vocabulary at a time.
  * The same call gives the same bits.  tokens == 0 launches nothing.
  * Errors: MRR_EUNSUPPORTED for another type or nranks outside [1, 32];
  * MRR_EINVAL for null pointers, cols 0 or over 2^20, tokens over 2^24, a
