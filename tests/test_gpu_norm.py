@@ -360,3 +360,25 @@ def test_sums_in_the_place_of_inputs_where_rows_end_inside_a_unit(rows, cols, t)
         out = src[(k + 1) % 4]
         mrr.check(forward(src[:3], src[3], None, None, src[k], out, None, None, rows, cols, t, "auto"))
         assert torch.equal(src[k], h) and torch.equal(out, y), k
+
+
+@pytest.mark.parametrize("cols", [700, 8200, 33000])
+def test_rows_four_gigabytes_apart(cols):
+    """All operands are columns of one buffer whose rows are 2^31 elements apart: every
+    offset but the first row's passes 32 bits."""
+    announce("norm far rows", cols)
+    g = seeded(cols)
+    rows, ld = 3, 1 << 31
+    room = torch.empty((rows - 1) * ld + 8 * 33024, dtype=torch.bfloat16, device="cuda")
+    view = [room.as_strided((rows, cols), (ld, 1), 33024 * k) for k in range(8)]
+    for v in view[:3]:
+        v.copy_(randn(g, rows, cols, t="bf16"))
+    mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    weight = randn(g, cols, t="f32", shift=1.0)
+    mrr.check(forward(view[:2], view[2], weight, None, view[3], view[4], mean, rstd, rows, cols, "bf16", "f32", ld, ld))
+    check_forward(view[:2], view[2], weight, None, view[3], view[4], mean, rstd, "bf16", cols)
+    n = mrr.mrr_layernorm_bwd_workspace_bytes(rows, cols)
+    ws, dw, db = torch.empty(n, dtype=torch.uint8, device="cuda"), torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+    mrr.check(mrr.mrr_layernorm_bwd(view[0], view[3], weight, mean, rstd, view[1], view[5], dw, db, rows, cols, ld, ld, "bf16",
+                                    "f32", ws, n))
+    check_backward(view[0], view[3], weight, mean, rstd, view[1], view[5], dw, db, "bf16", "f32", rows, cols)

@@ -449,3 +449,43 @@ def test_the_small_loss_of_a_sure_token_keeps_its_digits(tokens, t):
     want = float(torch.log1p(2999 * torch.exp(torch.tensor(-25.0, dtype=torch.float64))))
     assert float((loss.double() - want).abs().max()) <= 4 * U + 2 * U * want
     assert float((lse.double() - 25 - want).abs().max()) <= 4 * U + U * 26
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("tokens", [3, 6])
+def test_rows_four_gigabytes_apart(tokens, t):
+    """Operands and gradients are columns of one buffer whose rows are 2^31 elements apart."""
+    announce("xent far rows", tokens, t)
+    c = Case(tokens, [5], 72, t, 40)
+    ld = 1 << 31
+    room = torch.empty(5 * ld + 1024, dtype=TYPES[t], device="cuda")
+    view = [room.as_strided((n, 72), (ld, 1), 128 * k) for k, n in enumerate((tokens, 5, tokens, 5))]
+    view[0].copy_(c.hidden)
+    view[1].copy_(c.weights[0])
+    c.hidden, c.weights, c.ld = view[0], [view[1]], ld
+    c.forward()
+    torch.cuda.synchronize()
+    c.check_forward()
+    lse = c.lse.float()
+    c.backward(lse, c.dloss, dhidden=view[2], dweights=[view[3]])
+    torch.cuda.synchronize()
+    c.exact(lse, c.dloss)
+    c.check_backward()
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("tokens,rows,cols", [(5, [700, 3], 192), (17, [512, 300], 640), (40, [100] * 4, 1024), (64, [260], 128),
+                                              (64, [4000], 64), (100, [900, 40], 72), (300, [1000], 65), (1000, [130], 64)])
+def test_both_sides_of_the_rule_for_few_tokens(tokens, rows, cols, t):
+    """The shapes at which the way to the logits changes, hidden states in place and not."""
+    announce("xent few", t, tokens, rows, cols)
+    for pad in (0, 8, 1):
+        c = Case(tokens, rows, cols, t, tokens + cols + pad, pad=pad)
+        c.forward()
+        torch.cuda.synchronize()
+        c.check_forward()
+        lse = c.lse.float()
+        c.backward(lse, c.dloss)
+        torch.cuda.synchronize()
+        c.exact(lse, c.dloss)
+        c.check_backward()
