@@ -358,7 +358,16 @@ __global__ void __launch_bounds__(BT) norm_bwd_k(NormBwdArgs a) {
       }
     }
     if (!DX) continue;
-    s = row_sum<TPR>(s, lds[flip]);  // (with its barrier, dsum may lie in an input's place)
+    // Elements that two lanes store are read by both before either stores: dsum may lie in
+    // the place of any of the three, so they have arrived (are used) by the barrier.
+    if constexpr (AHEAD || TAIL) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        asm volatile("" ::"v"(now.dy[u]), "v"(now.h[u]));
+        if (a.dresidual) asm volatile("" ::"v"(now.res[u]));
+      }
+    }
+    s = row_sum<TPR>(s, lds[flip]);
     const float c1 = s.x * inv, c2 = s.y * inv;
     if (!AHEAD) __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the loads of this turn
 #pragma unroll
@@ -457,6 +466,11 @@ __device__ __forceinline__ void small_rows(const NormBwdArgs& a, float2 (*lds)[k
       g[e] *= w[j];
       if ((uint32_t)j >= over) s.x += g[e], s.y = __builtin_fmaf(g[e], xhat[e], s.y);
     }
+  }
+  // as above: what two lanes store has been read by both
+  if (a.dresidual) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) asm volatile("" ::"v"(res[u]));
   }
   s = row_sum<TPR>(s, lds[0]);
   if (mine >= a.rows) return;

@@ -382,3 +382,24 @@ def test_rows_four_gigabytes_apart(cols):
     mrr.check(mrr.mrr_layernorm_bwd(view[0], view[3], weight, mean, rstd, view[1], view[5], dw, db, rows, cols, ld, ld, "bf16",
                                     "f32", ws, n))
     check_backward(view[0], view[3], weight, mean, rstd, view[1], view[5], dw, db, "bf16", "f32", rows, cols)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(2000, 4104), (2000, 4101), (1500, 9000), (1500, 8201), (3000, 2051), (900, 2051)])
+def test_gradients_in_place_of_rows_whose_last_unit_two_waves_hold(rows, cols, t):
+    announce("norm_bwd in place", t, rows, cols)
+    g = seeded(rows)
+    src = [randn(g, rows, cols, t=t) for _ in range(3)]
+    mean = src[1].float().mean(1)
+    rstd = torch.rsqrt(src[1].float().var(1, unbiased=False) + EPS)
+    n = mrr.mrr_layernorm_bwd_workspace_bytes(rows, cols)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    first = None
+    for place in (None, 0, 1, 2, 2, 2):
+        x = [v.clone() for v in src]
+        dsum = torch.empty_like(x[0]) if place is None else x[place]
+        dw, db = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+        mrr.check(mrr.mrr_layernorm_bwd(x[0], x[1], None, mean, rstd, x[2], dsum, dw, db, rows, cols, cols, cols, t, "f32", ws, n))
+        first = first or (dsum, dw, db)
+        assert all(torch.equal(a, b) for a, b in zip(first, (dsum, dw, db))), place
+    check_backward(src[0], src[1], None, mean, rstd, src[2], *first, t, "f32", rows, cols)
