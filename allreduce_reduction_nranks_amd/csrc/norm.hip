@@ -111,7 +111,8 @@ constexpr int block_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
 
 // ONE: the workgroup has one set of rows, and all it reads is asked for at once (1 x 4096,
 // 8 ranks: 5.6 us a call in a graph, of which 4.5 are a call of any size).  TAIL:
-// rows may end inside a unit; without it, a unit is whole or not there.
+// rows may end inside a unit; without it, a unit is whole or not there.  4096 x 8192 bf16
+// of 4 ranks with residual: 83 us, 5.7 TB/s of the 6.6 that a copy reaches.
 template <int T, int TPR, int E, bool NTL, bool NTS, bool ONE, bool TAIL>
 __global__ void __launch_bounds__(block_threads(TPR)) norm_fwd_k(NormFwdArgs a) {
   constexpr int V = Vec<T>::VW, U = E / V, RPB = block_threads(TPR) / TPR;
@@ -284,7 +285,9 @@ template <int T> __global__ void __launch_bounds__(kWideThreads) norm_fwd_wide_k
 // A workgroup of BT lanes takes BT / TPR rows at a time, every gridDim-th such set; its
 // lanes keep the weight and bias gradients of their columns in registers over all of
 // them.  At the end the workgroup's rows are joined in LDS, in order, and written
-// once: the sums over rows take a fixed order.
+// once: the sums over rows take a fixed order.  16384 x 4096 bf16 with residual: 91 us,
+// 5.9 TB/s, and 4.6 for the join of the 256 workgroups' sums.
+//
 // DX: the gradient of h is wanted.  What is in flight at the end of a turn is known to
 // the compiler (a branch around some of the stores would make it wait for all of them
 // before the next turn's loads: 4 %, and 14 % of a call that loads ahead).
