@@ -279,14 +279,21 @@ static bool same(const Mat& a, const Mat& b) {
   return a.p == b.p && a.rows == b.rows && a.width == b.width && (a.pitch == b.pitch || a.rows < 2);
 }
 
-// An output may be exactly one of the first `in_place` inputs; any other
-// overlap with an input or another output is refused.
-static bool bad_overlap(const Mat* ins, int nin, int in_place, const Mat* outs, int nout) {
+// An output, which may be exactly one of the call's first `in_place` inputs.  Each has its
+// own number: of one row, a vector and a matrix look alike to same().
+struct Out {
+  Mat m;
+  int in_place;
+};
+
+// Any other overlap of an output with an input or another output is refused.
+static bool bad_overlap(const Mat* ins, int nin, const Out* outs, int nout) {
   for (int k = 0; k < nout; ++k) {
+    const Mat& m = outs[k].m;
     for (int i = 0; i < nin; ++i)
-      if (overlaps(outs[k], ins[i]) && !(i < in_place && same(outs[k], ins[i]))) return true;
+      if (overlaps(m, ins[i]) && !(i < outs[k].in_place && same(m, ins[i]))) return true;
     for (int j = 0; j < k; ++j)
-      if (overlaps(outs[k], outs[j])) return true;
+      if (overlaps(m, outs[j].m)) return true;
   }
   return false;
 }
@@ -845,12 +852,12 @@ mrr_status mrr_layernorm_fwd(const void* const* inputs, int nranks, const void* 
   const int in_place = nin;
   ins[nin++] = vec(weight, cols * ew);
   ins[nin++] = vec(bias, cols * ew);
-  const Mat outs[4] = {{sum, rows, cols * e, ld_out * e}, {out, rows, cols * e, ld_out * e},
-                       vec(mean, rows * 4), vec(rstd, rows * 4)};
+  const Out outs[4] = {{{sum, rows, cols * e, ld_out * e}, in_place}, {{out, rows, cols * e, ld_out * e}, in_place},
+                       {vec(mean, rows * 4), 0}, {vec(rstd, rows * 4), 0}};
   if (!aligned(residual, e) || !aligned(sum, e) || !aligned(out, e) || !aligned(weight, ew) ||
       !aligned(bias, ew) || !aligned(mean, 4) || !aligned(rstd, 4))
     return refuse(MRR_EALIGN, fn, "element alignment");
-  if (bad_overlap(ins, nin, in_place, outs, 4)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
+  if (bad_overlap(ins, nin, outs, 4)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
   for (int i = 0; sum && i < in_place; ++i) a.in_place |= ins[i].p == sum;
   a.residual = residual;
   a.weight = weight;
@@ -892,8 +899,8 @@ mrr_status mrr_layernorm_bwd(const void* dout, const void* sum, const void* weig
   const Mat ins[6] = {{dout, x.rows, x.width, x.pitch}, {sum, x.rows, x.width, x.pitch},
                       {dresidual, x.rows, x.width, x.pitch}, vec(weight, cols * ew),
                       vec(mean, rows * 4), vec(rstd, rows * 4)};
-  const Mat outs[4] = {{dsum, rows, cols * e, ld_out * e}, vec(dweight, cols * ew), vec(dbias, cols * ew),
-                       vec(params ? workspace : nullptr, need)};
+  const Out outs[4] = {{{dsum, rows, cols * e, ld_out * e}, 3}, {vec(dweight, cols * ew), 0}, {vec(dbias, cols * ew), 0},
+                       {vec(params ? workspace : nullptr, need), 0}};
   if (!aligned(dout, e) || !aligned(sum, e) || !aligned(dresidual, e) || !aligned(dsum, e) ||
       !aligned(weight, ew) || !aligned(dweight, ew) || !aligned(dbias, ew) || !aligned(mean, 4) ||
       !aligned(rstd, 4))
@@ -903,7 +910,7 @@ mrr_status mrr_layernorm_bwd(const void* dout, const void* sum, const void* weig
     if (!aligned(workspace, 16)) return refuse(MRR_EALIGN, fn, "workspace 16 bytes");
     if (workspace_bytes < need) return refuse(MRR_ESCRATCH, fn, "workspace too small");
   }
-  if (bad_overlap(ins, 6, 3, outs, 4)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
+  if (bad_overlap(ins, 6, outs, 4)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
   NormBwdArgs a{};
   a.dout = dout;
   a.sum = sum;
@@ -989,8 +996,8 @@ mrr_status mrr_linear_xent_fwd(const void* hidden, const void* const* weights, c
                                     workspace, workspace_bytes, need, ins, &nin))
     return st;
   if (!aligned(loss, 4) || !aligned(lse, 4)) return refuse(MRR_EALIGN, fn, "element alignment");
-  const Mat outs[3] = {vec(loss, tokens * 4), vec(lse, tokens * 4), vec(workspace, need)};
-  if (bad_overlap(ins, nin, 0, outs, 3)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
+  const Out outs[3] = {{vec(loss, tokens * 4), 0}, {vec(lse, tokens * 4), 0}, {vec(workspace, need), 0}};
+  if (bad_overlap(ins, nin, outs, 3)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
   XentCall c{};
   c.hidden = hidden;
   c.weights = weights;
@@ -1019,14 +1026,16 @@ mrr_status mrr_linear_xent_bwd(const void* hidden, const void* const* weights, c
   uint64_t vocab;
   if (mrr_status st = xent_shape(fn, rows, nranks, tokens, cols, t, &vocab)) return st;
   const size_t e = tsize(t);
-  Mat outs[kMaxRanks + 2];
+  Out outs[kMaxRanks + 2];
   int nout = 0;
-  outs[nout++] = {dhidden, tokens, cols * e, ld_hidden * e};
+  // the hidden states, first of the inputs, have been read when their gradient is written
+  // (a shard's is written while later pieces of the vocabulary read them)
+  outs[nout++] = {{dhidden, tokens, cols * e, ld_hidden * e}, 1};
   bool wanted = dhidden != nullptr;
   for (int r = 0; dweights && r < nranks; ++r) {
     if (!dweights[r] || !rows[r]) continue;
     if (!aligned(dweights[r], e)) return refuse(MRR_EALIGN, fn, "element alignment");
-    outs[nout++] = {dweights[r], rows[r], cols * e, ld_weight * e};
+    outs[nout++] = {{dweights[r], rows[r], cols * e, ld_weight * e}, 0};
     wanted = true;
   }
   if (!wanted) return refuse(MRR_EINVAL, fn, "no output");
@@ -1036,7 +1045,7 @@ mrr_status mrr_linear_xent_bwd(const void* hidden, const void* const* weights, c
       tokens ? xent_plan((uint32_t)tokens, (uint32_t)cols, rows, nranks, t, true).bytes : 0;
   if (tokens == 0) {
     if (ld_weight < cols || ld_weight > kMaxLd) return refuse(MRR_EINVAL, fn, "row stride out of range");
-    if (bad_overlap(ins, 0, 0, outs, nout)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
+    if (bad_overlap(ins, 0, outs, nout)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
   } else {
     if (mrr_status st = xent_operands(fn, hidden, weights, rows, nranks, targets, tokens, cols, ld_hidden, ld_weight, t,
                                       workspace, workspace_bytes, need, ins, &nin))
@@ -1046,9 +1055,8 @@ mrr_status mrr_linear_xent_bwd(const void* hidden, const void* const* weights, c
     if (!aligned(lse, 4) || !aligned(dloss, 4) || !aligned(dhidden, e)) return refuse(MRR_EALIGN, fn, "element alignment");
     ins[nin++] = vec(lse, tokens * 4);
     ins[nin++] = vec(dloss, ((tokens - 1) * dloss_stride + 1) * 4);
-    outs[nout++] = vec(workspace, need);
-    // the hidden states, first of ins, are copied before anything is written
-    if (bad_overlap(ins, nin, 1, outs, nout)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
+    outs[nout++] = {vec(workspace, need), 0};
+    if (bad_overlap(ins, nin, outs, nout)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
   }
   XentCall c{};
   c.hidden = hidden;
