@@ -429,10 +429,12 @@ def _rows_arg(x, nbytes: int, what: str) -> int:
 
 
 def _spaced_arg(x, nbytes: int, what: str) -> int:
-    """_rows_arg() for single values that a call takes at a stride of its own."""
+    """_rows_arg() for single values that a call takes at a stride of its own.  The span alone
+    counts: an expanded tensor (what autograd hands to a sum's gradient) has fewer bytes than
+    elements."""
     if x is None or isinstance(x, int):
         return x or 0
-    if x.nbytes < nbytes and _span(x) < nbytes:
+    if _span(x) < nbytes:
         raise ValueError("%s spans %d bytes, the call needs %d" % (what, _span(x), nbytes))
     return x.data_ptr()
 
