@@ -66,11 +66,10 @@ struct XentToken {
   int32_t target, pad;
 };
 
-// What the kernels of a call leave for each other.
+// What the kernels of a backward call leave for each other.
 struct XentScalars {
-  uint32_t count;                  // counted tokens
-  float unscale_dz;
-  float w, unscale_w, h, unscale_h;  // f32 operands
+  uint32_t count;    // counted tokens
+  float unscale_dz;  // f16: 1 / the scale of dz
 };
 
 struct XentArgs {
@@ -142,7 +141,7 @@ struct XentCall {
 struct XentPlan {
   uint32_t tpad, kpad, tiles, piece, splits, dh_tile;
   uint64_t h_plane, laid_plane, dz_plane;
-  uint64_t h, laid, dz, sum, token, idx, place, residue, hits, hits_first, scalars, most, part, zt;
+  uint64_t h, laid, dz, sum, token, idx, place, residue, hits, hits_first, scalars, part, zt;
   uint64_t bytes;
 };
 

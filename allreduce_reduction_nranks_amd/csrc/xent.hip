@@ -18,15 +18,17 @@
 // hidden states are gathered first, so nothing in an ignored token's row (not
 // even a NaN) reaches a gradient, and a batch pays for its counted tokens only.
 //
-// f32 operands are split into two f16 parts, x s = x1 + x2 to 22 bits, and a product
-// is x2 y1 + x1 y2 + x1 y1 in f32.  What is left out (x2 y2, and the bits below x2) is
-// at most 3 x 2^-22 of |x y| and on average below an f32 product's rounding, which a sum
-// of 64 such products already exceeds; three f16 products take a fifth of one f32
-// product's time in the matrix units.  s is a power of two for all of a tensor that
-// brings its largest value to 2^15, so an element's error is never above 2^-40 of the
-// largest.  An infinite x stays whole in x1, and the two smaller products read a copy
-// of x1 that has 0 in its place (else infinity would meet the zeros and the signs of
-// the other operand's x2 and give NaN): a row of -inf weights keeps its probability 0.
+// f32 operands are split into three bf16 parts, x = x1 + x2 + x3 exactly (8 bits each, with
+// the signs; from 2^-102 on), and a product is the sum of the 6 products x_i y_j with i + j <= 4 in f32,
+// smallest first.  What is left out is at most 2^-26 of |x y|, a quarter of an f32
+// product's rounding.  bf16 has f32's exponents: no operand is scaled, so that no row's
+// error depends on another row, nor on how a call is multiplied.  (Two f16 parts take three
+// products and two thirds of the laid-out bytes, but hold 22 bits and need one scale for all
+// of a tensor: with one row 10^8 times the others, those are off by 3e-4 of themselves.  1024 x
+// 32000 x 1024 forward: 394 us, 170 TFLOP/s; an f32 product's rate is 75.)  An infinite x stays
+// whole in x1, and the five smaller products read a copy of x1 that has 0 in its place (else
+// infinity would meet the zeros and the signs of the other operand's smaller parts and give
+// NaN): a row of -inf weights keeps its probability 0.
 #include "mrr_gemm.hpp"
 #include "mrr_internal.hpp"
 #include "mrr_ops.hpp"
@@ -36,11 +38,11 @@ namespace mrr {
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-constexpr int kPlanes = 3, kSegs = 3;  // x1, x2, x1 without infinities
+constexpr int kPlanes = 4, kSegs = 6;  // x1, x2, x3, x1 without infinities
 
 // Plane of A and of B in segment s of an f32 product.
-__device__ __forceinline__ uint32_t seg_a(uint32_t s) { return (0x021u >> (4 * s)) & 3u; }
-__device__ __forceinline__ uint32_t seg_b(uint32_t s) { return (0x012u >> (4 * s)) & 3u; }
+__device__ __forceinline__ uint32_t seg_a(uint32_t s) { return (0x031132u >> (4 * s)) & 3u; }
+__device__ __forceinline__ uint32_t seg_b(uint32_t s) { return (0x013123u >> (4 * s)) & 3u; }
 
 // ---- layouts of operands ---------------------------------------------------------
 // A product reads rows of a multiple of 64 elements, 16-byte aligned, zeros past
@@ -52,39 +54,28 @@ struct LayoutArgs {
   uint64_t ld_weight, ld_hidden, hidden_plane, weight_plane;  // bytes between planes
   uint64_t hidden_rows, weight_rows;
   uint8_t *hidden_dst, *weight_dst;
-  XentScalars* scalars;
-  const uint32_t* parts;  // f32: of find_most, 2 grid of them; null: scalars holds the scales
-  uint32_t parts_grid, tokens, cols, kpad, tile0, units_log2;
+  uint32_t tokens, cols, kpad, tile0, units_log2;
   uint32_t hidden_blocks, weight_blocks;  // workgroups of each
 };
 
 __device__ __forceinline__ void split(float x, uint32_t* p) {
   const bool finite = (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u;
-  p[0] = f32_to_f16(x);
-  p[1] = finite ? f32_to_f16(x - f16_to_f32(p[0])) : 0u;
-  p[2] = finite ? p[0] : 0u;
+  p[0] = f32_to_bf16(x);
+  // the largest values round to infinity: cut those off instead
+  if (finite && (p[0] & 0x7F80u) == 0x7F80u) p[0] = __float_as_uint(x) >> 16;
+  const float rest = finite ? x - bf16_to_f32(p[0]) : 0.0f;
+  p[1] = f32_to_bf16(rest);
+  p[2] = f32_to_bf16(rest - bf16_to_f32(p[1]));
+  p[3] = finite ? p[0] : 0u;
 }
 
 // The power of two that brings the largest of values with these bits (of |x|, finite)
-// to at most 2^n, kept where it and its inverse are normal.
-__device__ __forceinline__ float scale_to(uint32_t most, int n) {
+// to at most 2^14, kept where it and its inverse are normal.
+__device__ __forceinline__ float scale_to(uint32_t most) {
   uint32_t e = (most >> 23) + ((most & 0x7FFFFFu) ? 1u : 0u);
   e = e < 32u ? 32u : e > 254u ? 254u : e;
-  return most == 0 ? 1.0f : __uint_as_float((254u + n - e) << 23);
+  return most == 0 ? 1.0f : __uint_as_float((254u + 14u - e) << 23);
 }
-
-// Largest finite |x| of the weights and of the counted tokens' hidden states, as bits
-// (they order as the values do): one part a workgroup, joined by whoever needs the scale.
-constexpr uint32_t kMostParts = 1024;
-struct MostArgs {
-  XentVocab v;
-  const void* src;
-  const int64_t* targets;  // null: every row of src counts
-  int64_t ignore, vocab;
-  uint64_t ld_w, ld_src, src_rows;
-  uint32_t* parts;  // [2][grid]: weights, hidden states
-  uint32_t grid, cols, units_log2;
-};
 
 __device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* lds) {
 #pragma unroll
@@ -100,33 +91,6 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* lds) {
 
 __device__ __forceinline__ bool is_counted(int64_t target, int64_t ignore, int64_t vocab) {
   return target != ignore && target >= 0 && target < vocab;
-}
-
-// Workgroup `id` of the 2 grid.
-__device__ __forceinline__ void find_most(const MostArgs& a, uint32_t id, uint32_t* lds) {
-  const uint32_t lanes = 1u << a.units_log2, per = blockDim.x >> a.units_log2, hidden = id >= a.grid;
-  const uint32_t u0 = threadIdx.x & (lanes - 1), block = hidden ? id - a.grid : id;
-  uint32_t most = 0;
-  auto rows_of = [&](const void* base, uint64_t rows, uint64_t ld) {
-    for (uint64_t row = (uint64_t)block * per + (threadIdx.x >> a.units_log2); row < rows; row += (uint64_t)a.grid * per) {
-      if (hidden && a.targets && !is_counted(a.targets[row], a.ignore, a.vocab)) continue;
-      const uint8_t* p = at<kF32>(base, row * ld);
-#pragma unroll 4
-      for (uint32_t c = 4 * u0; c < a.cols; c += 4 * lanes) {
-        const u32x4 x = load_cols<kF32>(p, c, a.cols);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t u = x[e] & 0x7FFFFFFFu;
-          if (u < 0x7F800000u && u > most) most = u;
-        }
-      }
-    }
-  };
-  if (hidden) rows_of(a.src, a.src_rows, a.ld_src);
-  else
-    for (int r = 0; r < a.v.n; ++r) rows_of(a.v.w[r], a.v.rows[r], a.ld_w);
-  most = block_max(most, lds);
-  if (threadIdx.x == 0) a.parts[id] = most;
 }
 
 // ---- tokens of a backward call ---------------------------------------------------
@@ -150,7 +114,8 @@ struct TokensArgs {
 
 constexpr int kTokensThreads = 1024;
 
-__device__ __forceinline__ void sort_tokens(const TokensArgs& a, uint32_t* sums) {
+__global__ void __launch_bounds__(kTokensThreads) tokens_k(TokensArgs a) {
+  __shared__ uint32_t sums[kTokensThreads / 64];
   const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   float scale = 1.0f;
   if (a.scaled) {
@@ -160,7 +125,7 @@ __device__ __forceinline__ void sort_tokens(const TokensArgs& a, uint32_t* sums)
       const uint32_t u = __float_as_uint(a.dloss[t * a.dloss_stride]) & 0x7FFFFFFFu;
       if (is_counted(target, a.ignore, a.vocab) && u < 0x7F800000u && u > most) most = u;
     }
-    scale = scale_to(block_max(most, sums), 14);
+    scale = scale_to(block_max(most, sums));
     __syncthreads();
   }
   uint32_t before = 0;
@@ -195,18 +160,6 @@ __device__ __forceinline__ void sort_tokens(const TokensArgs& a, uint32_t* sums)
     a.scalars->count = before;
     a.scalars->unscale_dz = 1.0f / scale;
   }
-}
-
-// What a call finds out first: the tokens (its workgroup is the first) and, of f32
-// operands, the largest values.
-__global__ void __launch_bounds__(kTokensThreads) first_k(TokensArgs t, MostArgs m) {
-  __shared__ uint32_t lds[kTokensThreads / 64];
-  uint32_t id = blockIdx.x;
-  if (t.token) {
-    if (id == 0) return sort_tokens(t, lds);
-    --id;
-  }
-  find_most(m, id, lds);
 }
 
 // Counted tokens in the order of their targets' 256-row tiles, tokens of a tile in
@@ -252,7 +205,7 @@ __device__ __forceinline__ void sort_hits(const HitsArgs& a, uint32_t tile, uint
   }
 }
 
-template <int T> __device__ __forceinline__ void lay_row(const LayoutArgs& a, const uint8_t* src, uint8_t* dst, uint64_t plane, float scale, uint32_t u0) {
+template <int T> __device__ __forceinline__ void lay_row(const LayoutArgs& a, const uint8_t* src, uint8_t* dst, uint64_t plane, uint32_t u0) {
   const uint32_t lanes = 1u << a.units_log2, units = a.kpad / 8;
   for (uint32_t u = u0; u < units; u += lanes) {
     uint8_t* d = dst + 16 * (uint64_t)u;
@@ -268,7 +221,7 @@ template <int T> __device__ __forceinline__ void lay_row(const LayoutArgs& a, co
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         uint32_t q[kPlanes];
-        split(x[j] * scale, q);
+        split(x[j], q);
 #pragma unroll
         for (int k = 0; k < kPlanes; ++k) p[k][j] = q[k];
       }
@@ -292,27 +245,10 @@ template <int T> __global__ void __launch_bounds__(256) layout_k(LayoutArgs a, H
   if (!hidden) id -= a.hidden_blocks;
   if (!hidden && id >= a.weight_blocks) return sort_hits(h, id - a.weight_blocks, lds, lds + 4);
   const uint32_t per = 256u >> a.units_log2, sub = threadIdx.x >> a.units_log2, u0 = threadIdx.x & ((1u << a.units_log2) - 1);
-  float scale = 1.0f;
-  if constexpr (T == kF32) {
-    if (a.parts) {
-      uint32_t most = 0;
-      for (uint32_t k = threadIdx.x; k < a.parts_grid; k += 256) {
-        const uint32_t m = a.parts[(hidden ? a.parts_grid : 0) + k];
-        most = m > most ? m : most;
-      }
-      scale = scale_to(block_max(most, lds), 15);
-      if (id == 0 && threadIdx.x == 0) {
-        (hidden ? a.scalars->h : a.scalars->w) = scale;
-        (hidden ? a.scalars->unscale_h : a.scalars->unscale_w) = 1.0f / scale;
-      }
-    } else {
-      scale = hidden ? a.scalars->h : a.scalars->w;
-    }
-  }
   if (hidden) {
     for (uint64_t row = (uint64_t)id * per + sub; row < a.hidden_rows; row += (uint64_t)a.hidden_blocks * per) {
       const int64_t r = a.idx ? (int64_t)a.idx[row] : row < a.tokens ? (int64_t)row : -1;
-      lay_row<T>(a, r >= 0 ? at<T>(a.hidden, (uint64_t)r * a.ld_hidden) : nullptr, a.hidden_dst + row * a.kpad * 2, a.hidden_plane, scale, u0);
+      lay_row<T>(a, r >= 0 ? at<T>(a.hidden, (uint64_t)r * a.ld_hidden) : nullptr, a.hidden_dst + row * a.kpad * 2, a.hidden_plane, u0);
     }
   } else {
     for (uint64_t row = (uint64_t)id * per + sub; row < a.weight_rows; row += (uint64_t)a.weight_blocks * per) {
@@ -320,7 +256,7 @@ template <int T> __global__ void __launch_bounds__(256) layout_k(LayoutArgs a, H
       int sh = 0;
       while (tile >= a.v.first_tile[sh + 1]) ++sh;
       const uint32_t r = (tile - a.v.first_tile[sh]) * kTileV + (uint32_t)(row % kTileV);
-      lay_row<T>(a, r < a.v.rows[sh] ? at<T>(a.v.w[sh], (uint64_t)r * a.ld_weight) : nullptr, a.weight_dst + row * a.kpad * 2, a.weight_plane, scale, u0);
+      lay_row<T>(a, r < a.v.rows[sh] ? at<T>(a.v.w[sh], (uint64_t)r * a.ld_weight) : nullptr, a.weight_dst + row * a.kpad * 2, a.weight_plane, u0);
     }
   }
 }
@@ -364,7 +300,7 @@ template <bool F32> __device__ __forceinline__ float dz_of(float z, const XentTo
 
 // What 16 bits lose of a target's dz, nearly all of most rows' gradient: kept in f32
 // and added to the sums of both gradients, so that the rounding of dz does not show
-// in them.  (An f32 call's dz keeps 22 bits.)
+// in them.  (An f32 call's dz keeps its 24 bits.)
 template <int T> __device__ __forceinline__ float residue_of(float d) {
   const float r = d - to_f32<T>(from_f32<T>(d));
   return (__float_as_uint(r) & 0x7F800000u) != 0x7F800000u ? r : 0.0f;
@@ -394,7 +330,7 @@ template <int T, int N> __device__ __forceinline__ void store_dz(uint8_t* to, ui
 // each logit: what is left is an fma, an exponential (a quarter of the rate) and an
 // add or two.
 template <int T, int S, bool BWD, int SEG, bool FULL, class Prod>
-__device__ __forceinline__ void logits_out(const XentArgs& a, Prod& p, lds8* lds, float unscale, int wm, int wn, int lane,
+__device__ __forceinline__ void logits_out(const XentArgs& a, Prod& p, lds8* lds, int wm, int wn, int lane,
                                            uint32_t mt, uint32_t part, uint32_t t0, uint32_t tokens, uint32_t first,
                                            uint32_t left) {
   const uint32_t m0 = wm * Prod::FM * 32;
@@ -411,12 +347,6 @@ __device__ __forceinline__ void logits_out(const XentArgs& a, Prod& p, lds8* lds
     } else {
       const int64_t target = live ? a.targets[t] : -1;
       if (target >= first && target < (int64_t)first + left) hit = (uint32_t)(target - first) - m0;
-    }
-    if constexpr (SEG > 1) {
-#pragma unroll
-      for (int i = 0; i < Prod::FM; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) p.acc[i][j][e] *= unscale;
     }
     const bool hits = __any(hit < Prod::FM * 32u);
     if constexpr (!BWD) {
@@ -530,12 +460,11 @@ __global__ void __launch_bounds__(tile_threads(S)) logits_k(XentArgs a) {
   };
   Prod p;
   p.run((int)(a.kpad / kTileK) * SEG, (lds8*)lds, src);
-  const float unscale = SEG > 1 ? a.scalars->unscale_w * a.scalars->unscale_h : 1.0f;
 
   const int wm = wave / Prod::WN, wn = wave % Prod::WN;
   const uint32_t first = a.v.first_row[sh] + row0;  // of the whole vocabulary
-  if (left == (uint32_t)S && t0 + S <= tokens) logits_out<T, S, BWD, SEG, true>(a, p, (lds8*)lds, unscale, wm, wn, lane, mt, part, t0, tokens, first, left);
-  else logits_out<T, S, BWD, SEG, false>(a, p, (lds8*)lds, unscale, wm, wn, lane, mt, part, t0, tokens, first, left);
+  if (left == (uint32_t)S && t0 + S <= tokens) logits_out<T, S, BWD, SEG, true>(a, p, (lds8*)lds, wm, wn, lane, mt, part, t0, tokens, first, left);
+  else logits_out<T, S, BWD, SEG, false>(a, p, (lds8*)lds, wm, wn, lane, mt, part, t0, tokens, first, left);
 }
 
 // ---- logits of few tokens ----------------------------------------------------------
@@ -799,7 +728,7 @@ template <int T, int OUT, int S, int NS, int SEG> __device__ __forceinline__ voi
   Prod p;
   p.run((int)blocks * SEG, lds, src);
 
-  const float unscale = a.scalars->unscale_dz * (SEG > 1 ? a.scalars->unscale_h : 1.0f);
+  const float unscale = a.scalars->unscale_dz;
   constexpr int W = OUT == kF32 ? 4 : 8;
   const uint32_t first = a.v.first_row[sh] + row0;
   // tokens whose target may lie in this tile: its list, or of a short call all
@@ -909,7 +838,7 @@ template <int JT> __global__ void __launch_bounds__(kJoinThreads) join_k(XentJoi
 // Gradient rows of the hidden states: the splits' sums in order, rounded once; zeros
 // for a token that has no loss.
 template <int T> __global__ void __launch_bounds__(256) dhidden_join_k(XentArgs a) {
-  const float unscale = a.scalars->unscale_dz * (T == kF32 ? a.scalars->unscale_w : 1.0f);
+  const float unscale = a.scalars->unscale_dz;
   for (uint32_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
     const int32_t from = a.place[t];
     const uint8_t* w = nullptr;  // the target's row
@@ -1034,7 +963,6 @@ XentPlan xent_plan(uint32_t tokens, uint32_t cols, const size_t* rows, int nrank
     p.zt = take((uint64_t)tokens * 4);
   }
   p.scalars = take(sizeof(XentScalars));
-  p.most = take(t == kF32 ? 2 * kMostParts * 4 : 0);
   p.bytes = at;
   return p;
 }
@@ -1059,14 +987,15 @@ template <int T> void layout(LayoutArgs l, const HitsArgs& h, hipStream_t s) {
 // 16-token groups of a few_k workgroup, 0: logits_k.  Up to 64 tokens (f32: 4096), where it
 // takes less than the other way (times in us):
 // - the other way: the stages' time in large_rows(), and for a forward that lays the
-//   weights out first (f32) 14 bytes of each moved at 5 TB/s;
+//   weights out first (f32) 12 bytes of each moved at 5 TB/s;
 // - 16 bits: 5 and all that its workgroups load, 32 rows each, at 9 TB/s, as each 16 tokens
 //   read the weights again from the L2s.  (32000 x 4096, 1 / 4 / 8 / 16 tokens: 49 / 50 /
 //   55 / 63 against 51; 35 x 512 x 2560: 8 against 24.)  Rows that are not aligned take
 //   longer, so that there it is left to up to 4 tokens (50257 x 1023: 60 for 1 and 98 for
 //   16 against 68), which it takes in any case;
 // - f32: 5 and, for each weight, what its 4 bytes take at 4.4 TB/s or the products of 64
-//   tokens at 75 TFLOP/s (64 x 32000 x 4096: 220; 128: 440, against 540).
+//   tokens at 75 TFLOP/s (64 x 32000 x 4096: 222 against 596; 128: 424 against 602; 600 x
+//   3000 x 2048: 98 against 110).
 uint32_t few_groups(int t, uint32_t tokens, uint32_t rows, uint32_t tpad, uint32_t kpad, bool backward, bool direct) {
   if (t != kF32 && tokens <= 4) return 1;
   if (t != kF32 ? tokens > 64 || !direct : tokens > 4096) return 0;
@@ -1079,7 +1008,7 @@ uint32_t few_groups(int t, uint32_t tokens, uint32_t rows, uint32_t tpad, uint32
   const uint64_t stages = kpad / kTileK * (t == kF32 ? kSegs : 1), big = rows * (uint64_t)((tpad + 255) / 256), small = 2 * rows * (uint64_t)(tpad / 128);
   const uint64_t c256 = (big + 255) / 256 * (143 * stages + 900);
   const uint64_t c128 = small <= 256 ? 75 * stages + 600 : (small + 511) / 512 * (85 * stages + 600);
-  const double other = 0.01 * (double)(c256 < c128 ? c256 : c128) + (backward || t != kF32 ? 0 : 8 + weights * 14 / 5);
+  const double other = 0.01 * (double)(c256 < c128 ? c256 : c128) + (backward || t != kF32 ? 0 : 8 + weights * 12 / 5);
   return few < other ? groups : 0;
 }
 
@@ -1136,7 +1065,7 @@ template <int M, int T, int SEG> void grads(XentArgs& a, int dh_tile, bool dh, b
 
 // T: type of the caller's tensors.  M: type that multiplies.
 template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, hipStream_t s) {
-  constexpr int M = T == kF32 ? kF16 : T, SEG = T == kF32 ? kSegs : 1;
+  constexpr int M = T == kF32 ? kBF16 : T, SEG = T == kF32 ? kSegs : 1;
   uint8_t* ws = (uint8_t*)c.workspace;
   XentArgs a{};
   uint64_t vocab = 0;
@@ -1186,7 +1115,7 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
     a.ld_dh = c.ld_hidden;
     a.ld_dw = c.ld_weight;
     tk = TokensArgs{c.targets, c.lse, c.dloss, c.dloss_stride, c.ignore, (int64_t)vocab, (XentToken*)(ws + p.token),
-                    (int32_t*)(ws + p.idx), (int32_t*)(ws + p.place), scalars, c.tokens, p.tpad, T != kBF16};
+                    (int32_t*)(ws + p.idx), (int32_t*)(ws + p.place), scalars, c.tokens, p.tpad, T == kF16};
     // up to 64 tokens a tile's workgroup looks through them all
     if (T != kF32 && c.dweights && c.tokens > 64) {
       a.hits = (uint32_t*)(ws + p.hits);
@@ -1199,20 +1128,8 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
   }
   const bool lay = BWD || !groups;  // few_k reads the operands where they are
   LayoutArgs l{};
-  MostArgs m{};
-  if (T == kF32 && lay) {
-    // from 32 KiB a workgroup
-    const uint64_t n = (vocab * c.cols >> 13) + 1;
-    m = MostArgs{a.v, c.hidden, BWD ? c.targets : nullptr, c.ignore, (int64_t)vocab, c.ld_weight, c.ld_hidden, c.tokens,
-                 (uint32_t*)(ws + p.most), n < kMostParts ? (uint32_t)n : kMostParts, c.cols, 0};
-    while (m.units_log2 < 8 && (4u << m.units_log2) < c.cols) ++m.units_log2;
-    l.parts = m.parts;
-    l.parts_grid = m.grid;
-  }
-  if (const uint32_t grid = (BWD ? 1 : 0) + 2 * m.grid)
-    hipLaunchKernelGGL(first_k, dim3(grid), dim3(kTokensThreads), 0, s, tk, m);
+  if (BWD) hipLaunchKernelGGL(tokens_k, dim3(1), dim3(kTokensThreads), 0, s, tk);
   l.v = a.v;
-  l.scalars = scalars;
   l.hidden = c.hidden;
   l.idx = a.idx;
   l.tokens = c.tokens;
@@ -1247,7 +1164,6 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
     layout<T>(l, hits, s);
     // once for the call
     l.hidden_rows = hits.tiles = 0;
-    l.parts = nullptr;
     if (groups) few<T, BWD>(a, groups, s);
     else logits<M, BWD, SEG>(a, s);
     if constexpr (BWD) {

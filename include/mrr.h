@@ -487,8 +487,9 @@ mrr_status mrr_layernorm_bwd(const void* dout, const void* sum, const void* weig
  * The loss of a token that is sure of its target keeps its digits: it is the largest
  * logit less the target's, plus the log of a sum that is relative to the largest.
  * Every sum is f32.  f32 calls of few products (up to 4096 tokens; by time) multiply as
- * f32; others as sums of products of two f16 parts of each operand (22 bits, to 2^-40 of
- * a tensor's largest value), which is as exact as an f32 product and five times as fast.
+ * f32; others as sums of products of three bf16 parts, which hold an operand exactly.  What
+ * those leave out is 2^-26 of each product, less than an f32 product's rounding, and no
+ * row's error depends on the size of another row.
  * workspace: device, 16-byte aligned, mrr_linear_xent_workspace_bytes(...,
  * backward 0) bytes at least (else MRR_ESCRATCH), contents irrelevant before and
  * after.  It may not overlap anything else.
@@ -518,8 +519,9 @@ mrr_status mrr_linear_xent_fwd(const void* hidden, const void* const* weights, c
  *   dhidden[t][c]  = round( sum over v of dz[t][v] * weight[v][c] )
  *   dweight[v][c]  = round( sum over t of dz[t][v] * hidden[t][c] )
  * The logits are computed again, a piece of the vocabulary at a time; the piece's
- * dz is held in dtype (f16: scaled so that the largest |dloss| is 2^14; f32: so, in
- * two f16 parts), which rounds each dz once; sums are f32.
+ * dz is held in dtype, which rounds each dz once (f32: in three bf16 parts, exactly); sums
+ * are f32.  f16: dz is scaled so that the largest |dloss| is 2^14, and is off by up to 2^-39
+ * of the largest |dloss| as well: a token whose own is below 2^-20 of it loses digits.
  * Ignored tokens are left out: their dhidden is zero and nothing in their rows,
  * NaN included, reaches a gradient.
  *
