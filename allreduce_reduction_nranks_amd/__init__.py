@@ -88,6 +88,7 @@ def load_library() -> ctypes.CDLL:
             "mrr_layernorm_bwd_workspace_bytes": ([sz, sz], sz),
             "mrr_layernorm_bwd": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, sz, sz, sz, i, i, vp, sz, vp], i),
             "mrr_linear_xent_workspace_bytes": ([sz, sz, vp, i, i, i], sz),
+            "mrr_linear_xent_workspace_bytes_in_place": ([sz, sz, vp, i, i, i], sz),
             "mrr_linear_xent_fwd": ([vp, vp, vp, i, vp, i64, vp, vp, sz, sz, sz, sz, i, vp, sz, vp], i),
             "mrr_linear_xent_bwd": ([vp, vp, vp, i, vp, i64, vp, vp, sz, vp, vp, sz, sz, sz, sz, i, vp, sz, vp], i),
             "mrr_stream_copy": ([vp, vp, sz, vp], i),
@@ -546,6 +547,11 @@ def _sizes(rows, n: int):
 def mrr_linear_xent_workspace_bytes(tokens, cols, rows, nranks, dtype, backward) -> int:
     return load_library().mrr_linear_xent_workspace_bytes(tokens, cols, _sizes(rows, nranks), nranks, _dt(dtype),
                                                           1 if backward else 0)
+
+
+def mrr_linear_xent_workspace_bytes_in_place(tokens, cols, rows, nranks, dtype, backward) -> int:
+    return load_library().mrr_linear_xent_workspace_bytes_in_place(tokens, cols, _sizes(rows, nranks), nranks, _dt(dtype),
+                                                                   1 if backward else 0)
 
 
 def mrr_linear_xent_fwd(hidden, weights, rows, nranks, targets, ignore_index, loss, lse, tokens, cols,

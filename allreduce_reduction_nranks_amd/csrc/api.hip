@@ -952,29 +952,37 @@ size_t mrr_linear_xent_workspace_bytes(size_t tokens, size_t cols, const size_t*
   uint64_t vocab;
   if (tokens == 0 || xent_shape("mrr_linear_xent_workspace_bytes", rows, nranks, tokens, cols, dtype, &vocab))
     return 0;
-  return xent_plan((uint32_t)tokens, (uint32_t)cols, rows, nranks, dtype, backward != 0).bytes;
+  return xent_bytes((uint32_t)tokens, (uint32_t)cols, rows, nranks, dtype, backward != 0, false);
 }
 
-// What the two passes share: the operands' checks.
-static mrr_status xent_operands(const char* fn, const void* hidden, const void* const* weights, const size_t* rows,
-                                int nranks, const int64_t* targets, size_t tokens, size_t cols, size_t ld_hidden,
-                                size_t ld_weight, int t, void* workspace, size_t workspace_bytes, size_t need,
+size_t mrr_linear_xent_workspace_bytes_in_place(size_t tokens, size_t cols, const size_t* rows, int nranks,
+                                                mrr_dtype dtype, int backward) {
+  uint64_t vocab;
+  if (tokens == 0 || xent_shape("mrr_linear_xent_workspace_bytes_in_place", rows, nranks, tokens, cols, dtype, &vocab))
+    return 0;
+  return xent_bytes((uint32_t)tokens, (uint32_t)cols, rows, nranks, dtype, backward != 0, true);
+}
+
+// What the two passes share: the operands' checks.  need: bytes of the workspace that the
+// call uses.
+static mrr_status xent_operands(const char* fn, const XentCall& c, int t, bool backward, size_t workspace_bytes, size_t* need,
                                 Mat* ins, int* nin) {
   const size_t e = tsize(t);
-  if (ld_hidden < cols || ld_hidden > kMaxLd || ld_weight < cols || ld_weight > kMaxLd)
+  if (c.ld_hidden < c.cols || c.ld_hidden > kMaxLd || c.ld_weight < c.cols || c.ld_weight > kMaxLd)
     return refuse(MRR_EINVAL, fn, "row stride out of range");
-  if (!hidden || !weights || !targets || !workspace) return refuse(MRR_EINVAL, fn, "null pointer");
-  if (!aligned(hidden, e) || !aligned(targets, 8)) return refuse(MRR_EALIGN, fn, "element alignment");
-  if (!aligned(workspace, 16)) return refuse(MRR_EALIGN, fn, "workspace 16 bytes");
-  if (workspace_bytes < need) return refuse(MRR_ESCRATCH, fn, "workspace too small");
-  ins[(*nin)++] = {hidden, tokens, cols * e, ld_hidden * e};
-  ins[(*nin)++] = vec(targets, tokens * 8);
-  for (int r = 0; r < nranks; ++r) {
-    if (rows[r] == 0) continue;
-    if (!weights[r]) return refuse(MRR_EINVAL, fn, "null weight shard");
-    if (!aligned(weights[r], e)) return refuse(MRR_EALIGN, fn, "element alignment");
-    ins[(*nin)++] = {weights[r], rows[r], cols * e, ld_weight * e};
+  if (!c.hidden || !c.weights || !c.targets || !c.workspace) return refuse(MRR_EINVAL, fn, "null pointer");
+  if (!aligned(c.hidden, e) || !aligned(c.targets, 8)) return refuse(MRR_EALIGN, fn, "element alignment");
+  if (!aligned(c.workspace, 16)) return refuse(MRR_EALIGN, fn, "workspace 16 bytes");
+  ins[(*nin)++] = {c.hidden, c.tokens, c.cols * e, c.ld_hidden * e};
+  ins[(*nin)++] = vec(c.targets, (size_t)c.tokens * 8);
+  for (int r = 0; r < c.nranks; ++r) {
+    if (c.rows[r] == 0) continue;
+    if (!c.weights[r]) return refuse(MRR_EINVAL, fn, "null weight shard");
+    if (!aligned(c.weights[r], e)) return refuse(MRR_EALIGN, fn, "element alignment");
+    ins[(*nin)++] = {c.weights[r], c.rows[r], c.cols * e, c.ld_weight * e};
   }
+  *need = xent_ways(c, xent_plan(c.tokens, c.cols, c.rows, c.nranks, t, backward), t, backward).bytes;
+  if (workspace_bytes < *need) return refuse(MRR_ESCRATCH, fn, "workspace too small");
   return MRR_OK;
 }
 
@@ -989,15 +997,6 @@ mrr_status mrr_linear_xent_fwd(const void* hidden, const void* const* weights, c
   if (mrr_status st = xent_shape(fn, rows, nranks, tokens, cols, t, &vocab)) return st;
   if (tokens == 0) return MRR_OK;
   if (!loss && !lse) return refuse(MRR_EINVAL, fn, "no output");
-  Mat ins[kMaxRanks + 2];
-  int nin = 0;
-  const size_t need = xent_plan((uint32_t)tokens, (uint32_t)cols, rows, nranks, t, false).bytes;
-  if (mrr_status st = xent_operands(fn, hidden, weights, rows, nranks, targets, tokens, cols, ld_hidden, ld_weight, t,
-                                    workspace, workspace_bytes, need, ins, &nin))
-    return st;
-  if (!aligned(loss, 4) || !aligned(lse, 4)) return refuse(MRR_EALIGN, fn, "element alignment");
-  const Out outs[3] = {{vec(loss, tokens * 4), 0}, {vec(lse, tokens * 4), 0}, {vec(workspace, need), 0}};
-  if (bad_overlap(ins, nin, outs, 3)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
   XentCall c{};
   c.hidden = hidden;
   c.weights = weights;
@@ -1012,6 +1011,13 @@ mrr_status mrr_linear_xent_fwd(const void* hidden, const void* const* weights, c
   c.ld_hidden = ld_hidden;
   c.ld_weight = ld_weight;
   c.workspace = workspace;
+  Mat ins[kMaxRanks + 2];
+  int nin = 0;
+  size_t need;
+  if (mrr_status st = xent_operands(fn, c, t, false, workspace_bytes, &need, ins, &nin)) return st;
+  if (!aligned(loss, 4) || !aligned(lse, 4)) return refuse(MRR_EALIGN, fn, "element alignment");
+  const Out outs[3] = {{vec(loss, tokens * 4), 0}, {vec(lse, tokens * 4), 0}, {vec(workspace, need), 0}};
+  if (bad_overlap(ins, nin, outs, 3)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
   return hip_status(launch_xent_fwd(c, t, (hipStream_t)stream), fn);
 }
 
@@ -1039,25 +1045,6 @@ mrr_status mrr_linear_xent_bwd(const void* hidden, const void* const* weights, c
     wanted = true;
   }
   if (!wanted) return refuse(MRR_EINVAL, fn, "no output");
-  Mat ins[kMaxRanks + 4];
-  int nin = 0;
-  const size_t need =
-      tokens ? xent_plan((uint32_t)tokens, (uint32_t)cols, rows, nranks, t, true).bytes : 0;
-  if (tokens == 0) {
-    if (ld_weight < cols || ld_weight > kMaxLd) return refuse(MRR_EINVAL, fn, "row stride out of range");
-    if (bad_overlap(ins, 0, outs, nout)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
-  } else {
-    if (mrr_status st = xent_operands(fn, hidden, weights, rows, nranks, targets, tokens, cols, ld_hidden, ld_weight, t,
-                                      workspace, workspace_bytes, need, ins, &nin))
-      return st;
-    if (!lse || !dloss) return refuse(MRR_EINVAL, fn, "null pointer");
-    if (dloss_stride > kMaxLd) return refuse(MRR_EINVAL, fn, "dloss stride out of range");
-    if (!aligned(lse, 4) || !aligned(dloss, 4) || !aligned(dhidden, e)) return refuse(MRR_EALIGN, fn, "element alignment");
-    ins[nin++] = vec(lse, tokens * 4);
-    ins[nin++] = vec(dloss, ((tokens - 1) * dloss_stride + 1) * 4);
-    outs[nout++] = {vec(workspace, need), 0};
-    if (bad_overlap(ins, nin, outs, nout)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
-  }
   XentCall c{};
   c.hidden = hidden;
   c.weights = weights;
@@ -1075,6 +1062,22 @@ mrr_status mrr_linear_xent_bwd(const void* hidden, const void* const* weights, c
   c.ld_hidden = ld_hidden;
   c.ld_weight = ld_weight;
   c.workspace = workspace;
+  Mat ins[kMaxRanks + 4];
+  int nin = 0;
+  if (tokens == 0) {
+    if (ld_weight < cols || ld_weight > kMaxLd) return refuse(MRR_EINVAL, fn, "row stride out of range");
+    if (bad_overlap(ins, 0, outs, nout)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
+  } else {
+    size_t need;
+    if (mrr_status st = xent_operands(fn, c, t, true, workspace_bytes, &need, ins, &nin)) return st;
+    if (!lse || !dloss) return refuse(MRR_EINVAL, fn, "null pointer");
+    if (dloss_stride > kMaxLd) return refuse(MRR_EINVAL, fn, "dloss stride out of range");
+    if (!aligned(lse, 4) || !aligned(dloss, 4) || !aligned(dhidden, e)) return refuse(MRR_EALIGN, fn, "element alignment");
+    ins[nin++] = vec(lse, tokens * 4);
+    ins[nin++] = vec(dloss, ((tokens - 1) * dloss_stride + 1) * 4);
+    outs[nout++] = {vec(workspace, need), 0};
+    if (bad_overlap(ins, nin, outs, nout)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
+  }
   return hip_status(launch_xent_bwd(c, t, (hipStream_t)stream), fn);
 }
 

@@ -142,10 +142,20 @@ struct XentPlan {
   uint32_t tpad, kpad, tiles, piece, splits, dh_tile;
   uint64_t h_plane, laid_plane, dz_plane;
   uint64_t h, laid, dz, sum, token, idx, place, residue, hits, hits_first, scalars, part, zt;
-  uint64_t bytes;
+  uint64_t bytes_in_place, bytes;  // weights (and a forward's hidden states) read where they are, and laid out
 };
 
 XentPlan xent_plan(uint32_t tokens, uint32_t cols, const size_t* rows, int nranks, int t, bool backward);
+
+// How a call reads its operands.
+struct XentWays {
+  bool direct, hidden_direct;  // weights, hidden states where they are
+  uint32_t groups;             // few_k's 16-token groups, 0: tiles
+  uint64_t bytes;              // of the workspace
+};
+XentWays xent_ways(const XentCall& c, const XentPlan& p, int t, bool backward);
+// Workspace of a call of these sizes: of any operands, or (in_place) of such as are read where they are.
+uint64_t xent_bytes(uint32_t tokens, uint32_t cols, const size_t* rows, int nranks, int t, bool backward, bool in_place);
 hipError_t launch_xent_fwd(const XentCall& c, int t, hipStream_t stream);
 hipError_t launch_xent_bwd(const XentCall& c, int t, hipStream_t stream);
 

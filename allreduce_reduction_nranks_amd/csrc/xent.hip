@@ -939,8 +939,6 @@ XentPlan xent_plan(uint32_t tokens, uint32_t cols, const size_t* rows, int nrank
   };
   p.h_plane = (uint64_t)p.tpad * p.kpad * 2;
   p.laid_plane = (uint64_t)p.piece * kTileV * p.kpad * 2;
-  p.h = take(p.h_plane * planes);
-  p.laid = take(p.laid_plane * planes);
   if (backward) {
     p.dz_plane = (uint64_t)p.tpad * p.piece * kTileV * 2;
     p.dz = take(p.dz_plane * planes);
@@ -963,6 +961,11 @@ XentPlan xent_plan(uint32_t tokens, uint32_t cols, const size_t* rows, int nrank
     p.zt = take((uint64_t)tokens * 4);
   }
   p.scalars = take(sizeof(XentScalars));
+  // last what a call that reads its operands in place does without
+  if (backward) p.h = take(p.h_plane * planes);
+  p.bytes_in_place = at;
+  if (!backward) p.h = take(p.h_plane * planes);
+  p.laid = take(p.laid_plane * planes);
   p.bytes = at;
   return p;
 }
@@ -1011,6 +1014,29 @@ uint32_t few_groups(int t, uint32_t tokens, uint32_t rows, uint32_t tpad, uint32
   const double other = 0.01 * (double)(c256 < c128 ? c256 : c128) + (backward || t != kF32 ? 0 : 8 + weights * 12 / 5);
   return few < other ? groups : 0;
 }
+
+}  // namespace
+
+XentWays xent_ways(const XentCall& c, const XentPlan& p, int t, bool backward) {
+  XentWays w;
+  auto rows16 = [&](size_t ld) { return t != kF32 && c.cols % kTileK == 0 && ld % 8 == 0 && ld <= (1u << 22); };
+  w.direct = rows16(c.ld_weight);
+  for (int r = 0; r < c.nranks; ++r)
+    if (c.rows[r] && (uintptr_t)c.weights[r] % 16) w.direct = false;
+  w.hidden_direct = rows16(c.ld_hidden) && (uintptr_t)c.hidden % 16 == 0;
+  w.groups = few_groups(t, c.tokens, p.tiles, p.tpad, p.kpad, backward, w.direct && w.hidden_direct);
+  // few_k reads its operands where they are, a backward's gradients the weights alone
+  w.bytes = (backward ? w.direct : w.groups || (w.direct && w.hidden_direct)) ? p.bytes_in_place : p.bytes;
+  return w;
+}
+
+uint64_t xent_bytes(uint32_t tokens, uint32_t cols, const size_t* rows, int nranks, int t, bool backward, bool in_place) {
+  const XentPlan p = xent_plan(tokens, cols, rows, nranks, t, backward);
+  const bool can = in_place && t != kF32 && cols % kTileK == 0;
+  return can || (!backward && few_groups(t, tokens, p.tiles, p.tpad, p.kpad, backward, false)) ? p.bytes_in_place : p.bytes;
+}
+
+namespace {
 
 template <int T, bool BWD> void few(const XentArgs& a, uint32_t few, hipStream_t s) {
   const uint32_t tokens = BWD ? (uint32_t)up(a.tokens, kTileK) : a.tokens;
@@ -1069,7 +1095,9 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
   uint8_t* ws = (uint8_t*)c.workspace;
   XentArgs a{};
   uint64_t vocab = 0;
-  bool direct = T != kF32 && c.cols % kTileK == 0 && c.ld_weight % 8 == 0 && c.ld_weight <= (1u << 22);
+  const XentWays ways = xent_ways(c, p, T, BWD);
+  const bool direct = ways.direct, hidden_direct = ways.hidden_direct;
+  const uint32_t groups = ways.groups;
   a.v.n = c.nranks;
   for (int r = 0; r < c.nranks; ++r) {
     a.v.w[r] = c.weights[r];
@@ -1077,11 +1105,8 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
     a.v.first_row[r] = (uint32_t)vocab;
     a.v.first_tile[r + 1] = a.v.first_tile[r] + (uint32_t)(up(c.rows[r], kTileV) / kTileV);
     vocab += c.rows[r];
-    if (c.rows[r] && (uintptr_t)c.weights[r] % 16) direct = false;
     if (c.dweights) a.dw[r] = c.dweights[r];
   }
-  const bool hidden_direct = T != kF32 && c.cols % kTileK == 0 && c.ld_hidden % 8 == 0 && c.ld_hidden <= (1u << 22) && (uintptr_t)c.hidden % 16 == 0;
-  const uint32_t groups = few_groups(T, c.tokens, p.tiles, p.tpad, p.kpad, BWD, direct && hidden_direct);
   a.ldw = direct ? (uint32_t)c.ld_weight * 2 : p.kpad * 2;
   a.laid_plane = p.laid_plane;
   a.h = ws + p.h;

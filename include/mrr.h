@@ -494,9 +494,14 @@ mrr_status mrr_layernorm_bwd(const void* dout, const void* sum, const void* weig
  * backward 0) bytes at least (else MRR_ESCRATCH), contents irrelevant before and
  * after.  It may not overlap anything else.
  * Pointers are aligned to their element (MRR_EALIGN).  16-bit weights whose shards
- * are 16-byte aligned, with cols a multiple of 64 and ld_weight of 8, are read in
- * place, and so are hidden states in the forward; others, and f32 in calls of many
- * products, are first laid out in the workspace, 256 MiB of the vocabulary at a time.
+ * are 16-byte aligned, with cols a multiple of 64 and ld_weight of 8 (and at most
+ * 2^22), are read in place, and so are such hidden states in the forward; a forward of
+ * up to 4 tokens or of few f32 products reads any operands in place.  Others are first
+ * laid out in the workspace: hidden states whole, the vocabulary 256 MiB at a time (up
+ * to 1 GiB where fewer rows would leave compute units idle, 256 rows at least).  Calls
+ * whose weights (in the forward hidden states too) are read in place need only
+ * mrr_linear_xent_workspace_bytes_in_place() bytes, which has no room for them; it
+ * returns the other function's number for sizes that are never read in place.
  * The same call gives the same bits.  tokens == 0 launches nothing.
  * Errors: MRR_EUNSUPPORTED for another type or nranks outside [1, 32];
  * MRR_EINVAL for null pointers, cols 0 or over 2^20, tokens over 2^24, a
@@ -505,6 +510,8 @@ mrr_status mrr_layernorm_bwd(const void* dout, const void* sum, const void* weig
  * ------------------------------------------------------------------------ */
 size_t mrr_linear_xent_workspace_bytes(size_t tokens, size_t cols, const size_t* rows, int nranks,
                                        mrr_dtype dtype, int backward);
+size_t mrr_linear_xent_workspace_bytes_in_place(size_t tokens, size_t cols, const size_t* rows,
+                                                int nranks, mrr_dtype dtype, int backward);
 
 mrr_status mrr_linear_xent_fwd(const void* hidden, const void* const* weights, const size_t* rows,
                                int nranks, const int64_t* targets, int64_t ignore_index,
