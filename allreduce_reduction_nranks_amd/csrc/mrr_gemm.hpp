@@ -94,11 +94,12 @@ __device__ __forceinline__ u32x4 read_col(const lds8* lo, const lds8* hi) {
 
 // 16 bytes a lane from base + off to LDS, lane l's at lds + 16 l.  In assembly
 // because the compiler, given the builtin, waits for the loads in flight before it
-// reads the other stage's buffer; there is no output register, and sync() below
-// waits for them.
+// reads the other stage's buffer; there is no output register, and run() below
+// waits for them.  The LDS address goes in m0, as an operand that the compiler sets; the
+// wait state between the two is the statement's own.
 __device__ __forceinline__ void load_lds(const uint8_t* base, uint32_t off, lds8* lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               :: "s"((uint32_t)(uintptr_t)lds), "v"(off), "s"(base));
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :: "{m0}"((uint32_t)(uintptr_t)lds), "v"(off), "s"(base));
 }
 
 // The product over `steps` stages of 64 k, NS of them in LDS.  src(s, pa, pb, oa, ob) sets
