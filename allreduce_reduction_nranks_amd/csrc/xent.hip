@@ -1002,7 +1002,7 @@ template <int T> void layout(LayoutArgs l, const HitsArgs& h, hipStream_t s) {
 uint32_t few_groups(int t, uint32_t tokens, uint32_t rows, uint32_t tpad, uint32_t kpad, bool backward, bool direct) {
   if (t != kF32 && tokens <= 4) return 1;
   if (t != kF32 ? tokens > 64 || !direct : tokens > 4096) return 0;
-  const uint64_t wg16 = rows * (kTileV / 16) * ((tokens + 15) / 16);
+  const uint64_t wg16 = (uint64_t)rows * (kTileV / 16) * ((tokens + 15) / 16);
   // (f32: 4 groups load less, 2 fill the CUs: 130 x 3003 x 520)
   const uint32_t groups = t != kF32 || tokens <= 16 ? 1 : tokens <= 32 || wg16 < 16 * 256 ? 2 : 4;
   const double weights = (double)rows * kTileV * kpad * 1e-6;  // millions
