@@ -96,8 +96,9 @@ struct XentArgs {
   const XentToken* token;
   const int32_t* place;
   const int32_t* idx;
-  float* residue;               // [tpad]: what rounding took from the target's dz
-  uint32_t* hits;               // counted tokens by their target's tile, null: not sorted
+  uint32_t lo;                  // row of dz that holds what token 0's lost in rounding; 0: none do
+  float* residue;               // [tpad]: lo 0: what rounding took from the target's dz
+  uint32_t* hits;               // counted tokens by their target's tile
   uint32_t* hits_first;         // [tiles + 1]: a tile's first
   float* sum;                   // [splits][tpad][kpad]
   uint32_t splits, add;

@@ -104,11 +104,11 @@ struct TokensArgs {
   const float* dloss;
   uint64_t dloss_stride;
   int64_t ignore, vocab;
-  XentToken* token;  // [tpad]
-  int32_t* idx;      // [tpad]: source row, -1 past the counted ones
+  XentToken* token;  // [tpad], and again from lo on if that is not 0
+  int32_t* idx;      // [tpad]: source row, -1 where there is none; likewise
   int32_t* place;    // [tokens]: place among the counted ones, -1: ignored
   XentScalars* scalars;
-  uint32_t tokens, tpad;
+  uint32_t tokens, tpad, lo;
   int scaled;
 };
 
@@ -145,14 +145,20 @@ __global__ void __launch_bounds__(kTokensThreads) tokens_k(TokensArgs a) {
     }
     at += (uint32_t)__popcll(mask & ((1ull << lane) - 1));
     if (counted) {
-      a.token[at] = {a.lse[t], a.dloss[t * a.dloss_stride] * scale, (int32_t)target, 0};
+      const XentToken tk = {a.lse[t], a.dloss[t * a.dloss_stride] * scale, (int32_t)target, 0};
+      a.token[at] = tk;
       a.idx[at] = (int32_t)t;
+      if (a.lo) {
+        a.token[a.lo + at] = tk;
+        a.idx[a.lo + at] = (int32_t)t;
+      }
     }
     if (t < a.tokens) a.place[t] = counted ? (int32_t)at : -1;
     before += all;
     __syncthreads();
   }
   for (uint32_t t = before + tid; t < a.tpad; t += kTokensThreads) {
+    if (a.lo && t - a.lo < before) continue;
     a.token[t] = {0.0f, 0.0f, -1, 0};
     a.idx[t] = -1;
   }
@@ -298,9 +304,14 @@ template <bool F32> __device__ __forceinline__ float dz_of(float z, const XentTo
   return ((F32 ? __builtin_expf(x) : __builtin_amdgcn_exp2f(x * kLog2e)) - (hit ? 1.0f : 0.0f)) * tk.dl;
 }
 
-// What 16 bits lose of a target's dz, nearly all of most rows' gradient: kept in f32
-// and added to the sums of both gradients, so that the rounding of dz does not show
-// in them.  (An f32 call's dz keeps its 24 bits.)
+// What 16 bits lose of a dz.  Up to 64 tokens it is a second 16-bit part, in a row of its own:
+// a tile of 128 tokens has the place, and past 32 tokens the weights' gradient takes 64 more k
+// (64 x 32000 x 4096 bf16: 176 to 195 us).  Of more tokens only the target's is kept, nearly all of most rows'
+// gradient, in f32, and added to the sums of both gradients.  The others' one rounding is as
+// that of the gradient itself, but takes part in sums over tokens and rows: 4096 x 128256 x
+// 4096 bf16 gradients are 0.00166 off, which is their own rounding; rows that are no token's
+// target 0.0023.  (Two parts there would be five products for three.  An f32 call's dz keeps
+// its 24 bits.)
 template <int T> __device__ __forceinline__ float residue_of(float d) {
   const float r = d - to_f32<T>(from_f32<T>(d));
   return (__float_as_uint(r) & 0x7F800000u) != 0x7F800000u ? r : 0.0f;
@@ -334,10 +345,12 @@ __device__ __forceinline__ void logits_out(const XentArgs& a, Prod& p, lds8* lds
                                            uint32_t mt, uint32_t part, uint32_t t0, uint32_t tokens, uint32_t first,
                                            uint32_t left) {
   const uint32_t m0 = wm * Prod::FM * 32;
+  const uint32_t lo = BWD && S == 128 && SEG == 1 ? a.lo : 0u;  // up to 64 tokens: one tile of 128
 #pragma unroll
   for (int j = 0; j < Prod::FN; ++j) {
     const uint32_t t = t0 + (wn * Prod::FN + j) * 32 + (lane & 31);
-    const bool live = FULL || t < tokens;
+    const bool low = !FULL && lo && t >= lo;
+    const bool live = FULL || (low ? t - lo : t) < tokens;
     // the target's row of the wave's, if it is there
     uint32_t hit = ~0u;
     XentToken tk;
@@ -400,7 +413,13 @@ __device__ __forceinline__ void logits_out(const XentArgs& a, Prod& p, lds8* lds
             d = is ? p.acc[i][j][e] : d;
             mine |= is;
           }
-        if (SEG == 1 && mine) a.residue[t] = residue_of<T>(d);
+        if (SEG == 1 && mine && !lo) a.residue[t] = residue_of<T>(d);
+      }
+      if (SEG == 1 && low) {
+#pragma unroll
+        for (int i = 0; i < Prod::FM; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) p.acc[i][j][e] = residue_of<T>(p.acc[i][j][e]);
       }
       if (j == 0) __syncthreads();
       p.template rows_out<8>(lds, j, [](auto) {}, [&](int n, int m, const float (&d)[8]) {
@@ -495,8 +514,8 @@ template <int T, int NT, int R, bool BWD> __global__ void __launch_bounds__(256)
   __shared__ f32x4v red[4][R * NT][64];
   const uint32_t tokens = BWD ? a.scalars->count : a.tokens;
   const uint32_t t0 = blockIdx.y * (16 * NT);
-  // dz of the last 64 tokens' places past the counted ones is zero
-  if (t0 >= (BWD ? (tokens + kTileK - 1) / kTileK * kTileK : tokens)) return;
+  // dz of the last 64 tokens' places past the counted ones is zero, of those before the low parts too
+  if (t0 >= (!BWD ? tokens : a.lo ? a.lo : (tokens + kTileK - 1) / kTileK * kTileK)) return;
   constexpr uint32_t per = kTileV / (16 * R);
   const uint32_t mt = blockIdx.x / per, tile = a.tile0 + mt, sub = blockIdx.x % per * (16 * R);
   int sh = 0;
@@ -615,10 +634,13 @@ template <int T, int NT, int R, bool BWD> __global__ void __launch_bounds__(256)
       for (int e = 0; e < 4; ++e) {
         const uint32_t m = 16 * r + 4 * (lane >> 4) + e;
         d[e] = live && m < left ? dz_of<T == kF32>(z[r][e], tk, m == hit) : 0.0f;
-        if constexpr (T != kF32)
-          if (m == hit) a.residue[t] = residue_of<T>(d[e]);
       }
       store_dz<T, 4>(row + (16 * r + 4 * (lane >> 4)) * 2, a.dz_plane, d);
+      if constexpr (T != kF32) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[e] = residue_of<T>(d[e]);
+        store_dz<T, 4>(row + (uint64_t)a.lo * a.lddz + (16 * r + 4 * (lane >> 4)) * 2, 0, d);
+      }
     }
   }
 }
@@ -707,7 +729,8 @@ template <int T, int OUT, int S, int NS, int SEG> __device__ __forceinline__ voi
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   uint32_t col = c0 + col_src_chunk<S>(tid) * 8;
   col = (col < a.kpad ? col : a.kpad - 8) * 2;
-  const uint32_t blocks = (a.scalars->count + kTileK - 1) / kTileK;  // of 64 tokens; those past the last have dz 0
+  // of 64 tokens; those past the last have dz 0
+  const uint32_t count = a.scalars->count, blocks = count ? (a.lo + count + kTileK - 1) / kTileK : 0u;
   uint32_t k = 0, seg = 0;
   auto src = [&](int s, const uint8_t*& pa, const uint8_t*& pb, uint32_t (&oa)[Prod::L], uint32_t (&ob)[Prod::L]) {
     if (s == 0) {
@@ -731,15 +754,12 @@ template <int T, int OUT, int S, int NS, int SEG> __device__ __forceinline__ voi
   const float unscale = a.scalars->unscale_dz;
   constexpr int W = OUT == kF32 ? 4 : 8;
   const uint32_t first = a.v.first_row[sh] + row0;
-  // tokens whose target may lie in this tile: its list, or of a short call all
+  // the list of tokens whose target lies in this tile
   uint32_t h0 = 0, h1 = 0;
-  if constexpr (SEG == 1) {
-    h0 = a.hits ? a.hits_first[tile] : 0u;
-    h1 = a.hits ? a.hits_first[tile + 1] : a.scalars->count;
-  }
+  if (SEG == 1 && !a.lo) h0 = a.hits_first[tile], h1 = a.hits_first[tile + 1];
   // a lane's token of the list's k-th 64, and its target's row in the tile
   auto entry = [&](uint32_t k, uint32_t& t) {
-    t = k < h1 ? (a.hits ? a.hits[k] : k) : 0u;
+    t = k < h1 ? a.hits[k] : 0u;
     return k < h1 ? (uint32_t)a.token[t].target - first : ~0u;
   };
   uint32_t t0 = 0, r0 = ~0u;
@@ -844,7 +864,7 @@ template <int T> __global__ void __launch_bounds__(256) dhidden_join_k(XentArgs 
     const uint8_t* w = nullptr;  // the target's row
     float residue = 0.0f;
     if constexpr (T != kF32) {
-      if (from >= 0) {
+      if (from >= 0 && !a.lo) {
         const uint32_t target = (uint32_t)a.token[from].target;
         int sh = 0;
         while (target - a.v.first_row[sh] >= a.v.rows[sh]) ++sh;
@@ -856,15 +876,17 @@ template <int T> __global__ void __launch_bounds__(256) dhidden_join_k(XentArgs 
       float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       if (from >= 0) {
         const float* p = a.sum + (uint64_t)from * a.kpad + c;
+        const uint32_t parts = a.lo ? 2 * a.splits : a.splits;  // the low rows' sums after the others
 #pragma unroll 8
-        for (uint32_t s = 0; s < a.splits; ++s) {
-          const f32x4 y = *reinterpret_cast<const f32x4*>(p + (uint64_t)s * a.tpad * a.kpad);
+        for (uint32_t s = 0; s < parts; ++s) {
+          const uint32_t row = s < a.splits ? s * a.tpad : (s - a.splits) * a.tpad + a.lo;
+          const f32x4 y = *reinterpret_cast<const f32x4*>(p + (uint64_t)row * a.kpad);
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[e] += y[e];
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          if (T != kF32 && c + e < a.cols) x[e] = __builtin_fmaf(residue, load_elem<T>(w, c + e), x[e]);
+          if (T != kF32 && w && c + e < a.cols) x[e] = __builtin_fmaf(residue, load_elem<T>(w, c + e), x[e]);
           x[e] *= unscale;
         }
       }
@@ -1039,7 +1061,7 @@ uint64_t xent_bytes(uint32_t tokens, uint32_t cols, const size_t* rows, int nran
 namespace {
 
 template <int T, bool BWD> void few(const XentArgs& a, uint32_t few, hipStream_t s) {
-  const uint32_t tokens = BWD ? (uint32_t)up(a.tokens, kTileK) : a.tokens;
+  const uint32_t tokens = !BWD ? a.tokens : a.lo ? a.lo : (uint32_t)up(a.tokens, kTileK);
   const dim3 grid(a.ntiles * (kTileV / (16 * few)), (tokens + 16 * few - 1) / (16 * few));
   if (few == 1) hipLaunchKernelGGL((few_k<T, 1, 1, BWD>), grid, dim3(256), 0, s, a);
   if constexpr (T == kF32) {
@@ -1136,13 +1158,13 @@ template <int T, bool BWD> hipError_t run(const XentCall& c, const XentPlan& p, 
     a.place = (int32_t*)(ws + p.place);
     a.idx = (const int32_t*)(ws + p.idx);
     a.residue = (float*)(ws + p.residue);
+    a.lo = T == kF32 || c.tokens > 64 ? 0 : c.tokens > 32 ? 64 : 32;
     a.dhidden = c.dhidden;
     a.ld_dh = c.ld_hidden;
     a.ld_dw = c.ld_weight;
     tk = TokensArgs{c.targets, c.lse, c.dloss, c.dloss_stride, c.ignore, (int64_t)vocab, (XentToken*)(ws + p.token),
-                    (int32_t*)(ws + p.idx), (int32_t*)(ws + p.place), scalars, c.tokens, p.tpad, T == kF16};
-    // up to 64 tokens a tile's workgroup looks through them all
-    if (T != kF32 && c.dweights && c.tokens > 64) {
+                    (int32_t*)(ws + p.idx), (int32_t*)(ws + p.place), scalars, c.tokens, p.tpad, a.lo, T == kF16};
+    if (T != kF32 && c.dweights && !a.lo) {
       a.hits = (uint32_t*)(ws + p.hits);
       a.hits_first = (uint32_t*)(ws + p.hits_first);
       hits = HitsArgs{a.v, a.token, scalars, a.hits, a.hits_first, p.tiles};
