@@ -432,7 +432,10 @@ __device__ __forceinline__ void logits_out(const XentArgs& a, Prod& p, lds8* lds
 // Logits of one tile of S vocabulary rows by S tokens.  Forward: reduced to a
 // (max, sum) pair for each wave's rows, and the target's logit.
 // Backward: dz, vocabulary contiguous.  4096 x 128256 x 4096 bf16 forward: 3.2 ms, 1.34
-// PFLOP/s (a library product of that size 2.96 ms); backward, a quarter of it: 0.82 ms.
+// PFLOP/s (a library product of that size 2.96 ms); backward, a quarter of it for the 3690
+// tokens that count: 0.83 ms, 1.17.  What a tile does besides its products is not hidden (one
+// workgroup of 256 x 256 fills a CU's LDS): the matrix units multiply in 0.81 of the forward's
+// time at 64 stages a tile, in 0.67 at 25.
 template <int T, int S, int NS, bool BWD, int SEG>
 __global__ void __launch_bounds__(tile_threads(S)) logits_k(XentArgs a) {
   typedef Tile<T, false, false, S, NS> Prod;
@@ -808,8 +811,9 @@ template <int T, int OUT, int S, int NS, int SEG> __device__ __forceinline__ voi
 }
 
 // Both gradients of a piece: the first `dh_grid` workgroups (none: 0) take tiles of the
-// hidden states', the others of the weights'.  4096 x 32256 x 4096 bf16: 0.89 and 0.80 ms,
-// 1.21 and 1.36 PFLOP/s; 1001 x 32003 x 1023 f16, both: 135 us.
+// hidden states', the others of the weights'.  3690 counted tokens of 4096 x 32256 x 4096
+// bf16: 0.89 and 0.82 ms, 1.10 and 1.19 PFLOP/s (the matrix units multiply in 0.63 and 0.72 of
+// the time); 901 of 1001 x 32003 x 1023 f16, both: 135 us.
 template <int T, int OUT, int S, int NS, int SEG> __global__ void __launch_bounds__(tile_threads(S)) grads_k(XentArgs a, uint32_t dh_grid) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile<T, true, true, S, NS>::kLds];
   if (blockIdx.x < dh_grid) dhidden_tile<T, S, NS, SEG>(a, blockIdx.x, (lds8*)lds);
