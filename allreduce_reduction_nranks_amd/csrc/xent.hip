@@ -23,7 +23,7 @@
 // smallest first.  What is left out is at most 2^-26 of |x y|, a quarter of an f32
 // product's rounding.  bf16 has f32's exponents: no operand is scaled, so that no row's
 // error depends on another row, nor on how a call is multiplied.  (Two f16 parts take three
-// products and two thirds of the laid-out bytes, but hold 22 bits and need one scale for all
+// products and three quarters of the laid-out bytes, but hold 22 bits and need one scale for all
 // of a tensor: with one row 10^8 times the others, those are off by 3e-4 of themselves.  1024 x
 // 32000 x 1024 forward: 394 us, 170 TFLOP/s; an f32 product's rate is 75.)  An infinite x stays
 // whole in x1, and the five smaller products read a copy of x1 that has 0 in its place (else
@@ -639,7 +639,7 @@ template <int T, int NT, int R, bool BWD> __global__ void __launch_bounds__(256)
         d[e] = live && m < left ? dz_of<T == kF32>(z[r][e], tk, m == hit) : 0.0f;
       }
       store_dz<T, 4>(row + (16 * r + 4 * (lane >> 4)) * 2, a.dz_plane, d);
-      if constexpr (T != kF32) {
+      if constexpr (T != kF32) {  // up to 64 tokens: lo is not 0
 #pragma unroll
         for (int e = 0; e < 4; ++e) d[e] = residue_of<T>(d[e]);
         store_dz<T, 4>(row + (uint64_t)a.lo * a.lddz + (16 * r + 4 * (lane >> 4)) * 2, 0, d);

@@ -487,9 +487,9 @@ mrr_status mrr_layernorm_bwd(const void* dout, const void* sum, const void* weig
  * The loss of a token that is sure of its target keeps its digits: it is the largest
  * logit less the target's, plus the log of a sum that is relative to the largest.
  * Every sum is f32.  f32 calls of few products (up to 4096 tokens; by time) multiply as
- * f32; others as sums of products of three bf16 parts, which hold an operand exactly.  What
- * those leave out is 2^-26 of each product, less than an f32 product's rounding, and no
- * row's error depends on the size of another row.
+ * f32; others as sums of products of three bf16 parts, which hold an operand exactly (from
+ * 2^-102 on).  What those leave out is 2^-26 of each product, less than an f32 product's
+ * rounding, and no row's error depends on the size of another row.
  * workspace: device, 16-byte aligned, mrr_linear_xent_workspace_bytes(...,
  * backward 0) bytes at least (else MRR_ESCRATCH), contents irrelevant before and
  * after.  It may not overlap anything else.
