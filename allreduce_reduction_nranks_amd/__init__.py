@@ -91,6 +91,15 @@ def load_library() -> ctypes.CDLL:
             "mrr_linear_xent_workspace_bytes_in_place": ([sz, sz, vp, i, i, i], sz),
             "mrr_linear_xent_fwd": ([vp, vp, vp, i, vp, i64, vp, vp, sz, sz, sz, sz, i, vp, sz, vp], i),
             "mrr_linear_xent_bwd": ([vp, vp, vp, i, vp, i64, vp, vp, sz, vp, vp, sz, sz, sz, sz, i, vp, sz, vp], i),
+            "mrr_qknorm_rope_fwd": ([vp, i, vp, vp, vp, sz, vp, vp, vp, sz, vp, sz, sz, i, sz, vp, vp, f32, i, i, vp], i),
+            "mrr_qknorm_rope_bwd_workspace_bytes": ([sz, vp, sz], sz),
+            "mrr_qknorm_rope_bwd": ([vp, vp, vp, vp, vp, sz, vp, vp, vp, vp, sz, vp, sz, sz, i, sz, vp, vp, f32, i, i, vp,
+                                     sz, vp], i),
+            "mrr_orthogonalize_workspace_bytes": ([sz, sz, sz, i, i], sz),
+            "mrr_orthogonalize": ([vp, vp, sz, sz, sz, sz, sz, sz, sz, i, vp, f32, i, i, vp, sz, vp], i),
+            "mrr_muon_workspace_bytes": ([sz, sz, sz, i, i, i], sz),
+            "mrr_muon_step": ([vp, i, f32, vp, vp, f32, i, vp, vp, f32, f32, sz, sz, sz, sz, sz, sz, sz, i, vp, f32, i, i,
+                               i, vp, sz, vp], i),
             "mrr_stream_copy": ([vp, vp, sz, vp], i),
             "mrr_rank_buffer_pitch": ([sz, i], sz),
             "mrr_status_string": ([i], ctypes.c_char_p),
@@ -581,6 +590,116 @@ def mrr_linear_xent_bwd(hidden, weights, rows, nranks, targets, ignore_index, ls
         _spaced_arg(dloss, 4 * ((tokens - 1) * dloss_stride + 1) if tokens > 0 else 0, "dloss"), dloss_stride,
         _rows_arg(dhidden, nh, "dhidden"), _rows_args(dweights, len(need), need, "dweights"), tokens, cols, ld_hidden,
         ld_weight, t, _flat_arg(workspace, workspace_bytes, "workspace"), workspace_bytes, _stream(stream))
+
+
+def _three(xs, what: str):
+    """Packed host array of three sizes: of the queries, keys and values."""
+    if xs is None:
+        return None
+    if len(xs) != 3:
+        raise ValueError("%s has %d entries, not 3" % (what, len(xs)))
+    return _pack(xs)
+
+
+def _head_args(xs, tokens, heads, dim, lds, strides, esize, what: str):
+    """Packed addresses of the queries', keys' and values' tensors, each to span what its strides reach."""
+    if xs is None or heads is None or lds is None or strides is None:
+        return None
+    if len(xs) != 3:
+        raise ValueError("%s has %d entries, not 3" % (what, len(xs)))
+    ptrs = []
+    for k, x in enumerate(xs):
+        if x is None or not heads[k]:
+            ptrs.append(0)
+            continue
+        need = ((tokens - 1) * lds[k] + (heads[k] - 1) * strides[k] + dim) * esize if tokens > 0 and dim > 0 else 0
+        ptrs.append(_rows_arg(x, need, "%s[%d]" % (what, k)))
+    return _pack(ptrs)
+
+
+def mrr_qknorm_rope_fwd(inputs, nranks, q_weight, k_weight, table, table_rows, positions, sum, outs, tokens, heads, head_dim,
+                        rot_dim, pairs, ld_in, ld_outs, head_strides, eps, dtype, wdtype="auto", stream=None) -> int:
+    t = _dt(dtype)
+    tw = _wtype(t, wdtype)
+    e, wb = _ESIZE.get(t, 0), head_dim * _ESIZE.get(tw, 0)
+    counts, lds, strides = _three(heads, "heads"), _three(ld_outs, "ld_outs"), _three(head_strides, "head_strides")
+    need = _matrix_bytes(tokens, (heads[0] + heads[1] + heads[2]) * head_dim, ld_in, e) if heads is not None else 0
+    return load_library().mrr_qknorm_rope_fwd(
+        _rows_args(inputs, nranks, need, "inputs"), nranks, _flat_arg(q_weight, wb, "q_weight"),
+        _flat_arg(k_weight, wb, "k_weight"), _flat_arg(table, 4 * table_rows * rot_dim, "table"), table_rows,
+        _flat_arg(positions, 8 * tokens, "positions"), _rows_arg(sum, need, "sum"),
+        _head_args(outs, tokens, heads, head_dim, ld_outs, head_strides, e, "outs"), tokens, counts, head_dim, rot_dim,
+        1 if pairs else 0, ld_in, lds, strides, eps, t, tw, _stream(stream))
+
+
+def mrr_qknorm_rope_bwd_workspace_bytes(tokens, heads, head_dim) -> int:
+    return load_library().mrr_qknorm_rope_bwd_workspace_bytes(tokens, _three(heads, "heads"), head_dim)
+
+
+def mrr_qknorm_rope_bwd(douts, sum, q_weight, k_weight, table, table_rows, positions, dsum, dq_weight, dk_weight, tokens, heads,
+                        head_dim, rot_dim, pairs, ld_in, ld_douts, head_strides, eps, dtype, wdtype="auto", workspace=None,
+                        workspace_bytes=0, stream=None) -> int:
+    t = _dt(dtype)
+    tw = _wtype(t, wdtype)
+    e, wb = _ESIZE.get(t, 0), head_dim * _ESIZE.get(tw, 0)
+    counts, lds, strides = _three(heads, "heads"), _three(ld_douts, "ld_douts"), _three(head_strides, "head_strides")
+    need = _matrix_bytes(tokens, (heads[0] + heads[1] + heads[2]) * head_dim, ld_in, e) if heads is not None else 0
+    return load_library().mrr_qknorm_rope_bwd(
+        _head_args(douts, tokens, heads, head_dim, ld_douts, head_strides, e, "douts"), _rows_arg(sum, need, "sum"),
+        _flat_arg(q_weight, wb, "q_weight"), _flat_arg(k_weight, wb, "k_weight"),
+        _flat_arg(table, 4 * table_rows * rot_dim, "table"), table_rows, _flat_arg(positions, 8 * tokens, "positions"),
+        _rows_arg(dsum, need, "dsum"), _flat_arg(dq_weight, wb, "dq_weight"), _flat_arg(dk_weight, wb, "dk_weight"), tokens,
+        counts, head_dim, rot_dim, 1 if pairs else 0, ld_in, lds, strides, eps, t, tw,
+        _flat_arg(workspace, workspace_bytes, "workspace"), workspace_bytes, _stream(stream))
+
+
+def _batch_bytes(rows, cols, ld, batch, stride, esize) -> int:
+    """Bytes from the first element to the last of `batch` matrices, `stride` elements apart."""
+    return (batch - 1) * stride * esize + _matrix_bytes(rows, cols, ld, esize) if batch > 0 and rows > 0 and cols > 0 else 0
+
+
+def _coefficients(xs, steps):
+    """Host array of three floats a step."""
+    if xs is None:
+        return None
+    if len(xs) < 3 * steps:
+        raise ValueError("coefficients has %d entries, the call needs %d" % (len(xs), 3 * steps))
+    return struct.pack("%df" % len(xs), *xs)
+
+
+def mrr_orthogonalize_workspace_bytes(rows, cols, batch, dtype, products="auto") -> int:
+    return load_library().mrr_orthogonalize_workspace_bytes(rows, cols, batch, _dt(dtype), _dt(products))
+
+
+def mrr_orthogonalize(x, out, rows, cols, ld_in, ld_out, batch, stride_in, stride_out, steps, coefficients, eps, dtype,
+                      products="auto", workspace=None, workspace_bytes=0, stream=None) -> int:
+    t = _dt(dtype)
+    e = _ESIZE.get(t, 0)
+    return load_library().mrr_orthogonalize(
+        _rows_arg(x, _batch_bytes(rows, cols, ld_in, batch, stride_in, e), "x"),
+        _rows_arg(out, _batch_bytes(rows, cols, ld_out, batch, stride_out, e), "out"), rows, cols, ld_in, ld_out, batch, stride_in,
+        stride_out, steps, _coefficients(coefficients, steps), eps, t, _dt(products),
+        _flat_arg(workspace, workspace_bytes, "workspace"), workspace_bytes, _stream(stream))
+
+
+def mrr_muon_workspace_bytes(rows, cols, batch, wdtype, products="auto", nesterov=True) -> int:
+    return load_library().mrr_muon_workspace_bytes(rows, cols, batch, 1 if nesterov else 0, _dt(wdtype), _dt(products))
+
+
+def mrr_muon_step(grads, nranks, grad_scale, momentum, momentum_out, mu, nesterov, weight, weights_out, rate, decay, rows, cols,
+                  ld_grad, ld_weight, batch, stride_grad, stride_weight, steps, coefficients, eps, gdtype, wdtype="auto",
+                  products="auto", workspace=None, workspace_bytes=0, stream=None) -> int:
+    tg = _dt(gdtype)
+    tw = _wtype(tg, wdtype)
+    ng = _batch_bytes(rows, cols, ld_grad, batch, stride_grad, _ESIZE.get(tg, 0))
+    nm = _batch_bytes(rows, cols, ld_weight, batch, stride_weight, 4)
+    nw = nm // 4 * _ESIZE.get(tw, 0)
+    return load_library().mrr_muon_step(
+        _rows_args(grads, nranks, ng, "grads"), nranks, grad_scale, _rows_arg(momentum, nm, "momentum"),
+        _rows_arg(momentum_out, nm, "momentum_out"), mu, 1 if nesterov else 0, _rows_arg(weight, nw, "weight"),
+        _rows_args(weights_out, nranks, nw, "weights_out"), rate, decay, rows, cols, ld_grad, ld_weight, batch, stride_grad,
+        stride_weight, steps, _coefficients(coefficients, steps), eps, tg, tw, _dt(products),
+        _flat_arg(workspace, workspace_bytes, "workspace"), workspace_bytes, _stream(stream))
 
 
 def mrr_stream_copy(src, dst, nbytes, stream=None) -> int:

@@ -2,6 +2,7 @@
 // dispatch to the kernel launchers.  Every check that needs no device runs
 // before any HIP call, so a refused call never touches the GPU.
 #include <atomic>
+#include <math.h>
 #include <mutex>
 #include <stdio.h>
 #include <stdlib.h>
@@ -250,6 +251,12 @@ constexpr size_t kMaxCols = (size_t)1 << 20;
 constexpr size_t kMaxLd = (size_t)1 << 31;
 constexpr size_t kMaxTokens = (size_t)1 << 24;
 constexpr size_t kMaxVocab = (size_t)1 << 30;
+constexpr size_t kMaxHeadDim = 512;
+constexpr size_t kMaxHeads = 65535;
+constexpr size_t kMaxSpan = (size_t)1 << 40;
+constexpr size_t kMaxSide = 65536;  // of a matrix that is made orthogonal
+constexpr size_t kMaxBatch = 65535;
+constexpr int kMaxSteps = 64;
 
 static bool float_type(int t) { return t == kF32 || t == kF16 || t == kBF16; }
 
@@ -307,6 +314,106 @@ static mrr_status norm_shape(const char* fn, size_t rows, size_t cols, size_t ld
   if (rows > kMaxRows) return refuse(MRR_EINVAL, fn, "rows out of range");
   if (ld_in < cols || ld_in > kMaxLd || ld_out < cols || ld_out > kMaxLd)
     return refuse(MRR_EINVAL, fn, "row stride out of range");
+  return MRR_OK;
+}
+
+// Tokens x heads x dim elements of e bytes, `ld` between tokens and `hs` between heads: as a
+// matrix whose rows are the tokens or the heads, whichever are further apart.  False where
+// two elements share a place.
+static bool heads_mat(const void* p, size_t tokens, size_t heads, size_t dim, size_t ld, size_t hs, size_t e, Mat* m) {
+  const size_t across = (heads ? heads - 1 : 0) * hs + dim, along = (tokens ? tokens - 1 : 0) * ld + dim;
+  if ((heads < 2 || hs >= dim) && (tokens < 2 || ld >= across)) {
+    *m = {p, tokens, heads ? across * e : 0, ld * e};
+    return true;
+  }
+  *m = {p, heads, tokens ? along * e : 0, hs * e};
+  return (tokens < 2 || ld >= dim) && (heads < 2 || hs >= along);
+}
+
+// Types and sizes of a head norm call; MRR_OK, or the refusal.
+static mrr_status qk_shape(const char* fn, size_t tokens, const size_t* heads, size_t dim, size_t rot, size_t ld_in,
+                           const float* table, size_t table_rows, const int64_t* positions, float eps, int t, int* tw) {
+  if (*tw == MRR_AUTO) *tw = t;
+  if (!float_type(t) || (*tw != t && *tw != kF32)) return refuse(MRR_EUNSUPPORTED, fn, "type");
+  if (!heads) return refuse(MRR_EINVAL, fn, "null heads");
+  if (dim == 0 || dim > kMaxHeadDim) return refuse(MRR_EINVAL, fn, "head_dim out of range");
+  if (rot > dim || rot % 2) return refuse(MRR_EINVAL, fn, "rot_dim odd or over head_dim");
+  if (heads[0] > kMaxHeads || heads[1] > kMaxHeads || heads[2] > kMaxHeads) return refuse(MRR_EINVAL, fn, "heads out of range");
+  if (heads[0] + heads[1] + heads[2] == 0) return refuse(MRR_EINVAL, fn, "no heads");
+  if (tokens > kMaxRows) return refuse(MRR_EINVAL, fn, "tokens out of range");
+  if (ld_in < (heads[0] + heads[1] + heads[2]) * dim || ld_in > kMaxLd) return refuse(MRR_EINVAL, fn, "row stride out of range");
+  if (!(eps >= 0.0f)) return refuse(MRR_EINVAL, fn, "eps");
+  if (rot && tokens) {
+    if (!table) return refuse(MRR_EINVAL, fn, "null table");
+    if (table_rows > kMaxLd || table_rows == 0) return refuse(MRR_EINVAL, fn, "table_rows out of range");
+    if (!positions && tokens > table_rows) return refuse(MRR_EINVAL, fn, "more tokens than rows of the table");
+  }
+  if (!aligned(table, 4) || !aligned(positions, 8)) return refuse(MRR_EALIGN, fn, "element alignment");
+  return MRR_OK;
+}
+
+// Strides of a head norm call's three tensors, and what each spans.
+static mrr_status qk_heads(const char* fn, void* const* outs, const size_t* lds, const size_t* strides, size_t tokens,
+                           const size_t* heads, size_t dim, size_t e, QkArgs* a, Mat* mats) {
+  if (!outs || !lds || !strides) return refuse(MRR_EINVAL, fn, "null array");
+  for (int k = 0; k < 3; ++k) {
+    a->heads[k] = (uint32_t)heads[k];
+    if (!heads[k] || !outs[k]) {
+      mats[k] = vec(nullptr, 0);
+      continue;
+    }
+    if (lds[k] > kMaxLd || strides[k] > kMaxSpan) return refuse(MRR_EINVAL, fn, "stride out of range");
+    if (!aligned(outs[k], e)) return refuse(MRR_EALIGN, fn, "element alignment");
+    if (!heads_mat(outs[k], tokens, heads[k], dim, lds[k], strides[k], e, &mats[k]))
+      return refuse(MRR_EINVAL, fn, "strides put two elements in one place");
+    a->out[k] = outs[k];
+    a->ld_out[k] = lds[k];
+    a->hs_out[k] = strides[k];
+  }
+  return MRR_OK;
+}
+
+// `batch` matrices of rows x cols elements of e bytes, rows ld and matrices `stride`
+// elements apart.  False where two of their elements share a place.
+static bool batch_mat(const void* p, size_t rows, size_t cols, size_t ld, size_t batch, size_t stride, size_t e, Mat* m) {
+  const size_t span = (rows - 1) * ld + cols;
+  if (batch < 2) {
+    *m = {p, rows, cols * e, ld * e};
+    return true;
+  }
+  if (stride >= span) {
+    *m = {p, batch, span * e, stride * e};
+    return true;
+  }
+  const size_t across = (batch - 1) * stride + cols;
+  const bool fits = stride >= cols && (rows < 2 || ld >= across);
+  *m = fits ? Mat{p, rows, across * e, ld * e} : vec(p, ((batch - 1) * stride + span) * e);
+  return fits;
+}
+
+static const float kCoefficients[3] = {3.4445f, -4.7750f, 2.0315f};
+
+// Sizes, types and coefficients of a call of Newton-Schulz products; *parts: of its operands.
+static mrr_status ns_shape(const char* fn, size_t rows, size_t cols, size_t batch, int t, int products, int* parts) {
+  if (!float_type(t)) return refuse(MRR_EUNSUPPORTED, fn, "type");
+  if (products != MRR_AUTO && products != kF16 && products != kF32) return refuse(MRR_EUNSUPPORTED, fn, "products");
+  if (rows == 0 || cols == 0 || rows > kMaxSide || cols > kMaxSide) return refuse(MRR_EINVAL, fn, "rows or cols out of range");
+  if (batch > kMaxBatch) return refuse(MRR_EINVAL, fn, "batch out of range");
+  // the products of matrices with a short side cost little beside their launches, and one
+  // rounding counts for more in them (16 x 16: off by 2e-3 in one part)
+  const bool small = rows <= 64 || cols <= 64;
+  *parts = products == kF32 || (products == MRR_AUTO && t != kBF16) || small ? 2 : 1;
+  return MRR_OK;
+}
+
+static mrr_status ns_steps(const char* fn, int steps, const float** coefficients, float* own, float eps) {
+  if (steps < 1 || steps > kMaxSteps) return refuse(MRR_EINVAL, fn, "steps out of range");
+  if (!(eps >= 0.0f) || !(eps < INFINITY)) return refuse(MRR_EINVAL, fn, "eps");
+  if (!*coefficients) {
+    for (int k = 0; k < 3 * steps; ++k) own[k] = kCoefficients[k % 3];
+    *coefficients = own;
+  }
+  if (!ns_bounds(*coefficients, steps)) return refuse(MRR_EINVAL, fn, "coefficients let singular values grow too large");
   return MRR_OK;
 }
 }  // namespace mrr
@@ -1079,6 +1186,263 @@ mrr_status mrr_linear_xent_bwd(const void* hidden, const void* const* weights, c
     if (bad_overlap(ins, nin, outs, nout)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
   }
   return hip_status(launch_xent_bwd(c, t, (hipStream_t)stream), fn);
+}
+
+mrr_status mrr_qknorm_rope_fwd(const void* const* inputs, int nranks, const void* q_weight, const void* k_weight,
+                               const float* table, size_t table_rows, const int64_t* positions, void* sum,
+                               void* const* outs, size_t tokens, const size_t* heads, size_t head_dim, size_t rot_dim,
+                               int pairs, size_t ld_in, const size_t* ld_outs, const size_t* head_strides, float eps,
+                               mrr_dtype dtype, mrr_dtype wdtype, void* stream) {
+  static const char* fn = "mrr_qknorm_rope_fwd";
+  const int t = dtype;
+  int tw = wdtype;
+  if (nranks < 1 || nranks > kMaxRanks) return refuse(MRR_EUNSUPPORTED, fn, "nranks out of range");
+  if (mrr_status st = qk_shape(fn, tokens, heads, head_dim, rot_dim, ld_in, table, table_rows, positions, eps, t, &tw)) return st;
+  if (tokens == 0) return MRR_OK;
+  if (!inputs) return refuse(MRR_EINVAL, fn, "null pointer");
+  const size_t e = tsize(t), ew = tsize(tw), width = (heads[0] + heads[1] + heads[2]) * head_dim;
+  QkArgs a{};
+  Mat mats[3];
+  if (mrr_status st = qk_heads(fn, outs, ld_outs, head_strides, tokens, heads, head_dim, e, &a, mats)) return st;
+  if (!a.out[0] && !a.out[1] && !a.out[2] && !sum) return refuse(MRR_EINVAL, fn, "no output");
+  Mat ins[kMaxRanks + 4];
+  int nin = 0;
+  for (int r = 0; r < nranks; ++r) {
+    if (!inputs[r]) return refuse(MRR_EINVAL, fn, "null rank pointer");
+    if (!aligned(inputs[r], e)) return refuse(MRR_EALIGN, fn, "element alignment");
+    a.in[r] = inputs[r];
+    ins[nin++] = {inputs[r], tokens, width * e, ld_in * e};
+  }
+  const int in_place = nin;
+  ins[nin++] = vec(q_weight, head_dim * ew);
+  ins[nin++] = vec(k_weight, head_dim * ew);
+  ins[nin++] = vec(table, rot_dim ? table_rows * rot_dim * 4 : 0);
+  ins[nin++] = vec(positions, tokens * 8);
+  if (!aligned(sum, e) || !aligned(q_weight, ew) || !aligned(k_weight, ew)) return refuse(MRR_EALIGN, fn, "element alignment");
+  const Mat total{sum, tokens, width * e, ld_in * e};
+  const Out all[1] = {{total, in_place}};
+  if (bad_overlap(ins, nin, all, 1)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
+  // queries, keys and values may each take the place of theirs in an input
+  size_t first = 0;
+  for (int k = 0; k < 3; ++k) {
+    Mat own[kMaxRanks + 4];
+    for (int i = 0; i < nin; ++i) own[i] = ins[i];
+    const Out out[1] = {{mats[k], in_place}};
+    for (int r = 0; r < in_place; ++r) {
+      const Mat part{(const uint8_t*)inputs[r] + first * e, tokens, heads[k] * head_dim * e, ld_in * e};
+      if (same(mats[k], part) && (heads[k] < 2 || head_strides[k] == head_dim)) own[r] = part;
+    }
+    if (bad_overlap(own, nin, out, 1) || overlaps(mats[k], total)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
+    for (int j = 0; j < k; ++j)
+      if (overlaps(mats[k], mats[j])) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
+    first += heads[k] * head_dim;
+  }
+  a.sum = sum;
+  a.w[0] = q_weight;
+  a.w[1] = k_weight;
+  a.table = table;
+  a.positions = positions;
+  a.tokens = tokens;
+  a.ld_in = ld_in;
+  a.table_rows = table_rows;
+  a.dim = (uint32_t)head_dim;
+  a.rot = (uint32_t)rot_dim;
+  a.nranks = nranks;
+  a.pairs = pairs != 0;
+  a.wf32 = tw == kF32;
+  a.eps = eps;
+  a.skip_values = !a.out[2] && !sum;
+  return hip_status(launch_qk_fwd(a, t, (hipStream_t)stream), fn);
+}
+
+size_t mrr_qknorm_rope_bwd_workspace_bytes(size_t tokens, const size_t* heads, size_t head_dim) {
+  if (!heads || head_dim == 0 || head_dim > kMaxHeadDim || tokens > kMaxRows) return 0;
+  return (size_t)qk_bwd_groups() * 2 * head_dim * sizeof(float);
+}
+
+mrr_status mrr_qknorm_rope_bwd(const void* const* douts, const void* sum, const void* q_weight, const void* k_weight,
+                               const float* table, size_t table_rows, const int64_t* positions, void* dsum,
+                               void* dq_weight, void* dk_weight, size_t tokens, const size_t* heads, size_t head_dim,
+                               size_t rot_dim, int pairs, size_t ld_in, const size_t* ld_douts,
+                               const size_t* head_strides, float eps, mrr_dtype dtype, mrr_dtype wdtype,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  static const char* fn = "mrr_qknorm_rope_bwd";
+  const int t = dtype;
+  int tw = wdtype;
+  if (mrr_status st = qk_shape(fn, tokens, heads, head_dim, rot_dim, ld_in, table, table_rows, positions, eps, t, &tw)) return st;
+  const bool params = dq_weight || dk_weight;
+  if (!dsum && !params) return refuse(MRR_EINVAL, fn, "no output");
+  if (tokens == 0 && !params) return MRR_OK;
+  const size_t e = tsize(t), ew = tsize(tw), width = (heads[0] + heads[1] + heads[2]) * head_dim;
+  const size_t need = mrr_qknorm_rope_bwd_workspace_bytes(tokens, heads, head_dim);
+  QkArgs a{};
+  Mat mats[3];
+  if (mrr_status st = qk_heads(fn, (void* const*)douts, ld_douts, head_strides, tokens, heads, head_dim, e, &a, mats)) return st;
+  if (tokens && !sum) return refuse(MRR_EINVAL, fn, "null pointer");
+  if (!aligned(sum, e) || !aligned(dsum, e) || !aligned(q_weight, ew) || !aligned(k_weight, ew) || !aligned(dq_weight, ew) ||
+      !aligned(dk_weight, ew))
+    return refuse(MRR_EALIGN, fn, "element alignment");
+  if (params) {
+    if (!workspace) return refuse(MRR_EINVAL, fn, "null workspace");
+    if (!aligned(workspace, 16)) return refuse(MRR_EALIGN, fn, "workspace 16 bytes");
+    if (workspace_bytes < need) return refuse(MRR_ESCRATCH, fn, "workspace too small");
+  }
+  const Mat ins[8] = {{sum, tokens, width * e, ld_in * e}, mats[0], mats[1], mats[2], vec(q_weight, head_dim * ew),
+                      vec(k_weight, head_dim * ew), vec(table, rot_dim ? table_rows * rot_dim * 4 : 0), vec(positions, tokens * 8)};
+  const Out outs[4] = {{{dsum, tokens, width * e, ld_in * e}, 1}, {vec(dq_weight, head_dim * ew), 0},
+                       {vec(dk_weight, head_dim * ew), 0}, {vec(params ? workspace : nullptr, need), 0}};
+  if (bad_overlap(ins, 8, outs, 4)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
+  a.h = sum;
+  a.dsum = dsum;
+  a.w[0] = q_weight;
+  a.w[1] = k_weight;
+  a.dw[0] = dq_weight;
+  a.dw[1] = dk_weight;
+  a.partial = params ? (float*)workspace : nullptr;
+  a.table = table;
+  a.positions = positions;
+  a.tokens = tokens;
+  a.ld_in = ld_in;
+  a.table_rows = table_rows;
+  a.dim = (uint32_t)head_dim;
+  a.rot = (uint32_t)rot_dim;
+  a.pairs = pairs != 0;
+  a.wf32 = tw == kF32;
+  a.eps = eps;
+  a.skip_values = !dsum;
+  return hip_status(launch_qk_bwd(a, t, (hipStream_t)stream), fn);
+}
+
+size_t mrr_orthogonalize_workspace_bytes(size_t rows, size_t cols, size_t batch, mrr_dtype dtype, mrr_dtype products) {
+  int parts;
+  if (batch == 0 || ns_shape("mrr_orthogonalize_workspace_bytes", rows, cols, batch, dtype, products, &parts)) return 0;
+  return ns_plan(rows, cols, batch, parts, false).bytes;
+}
+
+mrr_status mrr_orthogonalize(const void* in, void* out, size_t rows, size_t cols, size_t ld_in, size_t ld_out,
+                             size_t batch, size_t stride_in, size_t stride_out, int steps, const float* coefficients,
+                             float eps, mrr_dtype dtype, mrr_dtype products, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  static const char* fn = "mrr_orthogonalize";
+  const int t = dtype;
+  int parts;
+  float own[3 * kMaxSteps];
+  if (mrr_status st = ns_shape(fn, rows, cols, batch, t, products, &parts)) return st;
+  if (mrr_status st = ns_steps(fn, steps, &coefficients, own, eps)) return st;
+  if (ld_in < cols || ld_in > kMaxLd || ld_out < cols || ld_out > kMaxLd || stride_in > kMaxSpan || stride_out > kMaxSpan)
+    return refuse(MRR_EINVAL, fn, "stride out of range");
+  if (batch == 0) return MRR_OK;
+  if (!in || !out || !workspace) return refuse(MRR_EINVAL, fn, "null pointer");
+  const size_t e = tsize(t);
+  if (!aligned(in, e) || !aligned(out, e)) return refuse(MRR_EALIGN, fn, "element alignment");
+  if (!aligned(workspace, 16)) return refuse(MRR_EALIGN, fn, "workspace 16 bytes");
+  const NsPlan p = ns_plan(rows, cols, batch, parts, false);
+  if (workspace_bytes < p.bytes) return refuse(MRR_ESCRATCH, fn, "workspace too small");
+  Mat ins[1], m;
+  batch_mat(in, rows, cols, ld_in, batch, stride_in, e, &ins[0]);
+  if (!batch_mat(out, rows, cols, ld_out, batch, stride_out, e, &m)) return refuse(MRR_EOVERLAP, fn, "results overlap each other");
+  const Out outs[2] = {{m, batch < 2 || (stride_in == stride_out && ld_in == ld_out) ? 1 : 0}, {vec(workspace, p.bytes), 0}};
+  if (bad_overlap(ins, 1, outs, 2)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
+  NsCall c{};
+  c.in = in;
+  c.out = out;
+  c.rows = rows;
+  c.cols = cols;
+  c.ld_in = ld_in;
+  c.ld_out = ld_out;
+  c.stride_in = stride_in;
+  c.stride_out = stride_out;
+  c.batch = (uint32_t)batch;
+  c.steps = steps;
+  c.coefficients = coefficients;
+  c.eps = eps;
+  c.workspace = workspace;
+  return hip_status(launch_orthogonalize(c, p, t, (hipStream_t)stream), fn);
+}
+
+size_t mrr_muon_workspace_bytes(size_t rows, size_t cols, size_t batch, int nesterov, mrr_dtype wdtype, mrr_dtype products) {
+  int parts;
+  if (batch == 0 || ns_shape("mrr_muon_workspace_bytes", rows, cols, batch, wdtype, products, &parts)) return 0;
+  return ns_plan(rows, cols, batch, parts, nesterov != 0).bytes;
+}
+
+mrr_status mrr_muon_step(const void* const* grads, int nranks, float grad_scale, const float* momentum,
+                         float* momentum_out, float mu, int nesterov, const void* weight, void* const* weights_out,
+                         float rate, float decay, size_t rows, size_t cols, size_t ld_grad, size_t ld_weight,
+                         size_t batch, size_t stride_grad, size_t stride_weight, int steps, const float* coefficients,
+                         float eps, mrr_dtype gdtype, mrr_dtype wdtype, mrr_dtype products, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  static const char* fn = "mrr_muon_step";
+  const int tg = gdtype, tw = wdtype == MRR_AUTO ? gdtype : wdtype;
+  int parts;
+  float own[3 * kMaxSteps];
+  if (nranks < 1 || nranks > kMaxRanks) return refuse(MRR_EUNSUPPORTED, fn, "nranks out of range");
+  if (!float_type(tg)) return refuse(MRR_EUNSUPPORTED, fn, "type");
+  if (mrr_status st = ns_shape(fn, rows, cols, batch, tw, products, &parts)) return st;
+  if (mrr_status st = ns_steps(fn, steps, &coefficients, own, eps)) return st;
+  if (!isfinite(grad_scale) || !isfinite(mu) || !isfinite(rate) || !isfinite(decay))
+    return refuse(MRR_EINVAL, fn, "a factor is not finite");
+  if (ld_grad < cols || ld_grad > kMaxLd || ld_weight < cols || ld_weight > kMaxLd || stride_grad > kMaxSpan || stride_weight > kMaxSpan)
+    return refuse(MRR_EINVAL, fn, "stride out of range");
+  if (batch == 0) return MRR_OK;
+  if (!grads || !momentum_out || !weight || !weights_out || !workspace) return refuse(MRR_EINVAL, fn, "null pointer");
+  const size_t eg = tsize(tg), ew = tsize(tw);
+  if (!aligned(momentum, 4) || !aligned(momentum_out, 4) || !aligned(weight, ew)) return refuse(MRR_EALIGN, fn, "element alignment");
+  if (!aligned(workspace, 16)) return refuse(MRR_EALIGN, fn, "workspace 16 bytes");
+  const NsPlan p = ns_plan(rows, cols, batch, parts, nesterov != 0);
+  if (workspace_bytes < p.bytes) return refuse(MRR_ESCRATCH, fn, "workspace too small");
+  MuonArgs m{};
+  NsLast z{};
+  Mat ins[kMaxRanks + 2];
+  Out outs[kMaxRanks + 2];
+  // the weights' and the momentum's own inputs come first and second; each output's place is checked by itself below
+  if (!batch_mat(weight, rows, cols, ld_weight, batch, stride_weight, ew, &ins[0]))
+    return refuse(MRR_EOVERLAP, fn, "matrices overlap each other");
+  batch_mat(momentum, rows, cols, ld_weight, batch, stride_weight, 4, &ins[1]);
+  int nin = 2, nout = 0;
+  for (int r = 0; r < nranks; ++r) {
+    if (!grads[r] || !weights_out[r]) return refuse(MRR_EINVAL, fn, "null rank pointer");
+    if (!aligned(grads[r], eg) || !aligned(weights_out[r], ew)) return refuse(MRR_EALIGN, fn, "element alignment");
+    m.grads[r] = grads[r];
+    z.out[r] = weights_out[r];
+    batch_mat(grads[r], rows, cols, ld_grad, batch, stride_grad, eg, &ins[nin++]);
+    batch_mat(weights_out[r], rows, cols, ld_weight, batch, stride_weight, ew, &outs[nout].m);
+    outs[nout++].in_place = 1;
+  }
+  outs[nout++] = {vec(workspace, p.bytes), 0};
+  // the momentum may take its own input's place alone
+  Mat mo;
+  batch_mat(momentum_out, rows, cols, ld_weight, batch, stride_weight, 4, &mo);
+  if (bad_overlap(ins, nin, outs, nout)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
+  for (int i = 0; i < nin; ++i)
+    if (overlaps(mo, ins[i]) && !(i == 1 && same(mo, ins[1]))) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
+  for (int k = 0; k < nout; ++k)
+    if (overlaps(mo, outs[k].m)) return refuse(MRR_EOVERLAP, fn, "an output overlaps");
+  m.momentum = momentum;
+  m.momentum_out = momentum_out;
+  m.u = nesterov ? (float*)workspace : nullptr;  // (its place is the plan's)
+  m.nranks = nranks;
+  m.grad_scale = grad_scale;
+  m.mu = mu;
+  m.ld_grad = ld_grad;
+  m.ld_weight = ld_weight;
+  m.stride_grad = stride_grad;
+  m.stride_weight = stride_weight;
+  z.weight = weight;
+  z.nranks = nranks;
+  z.keep = (float)(1.0 - (double)decay);
+  z.rate = rate;
+  z.ld = ld_weight;
+  z.stride = stride_weight;
+  NsCall c{};
+  c.rows = rows;
+  c.cols = cols;
+  c.batch = (uint32_t)batch;
+  c.steps = steps;
+  c.coefficients = coefficients;
+  c.eps = eps;
+  c.workspace = workspace;
+  return hip_status(launch_muon(c, p, m, z, tg, tw, (hipStream_t)stream), fn);
 }
 
 mrr_status mrr_stream_copy(const void* src, void* dst, size_t nbytes, void* stream) {

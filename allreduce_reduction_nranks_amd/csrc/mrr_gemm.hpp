@@ -80,10 +80,32 @@ template <int S> __device__ __forceinline__ uint32_t col_frag(int m0, int r, int
   return (uint32_t)(k * (2 * S) + unit * 64 + 32 * ((lane >> 4) & 1) + 8 * (lane & 3));
 }
 
+// ---- tiles -------------------------------------------------------------------------
+// Workgroup id to tile (m, n) of mt x nt, and to one of `splits` parts of k.  Workgroups
+// go to the 8 XCDs in turn; each XCD gets one contiguous run of the order, which walks 8
+// m tiles by all n tiles of a split, so that the tiles an XCD works on together share
+// operands in its L2.  (Splits dealt out over the XCDs instead: 231 us against 134 for
+// the hidden states' gradient of 700 x 50257 x 1600 f16.)
+__device__ __forceinline__ bool tile_of(uint32_t id, uint32_t mt, uint32_t nt, uint32_t splits, uint32_t& m, uint32_t& n,
+                                        uint32_t& split) {
+  const uint32_t tiles = mt * nt, total = tiles * splits, per = total / 8, extra = total % 8, x = id & 7, j = id >> 3;
+  if (j >= per + (x < extra ? 1u : 0u)) return false;
+  uint32_t t = x * per + (x < extra ? x : extra) + j;
+  split = t / tiles;
+  t -= split * tiles;
+  constexpr uint32_t G = 8;
+  const uint32_t g = t / (G * nt), rem = t - g * (G * nt), gm = mt - g * G < G ? mt - g * G : G;
+  m = g * G + rem % gm;
+  n = rem / gm;
+  return true;
+}
+inline uint32_t tile_grid(uint64_t tiles) { return (uint32_t)((tiles + 7) / 8 * 8); }
+
 typedef __attribute__((address_space(3))) uint8_t lds8;
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+typedef __attribute__((address_space(3))) float lds_f32;
 
 __device__ __forceinline__ u32x4 read_row(const lds8* p) { return *(const lds_u32x4*)p; }
 __device__ __forceinline__ u32x4 read_col(const lds8* lo, const lds8* hi) {
@@ -277,6 +299,60 @@ template <int T, bool ACOL, bool BCOL, int S, int NS> struct Tile {
       put((wave % WN * FN + j) * 32 + row, wave / WN * (FM * 32) + unit * W, x);
     }
     __builtin_amdgcn_wave_barrier();
+  }
+
+  // Hands out the accumulators of the wave's j-th 32 columns twice: by rows of n, as above,
+  // with row(n, m, x) free to change the W values, then (COLS) what it left by rows of m,
+  // col(m, n, x) for 8 consecutive n.
+  template <int W, bool COLS, class Row, class Col> __device__ __forceinline__ void both_out(lds8* lds, int j, Row&& row, Col&& col) const {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int kRow = FM * 128, kUnits = FM * 32 / W;
+    lds8* mine = lds + wave * (32 * kRow);
+    auto settle = [] {
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    };
+    const int n0 = (wave % WN * FN + j) * 32, m0 = wave / WN * (FM * 32);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int n = lane & 31, chunk = (i * 8 + 2 * q + (lane >> 5)) ^ (n & 15);
+        const f32x16& v = acc[i][j];
+        *(lds_f32x4*)(mine + n * kRow + chunk * 16) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+      }
+    settle();
+#pragma unroll 4
+    for (int r = 0; r < 32 * kUnits / 64; ++r) {
+      const int at = r * 64 + lane, n = at / kUnits, unit = at % kUnits;
+      float x[W];
+#pragma unroll
+      for (int b = 0; b < W / 4; ++b) {
+        const f32x4 v = *(const lds_f32x4*)(mine + n * kRow + (((unit * (W / 4) + b) ^ (n & 15)) << 4));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[4 * b + e] = v[e];
+      }
+      row(n0 + n, m0 + unit * W, x);
+      if constexpr (COLS) {
+#pragma unroll
+        for (int b = 0; b < W / 4; ++b)
+          *(lds_f32x4*)(mine + n * kRow + (((unit * (W / 4) + b) ^ (n & 15)) << 4)) = f32x4{x[4 * b], x[4 * b + 1], x[4 * b + 2], x[4 * b + 3]};
+      }
+    }
+    if constexpr (COLS) {
+      settle();
+#pragma unroll 2
+      for (int r = 0; r < FM * 2; ++r) {
+        const int m = r * 16 + (lane >> 2), n = (lane & 3) * 8;
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          x[e] = *(const lds_f32*)(mine + (n + e) * kRow + ((((m >> 2) ^ ((n + e) & 15)) << 4) | ((m & 3) << 2)));
+        col(m0 + m, n0 + n, x);
+      }
+    }
+    settle();
   }
 };
 

@@ -1,5 +1,6 @@
 // mrr_ops.hpp -- argument blocks and launchers of the operators that follow
-// the rank sum in a training step: layer norm and sharded cross entropy.
+// the rank sum in a training step: layer norm, head norms with rotation, sharded cross
+// entropy and the weights' update.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -49,6 +50,33 @@ struct NormBwdArgs {
 uint32_t norm_bwd_groups(uint64_t rows, uint32_t cols);
 hipError_t launch_norm_fwd(const NormFwdArgs& a, int t, hipStream_t stream);
 hipError_t launch_norm_bwd(NormBwdArgs a, int t, hipStream_t stream);
+
+// ---- head norms and rotation of a projection to queries, keys and values -----------------
+struct QkArgs {
+  const void* in[MRR_MAX_RANKS];  // forward
+  const void* h;          // backward: the forward's sum
+  void* sum;              // forward, may be null
+  void* dsum;             // backward, may be null
+  void* out[3];           // queries, keys, values (backward: their gradients, read); may be null
+  uint64_t ld_out[3], hs_out[3];  // elements between tokens, and between heads
+  const void* w[2];       // may be null: 1
+  void* dw[2];            // backward, may be null
+  float* partial;         // backward: [workgroups][2][dim], null: no weight gradient
+  const float* table;     // [table_rows][rot]: cosines, then sines
+  const int64_t* positions;  // may be null: 0, 1, ...
+  uint64_t tokens, ld_in, table_rows;
+  uint32_t heads[3], first_head[3];
+  uint32_t its[4];        // a token's iterations: the first of each kind, and their count
+  uint32_t chunk;         // iterations of a wave
+  uint32_t dim, rot;
+  int nranks, pairs, wf32, skip_values;
+  float eps;
+};
+
+// Sums of weight gradients that a backward call leaves to join, at most.
+uint64_t qk_bwd_groups();
+hipError_t launch_qk_fwd(QkArgs a, int t, hipStream_t stream);
+hipError_t launch_qk_bwd(QkArgs a, int t, hipStream_t stream);
 
 // ---- cross entropy over a sharded vocabulary ---------------------------------------
 // The shards' rows, each shard padded to whole tiles of 256 rows.
@@ -159,5 +187,72 @@ XentWays xent_ways(const XentCall& c, const XentPlan& p, int t, bool backward);
 uint64_t xent_bytes(uint32_t tokens, uint32_t cols, const size_t* rows, int nranks, int t, bool backward, bool in_place);
 hipError_t launch_xent_fwd(const XentCall& c, int t, hipStream_t stream);
 hipError_t launch_xent_bwd(const XentCall& c, int t, hipStream_t stream);
+
+// ---- Newton-Schulz products and the weights' update -----------------------------------
+// Matrices that a call reads: rows x cols, rows ld and matrices stride elements apart.
+struct NsSource {
+  const void* p;
+  uint64_t rows, cols, ld, stride;
+};
+
+// A step's operands: X in two f16 parts, O and B in one or two, parts one after the other.
+struct NsArgs {
+  const uint8_t* x;
+  uint8_t* y;            // what X becomes
+  uint8_t* o;            // A beside its diagonal
+  uint8_t* b;            // B beside its diagonal
+  float* d;              // A's diagonal
+  float* beta;           // a + B's
+  uint64_t x_plane, x_batch, o_plane, o_batch;  // bytes of a part, and of a matrix
+  uint32_t mp, np;       // sides of X, padded to whole tiles
+  uint32_t m64, n64;     // sides in units of 64 k
+  float ca, cb, cc;
+};
+
+// Where the last step's result goes.
+struct NsLast {
+  void* out[MRR_MAX_RANKS];
+  const void* weight;    // null: the result alone
+  int nranks;
+  float keep, rate;
+  uint64_t ld, stride;
+  uint32_t rows, cols;
+};
+
+struct MuonArgs {
+  const void* grads[MRR_MAX_RANKS];
+  const float* momentum;  // may be null: zeros
+  float* momentum_out;
+  float* u;               // null: the momentum itself is made orthogonal
+  int nranks;
+  float grad_scale, mu;
+  uint64_t rows, cols, ld_grad, ld_weight, stride_grad, stride_weight;
+};
+
+// A call as the C ABI received it.
+struct NsCall {
+  const void* in;
+  void* out;
+  uint64_t rows, cols, ld_in, ld_out, stride_in, stride_out;
+  uint32_t batch;
+  int steps;
+  const float* coefficients;
+  float eps;
+  void* workspace;
+};
+
+// Tiles and the workspace's parts (byte offsets) of a call.
+struct NsPlan {
+  uint32_t mp, np, tile, parts;
+  uint64_t x_plane, o_plane, x_bytes;
+  uint64_t x, o, b, d, beta, partial, u, bytes;
+};
+
+// Whether the parts' scales hold every step's values: singular values below 7.5 before a
+// step, |b x + c x^2| below 1000.
+bool ns_bounds(const float* coefficients, int steps);
+NsPlan ns_plan(uint64_t rows, uint64_t cols, uint64_t batch, int parts, bool with_u);
+hipError_t launch_orthogonalize(const NsCall& c, const NsPlan& p, int t, hipStream_t stream);
+hipError_t launch_muon(const NsCall& c, const NsPlan& p, MuonArgs m, NsLast z, int tg, int tw, hipStream_t stream);
 
 }  // namespace mrr

@@ -267,27 +267,6 @@ template <int T> __global__ void __launch_bounds__(256) layout_k(LayoutArgs a, H
   }
 }
 
-// ---- tiles -------------------------------------------------------------------------
-// Workgroup id to tile (m, n) of mt x nt, and to one of `splits` parts of k.  Workgroups
-// go to the 8 XCDs in turn; each XCD gets one contiguous run of the order, which walks 8
-// m tiles by all n tiles of a split, so that the tiles an XCD works on together share
-// operands in its L2.  (Splits dealt out over the XCDs instead: 231 us against 134 for
-// the hidden states' gradient of 700 x 50257 x 1600 f16.)
-__device__ __forceinline__ bool tile_of(uint32_t id, uint32_t mt, uint32_t nt, uint32_t splits, uint32_t& m, uint32_t& n,
-                                        uint32_t& split) {
-  const uint32_t tiles = mt * nt, total = tiles * splits, per = total / 8, extra = total % 8, x = id & 7, j = id >> 3;
-  if (j >= per + (x < extra ? 1u : 0u)) return false;
-  uint32_t t = x * per + (x < extra ? x : extra) + j;
-  split = t / tiles;
-  t -= split * tiles;
-  constexpr uint32_t G = 8;
-  const uint32_t g = t / (G * nt), rem = t - g * (G * nt), gm = mt - g * G < G ? mt - g * G : G;
-  m = g * G + rem % gm;
-  n = rem / gm;
-  return true;
-}
-uint32_t tile_grid(uint64_t tiles) { return (uint32_t)((tiles + 7) / 8 * 8); }
-
 // A pair of a forward: the largest logit z of some rows, and the sum of exp(z' - z) over
 // them.  The terms are exp2(fma(z', log2 e, -base)), base = z log2 e as rounded; what that
 // rounding takes is given back to the sum, so that the pair is as exact as its parts.

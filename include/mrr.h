@@ -553,6 +553,158 @@ mrr_status mrr_linear_xent_bwd(const void* hidden, const void* const* weights, c
                                void* workspace, size_t workspace_bytes, void* stream);
 
 /* --------------------------------------------------------------------------
+ * Head norms and rotation of a projection to queries, keys and values: what
+ * consumes its N partial results before attention.
+ *
+ *   h    = round_dtype( x_0 + x_1 + ... + x_{nranks-1} )     summed in rank order in f32
+ *   xhat = h / sqrt( mean over a head of h^2 + eps )
+ *   y    = round_dtype( R( xhat * weight ) )      queries and keys, each with their weight
+ *   y    = h                                      values
+ * A row of the inputs holds heads[0] query heads, heads[1] key heads and heads[2] value
+ * heads of head_dim elements, side by side.  R rotates the first rot_dim elements of a head
+ * by the token's angles and leaves the others: a pair (a, b) becomes (a cos - b sin, b cos +
+ * a sin).  pairs 0: element i < rot_dim / 2 pairs with i + rot_dim / 2; pairs 1: 2 i with
+ * 2 i + 1.  All in f32, rounded once.
+ *
+ * inputs:    host array of nranks (1..32) device pointers to rows of dtype (F32 | F16 |
+ *            BF16), one a token, ld_in elements apart; they may overlap each other.
+ * q_weight, k_weight: head_dim elements of wdtype: F32, or the data type (AUTO); NULL = 1.
+ * table:     table_rows rows of rot_dim f32: rot_dim / 2 cosines, then their sines, of
+ *            each position (NULL with rot_dim 0).
+ * positions: 64-bit row of the table for each token; NULL = 0, 1, 2, ...  A token whose
+ *            position is negative fills up a padded batch: nothing of it is read, and no
+ *            output of it is written.  A position of table_rows or more rotates by NaN.
+ * sum:       receives h (all heads), rows ld_in apart; NULL = not stored.
+ * outs:      host array of three device pointers: y of the queries, keys and values, or
+ *            NULL = not stored (as where there are no such heads).  Element d of head j of
+ *            token t lies at t * ld_outs[k] + j * head_strides[k] + d (so token by token
+ *            or head by head, in a buffer of its own or as columns of a wider one).
+ * sum may be exactly one of the inputs, and each of outs exactly its heads' columns of one;
+ * any other overlap of an output gives MRR_EOVERLAP.  Pointers are aligned to their
+ * element (MRR_EALIGN).  The same call gives the same bits.  tokens == 0 launches nothing.
+ * Errors: MRR_EUNSUPPORTED for another type or nranks outside [1, 32]; MRR_EINVAL for null
+ * pointers, head_dim 0 or over 512, rot_dim odd or over head_dim, a head count over
+ * 65535 or none at all, tokens over 2^31, ld_in below a row or over 2^31, strides that
+ * put two elements in one place, table_rows of 0 or over 2^31, without positions more
+ * tokens than table_rows, and an eps that is negative or NaN.
+ * ------------------------------------------------------------------------ */
+mrr_status mrr_qknorm_rope_fwd(const void* const* inputs, int nranks, const void* q_weight,
+                               const void* k_weight, const float* table, size_t table_rows,
+                               const int64_t* positions, void* sum, void* const* outs,
+                               size_t tokens, const size_t* heads, size_t head_dim,
+                               size_t rot_dim, int pairs, size_t ld_in, const size_t* ld_outs,
+                               const size_t* head_strides, float eps, mrr_dtype dtype,
+                               mrr_dtype wdtype, void* stream);
+
+/* --------------------------------------------------------------------------
+ * Gradient of mrr_qknorm_rope_fwd.  With u = R^T(dout), g = u * weight and rs =
+ * 1 / sqrt( mean(h^2) + eps ) of a head:
+ *   dsum    = round( rs * (g - xhat * mean(g * xhat)) )      queries and keys
+ *   dsum    = dout                                           values
+ *   dweight = round( sum over tokens and their heads of u * xhat )
+ * dsum is the gradient of every rank's input alike.  Sums are f32 and taken in a fixed order:
+ * the same call gives the same bits.
+ *
+ * douts, ld_douts, head_strides: gradients of the forward's outs, laid out as those; NULL =
+ * zero.  sum: the forward's h (with one rank its input), and dsum: rows ld_in apart.
+ * dsum, dq_weight and dk_weight may be NULL, not all three.  Rows of dsum of tokens with a
+ * negative position are zero, and nothing of them reaches a gradient.
+ * dsum may be exactly sum.
+ * workspace: device, 16-byte aligned, mrr_qknorm_rope_bwd_workspace_bytes(tokens, heads,
+ * head_dim) bytes at least (else MRR_ESCRATCH), contents irrelevant before and after;
+ * needed only with dq_weight or dk_weight.
+ * tokens == 0 sets the weight gradients to zero.  Errors as in the forward.
+ * ------------------------------------------------------------------------ */
+size_t mrr_qknorm_rope_bwd_workspace_bytes(size_t tokens, const size_t* heads, size_t head_dim);
+
+mrr_status mrr_qknorm_rope_bwd(const void* const* douts, const void* sum, const void* q_weight,
+                               const void* k_weight, const float* table, size_t table_rows,
+                               const int64_t* positions, void* dsum, void* dq_weight,
+                               void* dk_weight, size_t tokens, const size_t* heads,
+                               size_t head_dim, size_t rot_dim, int pairs, size_t ld_in,
+                               const size_t* ld_douts, const size_t* head_strides, float eps,
+                               mrr_dtype dtype, mrr_dtype wdtype, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* --------------------------------------------------------------------------
+ * Matrices made orthogonal by Newton-Schulz products.
+ *
+ *   X_0 = in / ( |in| + eps )                       |.| the Frobenius norm of a matrix
+ *   A = X X^T,  X <- a X + (b A + c A A) X          steps times
+ *   out = round_dtype( X )
+ * which takes each singular value s of X_0 through a s + b s^3 + c s^5 at each step and
+ * leaves the singular vectors (of matrices with more rows than columns the transpose is
+ * taken through the same steps).
+ *
+ * in, out: batch matrices of rows x cols elements of dtype (F32 | F16 | BF16), rows ld_in
+ *          (ld_out) and matrices stride_in (stride_out) elements apart.
+ * coefficients: host array of a, b, c of each step; NULL = 3.4445, -4.7750, 2.0315 at
+ *          every step, which bring singular values from 0.01 of the norm up to within 0.7 and
+ *          1.2 in 5 steps.
+ * products: precision of the products.  F32: operands in two f16 parts (22 bits), three
+ *          products of them for each: results as exact as f32 products give.  F16: operands
+ *          of 11 bits, diagonals and what a step adds to in f32 beside them: results off
+ *          by up to 1.1e-3 of their norm (bf16 itself rounds by 1.7e-3).  AUTO: F16 for
+ *          BF16 results, else F32.  Matrices with a side of 64 or less always take F32.
+ * Norms and sums are f32 or f64.  A matrix of zeros gives zeros; one that holds NaN or an
+ * infinity gives NaN.  The same call gives the same bits.
+ * out may be exactly in, with the same strides; any other overlap gives MRR_EOVERLAP.
+ * workspace: device, 16-byte aligned, mrr_orthogonalize_workspace_bytes(...) bytes at least
+ * (else MRR_ESCRATCH), contents irrelevant before and after.
+ * batch == 0 launches nothing.
+ * Errors: MRR_EUNSUPPORTED for another type or precision; MRR_EINVAL for null pointers,
+ * rows or cols of 0 or over 65536, a batch over 65535, steps outside [1, 64], a stride below
+ * a row or over 2^31 (matrices: 2^40), an eps that is negative or not finite, and coefficients
+ * with which singular values could pass 7.5 before a step, or |b x + c x^2| 1000 for any x up
+ * to their squares.
+ * ------------------------------------------------------------------------ */
+size_t mrr_orthogonalize_workspace_bytes(size_t rows, size_t cols, size_t batch, mrr_dtype dtype,
+                                         mrr_dtype products);
+
+mrr_status mrr_orthogonalize(const void* in, void* out, size_t rows, size_t cols, size_t ld_in,
+                             size_t ld_out, size_t batch, size_t stride_in, size_t stride_out,
+                             int steps, const float* coefficients, float eps, mrr_dtype dtype,
+                             mrr_dtype products, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* --------------------------------------------------------------------------
+ * The weights' update by mrr_orthogonalize (the Muon optimiser's step), from every rank's
+ * gradients to every rank's weights.
+ *
+ *   g            = grad_scale * ( G_0 + G_1 + ... + G_{nranks-1} )      in rank order, f32
+ *   momentum_out = mu * momentum + g
+ *   u            = g + mu * momentum_out (nesterov), or momentum_out
+ *   weights_out[r] = round_wdtype( (1 - decay) * weight - rate * X )    for every r,
+ * X what mrr_orthogonalize makes of u in f32, not rounded before.  rate and decay are
+ * taken as they are: factors for a matrix's sides, and rate * weight decay, are the caller's.
+ *
+ * grads:   host array of nranks (1..32) device pointers to batch matrices of gdtype (F32 |
+ *          F16 | BF16), rows ld_grad, matrices stride_grad elements apart; they may overlap.
+ * weight:  batch matrices of wdtype (F32 | F16 | BF16, or AUTO = gdtype), rows ld_weight,
+ *          matrices stride_weight elements apart; weights_out: host array of nranks device
+ *          pointers to such matrices.
+ * momentum, momentum_out: f32, laid out as the weights; momentum NULL = zeros (a first step).
+ * weights_out[r] may be exactly weight, and momentum_out exactly momentum; any other overlap
+ * of an output gives MRR_EOVERLAP.
+ * products: as in mrr_orthogonalize, AUTO by wdtype.
+ * workspace: as there, mrr_muon_workspace_bytes(...) bytes at least.
+ * Factors are values of the call: a captured graph replays those it was captured with.
+ * Errors as there; MRR_EUNSUPPORTED for nranks outside [1, 32]; MRR_EINVAL for a factor that
+ * is not finite.
+ * ------------------------------------------------------------------------ */
+size_t mrr_muon_workspace_bytes(size_t rows, size_t cols, size_t batch, int nesterov,
+                                mrr_dtype wdtype, mrr_dtype products);
+
+mrr_status mrr_muon_step(const void* const* grads, int nranks, float grad_scale,
+                         const float* momentum, float* momentum_out, float mu, int nesterov,
+                         const void* weight, void* const* weights_out, float rate, float decay,
+                         size_t rows, size_t cols, size_t ld_grad, size_t ld_weight, size_t batch,
+                         size_t stride_grad, size_t stride_weight, int steps,
+                         const float* coefficients, float eps, mrr_dtype gdtype, mrr_dtype wdtype,
+                         mrr_dtype products, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* --------------------------------------------------------------------------
  * Copy-kernel calibration (measurement aid, not part of the reduction).
  * Copies nbytes from src to dst with the launch scheme of the RS/AG kernels
  * (one single-wave workgroup per tile, residency capped through an unused
