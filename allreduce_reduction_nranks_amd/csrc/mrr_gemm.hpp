@@ -20,6 +20,11 @@
 // stage as well: the one barrier of a stage stands before its last quarter, when
 // all its reads are done, so that the stage's buffer can be refilled and the next
 // stage's first fragments fetched under that quarter's products.
+//
+// Operands in two parts (TWO) have their upper and lower 32 k side by side in a stage: the
+// product is upper times upper and the two crossed ones, three matrix instructions for four
+// fragments read, where three passes over whole parts would read six and load half as
+// much again.
 #pragma once
 
 #include <type_traits>
@@ -124,16 +129,17 @@ __device__ __forceinline__ void load_lds(const uint8_t* base, uint32_t off, lds8
                :: "{m0}"((uint32_t)(uintptr_t)lds), "v"(off), "s"(base));
 }
 
-// The product over `steps` stages of 64 k, NS of them in LDS.  src(s, pa, pb, oa, ob) sets
-// the (wave-uniform) addresses and the lane offsets of stage s; it is called once for
-// each s in order.
-template <int T, bool ACOL, bool BCOL, int S, int NS> struct Tile {
+// The product over `steps` stages of 64 k (TWO: 32 k in two parts), NS of them in LDS.  src(s,
+// pa, pb, oa, ob) sets the (wave-uniform) addresses and the lane offsets of stage s; it is
+// called once for each s in order.
+template <int T, bool ACOL, bool BCOL, int S, int NS, bool TWO = false> struct Tile {
   static constexpr int WN = S == 256 ? 4 : 2, WM = 2;        // waves along n and m
   static constexpr int FM = S / WM / 32, FN = S / WN / 32;   // 32 x 32 tiles of a wave
   static constexpr int kStage = S * kTileK * 2;                 // bytes of an operand's stage
   static constexpr int kLoad = tile_threads(S) * 16, L = kStage / kLoad;  // bytes of a load, loads of a lane
   static constexpr int kLds = 2 * NS * kStage;               // A's stages, then B's
-  static constexpr int Q = kTileK / 16;                      // quarters of a stage, which multiply together
+  static constexpr int P = TWO ? 2 : 1;                      // parts of an operand
+  static constexpr int Q = kTileK / 16 / P;                  // quarters of a stage, which multiply together (TWO: halves)
   f32x16 acc[FM][FN];
 
   template <class Src> __device__ __forceinline__ void run(int steps, lds8* lds, Src&& src) {
@@ -149,7 +155,7 @@ template <int T, bool ACOL, bool BCOL, int S, int NS> struct Tile {
     if (steps <= 0) return;
     // offsets of this lane's fragments in the present stage, and of its wave's loads in
     // the one that is filled next
-    constexpr int NA = ACOL ? 2 * FM : Q, NB = BCOL ? 2 * FN : Q;
+    constexpr int NA = ACOL ? 2 * FM : Q * P, NB = BCOL ? 2 * FN : Q * P;
     uint32_t fa[NA], fb[NB];
     uint32_t at = 0, fill = 0;
 #pragma unroll
@@ -160,32 +166,38 @@ template <int T, bool ACOL, bool BCOL, int S, int NS> struct Tile {
     lds8* const wave_lds = lds + wave * 1024;
     const uint8_t *pa, *pb;
     uint32_t oa[L], ob[L];
-    u32x4 va[2][FM], vb[2][FN];
+    u32x4 va[2][P][FM], vb[2][P][FN];
 
     auto fetch = [&](int i) {
       if (i < L) load_lds(pa, oa[i % L], wave_lds + fill + i * kLoad);
       else load_lds(pb, ob[i % L], wave_lds + fill + NS * kStage + (i - L) * kLoad);
     };
     auto filled = [&]() { fill = fill == (NS - 1) * kStage ? 0 : fill + kStage; };
-    auto read = [&](int f, int kk) {
+    auto read = [&](int f, int first) {
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        if constexpr (BCOL) vb[f][j] = read_col(lds + fb[2 * j] + kk * (32 * S), lds + fb[2 * j + 1] + kk * (32 * S));
-        else vb[f][j] = read_row(lds + fb[kk] + j * 4096);
-      }
+      for (int p = 0; p < P; ++p) {
+        const int kk = first + p * Q;
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        if constexpr (ACOL) va[f][i] = read_col(lds + fa[2 * i] + kk * (32 * S), lds + fa[2 * i + 1] + kk * (32 * S));
-        else va[f][i] = read_row(lds + fa[kk] + i * 4096);
+        for (int j = 0; j < FN; ++j) {
+          if constexpr (BCOL) vb[f][p][j] = read_col(lds + fb[2 * j] + kk * (32 * S), lds + fb[2 * j + 1] + kk * (32 * S));
+          else vb[f][p][j] = read_row(lds + fb[kk] + j * 4096);
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+          if constexpr (ACOL) va[f][p][i] = read_col(lds + fa[2 * i] + kk * (32 * S), lds + fa[2 * i + 1] + kk * (32 * S));
+          else va[f][p][i] = read_row(lds + fa[kk] + i * 4096);
+        }
       }
     };
-    auto product = [&](int f, int p) {
-      acc[p / FN][p % FN] = mfma<T>(va[f][p / FN], vb[f][p % FN], acc[p / FN][p % FN]);
+    // products of a quarter: TWO: the crossed parts first
+    constexpr int kTiles = FM * FN, kProducts = (TWO ? 3 : 1) * kTiles;
+    auto product = [&](int f, int n) {
+      const int p = n % kTiles, a = n / kTiles == 1 ? 1 : 0, b = TWO && n / kTiles == 0 ? 1 : 0;
+      acc[p / FN][p % FN] = mfma<T>(va[f][a][p / FN], vb[f][b][p % FN], acc[p / FN][p % FN]);
     };
-    constexpr int kProducts = FM * FN;
     // fragments f multiply while the others are read from quarter kk
     auto quarter = [&](int f, int kk) {
-      constexpr int reads = (ACOL ? 2 : 1) * FM + (BCOL ? 2 : 1) * FN;
+      constexpr int reads = ((ACOL ? 2 : 1) * FM + (BCOL ? 2 : 1) * FN) * P;
       constexpr int each = (reads + kProducts - 1) / kProducts;
       read(f ^ 1, kk);
 #pragma unroll
@@ -301,12 +313,58 @@ template <int T, bool ACOL, bool BCOL, int S, int NS> struct Tile {
     __builtin_amdgcn_wave_barrier();
   }
 
-  // Hands out the accumulators of the wave's j-th 32 columns twice: by rows of n, as above,
-  // with row(n, m, x) free to change the W values, then (COLS) what it left by rows of m,
-  // col(m, n, x) for 8 consecutive n.
-  template <int W, bool COLS, class Row, class Col> __device__ __forceinline__ void both_out(lds8* lds, int j, Row&& row, Col&& col) const {
+  // Adds the other splits' accumulators to this one's, in the order of the splits, in the
+  // workgroup that comes last: true there, false in the others, which are done.  part:
+  // [splits] S x S values of this tile; counter: 0 before, and left so.  Nothing waits.
+  // The values go past the L2 caches, which the XCDs do not share (agent scope), and a wave's
+  // have arrived when its count of stores in flight is 0: no cache has to be written back or
+  // emptied, which takes several microseconds where every workgroup asks for it.
+  __device__ __forceinline__ bool join(lds8* lds, float* part, uint32_t* counter, uint32_t split, uint32_t splits) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    constexpr int kRow = FM * 128, kUnits = FM * 32 / W;
+    float* const mine = part + wave * (FM * FN * 1024) + lane;
+#pragma unroll
+    for (int t = 0; t < FM * FN; ++t)
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        __hip_atomic_store(mine + split * (S * S) + (t * 16 + e) * 64, acc[t / FN][t % FN][e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    typedef __attribute__((address_space(3))) uint32_t lds_u32;
+    if (threadIdx.x == 0) *(lds_u32*)lds = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    const bool last = *(lds_u32*)lds == splits - 1;
+    __syncthreads();
+    if (!last) return false;
+    if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+    for (int t = 0; t < FM * FN; ++t)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[t / FN][t % FN][e] = 0.0f;
+    for (uint32_t s = 0; s < splits; ++s) {
+#pragma unroll
+      for (int t = 0; t < FM * FN; ++t) {
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          v[e] = __hip_atomic_load(mine + s * (S * S) + (t * 16 + e) * 64, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[t / FN][t % FN][e] += v[e];
+        if (t & 1) __builtin_amdgcn_sched_barrier(0);  // (registers for two tiles' loads in flight)
+      }
+    }
+    return true;
+  }
+
+  // Hands out the accumulators of the wave's j-th 32 columns twice: by rows of n, as above,
+  // with row(n, m, x, in) free to change the W values, then (COLS) what it left by rows of m,
+  // col(m, n, x) for 8 consecutive n.  in = pre(n, m) is what row() reads from memory: it is
+  // called for several rows before the first of them stores, and for the first of them
+  // before the accumulators go to LDS.
+  template <int W, bool COLS, class Pre, class Row, class Col>
+  __device__ __forceinline__ void both_out(lds8* lds, int j, Pre&& pre, Row&& row, Col&& col) const {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int kRow = FM * 128, kUnits = FM * 32 / W, kSwap = FM == 1 ? 7 : 15;
+    constexpr int kTurns = 32 * kUnits / 64, kAhead = kTurns < 4 ? kTurns : 4;
     lds8* mine = lds + wave * (32 * kRow);
     auto settle = [] {
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -314,30 +372,42 @@ template <int T, bool ACOL, bool BCOL, int S, int NS> struct Tile {
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     };
     const int n0 = (wave % WN * FN + j) * 32, m0 = wave / WN * (FM * 32);
+    auto n_of = [&](int r) { return (r * 64 + lane) / kUnits; };
+    auto unit_of = [&](int r) { return (r * 64 + lane) % kUnits; };
+    decltype(pre(0, 0)) in[kAhead];
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r) in[r] = pre(n0 + n_of(r), m0 + unit_of(r) * W);
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int n = lane & 31, chunk = (i * 8 + 2 * q + (lane >> 5)) ^ (n & 15);
+        const int n = lane & 31, chunk = (i * 8 + 2 * q + (lane >> 5)) ^ (n & kSwap);
         const f32x16& v = acc[i][j];
         *(lds_f32x4*)(mine + n * kRow + chunk * 16) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
       }
     settle();
-#pragma unroll 4
-    for (int r = 0; r < 32 * kUnits / 64; ++r) {
-      const int at = r * 64 + lane, n = at / kUnits, unit = at % kUnits;
-      float x[W];
 #pragma unroll
-      for (int b = 0; b < W / 4; ++b) {
-        const f32x4 v = *(const lds_f32x4*)(mine + n * kRow + (((unit * (W / 4) + b) ^ (n & 15)) << 4));
+    for (int r0 = 0; r0 < kTurns; r0 += kAhead) {
+      if (r0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[4 * b + e] = v[e];
+        for (int r = 0; r < kAhead; ++r) in[r] = pre(n0 + n_of(r0 + r), m0 + unit_of(r0 + r) * W);
       }
-      row(n0 + n, m0 + unit * W, x);
-      if constexpr (COLS) {
 #pragma unroll
-        for (int b = 0; b < W / 4; ++b)
-          *(lds_f32x4*)(mine + n * kRow + (((unit * (W / 4) + b) ^ (n & 15)) << 4)) = f32x4{x[4 * b], x[4 * b + 1], x[4 * b + 2], x[4 * b + 3]};
+      for (int r = 0; r < kAhead; ++r) {
+        const int n = n_of(r0 + r), unit = unit_of(r0 + r);
+        float x[W];
+#pragma unroll
+        for (int b = 0; b < W / 4; ++b) {
+          const f32x4 v = *(const lds_f32x4*)(mine + n * kRow + (((unit * (W / 4) + b) ^ (n & kSwap)) << 4));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[4 * b + e] = v[e];
+        }
+        row(n0 + n, m0 + unit * W, x, in[r]);
+        if constexpr (COLS) {
+#pragma unroll
+          for (int b = 0; b < W / 4; ++b)
+            *(lds_f32x4*)(mine + n * kRow + (((unit * (W / 4) + b) ^ (n & kSwap)) << 4)) = f32x4{x[4 * b], x[4 * b + 1], x[4 * b + 2], x[4 * b + 3]};
+        }
       }
     }
     if constexpr (COLS) {
@@ -348,7 +418,7 @@ template <int T, bool ACOL, bool BCOL, int S, int NS> struct Tile {
         float x[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          x[e] = *(const lds_f32*)(mine + (n + e) * kRow + ((((m >> 2) ^ ((n + e) & 15)) << 4) | ((m & 3) << 2)));
+          x[e] = *(const lds_f32*)(mine + (n + e) * kRow + ((((m >> 2) ^ ((n + e) & kSwap)) << 4) | ((m & 3) << 2)));
         col(m0 + m, n0 + n, x);
       }
     }

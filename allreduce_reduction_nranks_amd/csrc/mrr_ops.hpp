@@ -195,7 +195,7 @@ struct NsSource {
   uint64_t rows, cols, ld, stride;
 };
 
-// A step's operands: X in two f16 parts, O and B in one or two, parts one after the other.
+// A step's operands: X in two f16 parts, O and B in one or two.
 struct NsArgs {
   const uint8_t* x;
   uint8_t* y;            // what X becomes
@@ -203,9 +203,12 @@ struct NsArgs {
   uint8_t* b;            // B beside its diagonal
   float* d;              // A's diagonal
   float* beta;           // a + B's
-  uint64_t x_plane, x_batch, o_plane, o_batch;  // bytes of a part, and of a matrix
+  float* part;           // sums of the products' splits
+  uint32_t* counter;     // splits that are done, of each tile
+  uint64_t x_plane, x_batch, o_batch;  // bytes from upper to lower parts, and of a matrix
   uint32_t mp, np;       // sides of X, padded to whole tiles
-  uint32_t m64, n64;     // sides in units of 64 k
+  uint32_t m_stages, n_stages;  // sides in stages of the products
+  uint32_t counters;     // of a matrix
   float ca, cb, cc;
 };
 
@@ -217,6 +220,7 @@ struct NsLast {
   float keep, rate;
   uint64_t ld, stride;
   uint32_t rows, cols;
+  int type;
 };
 
 struct MuonArgs {
@@ -241,11 +245,18 @@ struct NsCall {
   void* workspace;
 };
 
-// Tiles and the workspace's parts (byte offsets) of a call.
+// How a product is done: side of its tiles, stages in flight, parts of k, and the time expected.
+struct NsWay {
+  uint32_t tile, stages, splits;
+  double us;
+};
+
+// Products and the workspace's parts (byte offsets) of a call.
 struct NsPlan {
-  uint32_t mp, np, tile, parts;
+  NsWay gram, square, apply;
+  uint32_t mp, np, parts, m_stages, n_stages, counters;
   uint64_t x_plane, o_plane, x_bytes;
-  uint64_t x, o, b, d, beta, partial, u, bytes;
+  uint64_t x, o, b, d, beta, partial, part, counter, u, bytes;
 };
 
 // Whether the parts' scales hold every step's values: singular values below 7.5 before a

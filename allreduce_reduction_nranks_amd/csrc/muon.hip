@@ -38,29 +38,51 @@ namespace {
 constexpr float kScaleX = 8192.0f, kScaleA = 512.0f, kScaleB = 64.0f;
 
 // ---- parts -------------------------------------------------------------------------
+// A matrix of `cols` columns (a multiple of 64) whose products take upper parts (TWO false):
+// rows of f16, and the lower parts, of X alone, in a plane of their own.  In two parts:
+// blocks of 32 columns, 64 bytes of upper parts and 64 of lower ones, which is what a
+// stage of the products takes of a row.
+template <bool TWO> __device__ __forceinline__ uint64_t place(uint32_t row, uint32_t col, uint32_t cols) {
+  return TWO ? (uint64_t)row * cols * 4 + (col >> 5) * 128 + (col & 31) * 2 : ((uint64_t)row * cols + col) * 2;
+}
+struct Raw8 {
+  u32x4 hi, lo;
+};
 // 8 values to an upper f16 part and what it leaves.
-__device__ __forceinline__ void split8(const float* x, u32x4& hi, u32x4& lo) {
+__device__ __forceinline__ Raw8 split8(const float* x) {
+  Raw8 r;
   float h[8], l[8];
-  hi = encode16<kF16>(x);
-  decode16<kF16>(hi, h);
+  r.hi = encode16<kF16>(x);
+  decode16<kF16>(r.hi, h);
 #pragma unroll
   for (int e = 0; e < 8; ++e) l[e] = x[e] - h[e];
-  lo = encode16<kF16>(l);
+  r.lo = encode16<kF16>(l);
+  return r;
 }
-template <bool LO> __device__ __forceinline__ void join8(const uint8_t* p, uint64_t plane, float* x) {
-  decode16<kF16>(*reinterpret_cast<const u32x4*>(p), x);
-  if constexpr (LO) {
-    float l[8];
-    decode16<kF16>(*reinterpret_cast<const u32x4*>(p + plane), l);
+__device__ __forceinline__ void join8(const Raw8& r, float* x) {
+  float l[8];
+  decode16<kF16>(r.hi, x);
+  decode16<kF16>(r.lo, l);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] += l[e];
-  }
+  for (int e = 0; e < 8; ++e) x[e] += l[e];
 }
-template <bool LO> __device__ __forceinline__ void store_parts(uint8_t* p, uint64_t plane, const float* x) {
-  u32x4 hi, lo;
-  split8(x, hi, lo);
-  *reinterpret_cast<u32x4*>(p) = hi;
-  if constexpr (LO) *reinterpret_cast<u32x4*>(p + plane) = lo;
+// X, in two parts in any case: `plane` from the upper to the lower ones.
+__device__ __forceinline__ Raw8 load_parts(const uint8_t* p, uint64_t plane) {
+  return {*reinterpret_cast<const u32x4*>(p), *reinterpret_cast<const u32x4*>(p + plane)};
+}
+__device__ __forceinline__ void store_parts(uint8_t* p, uint64_t plane, const float* x) {
+  const Raw8 r = split8(x);
+  *reinterpret_cast<u32x4*>(p) = r.hi;
+  *reinterpret_cast<u32x4*>(p + plane) = r.lo;
+}
+// O and B, in one part or two.
+template <bool TWO> __device__ __forceinline__ Raw8 load_operand(const uint8_t* p) {
+  if constexpr (TWO) return load_parts(p, 64);
+  return {*reinterpret_cast<const u32x4*>(p), u32x4{0u, 0u, 0u, 0u}};
+}
+template <bool TWO> __device__ __forceinline__ void store_operand(uint8_t* p, const float* x) {
+  if constexpr (TWO) store_parts(p, 64, x);
+  else *reinterpret_cast<u32x4*>(p) = encode16<kF16>(x);
 }
 
 // 8 values of type T, of which the first n exist.
@@ -163,8 +185,15 @@ __device__ __forceinline__ float inverse_norm(const double* partial, uint32_t pa
   return norm == 0.0 ? 0.0f : (float)((double)kScaleX / norm);
 }
 
+// The counters of the products' splits, of this matrix, set to zero by its first workgroup.
+__device__ __forceinline__ void clear_counters(const NsArgs& a) {
+  if (blockIdx.x) return;
+  for (uint32_t i = threadIdx.x; i < a.counters; i += kSumThreads) a.counter[blockIdx.y * a.counters + i] = 0;
+}
+
 // X_0 in two parts, padded with zeros to whole tiles.
-template <int T> __global__ void __launch_bounds__(kSumThreads) spread_k(NsSource src, NsArgs a, const double* partial, uint32_t parts, float eps) {
+template <int T, bool TWO> __global__ void __launch_bounds__(kSumThreads) spread_k(NsSource src, NsArgs a, const double* partial, uint32_t parts, float eps) {
+  clear_counters(a);
   const float scale = inverse_norm(partial, parts, eps);
   const uint8_t* base = (const uint8_t*)src.p + blockIdx.y * src.stride * Ty<T>::size;
   uint8_t* to = a.y + blockIdx.y * a.x_batch;
@@ -179,13 +208,14 @@ template <int T> __global__ void __launch_bounds__(kSumThreads) spread_k(NsSourc
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] *= scale;
     }
-    store_parts<true>(to + u * 16, a.x_plane, x);
+    store_parts(to + place<TWO>(row, c, a.np), a.x_plane, x);
   }
 }
 
 // The same of the transpose: 64 x 64 through LDS.
-template <int T> __global__ void __launch_bounds__(kSumThreads) turn_k(NsSource src, NsArgs a, const double* partial, uint32_t parts, float eps) {
+template <int T, bool TWO> __global__ void __launch_bounds__(kSumThreads) turn_k(NsSource src, NsArgs a, const double* partial, uint32_t parts, float eps) {
   __shared__ float lds[64][65];
+  clear_counters(a);
   const float scale = inverse_norm(partial, parts, eps);
   const uint8_t* base = (const uint8_t*)src.p + blockIdx.y * src.stride * Ty<T>::size;
   uint8_t* to = a.y + blockIdx.y * a.x_batch;
@@ -208,17 +238,19 @@ template <int T> __global__ void __launch_bounds__(kSumThreads) turn_k(NsSource 
     float x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = lds[r][c + e] * scale;
-    store_parts<true>(to + ((uint64_t)(c0 + r) * a.np + r0 + c) * 2, a.x_plane, x);
+    store_parts(to + place<TWO>(c0 + r, r0 + c, a.np), a.x_plane, x);
   }
 }
 
 // ---- the products -------------------------------------------------------------------
-// The id-th tile (row, column <= row) on or below the diagonal, `side` tiles a side; XCDs
-// get contiguous runs of the rows.
-__device__ __forceinline__ bool lower_tile(uint32_t id, uint32_t side, uint32_t& r, uint32_t& c) {
-  const uint32_t total = side * (side + 1) / 2, per = total / 8, extra = total % 8, x = id & 7, j = id >> 3;
+// The id-th tile (row, column <= row) on or below the diagonal, `side` tiles a side, and one
+// of `splits` parts of k; XCDs get contiguous runs of the rows.
+__device__ __forceinline__ bool lower_tile(uint32_t id, uint32_t side, uint32_t splits, uint32_t& r, uint32_t& c, uint32_t& split) {
+  const uint32_t tiles = side * (side + 1) / 2, total = tiles * splits, per = total / 8, extra = total % 8, x = id & 7, j = id >> 3;
   if (j >= per + (x < extra ? 1u : 0u)) return false;
-  const uint32_t t = x * per + (x < extra ? x : extra) + j;
+  uint32_t t = x * per + (x < extra ? x : extra) + j;
+  split = t / tiles;
+  t -= split * tiles;
   r = (uint32_t)((__builtin_sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
   while (r * (r + 1) / 2 > t) --r;
   while ((r + 1) * (r + 2) / 2 <= t) ++r;
@@ -226,156 +258,176 @@ __device__ __forceinline__ bool lower_tile(uint32_t id, uint32_t side, uint32_t&
   return true;
 }
 
-// Parts that a product's seg-th pass takes: the small terms first.
-template <int PL> __device__ __forceinline__ uint32_t part_a(uint32_t seg) { return PL == 2 && seg == 0 ? 1u : 0u; }
-template <int PL> __device__ __forceinline__ uint32_t part_b(uint32_t seg) { return PL == 2 && seg == 1 ? 1u : 0u; }
+// The sums of `tile`'s splits, in the workgroup that comes last: true there.
+// (Calls for tiles of 256 have enough of them.)
+template <int S, class Prod> __device__ __forceinline__ bool whole(Prod& p, const NsArgs& a, uint32_t tile, uint32_t tiles, uint32_t split,
+                                                                   uint32_t splits, lds8* lds) {
+  __syncthreads();
+  if (S == 256 || splits == 1) return true;
+  const uint64_t of = (uint64_t)blockIdx.y * tiles + tile;
+  return p.join(lds, a.part + of * splits * S * S, a.counter + blockIdx.y * a.counters + tile, split, splits);
+}
 
-// A tile of P P^T for P = X (A = X X^T) or O (O O): both operands are rows of P.
-template <int S, int NS, int PL> __device__ __forceinline__ void
-square_tile(Tile<kF16, false, false, S, NS>& p, const uint8_t* base, uint64_t plane, uint32_t ld, uint32_t k64, uint32_t m0,
-            uint32_t n0, lds8* lds) {
-  typedef Tile<kF16, false, false, S, NS> Prod;
+// A tile of P P^T for P = X (A = X X^T) or O (O O): both operands are rows of P, ld bytes
+// apart, of `stages` 128 bytes.
+template <class Prod, int S> __device__ __forceinline__ void square_tile(Prod& p, const uint8_t* base, uint64_t ld, uint32_t stages, uint32_t m0,
+                                                                         uint32_t n0, uint32_t split, uint32_t splits, lds8* lds) {
   const int tid = threadIdx.x;
-  uint32_t k = 0, seg = 0;
+  uint32_t k = stages * split / splits;
+  const uint32_t k1 = stages * (split + 1) / splits;
   auto src = [&](int s, const uint8_t*& pa, const uint8_t*& pb, uint32_t (&oa)[Prod::L], uint32_t (&ob)[Prod::L]) {
     if (s == 0) {
 #pragma unroll
-      for (int i = 0; i < Prod::L; ++i) oa[i] = ob[i] = row_src_row<S>(tid, i) * ld + row_src_chunk(tid) * 16;
+      for (int i = 0; i < Prod::L; ++i) oa[i] = ob[i] = row_src_row<S>(tid, i) * (uint32_t)ld + row_src_chunk(tid) * 16;
     }
-    const uint8_t* at = base + (uint64_t)k * (kTileK * 2);
-    pa = at + (uint64_t)m0 * ld + part_a<PL>(seg) * plane;
-    pb = at + (uint64_t)n0 * ld + part_b<PL>(seg) * plane;
-    if (++k == k64) k = 0, ++seg;
+    const uint8_t* at = base + (uint64_t)k * 128;
+    pa = at + m0 * ld;
+    pb = at + n0 * ld;
+    ++k;
   };
-  p.run((int)k64 * (PL == 2 ? 3 : 1), lds, src);
+  p.run((int)(k1 - k), lds, src);
 }
 
 // A = X X^T: what lies beside the diagonal to O, the diagonal to d.
-template <int S, int NS, int PL> __global__ void __launch_bounds__(tile_threads(S)) gram_k(NsArgs a) {
-  typedef Tile<kF16, false, false, S, NS> Prod;
+template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_threads(S)) gram_k(NsArgs a, uint32_t splits) {
+  typedef Tile<kF16, false, false, S, NS, TWO> Prod;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
-  uint32_t r, c;
-  if (!lower_tile(blockIdx.x, a.mp / S, r, c)) return;
+  uint32_t r, c, split;
+  const uint32_t side = a.mp / S;
+  if (!lower_tile(blockIdx.x, side, splits, r, c, split)) return;
   const uint32_t m0 = r * S, n0 = c * S;
   Prod p;
-  square_tile<S, NS, PL>(p, a.x + blockIdx.y * a.x_batch, a.x_plane, a.np * 2, a.n64, m0, n0, (lds8*)lds);
-  __syncthreads();
+  square_tile<Prod, S>(p, a.x + blockIdx.y * a.x_batch, (uint64_t)a.np * (TWO ? 4 : 2), a.n_stages, m0, n0, split, splits, (lds8*)lds);
+  if (!whole<S>(p, a, r * (r + 1) / 2 + c, side * (side + 1) / 2, split, splits, (lds8*)lds)) return;
   uint8_t* o = a.o + blockIdx.y * a.o_batch;
   float* d = a.d + blockIdx.y * a.mp;
   constexpr float unscale = 1.0f / (kScaleX * kScaleX);
 #pragma unroll
   for (int j = 0; j < Prod::FN; ++j)
-    p.template both_out<8, true>((lds8*)lds, j, [&](int n, int m, float (&x)[8]) {
+    p.template both_out<8, true>((lds8*)lds, j, [](int, int) { return 0; }, [&](int n, int m, float (&x)[8], int) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         x[e] *= unscale;
         if (n0 + n == m0 + m + e) d[n0 + n] = x[e], x[e] = 0.0f;
         x[e] *= kScaleA;
       }
-      store_parts<PL == 2>(o + ((uint64_t)(n0 + n) * a.mp + m0 + m) * 2, a.o_plane, x);
+      store_operand<TWO>(o + place<TWO>(n0 + n, m0 + m, a.mp), x);
     }, [&](int m, int n, const float (&x)[8]) {
-      if (r != c) store_parts<PL == 2>(o + ((uint64_t)(m0 + m) * a.mp + n0 + n) * 2, a.o_plane, x);
+      if (r != c) store_operand<TWO>(o + place<TWO>(m0 + m, n0 + n, a.mp), x);
     });
 }
 
 // B = b A + c A^2: what lies beside the diagonal to B, a + its diagonal to beta.
-template <int S, int NS, int PL> __global__ void __launch_bounds__(tile_threads(S)) square_k(NsArgs a) {
-  typedef Tile<kF16, false, false, S, NS> Prod;
+template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_threads(S)) square_k(NsArgs a, uint32_t splits) {
+  typedef Tile<kF16, false, false, S, NS, TWO> Prod;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
-  uint32_t r, c;
-  if (!lower_tile(blockIdx.x, a.mp / S, r, c)) return;
+  uint32_t r, c, split;
+  const uint32_t side = a.mp / S;
+  if (!lower_tile(blockIdx.x, side, splits, r, c, split)) return;
   const uint32_t m0 = r * S, n0 = c * S;
   const uint8_t* o = a.o + blockIdx.y * a.o_batch;
   uint8_t* b = a.b + blockIdx.y * a.o_batch;
   const float* d = a.d + blockIdx.y * a.mp;
   float* beta = a.beta + blockIdx.y * a.mp;
   Prod p;
-  square_tile<S, NS, PL>(p, o, a.o_plane, a.mp * 2, a.m64, m0, n0, (lds8*)lds);
-  __syncthreads();
+  square_tile<Prod, S>(p, o, (uint64_t)a.mp * (TWO ? 4 : 2), a.m_stages, m0, n0, split, splits, (lds8*)lds);
+  if (!whole<S>(p, a, r * (r + 1) / 2 + c, side * (side + 1) / 2, split, splits, (lds8*)lds)) return;
   constexpr float unscale = 1.0f / (kScaleA * kScaleA);
+  struct In {
+    Raw8 o;
+    f32x4 dm[2];
+    float dn;
+  };
 #pragma unroll
   for (int j = 0; j < Prod::FN; ++j)
-    p.template both_out<8, true>((lds8*)lds, j, [&](int n, int m, float (&x)[8]) {
-      const uint64_t at = ((uint64_t)(n0 + n) * a.mp + m0 + m) * 2;
+    p.template both_out<8, true>((lds8*)lds, j, [&](int n, int m) {
+      const f32x4* dm = reinterpret_cast<const f32x4*>(d + m0 + m);
+      return In{load_operand<TWO>(o + place<TWO>(n0 + n, m0 + m, a.mp)), {dm[0], dm[1]}, d[n0 + n]};
+    }, [&](int n, int m, float (&x)[8], const In& in) {
       float y[8];
-      join8<PL == 2>(o + at, a.o_plane, y);
-      const float dn = d[n0 + n];
+      if constexpr (TWO) join8(in.o, y);
+      else decode16<kF16>(in.o.hi, y);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float dm = d[m0 + m + e], off = y[e] * (1.0f / kScaleA), sq = x[e] * unscale;
-        x[e] = (a.cb * off + a.cc * (sq + (dn + dm) * off)) * kScaleB;
-        if (n0 + n == m0 + m + e) beta[n0 + n] = a.ca + (a.cb * dn + a.cc * (sq + dn * dn)), x[e] = 0.0f;
+        const float dm = in.dm[e / 4][e % 4], off = y[e] * (1.0f / kScaleA), sq = x[e] * unscale;
+        x[e] = (a.cb * off + a.cc * (sq + (in.dn + dm) * off)) * kScaleB;
+        if (n0 + n == m0 + m + e) beta[n0 + n] = a.ca + (a.cb * in.dn + a.cc * (sq + in.dn * in.dn)), x[e] = 0.0f;
       }
-      store_parts<PL == 2>(b + at, a.o_plane, x);
+      store_operand<TWO>(b + place<TWO>(n0 + n, m0 + m, a.mp), x);
     }, [&](int m, int n, const float (&x)[8]) {
-      if (r != c) store_parts<PL == 2>(b + ((uint64_t)(m0 + m) * a.mp + n0 + n) * 2, a.o_plane, x);
+      if (r != c) store_operand<TWO>(b + place<TWO>(m0 + m, n0 + n, a.mp), x);
     });
 }
 
 // Results of the last step: X, or the weights' update by it, of 8 values of a row of the
 // result, n of them in it.
-template <int OUT> __device__ __forceinline__ void put_result(const NsLast& z, uint64_t at8, int n, float* x) {
+template <int T> __device__ __forceinline__ void put_typed(const NsLast& z, uint64_t i, int n, float* x) {
   if (z.weight) {
     float w[8];
-    load8<OUT>(at<OUT>(z.weight, at8), n, w);
+    load8<T>(at<T>(z.weight, i), n, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = __builtin_fmaf(-z.rate, x[e], z.keep * w[e]);
   }
-  for (int r = 0; r < z.nranks; ++r) store8<OUT>(at<OUT>(z.out[r], at8), n, x);
+  for (int r = 0; r < z.nranks; ++r) store8<T>(at<T>(z.out[r], i), n, x);
+}
+__device__ __forceinline__ void put_result(const NsLast& z, uint32_t row, uint32_t col, float* x) {
+  if (row >= z.rows || col >= z.cols) return;
+  const uint64_t i = blockIdx.y * z.stride + (uint64_t)row * z.ld + col;
+  const int n = z.cols - col < 8 ? (int)(z.cols - col) : 8;
+  if (z.type == kF32) put_typed<kF32>(z, i, n, x);
+  else if (z.type == kF16) put_typed<kF16>(z, i, n, x);
+  else put_typed<kBF16>(z, i, n, x);
 }
 
-// X <- (a + diag B) X + off(B) X, in parts (OUT 0) or as the result.
-template <int S, int NS, int PL, int OUT, bool TURN> __global__ void __launch_bounds__(tile_threads(S)) apply_k(NsArgs a, NsLast z) {
-  typedef Tile<kF16, true, false, S, NS> Prod;
+// X <- (a + diag B) X + off(B) X, in parts (LAST false) or as the result, TURN: transposed.
+template <int S, int NS, bool TWO, bool LAST, bool TURN>
+__global__ void __launch_bounds__(tile_threads(S)) apply_k(NsArgs a, NsLast z, uint32_t splits) {
+  typedef Tile<kF16, true, false, S, NS, TWO> Prod;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
   uint32_t mt, nt, split;
-  if (!tile_of(blockIdx.x, a.np / S, a.mp / S, 1, mt, nt, split)) return;
+  if (!tile_of(blockIdx.x, a.np / S, a.mp / S, splits, mt, nt, split)) return;
   const uint32_t j0 = mt * S, i0 = nt * S;  // column and row of X
   const uint8_t* x = a.x + blockIdx.y * a.x_batch;
   const uint8_t* b = a.b + blockIdx.y * a.o_batch;
   const float* beta = a.beta + blockIdx.y * a.mp;
   const int tid = threadIdx.x;
-  const uint32_t ldx = a.np * 2, ldb = a.mp * 2;
-  uint32_t k = 0, seg = 0;
+  const uint32_t ldx = a.np * (TWO ? 4 : 2), ldb = a.mp * (TWO ? 4 : 2);
+  uint32_t k = a.m_stages * split / splits;
+  const uint32_t k1 = a.m_stages * (split + 1) / splits;
   auto src = [&](int s, const uint8_t*& pa, const uint8_t*& pb, uint32_t (&oa)[Prod::L], uint32_t (&ob)[Prod::L]) {
     if (s == 0) {
 #pragma unroll
       for (int i = 0; i < Prod::L; ++i) {
-        oa[i] = col_src_k<S>(tid, i) * ldx + col_src_chunk<S>(tid) * 16;
+        const uint32_t kk = col_src_k<S>(tid, i), col = col_src_chunk<S>(tid) * 8;
+        oa[i] = TWO ? (kk & 31) * ldx + (kk >> 5) * 64 + (col >> 5) * 128 + (col & 31) * 2 : kk * ldx + col * 2;
         ob[i] = row_src_row<S>(tid, i) * ldb + row_src_chunk(tid) * 16;
       }
     }
-    pa = x + part_a<PL>(seg) * a.x_plane + (uint64_t)k * kTileK * ldx + j0 * 2;
-    pb = b + part_b<PL>(seg) * a.o_plane + (uint64_t)i0 * ldb + (uint64_t)k * (kTileK * 2);
-    if (++k == a.m64) k = 0, ++seg;
+    pa = x + (uint64_t)k * (TWO ? 32 : 64) * ldx + j0 * (TWO ? 4 : 2);
+    pb = b + (uint64_t)i0 * ldb + (uint64_t)k * 128;
+    ++k;
   };
   Prod p;
-  p.run((int)a.m64 * (PL == 2 ? 3 : 1), (lds8*)lds, src);
-  __syncthreads();
+  p.run((int)(k1 - k), (lds8*)lds, src);
+  if (!whole<S>(p, a, mt * (a.mp / S) + nt, (a.np / S) * (a.mp / S), split, splits, (lds8*)lds)) return;
+  struct In {
+    Raw8 x;
+    float beta;
+  };
 #pragma unroll
   for (int j = 0; j < Prod::FN; ++j)
-    p.template both_out<8, TURN>((lds8*)lds, j, [&](int n, int m, float (&v)[8]) {
-      const uint32_t row = i0 + n, col = j0 + m;
-      const uint64_t at = ((uint64_t)row * a.np + col) * 2;
+    p.template both_out<8, LAST && TURN>((lds8*)lds, j, [&](int n, int m) {
+      return In{load_parts(x + place<TWO>(i0 + n, j0 + m, a.np), a.x_plane), beta[i0 + n]};
+    }, [&](int n, int m, float (&v)[8], const In& in) {
       float y[8];
-      join8<true>(x + at, a.x_plane, y);
-      const float bt = beta[row];
-      if constexpr (OUT == 0) {
+      join8(in.x, y);
+      constexpr float unscale = LAST ? 1.0f / kScaleX : 1.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(v[e], 1.0f / kScaleB, bt * y[e]);
-        store_parts<true>(a.y + blockIdx.y * a.x_batch + at, a.x_plane, v);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(v[e], 1.0f / (kScaleB * kScaleX), bt * y[e] * (1.0f / kScaleX));
-        if (!TURN && row < z.rows && col < z.cols)
-          put_result<OUT>(z, blockIdx.y * z.stride + (uint64_t)row * z.ld + col, z.cols - col < 8 ? (int)(z.cols - col) : 8, v);
-      }
+      for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(v[e], unscale / kScaleB, in.beta * y[e] * unscale);
+      if constexpr (!LAST) store_parts(a.y + blockIdx.y * a.x_batch + place<TWO>(i0 + n, j0 + m, a.np), a.x_plane, v);
+      else if constexpr (!TURN) put_result(z, i0 + n, j0 + m, v);
     }, [&](int m, int n, float (&v)[8]) {
-      if constexpr (OUT != 0) {
-        const uint32_t row = j0 + m, col = i0 + n;
-        if (row < z.rows && col < z.cols)
-          put_result<OUT>(z, blockIdx.y * z.stride + (uint64_t)row * z.ld + col, z.cols - col < 8 ? (int)(z.cols - col) : 8, v);
-      }
+      if constexpr (LAST) put_result(z, j0 + m, i0 + n, v);
     });
 }
 
@@ -383,27 +435,39 @@ template <int S, int NS, int PL, int OUT, bool TURN> __global__ void __launch_bo
 uint32_t up(uint32_t n, uint32_t to) { return (n + to - 1) / to * to; }
 uint64_t up64(uint64_t n) { return (n + 255) / 256 * 256; }
 
-template <int S, int PL> void products(const NsArgs& a, uint32_t batch, hipStream_t s) {
-  const uint32_t side = a.mp / S;
-  const dim3 grid(tile_grid((uint64_t)side * (side + 1) / 2), batch), block(tile_threads(S));
-  hipLaunchKernelGGL((gram_k<S, 2, PL>), grid, block, 0, s, a);
-  hipLaunchKernelGGL((square_k<S, 2, PL>), grid, block, 0, s, a);
+// The three ways of a product: side of its tiles, stages in flight.
+template <class Go> void way(const NsWay& w, bool two, Go&& go) {
+#define MRR_WAY(s, ns, t) go(std::integral_constant<int, s>(), std::integral_constant<int, ns>(), std::bool_constant<t>())
+  if (two) {
+    if (w.tile == 64) MRR_WAY(64, 4, true);
+    else if (w.stages == 4) MRR_WAY(128, 4, true);
+    else MRR_WAY(128, 2, true);
+  } else {
+    if (w.tile == 64) MRR_WAY(64, 4, false);
+    else if (w.tile == 256) MRR_WAY(256, 2, false);
+    else if (w.stages == 4) MRR_WAY(128, 4, false);
+    else MRR_WAY(128, 2, false);
+  }
+#undef MRR_WAY
 }
 
-template <int S, int PL> void apply(const NsArgs& a, const NsLast& z, uint32_t batch, int out, bool turn, hipStream_t s) {
-  const dim3 grid(tile_grid((uint64_t)(a.mp / S) * (a.np / S)), batch), block(tile_threads(S));
-  auto go = [&](auto o, auto t) { hipLaunchKernelGGL((apply_k<S, 2, PL, o, t>), grid, block, 0, s, a, z); };
-  constexpr std::true_type yes;
-  constexpr std::false_type no;
-  if (out == 0) go(std::integral_constant<int, 0>(), no);
-  else if (out == kF32) turn ? go(std::integral_constant<int, kF32>(), yes) : go(std::integral_constant<int, kF32>(), no);
-  else if (out == kF16) turn ? go(std::integral_constant<int, kF16>(), yes) : go(std::integral_constant<int, kF16>(), no);
-  else turn ? go(std::integral_constant<int, kBF16>(), yes) : go(std::integral_constant<int, kBF16>(), no);
-}
-
-template <int S> void step(const NsArgs& a, const NsLast& z, uint32_t batch, int parts, int out, bool turn, hipStream_t s) {
-  if (parts == 2) products<S, 2>(a, batch, s), apply<S, 2>(a, z, batch, out, turn, s);
-  else products<S, 1>(a, batch, s), apply<S, 1>(a, z, batch, out, turn, s);
+void step(const NsPlan& p, const NsArgs& a, const NsLast& z, uint32_t batch, bool last, bool turn, hipStream_t st) {
+  auto lower = [&](const NsWay& w) {
+    const uint64_t side = a.mp / w.tile;
+    return dim3(tile_grid(side * (side + 1) / 2 * w.splits), batch);
+  };
+  way(p.gram, p.parts == 2, [&](auto s, auto ns, auto two) {
+    hipLaunchKernelGGL((gram_k<s, ns, two>), lower(p.gram), dim3(tile_threads(s)), 0, st, a, p.gram.splits);
+  });
+  way(p.square, p.parts == 2, [&](auto s, auto ns, auto two) {
+    hipLaunchKernelGGL((square_k<s, ns, two>), lower(p.square), dim3(tile_threads(s)), 0, st, a, p.square.splits);
+  });
+  way(p.apply, p.parts == 2, [&](auto s, auto ns, auto two) {
+    const dim3 grid(tile_grid((uint64_t)(a.mp / s) * (a.np / s) * p.apply.splits), batch), block(tile_threads(s));
+    if (!last) hipLaunchKernelGGL((apply_k<s, ns, two, false, false>), grid, block, 0, st, a, z, p.apply.splits);
+    else if (!turn) hipLaunchKernelGGL((apply_k<s, ns, two, true, false>), grid, block, 0, st, a, z, p.apply.splits);
+    else hipLaunchKernelGGL((apply_k<s, ns, two, true, true>), grid, block, 0, st, a, z, p.apply.splits);
+  });
 }
 
 // Workgroups of the passes over a matrix that sum its squares.
@@ -413,45 +477,46 @@ uint32_t sum_parts(uint64_t rows, uint64_t cols) {
 }
 
 // X_0 from the source, its squares summed already; then the steps.
-hipError_t run_steps(const NsCall& c, const NsPlan& p, const NsSource& src, int t, uint32_t parts, const NsLast& z, int out, hipStream_t s) {
+hipError_t run_steps(const NsCall& c, const NsPlan& p, const NsSource& src, int t, uint32_t parts, const NsLast& z, hipStream_t s) {
   uint8_t* ws = (uint8_t*)c.workspace;
   const double* partial = (const double*)(ws + p.partial);
+  const bool two = p.parts == 2, turn = c.rows > c.cols;
   NsArgs a{};
   a.x = a.y = ws + p.x;
   a.o = ws + p.o;
   a.b = ws + p.b;
   a.d = (float*)(ws + p.d);
   a.beta = (float*)(ws + p.beta);
-  a.x_plane = p.x_plane;
+  a.part = (float*)(ws + p.part);
+  a.counter = (uint32_t*)(ws + p.counter);
+  a.counters = p.counters;
+  a.x_plane = two ? 64 : p.x_plane;
   a.x_batch = 2 * p.x_plane;
-  a.o_plane = p.o_plane;
   a.o_batch = p.parts * p.o_plane;
   a.mp = p.mp;
   a.np = p.np;
-  const bool turn = c.rows > c.cols;
-  a.m64 = (uint32_t)((turn ? c.cols : c.rows) + kTileK - 1) / kTileK;
-  a.n64 = (uint32_t)((turn ? c.rows : c.cols) + kTileK - 1) / kTileK;
-  auto begin = [&](auto type) {
+  a.m_stages = p.m_stages;
+  a.n_stages = p.n_stages;
+  auto begin = [&](auto type, auto tw) {
     if (turn) {
-      hipLaunchKernelGGL((turn_k<type>), dim3(a.mp / 64 * (a.np / 64), c.batch), dim3(kSumThreads), 0, s, src, a, partial, parts, c.eps);
+      hipLaunchKernelGGL((turn_k<type, tw>), dim3(a.mp / 64 * (a.np / 64), c.batch), dim3(kSumThreads), 0, s, src, a, partial, parts, c.eps);
     } else {
       const uint64_t blocks = ((uint64_t)a.mp * a.np / 8 + kSumThreads - 1) / kSumThreads;
-      hipLaunchKernelGGL((spread_k<type>), dim3((uint32_t)(blocks < 4096 ? blocks : 4096), c.batch), dim3(kSumThreads), 0, s, src, a, partial,
-                         parts, c.eps);
+      hipLaunchKernelGGL((spread_k<type, tw>), dim3((uint32_t)(blocks < 4096 ? blocks : 4096), c.batch), dim3(kSumThreads), 0, s, src, a,
+                         partial, parts, c.eps);
     }
   };
-  if (t == kF32) begin(std::integral_constant<int, kF32>());
-  else if (t == kF16) begin(std::integral_constant<int, kF16>());
-  else begin(std::integral_constant<int, kBF16>());
+  auto typed = [&](auto type) { two ? begin(type, std::true_type()) : begin(type, std::false_type()); };
+  if (t == kF32) typed(std::integral_constant<int, kF32>());
+  else if (t == kF16) typed(std::integral_constant<int, kF16>());
+  else typed(std::integral_constant<int, kBF16>());
   for (int k = 0; k < c.steps; ++k) {
     a.x = ws + p.x + (k % 2) * p.x_bytes;
     a.y = ws + p.x + ((k + 1) % 2) * p.x_bytes;
     a.ca = c.coefficients[3 * k];
     a.cb = c.coefficients[3 * k + 1];
     a.cc = c.coefficients[3 * k + 2];
-    const int to = k + 1 == c.steps ? out : 0;
-    if (p.tile == 256) step<256>(a, z, c.batch, p.parts, to, turn, s);
-    else step<128>(a, z, c.batch, p.parts, to, turn, s);
+    step(p, a, z, c.batch, k + 1 == c.steps, turn, s);
   }
   return hipGetLastError();
 }
@@ -491,18 +556,69 @@ bool ns_bounds(const float* co, int steps) {
   return true;
 }
 
+// The way of a product that a model of its time finds shortest: `tiles(s)` tiles of side s,
+// in `stages` stages.  The times were measured with 256 CUs: a stage of a workgroup that has
+// its CU to itself (64: what one CU draws from beyond its L2, 16 KiB in 0.25 us, bounds
+// it, and neither more stages in flight nor fewer waits for LDS change that), of all that a
+// CU holds, and what a workgroup's launch, first loads and end take.  520 x 1600 f32: 156 us
+// with tiles of 64, 408 with 128; 2048 x 2048 bf16 394 with 64, 365 with 128 and four stages in
+// flight, 429 with two; 4096 x 4096 bf16 1815 with 128, 1467 with 256.  Splits of k: 8192 x 256 bf16
+// 194 us without, 125 with 8 in the gram product.
+template <class Tiles> static NsWay choose(uint32_t pad, bool two, uint64_t batch, uint32_t stages, Tiles&& tiles) {
+  struct Kind {
+    uint32_t tile, ns, per_cu;
+    double alone, full, rest, join;  // microseconds
+  };
+  static const Kind one[] = {{64, 4, 2, 0.23, 0.33, 4.0, 0.8}, {128, 4, 1, 0.45, 0.65, 5.5, 4.0}, {128, 2, 2, 0.62, 0.90, 5.5, 4.0},
+                             {256, 2, 1, 1.43, 1.43, 14.0, 0.0}};
+  static const Kind parts2[] = {{64, 4, 2, 0.23, 0.42, 4.0, 0.8}, {128, 4, 1, 0.55, 0.75, 5.5, 4.0}, {128, 2, 2, 0.65, 1.04, 5.5, 4.0}};
+  const Kind* kinds = two ? parts2 : one;
+  NsWay best{};
+  double least = 1e30;
+  for (int i = 0; i < (two ? 3 : 4); ++i) {
+    const Kind& k = kinds[i];
+    if (k.tile > pad) continue;
+    for (uint32_t splits = 1; splits <= (k.tile == 256 ? 1u : 8u) && splits <= stages; splits *= 2) {
+      const uint64_t groups = tiles(k.tile) * batch * splits, slots = 256 * k.per_cu, rounds = groups / slots, rest = groups % slots;
+      if (splits > 1 && groups > 512) break;
+      const double per = (stages + splits - 1) / splits;
+      const double last = rest ? per * (rest > 256 || rounds ? k.full : k.alone) + k.rest : 0.0;
+      const double t = rounds * (per * k.full + k.rest) + last + (splits > 1 ? 2.0 + splits * k.join : 0.0);
+      if (t < least) least = t, best = {k.tile, k.ns, splits, t};
+    }
+  }
+  return best;
+}
+
 NsPlan ns_plan(uint64_t rows, uint64_t cols, uint64_t batch, int parts, bool with_u) {
   NsPlan p{};
   const uint32_t m = (uint32_t)(rows < cols ? rows : cols), n = (uint32_t)(rows < cols ? cols : rows);
+  const bool two = parts == 2;
+  const uint32_t deep = two ? 32 : 64;  // k of a stage
   p.parts = parts;
-  const uint64_t big = (uint64_t)(up(m, 256) / 256) * (up(n, 256) / 256) * batch;
-  p.tile = big >= 200 ? 256 : 128;
-  p.mp = up(m, p.tile);
-  p.np = up(n, p.tile);
+  p.m_stages = (m + deep - 1) / deep;
+  p.n_stages = (n + deep - 1) / deep;
+  double least = 1e30;
+  for (uint32_t pad = 64; pad <= (two ? 128u : 256u); pad *= 2) {
+    const uint32_t mp = up(m, pad), np = up(n, pad);
+    auto lower = [&](uint32_t s) { return (uint64_t)(mp / s) * (mp / s + 1) / 2; };
+    const NsWay g = choose(pad, two, batch, p.n_stages, lower), q = choose(pad, two, batch, p.m_stages, lower),
+                x = choose(pad, two, batch, p.m_stages, [&](uint32_t s) { return (uint64_t)(mp / s) * (np / s); });
+    const double t = g.us + q.us + x.us;
+    if (t < least) least = t, p.gram = g, p.square = q, p.apply = x, p.mp = mp, p.np = np;
+  }
   p.x_plane = (uint64_t)p.mp * p.np * 2;
   p.o_plane = (uint64_t)p.mp * p.mp * 2;
   p.x_bytes = 2 * p.x_plane * batch;
   const uint64_t o_bytes = parts * p.o_plane * batch;
+  auto part_bytes = [&](const NsWay& w, uint64_t tiles) {
+    if (w.splits < 2) return (uint64_t)0;
+    if (tiles > p.counters) p.counters = (uint32_t)tiles;
+    return tiles * batch * w.splits * w.tile * w.tile * 4;
+  };
+  auto lower = [&](const NsWay& w) { return part_bytes(w, (uint64_t)(p.mp / w.tile) * (p.mp / w.tile + 1) / 2); };
+  uint64_t most = lower(p.gram);
+  for (uint64_t b : {lower(p.square), part_bytes(p.apply, (uint64_t)(p.mp / p.apply.tile) * (p.np / p.apply.tile))}) most = b > most ? b : most;
   uint64_t at = 0;
   auto take = [&](uint64_t bytes) {
     const uint64_t here = at;
@@ -515,6 +631,8 @@ NsPlan ns_plan(uint64_t rows, uint64_t cols, uint64_t batch, int parts, bool wit
   p.d = take((uint64_t)p.mp * 4 * batch);
   p.beta = take((uint64_t)p.mp * 4 * batch);
   p.partial = take((uint64_t)kSumThreads * 8 * batch);
+  p.part = take(most);
+  p.counter = take((uint64_t)p.counters * 4 * batch);
   p.u = with_u ? take(rows * cols * 4 * batch) : 0;
   p.bytes = at;
   return p;
@@ -534,7 +652,8 @@ hipError_t launch_orthogonalize(const NsCall& c, const NsPlan& p, int t, hipStre
   z.cols = (uint32_t)c.cols;
   z.ld = c.ld_out;
   z.stride = c.stride_out;
-  return run_steps(c, p, src, t, parts, z, t, s);
+  z.type = t;
+  return run_steps(c, p, src, t, parts, z, s);
 }
 
 hipError_t launch_muon(const NsCall& c, const NsPlan& p, MuonArgs m, NsLast z, int tg, int tw, hipStream_t s) {
@@ -553,7 +672,8 @@ hipError_t launch_muon(const NsCall& c, const NsPlan& p, MuonArgs m, NsLast z, i
   else hipLaunchKernelGGL(momentum_k<kBF16>, grid, block, 0, s, m, partial);
   z.rows = (uint32_t)c.rows;
   z.cols = (uint32_t)c.cols;
-  return run_steps(c, p, src, kF32, parts, z, tw, s);
+  z.type = tw;
+  return run_steps(c, p, src, kF32, parts, z, s);
 }
 
 }  // namespace mrr
