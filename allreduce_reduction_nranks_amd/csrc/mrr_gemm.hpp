@@ -14,7 +14,8 @@
 // Two sizes of tile, S x S.  256: 8 waves, 2 a SIMD, each with 128 x 64 accumulators;
 // a stage's products take 2048 cycles of a CU's matrix units against 1536 of LDS reads.
 // 128: 4 waves with 64 x 64 each, two workgroups a CU; as many cycles of LDS reads as of
-// products, but four times the workgroups, for calls with too few large tiles.  Matrix
+// products, but four times the workgroups, for calls with too few large tiles.  Of row
+// operands alone also 192 (4 waves with 96 x 96) and 64 (4 waves, 32 x 32).  Matrix
 // instructions are 32x32x16.  The fragments of the
 // next 16 k are read while those of the present ones multiply, over the end of a
 // stage as well: the one barrier of a stage stands before its last quarter, when
@@ -363,8 +364,8 @@ template <int T, bool ACOL, bool BCOL, int S, int NS, bool TWO = false> struct T
   template <int W, bool COLS, class Pre, class Row, class Col>
   __device__ __forceinline__ void both_out(lds8* lds, int j, Pre&& pre, Row&& row, Col&& col) const {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    constexpr int kRow = FM * 128, kUnits = FM * 32 / W, kSwap = FM == 1 ? 7 : 15;
-    constexpr int kTurns = 32 * kUnits / 64, kAhead = kTurns < 4 ? kTurns : 4;
+    constexpr int kRow = FM * 128, kUnits = FM * 32 / W, kSwap = FM % 2 ? 7 : 15;
+    constexpr int kTurns = 32 * kUnits / 64, kAhead = kTurns % 4 == 0 ? 4 : kTurns % 3 == 0 ? 3 : kTurns;
     lds8* mine = lds + wave * (32 * kRow);
     auto settle = [] {
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");

@@ -106,6 +106,7 @@ template <int T> __device__ __forceinline__ void store8(void* p, int n, const fl
 // ---- what comes before the products ----------------------------------------------------
 // Sums of squares are f64: f32 would overflow on large gradients and vanish on small ones.
 constexpr int kSumThreads = 256;
+constexpr uint32_t kMaxParts = 1024;  // workgroups that sum a matrix's squares
 
 __device__ __forceinline__ void block_sum(double s, double* to) {
   __shared__ double lds[kSumThreads / 64];
@@ -137,6 +138,7 @@ template <int T> __global__ void __launch_bounds__(kSumThreads) squares_k(NsSour
 
 // g = scale sum of the ranks' gradients (rank order, f32), m' = mu m + g, and the squares of
 // u = g + mu m' or m'.  u has a buffer of its own with `nesterov` only.
+constexpr int kAtOnce = 4;  // ranks whose loads are in flight together
 template <int T> __global__ void __launch_bounds__(kSumThreads) momentum_k(MuonArgs a, double* partial) {
   const uint64_t units = (a.cols + 7) / 8, total = units * a.rows, y = blockIdx.y;
   double s = 0.0;
@@ -145,16 +147,24 @@ template <int T> __global__ void __launch_bounds__(kSumThreads) momentum_k(MuonA
     const int n = a.cols - c < 8 ? (int)(a.cols - c) : 8;
     const uint64_t from = y * a.stride_grad + row * a.ld_grad + c, to = y * a.stride_weight + row * a.ld_weight + c;
     float g[8], m[8];
-    load8<T>(at<T>(a.grads[0], from), n, g);
-    for (int r = 1; r < a.nranks; ++r) {
-      float x[8];
-      load8<T>(at<T>(a.grads[r], from), n, x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) g[e] += x[e];
+    for (int e = 0; e < 8; ++e) g[e] = -0.0f, m[e] = 0.0f;  // (the first sum is then exactly the first gradient)
+    if (a.momentum) load8<kF32>(a.momentum + to, n, m);
+    for (int r0 = 0; r0 < a.nranks; r0 += kAtOnce) {
+      float x[kAtOnce][8];
+#pragma unroll
+      for (int r = 0; r < kAtOnce; ++r)
+        if (r0 + r < a.nranks) load8<T>(at<T>(a.grads[r0 + r], from), n, x[r]);
+#pragma unroll
+      for (int r = 0; r < kAtOnce; ++r) {
+        if (r0 + r < a.nranks) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) g[e] += x[r][e];
+        }
+      }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) g[e] *= a.grad_scale, m[e] = 0.0f;
-    if (a.momentum) load8<kF32>(a.momentum + to, n, m);
+    for (int e = 0; e < 8; ++e) g[e] *= a.grad_scale;
 #pragma unroll
     for (int e = 0; e < 8; ++e) m[e] = __builtin_fmaf(a.mu, m[e], g[e]);
     store8<kF32>(a.momentum_out + to, n, m);
@@ -172,7 +182,10 @@ template <int T> __global__ void __launch_bounds__(kSumThreads) momentum_k(MuonA
 // 1 / (norm + eps), times X's scale; every thread of the workgroup has it.
 __device__ __forceinline__ float inverse_norm(const double* partial, uint32_t parts, float eps) {
   __shared__ double lds[kSumThreads / 64];
-  double s = threadIdx.x < parts ? partial[(uint64_t)blockIdx.y * parts + threadIdx.x] : 0.0;
+  double s = 0.0;
+#pragma unroll
+  for (uint32_t i = 0; i < kMaxParts; i += kSumThreads)
+    if (i + threadIdx.x < parts) s += partial[(uint64_t)blockIdx.y * parts + i + threadIdx.x];
 #pragma unroll
   for (int m = 32; m > 0; m >>= 1) s += __shfl_xor(s, m);
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = s;
@@ -244,41 +257,64 @@ template <int T, bool TWO> __global__ void __launch_bounds__(kSumThreads) turn_k
 
 // ---- the products -------------------------------------------------------------------
 // The id-th tile (row, column <= row) on or below the diagonal, `side` tiles a side, and one
-// of `splits` parts of k; XCDs get contiguous runs of the rows.
+// of `splits` parts of k.  Each XCD gets a contiguous run of an order that walks 6 rows at a
+// time, column by column, so that the tiles it works on together share operands in its L2.
 __device__ __forceinline__ bool lower_tile(uint32_t id, uint32_t side, uint32_t splits, uint32_t& r, uint32_t& c, uint32_t& split) {
   const uint32_t tiles = side * (side + 1) / 2, total = tiles * splits, per = total / 8, extra = total % 8, x = id & 7, j = id >> 3;
   if (j >= per + (x < extra ? 1u : 0u)) return false;
   uint32_t t = x * per + (x < extra ? x : extra) + j;
   split = t / tiles;
   t -= split * tiles;
-  r = (uint32_t)((__builtin_sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
-  while (r * (r + 1) / 2 > t) --r;
-  while ((r + 1) * (r + 2) / 2 <= t) ++r;
-  c = t - r * (r + 1) / 2;
+  constexpr uint32_t G = 6;
+  uint32_t r0 = 0, rows = side < G ? side : G;
+  // a group of rows: r0 whole columns, then its triangle
+  while (t >= r0 * rows + rows * (rows + 1) / 2) {
+    t -= r0 * rows + rows * (rows + 1) / 2;
+    r0 += rows;
+    rows = side - r0 < G ? side - r0 : G;
+  }
+  if (t < r0 * rows) {
+    c = t / rows;
+    r = r0 + t % rows;
+  } else {
+    t -= r0 * rows;
+    c = r0;
+    for (uint32_t n = rows; t >= n; --n) t -= n, ++c;
+    r = c + t;
+  }
+  r = __builtin_amdgcn_readfirstlane(r);
+  c = __builtin_amdgcn_readfirstlane(c);
   return true;
 }
 
 // The sums of `tile`'s splits, in the workgroup that comes last: true there.
-// (Calls for tiles of 256 have enough of them.)
+// (Calls for tiles of 192 or more have enough of them.)
 template <int S, class Prod> __device__ __forceinline__ bool whole(Prod& p, const NsArgs& a, uint32_t tile, uint32_t tiles, uint32_t split,
                                                                    uint32_t splits, lds8* lds) {
   __syncthreads();
-  if (S == 256 || splits == 1) return true;
+  if (S >= 192 || splits == 1) return true;
   const uint64_t of = (uint64_t)blockIdx.y * tiles + tile;
   return p.join(lds, a.part + of * splits * S * S, a.counter + blockIdx.y * a.counters + tile, split, splits);
 }
 
 // A tile of P P^T for P = X (A = X X^T) or O (O O): both operands are rows of P, ld bytes
 // apart, of `stages` 128 bytes.
-template <class Prod, int S> __device__ __forceinline__ void square_tile(Prod& p, const uint8_t* base, uint64_t ld, uint32_t stages, uint32_t m0,
-                                                                         uint32_t n0, uint32_t split, uint32_t splits, lds8* lds) {
+template <class Prod, int S> __device__ __forceinline__ void square_tile(Prod& p, const uint8_t* base, uint64_t ld, uint32_t stages, uint32_t rows,
+                                                                         uint32_t m0, uint32_t n0, uint32_t split, uint32_t splits, lds8* lds) {
   const int tid = threadIdx.x;
   uint32_t k = stages * split / splits;
   const uint32_t k1 = stages * (split + 1) / splits;
   auto src = [&](int s, const uint8_t*& pa, const uint8_t*& pb, uint32_t (&oa)[Prod::L], uint32_t (&ob)[Prod::L]) {
     if (s == 0) {
 #pragma unroll
-      for (int i = 0; i < Prod::L; ++i) oa[i] = ob[i] = row_src_row<S>(tid, i) * (uint32_t)ld + row_src_chunk(tid) * 16;
+      for (int i = 0; i < Prod::L; ++i) {
+        const uint32_t r = row_src_row<S>(tid, i);
+        oa[i] = ob[i] = r * (uint32_t)ld + row_src_chunk(tid) * 16;
+        if (S == 192) {  // (of sides that 192 does not divide: rows past the last are the last)
+          oa[i] = (m0 + r < rows ? r : rows - 1 - m0) * (uint32_t)ld + row_src_chunk(tid) * 16;
+          ob[i] = (n0 + r < rows ? r : rows - 1 - n0) * (uint32_t)ld + row_src_chunk(tid) * 16;
+        }
+      }
     }
     const uint8_t* at = base + (uint64_t)k * 128;
     pa = at + m0 * ld;
@@ -293,11 +329,11 @@ template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_thread
   typedef Tile<kF16, false, false, S, NS, TWO> Prod;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
   uint32_t r, c, split;
-  const uint32_t side = a.mp / S;
+  const uint32_t side = (a.mp + S - 1) / S;
   if (!lower_tile(blockIdx.x, side, splits, r, c, split)) return;
   const uint32_t m0 = r * S, n0 = c * S;
   Prod p;
-  square_tile<Prod, S>(p, a.x + blockIdx.y * a.x_batch, (uint64_t)a.np * (TWO ? 4 : 2), a.n_stages, m0, n0, split, splits, (lds8*)lds);
+  square_tile<Prod, S>(p, a.x + blockIdx.y * a.x_batch, (uint64_t)a.np * (TWO ? 4 : 2), a.n_stages, a.mp, m0, n0, split, splits, (lds8*)lds);
   if (!whole<S>(p, a, r * (r + 1) / 2 + c, side * (side + 1) / 2, split, splits, (lds8*)lds)) return;
   uint8_t* o = a.o + blockIdx.y * a.o_batch;
   float* d = a.d + blockIdx.y * a.mp;
@@ -305,6 +341,7 @@ template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_thread
 #pragma unroll
   for (int j = 0; j < Prod::FN; ++j)
     p.template both_out<8, true>((lds8*)lds, j, [](int, int) { return 0; }, [&](int n, int m, float (&x)[8], int) {
+      if (S == 192 && (n0 + n >= a.mp || m0 + m >= a.mp)) return;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         x[e] *= unscale;
@@ -313,7 +350,7 @@ template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_thread
       }
       store_operand<TWO>(o + place<TWO>(n0 + n, m0 + m, a.mp), x);
     }, [&](int m, int n, const float (&x)[8]) {
-      if (r != c) store_operand<TWO>(o + place<TWO>(m0 + m, n0 + n, a.mp), x);
+      if (r != c && (S != 192 || m0 + m < a.mp)) store_operand<TWO>(o + place<TWO>(m0 + m, n0 + n, a.mp), x);
     });
 }
 
@@ -322,7 +359,7 @@ template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_thread
   typedef Tile<kF16, false, false, S, NS, TWO> Prod;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
   uint32_t r, c, split;
-  const uint32_t side = a.mp / S;
+  const uint32_t side = (a.mp + S - 1) / S;
   if (!lower_tile(blockIdx.x, side, splits, r, c, split)) return;
   const uint32_t m0 = r * S, n0 = c * S;
   const uint8_t* o = a.o + blockIdx.y * a.o_batch;
@@ -330,7 +367,7 @@ template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_thread
   const float* d = a.d + blockIdx.y * a.mp;
   float* beta = a.beta + blockIdx.y * a.mp;
   Prod p;
-  square_tile<Prod, S>(p, o, (uint64_t)a.mp * (TWO ? 4 : 2), a.m_stages, m0, n0, split, splits, (lds8*)lds);
+  square_tile<Prod, S>(p, o, (uint64_t)a.mp * (TWO ? 4 : 2), a.m_stages, a.mp, m0, n0, split, splits, (lds8*)lds);
   if (!whole<S>(p, a, r * (r + 1) / 2 + c, side * (side + 1) / 2, split, splits, (lds8*)lds)) return;
   constexpr float unscale = 1.0f / (kScaleA * kScaleA);
   struct In {
@@ -341,9 +378,12 @@ template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_thread
 #pragma unroll
   for (int j = 0; j < Prod::FN; ++j)
     p.template both_out<8, true>((lds8*)lds, j, [&](int n, int m) {
-      const f32x4* dm = reinterpret_cast<const f32x4*>(d + m0 + m);
-      return In{load_operand<TWO>(o + place<TWO>(n0 + n, m0 + m, a.mp)), {dm[0], dm[1]}, d[n0 + n]};
+      const bool in = S != 192 || (n0 + n < a.mp && m0 + m < a.mp);
+      const uint32_t row = in ? n0 + n : n0, col = in ? m0 + m : m0;
+      const f32x4* dm = reinterpret_cast<const f32x4*>(d + col);
+      return In{load_operand<TWO>(o + place<TWO>(row, col, a.mp)), {dm[0], dm[1]}, d[row]};
     }, [&](int n, int m, float (&x)[8], const In& in) {
+      if (S == 192 && (n0 + n >= a.mp || m0 + m >= a.mp)) return;
       float y[8];
       if constexpr (TWO) join8(in.o, y);
       else decode16<kF16>(in.o.hi, y);
@@ -355,7 +395,7 @@ template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_thread
       }
       store_operand<TWO>(b + place<TWO>(n0 + n, m0 + m, a.mp), x);
     }, [&](int m, int n, const float (&x)[8]) {
-      if (r != c) store_operand<TWO>(b + place<TWO>(m0 + m, n0 + n, a.mp), x);
+      if (r != c && (S != 192 || m0 + m < a.mp)) store_operand<TWO>(b + place<TWO>(m0 + m, n0 + n, a.mp), x);
     });
 }
 
@@ -435,34 +475,37 @@ __global__ void __launch_bounds__(tile_threads(S)) apply_k(NsArgs a, NsLast z, u
 uint32_t up(uint32_t n, uint32_t to) { return (n + to - 1) / to * to; }
 uint64_t up64(uint64_t n) { return (n + 255) / 256 * 256; }
 
-// The three ways of a product: side of its tiles, stages in flight.
-template <class Go> void way(const NsWay& w, bool two, Go&& go) {
-#define MRR_WAY(s, ns, t) go(std::integral_constant<int, s>(), std::integral_constant<int, ns>(), std::bool_constant<t>())
-  if (two) {
-    if (w.tile == 64) MRR_WAY(64, 4, true);
-    else if (w.stages == 4) MRR_WAY(128, 4, true);
-    else MRR_WAY(128, 2, true);
-  } else {
-    if (w.tile == 64) MRR_WAY(64, 4, false);
-    else if (w.tile == 256) MRR_WAY(256, 2, false);
-    else if (w.stages == 4) MRR_WAY(128, 4, false);
-    else MRR_WAY(128, 2, false);
-  }
+// The ways of a product: side of its tiles, stages in flight.  SQUARE: of row operands alone.
+template <bool SQUARE, class Go> void way(const NsWay& w, bool two, Go&& go) {
+  auto pick = [&](auto t) {
+#define MRR_WAY(s, ns) go(std::integral_constant<int, s>(), std::integral_constant<int, ns>(), t)
+    if (w.tile == 64) MRR_WAY(64, 4);
+    else if (w.tile == 128 && w.stages == 4) MRR_WAY(128, 4);
+    else if (w.tile == 128) MRR_WAY(128, 2);
+    if constexpr (SQUARE) {
+      if (w.tile == 192) MRR_WAY(192, 3);
+    }
+    if constexpr (!decltype(t)::value) {
+      if (w.tile == 256) MRR_WAY(256, 2);
+    }
 #undef MRR_WAY
+  };
+  if (two) pick(std::true_type());
+  else pick(std::false_type());
 }
 
 void step(const NsPlan& p, const NsArgs& a, const NsLast& z, uint32_t batch, bool last, bool turn, hipStream_t st) {
   auto lower = [&](const NsWay& w) {
-    const uint64_t side = a.mp / w.tile;
+    const uint64_t side = (a.mp + w.tile - 1) / w.tile;
     return dim3(tile_grid(side * (side + 1) / 2 * w.splits), batch);
   };
-  way(p.gram, p.parts == 2, [&](auto s, auto ns, auto two) {
+  way<true>(p.gram, p.parts == 2, [&](auto s, auto ns, auto two) {
     hipLaunchKernelGGL((gram_k<s, ns, two>), lower(p.gram), dim3(tile_threads(s)), 0, st, a, p.gram.splits);
   });
-  way(p.square, p.parts == 2, [&](auto s, auto ns, auto two) {
+  way<true>(p.square, p.parts == 2, [&](auto s, auto ns, auto two) {
     hipLaunchKernelGGL((square_k<s, ns, two>), lower(p.square), dim3(tile_threads(s)), 0, st, a, p.square.splits);
   });
-  way(p.apply, p.parts == 2, [&](auto s, auto ns, auto two) {
+  way<false>(p.apply, p.parts == 2, [&](auto s, auto ns, auto two) {
     const dim3 grid(tile_grid((uint64_t)(a.mp / s) * (a.np / s) * p.apply.splits), batch), block(tile_threads(s));
     if (!last) hipLaunchKernelGGL((apply_k<s, ns, two, false, false>), grid, block, 0, st, a, z, p.apply.splits);
     else if (!turn) hipLaunchKernelGGL((apply_k<s, ns, two, true, false>), grid, block, 0, st, a, z, p.apply.splits);
@@ -473,7 +516,7 @@ void step(const NsPlan& p, const NsArgs& a, const NsLast& z, uint32_t batch, boo
 // Workgroups of the passes over a matrix that sum its squares.
 uint32_t sum_parts(uint64_t rows, uint64_t cols) {
   const uint64_t n = rows * cols / (kSumThreads * 32) + 1;
-  return n < kSumThreads ? (uint32_t)n : (uint32_t)kSumThreads;
+  return n < kMaxParts ? (uint32_t)n : kMaxParts;
 }
 
 // X_0 from the source, its squares summed already; then the steps.
@@ -562,23 +605,25 @@ bool ns_bounds(const float* co, int steps) {
 // it, and neither more stages in flight nor fewer waits for LDS change that), of all that a
 // CU holds, and what a workgroup's launch, first loads and end take.  520 x 1600 f32: 156 us
 // with tiles of 64, 408 with 128; 2048 x 2048 bf16 394 with 64, 365 with 128 and four stages in
-// flight, 429 with two; 4096 x 4096 bf16 1815 with 128, 1467 with 256.  Splits of k: 8192 x 256 bf16
+// flight, 429 with two; 4096 x 4096 bf16 1815 with 128, 1490 with 256, 1450 with 192 for the
+// symmetric products (the 136 tiles of 256 leave CUs idle, the 253 of 192 do not).  Splits of k: 8192 x 256 bf16
 // 194 us without, 125 with 8 in the gram product.
-template <class Tiles> static NsWay choose(uint32_t pad, bool two, uint64_t batch, uint32_t stages, Tiles&& tiles) {
+template <class Tiles> static NsWay choose(uint32_t pad, bool two, bool square, uint64_t batch, uint32_t stages, Tiles&& tiles) {
   struct Kind {
     uint32_t tile, ns, per_cu;
     double alone, full, rest, join;  // microseconds
   };
   static const Kind one[] = {{64, 4, 2, 0.23, 0.33, 4.0, 0.8}, {128, 4, 1, 0.45, 0.65, 5.5, 4.0}, {128, 2, 2, 0.62, 0.90, 5.5, 4.0},
-                             {256, 2, 1, 1.43, 1.43, 14.0, 0.0}};
-  static const Kind parts2[] = {{64, 4, 2, 0.23, 0.42, 4.0, 0.8}, {128, 4, 1, 0.55, 0.75, 5.5, 4.0}, {128, 2, 2, 0.65, 1.04, 5.5, 4.0}};
+                             {192, 3, 1, 0.98, 0.98, 20.0, 0.0}, {256, 2, 1, 1.43, 1.43, 14.0, 0.0}};
+  static const Kind parts2[] = {{64, 4, 2, 0.23, 0.42, 4.0, 0.8}, {128, 4, 1, 0.55, 0.75, 5.5, 4.0}, {128, 2, 2, 0.65, 1.04, 5.5, 4.0},
+                                 {192, 3, 1, 1.60, 1.60, 20.0, 0.0}};
   const Kind* kinds = two ? parts2 : one;
   NsWay best{};
   double least = 1e30;
-  for (int i = 0; i < (two ? 3 : 4); ++i) {
+  for (int i = 0; i < (two ? 4 : 5); ++i) {
     const Kind& k = kinds[i];
-    if (k.tile > pad) continue;
-    for (uint32_t splits = 1; splits <= (k.tile == 256 ? 1u : 8u) && splits <= stages; splits *= 2) {
+    if (k.tile == 192 ? !square : k.tile > pad) continue;
+    for (uint32_t splits = 1; splits <= (k.tile >= 192 ? 1u : 8u) && splits <= stages; splits *= 2) {
       const uint64_t groups = tiles(k.tile) * batch * splits, slots = 256 * k.per_cu, rounds = groups / slots, rest = groups % slots;
       if (splits > 1 && groups > 512) break;
       const double per = (stages + splits - 1) / splits;
@@ -601,9 +646,9 @@ NsPlan ns_plan(uint64_t rows, uint64_t cols, uint64_t batch, int parts, bool wit
   double least = 1e30;
   for (uint32_t pad = 64; pad <= (two ? 128u : 256u); pad *= 2) {
     const uint32_t mp = up(m, pad), np = up(n, pad);
-    auto lower = [&](uint32_t s) { return (uint64_t)(mp / s) * (mp / s + 1) / 2; };
-    const NsWay g = choose(pad, two, batch, p.n_stages, lower), q = choose(pad, two, batch, p.m_stages, lower),
-                x = choose(pad, two, batch, p.m_stages, [&](uint32_t s) { return (uint64_t)(mp / s) * (np / s); });
+    auto lower = [&](uint32_t s) { return (uint64_t)((mp + s - 1) / s) * ((mp + s - 1) / s + 1) / 2; };
+    const NsWay g = choose(pad, two, true, batch, p.n_stages, lower), q = choose(pad, two, true, batch, p.m_stages, lower),
+                x = choose(pad, two, false, batch, p.m_stages, [&](uint32_t s) { return (uint64_t)(mp / s) * (np / s); });
     const double t = g.us + q.us + x.us;
     if (t < least) least = t, p.gram = g, p.square = q, p.apply = x, p.mp = mp, p.np = np;
   }
@@ -630,7 +675,7 @@ NsPlan ns_plan(uint64_t rows, uint64_t cols, uint64_t batch, int parts, bool wit
   p.b = take(o_bytes);
   p.d = take((uint64_t)p.mp * 4 * batch);
   p.beta = take((uint64_t)p.mp * 4 * batch);
-  p.partial = take((uint64_t)kSumThreads * 8 * batch);
+  p.partial = take((uint64_t)kMaxParts * 8 * batch);
   p.part = take(most);
   p.counter = take((uint64_t)p.counters * 4 * batch);
   p.u = with_u ? take(rows * cols * 4 * batch) : 0;

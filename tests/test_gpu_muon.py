@@ -95,8 +95,9 @@ def modelled_steps(x, two, co, steps):
         m = product32(xp, xp)
         d = m.diagonal().clone()
         o = part(m - torch.diag(d), 512.0)
-        n = r32(r32(b * o) + r32(c * r32(product32(o, o) + r32(r32(d[:, None] + d[None]) * o))))
-        beta = r32(a + r32(r32(b * d) + r32(c * r32(product32(o, o).diagonal() + r32(d * d)))))
+        oo = product32(o, o)
+        n = r32(r32(b * o) + r32(c * r32(oo + r32(r32(d[:, None] + d[None]) * o))))
+        beta = r32(a + r32(r32(b * d) + r32(c * r32(oo.diagonal() + r32(d * d)))))
         n.fill_diagonal_(0)
         x = r32(r32(beta[:, None] * x) + product32(part(n, 64.0), xp.T.contiguous()))
         if k + 1 < steps:
@@ -142,6 +143,16 @@ def test_orthogonalize(rows, cols, batch, t, products):
     rel, two = torch.finfo(TYPES[t]).eps / 2, is_two(rows, cols, t, products)
     for k in sorted({0, batch // 2, batch - 1}):
         close(out[k], exact(x[k]), modelled(x[k], two), rel, "matrix %d" % k)
+
+
+@pytest.mark.parametrize("t,n", [("bf16", 3900), ("f32", 4001)])
+def test_tiles_that_the_padded_side_is_no_multiple_of(t, n):
+    announce("orth large", t, n)
+    g = seeded(n)
+    x = gradient(g, n, n + 100, noise=0.5).to(TYPES[t])
+    out = torch.full_like(x, float("nan"))
+    mrr.check(orth(x, out, n, n + 100, 1, t))
+    close(out, exact(x), modelled(x, t != "bf16"), torch.finfo(TYPES[t]).eps / 2, "large")
 
 
 @pytest.mark.parametrize("kind", ["noise", "few directions", "steep", "one column", "equal rows"])
