@@ -607,13 +607,13 @@ def _head_args(xs, tokens, heads, dim, lds, strides, esize, what: str):
         return None
     if len(xs) != 3:
         raise ValueError("%s has %d entries, not 3" % (what, len(xs)))
-    ptrs = []
+    ptrs = [0, 0, 0]
     for k, x in enumerate(xs):
-        if x is None or not heads[k]:
-            ptrs.append(0)
+        n = heads[k]
+        if x is None or not n:
             continue
-        need = ((tokens - 1) * lds[k] + (heads[k] - 1) * strides[k] + dim) * esize if tokens > 0 and dim > 0 else 0
-        ptrs.append(_rows_arg(x, need, "%s[%d]" % (what, k)))
+        need = ((tokens - 1) * lds[k] + (n - 1) * strides[k] + dim) * esize if tokens > 0 and dim > 0 else 0
+        ptrs[k] = _rows_arg(x, need, "%s[%d]" % (what, k) if type(x) is int else what)
     return _pack(ptrs)
 
 

@@ -145,7 +145,7 @@ def test_orthogonalize(rows, cols, batch, t, products):
         close(out[k], exact(x[k]), modelled(x[k], two), rel, "matrix %d" % k)
 
 
-@pytest.mark.parametrize("t,n", [("bf16", 3900), ("f32", 4001)])
+@pytest.mark.parametrize("t,n", [("bf16", 4001), ("f32", 4001)])
 def test_tiles_that_the_padded_side_is_no_multiple_of(t, n):
     announce("orth large", t, n)
     g = seeded(n)
