@@ -324,23 +324,21 @@ template <class Prod, int S> __device__ __forceinline__ void square_tile(Prod& p
   p.run((int)(k1 - k), lds, src);
 }
 
-// A = X X^T: what lies beside the diagonal to O, the diagonal to d.
-template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_threads(S)) gram_k(NsArgs a, uint32_t splits) {
+// A = X X^T, tile (r, c): what lies beside the diagonal to O, the diagonal to d.  False in a
+// workgroup whose split is not the last.
+template <int S, int NS, bool TWO> __device__ __forceinline__ bool gram_tile(const NsArgs& a, uint32_t r, uint32_t c, uint32_t split,
+                                                                             uint32_t splits, lds8* lds) {
   typedef Tile<kF16, false, false, S, NS, TWO> Prod;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
-  uint32_t r, c, split;
-  const uint32_t side = (a.mp + S - 1) / S;
-  if (!lower_tile(blockIdx.x, side, splits, r, c, split)) return;
-  const uint32_t m0 = r * S, n0 = c * S;
+  const uint32_t m0 = r * S, n0 = c * S, side = (a.mp + S - 1) / S;
   Prod p;
-  square_tile<Prod, S>(p, a.x + blockIdx.y * a.x_batch, (uint64_t)a.np * (TWO ? 4 : 2), a.n_stages, a.mp, m0, n0, split, splits, (lds8*)lds);
-  if (!whole<S>(p, a, r * (r + 1) / 2 + c, side * (side + 1) / 2, split, splits, (lds8*)lds)) return;
+  square_tile<Prod, S>(p, a.x + blockIdx.y * a.x_batch, (uint64_t)a.np * (TWO ? 4 : 2), a.n_stages, a.mp, m0, n0, split, splits, lds);
+  if (!whole<S>(p, a, r * (r + 1) / 2 + c, side * (side + 1) / 2, split, splits, lds)) return false;
   uint8_t* o = a.o + blockIdx.y * a.o_batch;
   float* d = a.d + blockIdx.y * a.mp;
   constexpr float unscale = 1.0f / (kScaleX * kScaleX);
 #pragma unroll
   for (int j = 0; j < Prod::FN; ++j)
-    p.template both_out<8, true>((lds8*)lds, j, [](int, int) { return 0; }, [&](int n, int m, float (&x)[8], int) {
+    p.template both_out<8, true>(lds, j, [](int, int) { return 0; }, [&](int n, int m, float (&x)[8], int) {
       if (S == 192 && (n0 + n >= a.mp || m0 + m >= a.mp)) return;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -352,23 +350,21 @@ template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_thread
     }, [&](int m, int n, const float (&x)[8]) {
       if (r != c && (S != 192 || m0 + m < a.mp)) store_operand<TWO>(o + place<TWO>(m0 + m, n0 + n, a.mp), x);
     });
+  return true;
 }
 
-// B = b A + c A^2: what lies beside the diagonal to B, a + its diagonal to beta.
-template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_threads(S)) square_k(NsArgs a, uint32_t splits) {
+// B = b A + c A^2, tile (r, c): what lies beside the diagonal to B, a + its diagonal to beta.
+template <int S, int NS, bool TWO> __device__ __forceinline__ void poly_tile(const NsArgs& a, uint32_t r, uint32_t c, uint32_t split,
+                                                                             uint32_t splits, lds8* lds) {
   typedef Tile<kF16, false, false, S, NS, TWO> Prod;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
-  uint32_t r, c, split;
-  const uint32_t side = (a.mp + S - 1) / S;
-  if (!lower_tile(blockIdx.x, side, splits, r, c, split)) return;
-  const uint32_t m0 = r * S, n0 = c * S;
+  const uint32_t m0 = r * S, n0 = c * S, side = (a.mp + S - 1) / S;
   const uint8_t* o = a.o + blockIdx.y * a.o_batch;
   uint8_t* b = a.b + blockIdx.y * a.o_batch;
   const float* d = a.d + blockIdx.y * a.mp;
   float* beta = a.beta + blockIdx.y * a.mp;
   Prod p;
-  square_tile<Prod, S>(p, o, (uint64_t)a.mp * (TWO ? 4 : 2), a.m_stages, a.mp, m0, n0, split, splits, (lds8*)lds);
-  if (!whole<S>(p, a, r * (r + 1) / 2 + c, side * (side + 1) / 2, split, splits, (lds8*)lds)) return;
+  square_tile<Prod, S>(p, o, (uint64_t)a.mp * (TWO ? 4 : 2), a.m_stages, a.mp, m0, n0, split, splits, lds);
+  if (!whole<S>(p, a, r * (r + 1) / 2 + c, side * (side + 1) / 2, split, splits, lds)) return;
   constexpr float unscale = 1.0f / (kScaleA * kScaleA);
   struct In {
     Raw8 o;
@@ -377,7 +373,7 @@ template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_thread
   };
 #pragma unroll
   for (int j = 0; j < Prod::FN; ++j)
-    p.template both_out<8, true>((lds8*)lds, j, [&](int n, int m) {
+    p.template both_out<8, true>(lds, j, [&](int n, int m) {
       const bool in = S != 192 || (n0 + n < a.mp && m0 + m < a.mp);
       const uint32_t row = in ? n0 + n : n0, col = in ? m0 + m : m0;
       const f32x4* dm = reinterpret_cast<const f32x4*>(d + col);
@@ -397,6 +393,32 @@ template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_thread
     }, [&](int m, int n, const float (&x)[8]) {
       if (r != c && (S != 192 || m0 + m < a.mp)) store_operand<TWO>(b + place<TWO>(m0 + m, n0 + n, a.mp), x);
     });
+}
+
+template <int S, int NS, bool TWO> constexpr int square_lds() { return Tile<kF16, false, false, S, NS, TWO>::kLds; }
+
+template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_threads(S)) gram_k(NsArgs a, uint32_t splits) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[square_lds<S, NS, TWO>()];
+  uint32_t r, c, split;
+  if (lower_tile(blockIdx.x, (a.mp + S - 1) / S, splits, r, c, split)) gram_tile<S, NS, TWO>(a, r, c, split, splits, (lds8*)lds);
+}
+
+template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_threads(S)) square_k(NsArgs a, uint32_t splits) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[square_lds<S, NS, TWO>()];
+  uint32_t r, c, split;
+  if (lower_tile(blockIdx.x, (a.mp + S - 1) / S, splits, r, c, split)) poly_tile<S, NS, TWO>(a, r, c, split, splits, (lds8*)lds);
+}
+
+// Both, of matrices that are one tile high: the workgroup that has A goes on to B (what it has
+// stored it reads back past a barrier).  12 matrices of 64 x 768 f32: 95 us with two
+// launches a step, 89 with one.
+template <int NS, bool TWO> __global__ void __launch_bounds__(tile_threads(64)) short_k(NsArgs a, uint32_t splits) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[square_lds<64, NS, TWO>()];
+  uint32_t r, c, split;
+  if (!lower_tile(blockIdx.x, 1, splits, r, c, split) || !gram_tile<64, NS, TWO>(a, 0, 0, split, splits, (lds8*)lds)) return;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  poly_tile<64, NS, TWO>(a, 0, 0, 0, 1, (lds8*)lds);
 }
 
 // Results of the last step: X, or the weights' update by it, of 8 values of a row of the
@@ -497,16 +519,21 @@ template <bool SQUARE, class Go> void way(const NsWay& w, bool two, Go&& go) {
 void step(const NsPlan& p, const NsArgs& a, const NsLast& z, uint32_t batch, bool last, bool turn, hipStream_t st) {
   auto lower = [&](const NsWay& w) {
     const uint64_t side = (a.mp + w.tile - 1) / w.tile;
-    return dim3(tile_grid(side * (side + 1) / 2 * w.splits), batch);
+    return dim3((uint32_t)(side * (side + 1) / 2 * w.splits), batch);
   };
-  way<true>(p.gram, p.parts == 2, [&](auto s, auto ns, auto two) {
-    hipLaunchKernelGGL((gram_k<s, ns, two>), lower(p.gram), dim3(tile_threads(s)), 0, st, a, p.gram.splits);
-  });
-  way<true>(p.square, p.parts == 2, [&](auto s, auto ns, auto two) {
-    hipLaunchKernelGGL((square_k<s, ns, two>), lower(p.square), dim3(tile_threads(s)), 0, st, a, p.square.splits);
-  });
+  if (a.mp == 64) {
+    // (sides of up to 64 always have two parts)
+    hipLaunchKernelGGL((short_k<4, true>), lower(p.gram), dim3(tile_threads(64)), 0, st, a, p.gram.splits);
+  } else {
+    way<true>(p.gram, p.parts == 2, [&](auto s, auto ns, auto two) {
+      hipLaunchKernelGGL((gram_k<s, ns, two>), lower(p.gram), dim3(tile_threads(s)), 0, st, a, p.gram.splits);
+    });
+    way<true>(p.square, p.parts == 2, [&](auto s, auto ns, auto two) {
+      hipLaunchKernelGGL((square_k<s, ns, two>), lower(p.square), dim3(tile_threads(s)), 0, st, a, p.square.splits);
+    });
+  }
   way<false>(p.apply, p.parts == 2, [&](auto s, auto ns, auto two) {
-    const dim3 grid(tile_grid((uint64_t)(a.mp / s) * (a.np / s) * p.apply.splits), batch), block(tile_threads(s));
+    const dim3 grid((a.mp / s) * (a.np / s) * p.apply.splits, batch), block(tile_threads(s));
     if (!last) hipLaunchKernelGGL((apply_k<s, ns, two, false, false>), grid, block, 0, st, a, z, p.apply.splits);
     else if (!turn) hipLaunchKernelGGL((apply_k<s, ns, two, true, false>), grid, block, 0, st, a, z, p.apply.splits);
     else hipLaunchKernelGGL((apply_k<s, ns, two, true, true>), grid, block, 0, st, a, z, p.apply.splits);
