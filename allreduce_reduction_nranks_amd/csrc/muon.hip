@@ -255,6 +255,57 @@ template <int T, bool TWO> __global__ void __launch_bounds__(kSumThreads) turn_k
   }
 }
 
+// Both passes over a matrix of few elements, by one workgroup: a launch less (50 x 50 f32: 51 us
+// a call, 54 with two; 64 x 768, no less, and 768 x 64 half as long again).  TURN: the transpose,
+// read element by element.
+constexpr int kFewThreads = 1024;
+constexpr uint64_t kFewElements = 16384;
+
+template <int T, bool TWO, bool TURN> __global__ void __launch_bounds__(kFewThreads) few_k(NsSource src, NsArgs a, float eps) {
+  __shared__ double lds[kFewThreads / 64];
+  const uint8_t* base = (const uint8_t*)src.p + blockIdx.y * src.stride * Ty<T>::size;
+  uint8_t* to = a.y + blockIdx.y * a.x_batch;
+  for (uint32_t i = threadIdx.x; i < a.counters; i += kFewThreads) a.counter[blockIdx.y * a.counters + i] = 0;
+  const uint32_t rows = (uint32_t)(TURN ? src.cols : src.rows), cols = (uint32_t)(TURN ? src.rows : src.cols);  // of X
+  const uint32_t units = a.np / 8, total = units * a.mp;
+  auto load = [&](uint32_t row, uint32_t c, float* x) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+    if (row >= rows || c >= cols) return;
+    const int n = cols - c < 8 ? (int)(cols - c) : 8;
+    if constexpr (TURN) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < n) x[e] = load_elem<T>(base, (c + e) * src.ld + row);
+    } else {
+      load8<T>(base + (row * src.ld + c) * Ty<T>::size, n, x);
+    }
+  };
+  double s = 0.0;
+  for (uint32_t u = threadIdx.x; u < total; u += kFewThreads) {
+    float x[8];
+    load(u / units, u % units * 8, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = __builtin_fma((double)x[e], (double)x[e], s);
+  }
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) s += __shfl_xor(s, m);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = s;
+  __syncthreads();
+  s = lds[0];
+#pragma unroll
+  for (int k = 1; k < kFewThreads / 64; ++k) s += lds[k];
+  const double norm = __builtin_sqrt(s) + (double)eps;
+  const float scale = norm == 0.0 ? 0.0f : (float)((double)kScaleX / norm);
+  for (uint32_t u = threadIdx.x; u < total; u += kFewThreads) {
+    float x[8];
+    load(u / units, u % units * 8, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] *= scale;
+    store_parts(to + place<TWO>(u / units, u % units * 8, a.np), a.x_plane, x);
+  }
+}
+
 // ---- the products -------------------------------------------------------------------
 // The id-th tile (row, column <= row) on or below the diagonal, `side` tiles a side, and one
 // of `splits` parts of k.  Each XCD gets a contiguous run of an order that walks 6 rows at a
@@ -546,7 +597,8 @@ uint32_t sum_parts(uint64_t rows, uint64_t cols) {
   return n < kMaxParts ? (uint32_t)n : kMaxParts;
 }
 
-// X_0 from the source, its squares summed already; then the steps.
+// X_0 from the source, its squares summed already (parts of them; 0: few elements, not yet); then
+// the steps.
 hipError_t run_steps(const NsCall& c, const NsPlan& p, const NsSource& src, int t, uint32_t parts, const NsLast& z, hipStream_t s) {
   uint8_t* ws = (uint8_t*)c.workspace;
   const double* partial = (const double*)(ws + p.partial);
@@ -568,7 +620,10 @@ hipError_t run_steps(const NsCall& c, const NsPlan& p, const NsSource& src, int 
   a.m_stages = p.m_stages;
   a.n_stages = p.n_stages;
   auto begin = [&](auto type, auto tw) {
-    if (turn) {
+    if (parts == 0) {
+      if (turn) hipLaunchKernelGGL((few_k<type, tw, true>), dim3(1, c.batch), dim3(kFewThreads), 0, s, src, a, c.eps);
+      else hipLaunchKernelGGL((few_k<type, tw, false>), dim3(1, c.batch), dim3(kFewThreads), 0, s, src, a, c.eps);
+    } else if (turn) {
       hipLaunchKernelGGL((turn_k<type, tw>), dim3(a.mp / 64 * (a.np / 64), c.batch), dim3(kSumThreads), 0, s, src, a, partial, parts, c.eps);
     } else {
       const uint64_t blocks = ((uint64_t)a.mp * a.np / 8 + kSumThreads - 1) / kSumThreads;
@@ -712,11 +767,13 @@ NsPlan ns_plan(uint64_t rows, uint64_t cols, uint64_t batch, int parts, bool wit
 
 hipError_t launch_orthogonalize(const NsCall& c, const NsPlan& p, int t, hipStream_t s) {
   const NsSource src{c.in, c.rows, c.cols, c.ld_in, c.stride_in};
-  const uint32_t parts = sum_parts(c.rows, c.cols);
+  const uint32_t parts = (uint64_t)p.mp * p.np <= kFewElements ? 0 : sum_parts(c.rows, c.cols);
   double* partial = (double*)((uint8_t*)c.workspace + p.partial);
-  if (t == kF32) squares<kF32>(src, c.batch, parts, partial, s);
-  else if (t == kF16) squares<kF16>(src, c.batch, parts, partial, s);
-  else squares<kBF16>(src, c.batch, parts, partial, s);
+  if (parts) {
+    if (t == kF32) squares<kF32>(src, c.batch, parts, partial, s);
+    else if (t == kF16) squares<kF16>(src, c.batch, parts, partial, s);
+    else squares<kBF16>(src, c.batch, parts, partial, s);
+  }
   NsLast z{};
   z.out[0] = c.out;
   z.nranks = 1;

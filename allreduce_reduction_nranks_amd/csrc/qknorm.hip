@@ -514,17 +514,21 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_k(QkArgs a) {
     pos = position(w.t);
     if (pos >= 0) fetch(w);
   }
-  stage_weights<T>(a, weights);
+  // (the first token's before the weights, whose barrier waits for both)
   Angles<V> angles[K];
-  for (bool fresh = true; w.t < a.tokens;) {
+  auto turn = [&]() __attribute__((always_inline)) {
+    if (!(FULL || a.rot) || pos < 0 || first >= a.its[2]) return;
+#pragma unroll
+    for (int k = 0; k < K; ++k) load_angles<V, LPH, PAIRS, FULL>(a, Unit<V, LPH, PAIRS, FULL>(a.dim, a.rot, at_lane + k * LPH), pos, angles[k]);
+  };
+  if (w.t < a.tokens) turn();
+  stage_weights<T>(a, weights);
+  for (bool fresh = false; w.t < a.tokens;) {
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int s = 0; s < 2; ++s) now_d[k][s] = next_d[k][s], now_h[k][s] = next_h[k][s];
-    if (fresh && a.rot && pos >= 0 && first < a.its[2]) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) load_angles<V, LPH, PAIRS, FULL>(a, Unit<V, LPH, PAIRS, FULL>(a.dim, a.rot, at_lane + k * LPH), pos, angles[k]);
-    }
+    if (fresh) turn();
     const Walk cur = w;
     const int64_t cur_pos = pos;
     w.next(first, end, step);
