@@ -179,8 +179,20 @@ template <int T> __global__ void __launch_bounds__(kSumThreads) momentum_k(MuonA
   block_sum(s, partial + y * gridDim.x + blockIdx.x);
 }
 
-// 1 / (norm + eps), times X's scale; every thread of the workgroup has it.
-__device__ __forceinline__ float inverse_norm(const double* partial, uint32_t parts, float eps) {
+// X's scale over (norm + eps) for a sum of squares, as a power of two and the rest: norms at
+// both ends of f32's range have inverses past the other.
+struct Factor {
+  float power, rest;
+  __device__ __forceinline__ Factor(double squares, float eps) {
+    const double norm = __builtin_sqrt(squares) + (double)eps, f = (double)kScaleX / norm;
+    power = f > 0x1p100 ? 0x1p100f : f < 0x1p-100 ? 0x1p-100f : 1.0f;
+    rest = norm == 0.0 ? 0.0f : (float)(f / (double)power);  // (a matrix of zeros, without eps, stays one)
+  }
+  __device__ __forceinline__ float operator()(float x) const { return x * power * rest; }
+};
+
+// The same in every thread of the workgroup.
+__device__ __forceinline__ Factor inverse_norm(const double* partial, uint32_t parts, float eps) {
   __shared__ double lds[kSumThreads / 64];
   double s = 0.0;
 #pragma unroll
@@ -193,9 +205,7 @@ __device__ __forceinline__ float inverse_norm(const double* partial, uint32_t pa
   s = lds[0];
 #pragma unroll
   for (int k = 1; k < kSumThreads / 64; ++k) s += lds[k];
-  const double norm = __builtin_sqrt(s) + (double)eps;
-  // a matrix of zeros, without eps, stays one
-  return norm == 0.0 ? 0.0f : (float)((double)kScaleX / norm);
+  return Factor(s, eps);
 }
 
 // The counters of the products' splits, of this matrix, set to zero by its first workgroup.
@@ -207,7 +217,7 @@ __device__ __forceinline__ void clear_counters(const NsArgs& a) {
 // X_0 in two parts, padded with zeros to whole tiles.
 template <int T, bool TWO> __global__ void __launch_bounds__(kSumThreads) spread_k(NsSource src, NsArgs a, const double* partial, uint32_t parts, float eps) {
   clear_counters(a);
-  const float scale = inverse_norm(partial, parts, eps);
+  const Factor scale = inverse_norm(partial, parts, eps);
   const uint8_t* base = (const uint8_t*)src.p + blockIdx.y * src.stride * Ty<T>::size;
   uint8_t* to = a.y + blockIdx.y * a.x_batch;
   const uint32_t units = a.np / 8;
@@ -219,7 +229,7 @@ template <int T, bool TWO> __global__ void __launch_bounds__(kSumThreads) spread
       const uint64_t left = src.cols - c;
       load8<T>(base + (row * src.ld + c) * Ty<T>::size, left < 8 ? (int)left : 8, x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= scale;
+      for (int e = 0; e < 8; ++e) x[e] = scale(x[e]);
     }
     store_parts(to + place<TWO>(row, c, a.np), a.x_plane, x);
   }
@@ -229,7 +239,7 @@ template <int T, bool TWO> __global__ void __launch_bounds__(kSumThreads) spread
 template <int T, bool TWO> __global__ void __launch_bounds__(kSumThreads) turn_k(NsSource src, NsArgs a, const double* partial, uint32_t parts, float eps) {
   __shared__ float lds[64][65];
   clear_counters(a);
-  const float scale = inverse_norm(partial, parts, eps);
+  const Factor scale = inverse_norm(partial, parts, eps);
   const uint8_t* base = (const uint8_t*)src.p + blockIdx.y * src.stride * Ty<T>::size;
   uint8_t* to = a.y + blockIdx.y * a.x_batch;
   const uint32_t across = a.mp / 64, r0 = blockIdx.x / across * 64, c0 = blockIdx.x % across * 64;  // of the source
@@ -250,7 +260,7 @@ template <int T, bool TWO> __global__ void __launch_bounds__(kSumThreads) turn_k
     const uint32_t r = k * 32 + threadIdx.x / 8, c = threadIdx.x % 8 * 8;  // of X
     float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = lds[r][c + e] * scale;
+    for (int e = 0; e < 8; ++e) x[e] = scale(lds[r][c + e]);
     store_parts(to + place<TWO>(c0 + r, r0 + c, a.np), a.x_plane, x);
   }
 }
@@ -295,13 +305,12 @@ template <int T, bool TWO, bool TURN> __global__ void __launch_bounds__(kFewThre
   s = lds[0];
 #pragma unroll
   for (int k = 1; k < kFewThreads / 64; ++k) s += lds[k];
-  const double norm = __builtin_sqrt(s) + (double)eps;
-  const float scale = norm == 0.0 ? 0.0f : (float)((double)kScaleX / norm);
+  const Factor scale(s, eps);
   for (uint32_t u = threadIdx.x; u < total; u += kFewThreads) {
     float x[8];
     load(u / units, u % units * 8, x);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= scale;
+    for (int e = 0; e < 8; ++e) x[e] = scale(x[e]);
     store_parts(to + place<TWO>(u / units, u % units * 8, a.np), a.x_plane, x);
   }
 }
@@ -655,7 +664,8 @@ template <int T> void squares(const NsSource& src, uint32_t batch, uint32_t part
 }  // namespace
 
 bool ns_bounds(const float* co, int steps) {
-  // the largest singular value before a step, and the polynomial's largest over all below
+  // the largest singular value before a step, and the polynomial's largest over all below;
+  // 1 % above it, for what rounding adds
   double top = 1.0;
   for (int k = 0; k < steps; ++k) {
     const double a = co[3 * k], b = co[3 * k + 1], c = co[3 * k + 2], l = top * top;
@@ -676,7 +686,7 @@ bool ns_bounds(const float* co, int steps) {
       if (r > 0.0 && r < l) next = fmax(next, value(r));
     }
     if (!(next < 1e30)) return false;
-    top = next;
+    top = 1.01 * next;
   }
   return true;
 }

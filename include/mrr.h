@@ -564,7 +564,7 @@ mrr_status mrr_linear_xent_bwd(const void* hidden, const void* const* weights, c
  * heads of head_dim elements, side by side.  R rotates the first rot_dim elements of a head
  * by the token's angles and leaves the others: a pair (a, b) becomes (a cos - b sin, b cos +
  * a sin).  pairs 0: element i < rot_dim / 2 pairs with i + rot_dim / 2; pairs 1: 2 i with
- * 2 i + 1.  All in f32, rounded once.
+ * 2 i + 1.  All in f32, rounded once (a head of elements over 1.8e19 has no norm in f32).
  *
  * inputs:    host array of nranks (1..32) device pointers to rows of dtype (F32 | F16 |
  *            BF16), one a token, ld_in elements apart; they may overlap each other.
@@ -584,8 +584,9 @@ mrr_status mrr_linear_xent_bwd(const void* hidden, const void* const* weights, c
  * element (MRR_EALIGN).  The same call gives the same bits.  tokens == 0 launches nothing.
  * Errors: MRR_EUNSUPPORTED for another type or nranks outside [1, 32]; MRR_EINVAL for null
  * pointers, head_dim 0 or over 512, rot_dim odd or over head_dim, a head count over
- * 65535 or none at all, tokens over 2^31, ld_in below a row or over 2^31, strides that
- * put two elements in one place, table_rows of 0 or over 2^31, without positions more
+ * 65535 or none at all, tokens over 2^31, ld_in below a row or over 2^31, a stride between
+ * tokens over 2^31 or between heads over 2^40, strides that put two elements in one place or
+ * keep neither tokens nor heads apart as rows, table_rows of 0 or over 2^31, without positions more
  * tokens than table_rows, and an eps that is negative or NaN.
  * ------------------------------------------------------------------------ */
 mrr_status mrr_qknorm_rope_fwd(const void* const* inputs, int nranks, const void* q_weight,
@@ -648,15 +649,16 @@ mrr_status mrr_qknorm_rope_bwd(const void* const* douts, const void* sum, const 
  *          BF16 results, else F32.  Matrices with a side of 64 or less always take F32.
  * Norms and sums are f32 or f64.  A matrix of zeros gives zeros; one that holds NaN or an
  * infinity gives NaN.  The same call gives the same bits.
- * out may be exactly in, with the same strides; any other overlap gives MRR_EOVERLAP.
+ * out may be exactly in, with the same strides; any other overlap gives MRR_EOVERLAP, as do
+ * results of which neither the matrices nor their rows lie apart.
  * workspace: device, 16-byte aligned, mrr_orthogonalize_workspace_bytes(...) bytes at least
  * (else MRR_ESCRATCH), contents irrelevant before and after.
  * batch == 0 launches nothing.
  * Errors: MRR_EUNSUPPORTED for another type or precision; MRR_EINVAL for null pointers,
  * rows or cols of 0 or over 65536, a batch over 65535, steps outside [1, 64], a stride below
  * a row or over 2^31 (matrices: 2^40), an eps that is negative or not finite, and coefficients
- * with which singular values could pass 7.5 before a step, or |b x + c x^2| 1000 for any x up
- * to their squares.
+ * with which singular values could come within 1 % of 7.5 before a step, or |b x + c x^2|
+ * pass 1000 for any x up to their squares.
  * ------------------------------------------------------------------------ */
 size_t mrr_orthogonalize_workspace_bytes(size_t rows, size_t cols, size_t batch, mrr_dtype dtype,
                                          mrr_dtype products);
