@@ -87,22 +87,30 @@ template <int S> __device__ __forceinline__ uint32_t col_frag(int m0, int r, int
 }
 
 // ---- tiles -------------------------------------------------------------------------
-// Workgroup id to tile (m, n) of mt x nt, and to one of `splits` parts of k.  Workgroups
-// go to the 8 XCDs in turn; each XCD gets one contiguous run of the order, which walks 8
-// m tiles by all n tiles of a split, so that the tiles an XCD works on together share
-// operands in its L2.  (Splits dealt out over the XCDs instead: 231 us against 134 for
-// the hidden states' gradient of 700 x 50257 x 1600 f16.)
-__device__ __forceinline__ bool tile_of(uint32_t id, uint32_t mt, uint32_t nt, uint32_t splits, uint32_t& m, uint32_t& n,
-                                        uint32_t& split) {
-  const uint32_t tiles = mt * nt, total = tiles * splits, per = total / 8, extra = total % 8, x = id & 7, j = id >> 3;
-  if (j >= per + (x < extra ? 1u : 0u)) return false;
-  uint32_t t = x * per + (x < extra ? x : extra) + j;
-  split = t / tiles;
-  t -= split * tiles;
+// Workgroups go to the 8 XCDs in turn; each XCD gets one contiguous run of `total` places in
+// an order of tiles, so that the tiles it works on together share operands in its L2.
+__device__ __forceinline__ bool place_of(uint32_t id, uint32_t total, uint32_t& t) {
+  const uint32_t per = total / 8, extra = total % 8, x = id & 7, j = id >> 3;
+  t = x * per + (x < extra ? x : extra) + j;
+  return j < per + (x < extra ? 1u : 0u);
+}
+// Place t of an order that walks 8 m tiles by all n tiles: tile (m, n) of mt x nt.
+__device__ __forceinline__ void tile_at(uint32_t t, uint32_t mt, uint32_t nt, uint32_t& m, uint32_t& n) {
   constexpr uint32_t G = 8;
   const uint32_t g = t / (G * nt), rem = t - g * (G * nt), gm = mt - g * G < G ? mt - g * G : G;
   m = g * G + rem % gm;
   n = rem / gm;
+}
+// Workgroup id to tile (m, n) of mt x nt, and to one of `splits` parts of k, each of which is
+// walked as a whole.  (Splits dealt out over the XCDs instead: 231 us against 134 for the
+// hidden states' gradient of 700 x 50257 x 1600 f16.)
+__device__ __forceinline__ bool tile_of(uint32_t id, uint32_t mt, uint32_t nt, uint32_t splits, uint32_t& m, uint32_t& n,
+                                        uint32_t& split) {
+  uint32_t t;
+  const uint32_t tiles = mt * nt;
+  if (!place_of(id, tiles * splits, t)) return false;
+  split = t / tiles;
+  tile_at(t - split * tiles, mt, nt, m, n);
   return true;
 }
 inline uint32_t tile_grid(uint64_t tiles) { return (uint32_t)((tiles + 7) / 8 * 8); }

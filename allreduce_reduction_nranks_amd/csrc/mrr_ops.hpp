@@ -206,6 +206,7 @@ struct NsArgs {
   float* part;           // sums of the products' splits
   uint32_t* counter;     // splits that are done, of each tile
   uint64_t x_plane, x_batch, o_batch;  // bytes from upper to lower parts, and of a matrix
+  uint32_t batch;
   uint32_t mp, np;       // sides of X, padded to whole tiles
   uint32_t m_stages, n_stages;  // sides in stages of the products
   uint32_t counters;     // of a matrix

@@ -316,15 +316,25 @@ template <int T, bool TWO, bool TURN> __global__ void __launch_bounds__(kFewThre
 }
 
 // ---- the products -------------------------------------------------------------------
-// The id-th tile (row, column <= row) on or below the diagonal, `side` tiles a side, and one
-// of `splits` parts of k.  Each XCD gets a contiguous run of an order that walks 6 rows at a
-// time, column by column, so that the tiles it works on together share operands in its L2.
-__device__ __forceinline__ bool lower_tile(uint32_t id, uint32_t side, uint32_t splits, uint32_t& r, uint32_t& c, uint32_t& split) {
-  const uint32_t tiles = side * (side + 1) / 2, total = tiles * splits, per = total / 8, extra = total % 8, x = id & 7, j = id >> 3;
-  if (j >= per + (x < extra ? 1u : 0u)) return false;
-  uint32_t t = x * per + (x < extra ? x : extra) + j;
-  split = t / tiles;
-  t -= split * tiles;
+// Of a workgroup: its matrix, and one of `splits` parts of k.  An XCD gets whole matrices, or as
+// much of one, where there are several: 4 matrices of 1024 x 4096 bf16 525 us, 561 with each of
+// them spread over all XCDs.
+struct Part {
+  uint32_t mat, split, tile;
+};
+__device__ __forceinline__ bool part_of(const NsArgs& a, uint32_t tiles, uint32_t splits, Part& p) {
+  uint32_t t;
+  if (!place_of(blockIdx.x, tiles * splits * a.batch, t)) return false;
+  p.mat = __builtin_amdgcn_readfirstlane(t / (tiles * splits));
+  t -= p.mat * (tiles * splits);
+  p.split = __builtin_amdgcn_readfirstlane(t / tiles);
+  p.tile = t - p.split * tiles;
+  return true;
+}
+
+// Place t of an order of the tiles (row, column <= row) on and below the diagonal, `side` tiles a
+// side, that walks 6 rows at a time, column by column.
+__device__ __forceinline__ void lower_tile(uint32_t t, uint32_t side, uint32_t& r, uint32_t& c) {
   constexpr uint32_t G = 6;
   uint32_t r0 = 0, rows = side < G ? side : G;
   // a group of rows: r0 whole columns, then its triangle
@@ -344,17 +354,16 @@ __device__ __forceinline__ bool lower_tile(uint32_t id, uint32_t side, uint32_t 
   }
   r = __builtin_amdgcn_readfirstlane(r);
   c = __builtin_amdgcn_readfirstlane(c);
-  return true;
 }
 
 // The sums of `tile`'s splits, in the workgroup that comes last: true there.
 // (Calls for tiles of 192 or more have enough of them.)
-template <int S, class Prod> __device__ __forceinline__ bool whole(Prod& p, const NsArgs& a, uint32_t tile, uint32_t tiles, uint32_t split,
-                                                                   uint32_t splits, lds8* lds) {
+template <int S, class Prod> __device__ __forceinline__ bool whole(Prod& p, const NsArgs& a, uint32_t mat, uint32_t tile, uint32_t tiles,
+                                                                   uint32_t split, uint32_t splits, lds8* lds) {
   __syncthreads();
   if (S >= 192 || splits == 1) return true;
-  const uint64_t of = (uint64_t)blockIdx.y * tiles + tile;
-  return p.join(lds, a.part + of * splits * S * S, a.counter + blockIdx.y * a.counters + tile, split, splits);
+  const uint64_t of = (uint64_t)mat * tiles + tile;
+  return p.join(lds, a.part + of * splits * S * S, a.counter + mat * a.counters + tile, split, splits);
 }
 
 // A tile of P P^T for P = X (A = X X^T) or O (O O): both operands are rows of P, ld bytes
@@ -386,15 +395,15 @@ template <class Prod, int S> __device__ __forceinline__ void square_tile(Prod& p
 
 // A = X X^T, tile (r, c): what lies beside the diagonal to O, the diagonal to d.  False in a
 // workgroup whose split is not the last.
-template <int S, int NS, bool TWO> __device__ __forceinline__ bool gram_tile(const NsArgs& a, uint32_t r, uint32_t c, uint32_t split,
+template <int S, int NS, bool TWO> __device__ __forceinline__ bool gram_tile(const NsArgs& a, uint32_t mat, uint32_t r, uint32_t c, uint32_t split,
                                                                              uint32_t splits, lds8* lds) {
   typedef Tile<kF16, false, false, S, NS, TWO> Prod;
   const uint32_t m0 = r * S, n0 = c * S, side = (a.mp + S - 1) / S;
   Prod p;
-  square_tile<Prod, S>(p, a.x + blockIdx.y * a.x_batch, (uint64_t)a.np * (TWO ? 4 : 2), a.n_stages, a.mp, m0, n0, split, splits, lds);
-  if (!whole<S>(p, a, r * (r + 1) / 2 + c, side * (side + 1) / 2, split, splits, lds)) return false;
-  uint8_t* o = a.o + blockIdx.y * a.o_batch;
-  float* d = a.d + blockIdx.y * a.mp;
+  square_tile<Prod, S>(p, a.x + mat * a.x_batch, (uint64_t)a.np * (TWO ? 4 : 2), a.n_stages, a.mp, m0, n0, split, splits, lds);
+  if (!whole<S>(p, a, mat, r * (r + 1) / 2 + c, side * (side + 1) / 2, split, splits, lds)) return false;
+  uint8_t* o = a.o + mat * a.o_batch;
+  float* d = a.d + mat * a.mp;
   constexpr float unscale = 1.0f / (kScaleX * kScaleX);
 #pragma unroll
   for (int j = 0; j < Prod::FN; ++j)
@@ -414,17 +423,17 @@ template <int S, int NS, bool TWO> __device__ __forceinline__ bool gram_tile(con
 }
 
 // B = b A + c A^2, tile (r, c): what lies beside the diagonal to B, a + its diagonal to beta.
-template <int S, int NS, bool TWO> __device__ __forceinline__ void poly_tile(const NsArgs& a, uint32_t r, uint32_t c, uint32_t split,
+template <int S, int NS, bool TWO> __device__ __forceinline__ void poly_tile(const NsArgs& a, uint32_t mat, uint32_t r, uint32_t c, uint32_t split,
                                                                              uint32_t splits, lds8* lds) {
   typedef Tile<kF16, false, false, S, NS, TWO> Prod;
   const uint32_t m0 = r * S, n0 = c * S, side = (a.mp + S - 1) / S;
-  const uint8_t* o = a.o + blockIdx.y * a.o_batch;
-  uint8_t* b = a.b + blockIdx.y * a.o_batch;
-  const float* d = a.d + blockIdx.y * a.mp;
-  float* beta = a.beta + blockIdx.y * a.mp;
+  const uint8_t* o = a.o + mat * a.o_batch;
+  uint8_t* b = a.b + mat * a.o_batch;
+  const float* d = a.d + mat * a.mp;
+  float* beta = a.beta + mat * a.mp;
   Prod p;
   square_tile<Prod, S>(p, o, (uint64_t)a.mp * (TWO ? 4 : 2), a.m_stages, a.mp, m0, n0, split, splits, lds);
-  if (!whole<S>(p, a, r * (r + 1) / 2 + c, side * (side + 1) / 2, split, splits, lds)) return;
+  if (!whole<S>(p, a, mat, r * (r + 1) / 2 + c, side * (side + 1) / 2, split, splits, lds)) return;
   constexpr float unscale = 1.0f / (kScaleA * kScaleA);
   struct In {
     Raw8 o;
@@ -459,14 +468,22 @@ template <int S, int NS, bool TWO> constexpr int square_lds() { return Tile<kF16
 
 template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_threads(S)) gram_k(NsArgs a, uint32_t splits) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[square_lds<S, NS, TWO>()];
-  uint32_t r, c, split;
-  if (lower_tile(blockIdx.x, (a.mp + S - 1) / S, splits, r, c, split)) gram_tile<S, NS, TWO>(a, r, c, split, splits, (lds8*)lds);
+  const uint32_t side = (a.mp + S - 1) / S;
+  uint32_t r, c;
+  Part p;
+  if (!part_of(a, side * (side + 1) / 2, splits, p)) return;
+  lower_tile(p.tile, side, r, c);
+  gram_tile<S, NS, TWO>(a, p.mat, r, c, p.split, splits, (lds8*)lds);
 }
 
 template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_threads(S)) square_k(NsArgs a, uint32_t splits) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[square_lds<S, NS, TWO>()];
-  uint32_t r, c, split;
-  if (lower_tile(blockIdx.x, (a.mp + S - 1) / S, splits, r, c, split)) poly_tile<S, NS, TWO>(a, r, c, split, splits, (lds8*)lds);
+  const uint32_t side = (a.mp + S - 1) / S;
+  uint32_t r, c;
+  Part p;
+  if (!part_of(a, side * (side + 1) / 2, splits, p)) return;
+  lower_tile(p.tile, side, r, c);
+  poly_tile<S, NS, TWO>(a, p.mat, r, c, p.split, splits, (lds8*)lds);
 }
 
 // Both, of matrices that are one tile high: the workgroup that has A goes on to B (what it has
@@ -474,11 +491,11 @@ template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_thread
 // launches a step, 89 with one.
 template <int NS, bool TWO> __global__ void __launch_bounds__(tile_threads(64)) short_k(NsArgs a, uint32_t splits) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[square_lds<64, NS, TWO>()];
-  uint32_t r, c, split;
-  if (!lower_tile(blockIdx.x, 1, splits, r, c, split) || !gram_tile<64, NS, TWO>(a, 0, 0, split, splits, (lds8*)lds)) return;
+  Part p;
+  if (!part_of(a, 1, splits, p) || !gram_tile<64, NS, TWO>(a, p.mat, 0, 0, p.split, splits, (lds8*)lds)) return;
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  poly_tile<64, NS, TWO>(a, 0, 0, 0, 1, (lds8*)lds);
+  poly_tile<64, NS, TWO>(a, p.mat, 0, 0, 0, 1, (lds8*)lds);
 }
 
 // Results of the last step: X, or the weights' update by it, of 8 values of a row of the
@@ -492,9 +509,9 @@ template <int T> __device__ __forceinline__ void put_typed(const NsLast& z, uint
   }
   for (int r = 0; r < z.nranks; ++r) store8<T>(at<T>(z.out[r], i), n, x);
 }
-__device__ __forceinline__ void put_result(const NsLast& z, uint32_t row, uint32_t col, float* x) {
+__device__ __forceinline__ void put_result(const NsLast& z, uint32_t mat, uint32_t row, uint32_t col, float* x) {
   if (row >= z.rows || col >= z.cols) return;
-  const uint64_t i = blockIdx.y * z.stride + (uint64_t)row * z.ld + col;
+  const uint64_t i = mat * z.stride + (uint64_t)row * z.ld + col;
   const int n = z.cols - col < 8 ? (int)(z.cols - col) : 8;
   if (z.type == kF32) put_typed<kF32>(z, i, n, x);
   else if (z.type == kF16) put_typed<kF16>(z, i, n, x);
@@ -506,12 +523,15 @@ template <int S, int NS, bool TWO, bool LAST, bool TURN>
 __global__ void __launch_bounds__(tile_threads(S)) apply_k(NsArgs a, NsLast z, uint32_t splits) {
   typedef Tile<kF16, true, false, S, NS, TWO> Prod;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
-  uint32_t mt, nt, split;
-  if (!tile_of(blockIdx.x, a.np / S, a.mp / S, splits, mt, nt, split)) return;
+  uint32_t mt, nt;
+  Part at;
+  if (!part_of(a, a.np / S * (a.mp / S), splits, at)) return;
+  tile_at(at.tile, a.np / S, a.mp / S, mt, nt);
+  const uint32_t mat = at.mat, split = at.split;
   const uint32_t j0 = mt * S, i0 = nt * S;  // column and row of X
-  const uint8_t* x = a.x + blockIdx.y * a.x_batch;
-  const uint8_t* b = a.b + blockIdx.y * a.o_batch;
-  const float* beta = a.beta + blockIdx.y * a.mp;
+  const uint8_t* x = a.x + mat * a.x_batch;
+  const uint8_t* b = a.b + mat * a.o_batch;
+  const float* beta = a.beta + mat * a.mp;
   const int tid = threadIdx.x;
   const uint32_t ldx = a.np * (TWO ? 4 : 2), ldb = a.mp * (TWO ? 4 : 2);
   uint32_t k = a.m_stages * split / splits;
@@ -531,7 +551,7 @@ __global__ void __launch_bounds__(tile_threads(S)) apply_k(NsArgs a, NsLast z, u
   };
   Prod p;
   p.run((int)(k1 - k), (lds8*)lds, src);
-  if (!whole<S>(p, a, mt * (a.mp / S) + nt, (a.np / S) * (a.mp / S), split, splits, (lds8*)lds)) return;
+  if (!whole<S>(p, a, mat, mt * (a.mp / S) + nt, (a.np / S) * (a.mp / S), split, splits, (lds8*)lds)) return;
   struct In {
     Raw8 x;
     float beta;
@@ -546,10 +566,10 @@ __global__ void __launch_bounds__(tile_threads(S)) apply_k(NsArgs a, NsLast z, u
       constexpr float unscale = LAST ? 1.0f / kScaleX : 1.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(v[e], unscale / kScaleB, in.beta * y[e] * unscale);
-      if constexpr (!LAST) store_parts(a.y + blockIdx.y * a.x_batch + place<TWO>(i0 + n, j0 + m, a.np), a.x_plane, v);
-      else if constexpr (!TURN) put_result(z, i0 + n, j0 + m, v);
+      if constexpr (!LAST) store_parts(a.y + mat * a.x_batch + place<TWO>(i0 + n, j0 + m, a.np), a.x_plane, v);
+      else if constexpr (!TURN) put_result(z, mat, i0 + n, j0 + m, v);
     }, [&](int m, int n, float (&v)[8]) {
-      if constexpr (LAST) put_result(z, j0 + m, i0 + n, v);
+      if constexpr (LAST) put_result(z, mat, j0 + m, i0 + n, v);
     });
 }
 
@@ -579,7 +599,7 @@ template <bool SQUARE, class Go> void way(const NsWay& w, bool two, Go&& go) {
 void step(const NsPlan& p, const NsArgs& a, const NsLast& z, uint32_t batch, bool last, bool turn, hipStream_t st) {
   auto lower = [&](const NsWay& w) {
     const uint64_t side = (a.mp + w.tile - 1) / w.tile;
-    return dim3((uint32_t)(side * (side + 1) / 2 * w.splits), batch);
+    return dim3((uint32_t)(side * (side + 1) / 2 * w.splits * batch));
   };
   if (a.mp == 64) {
     // (sides of up to 64 always have two parts)
@@ -593,7 +613,7 @@ void step(const NsPlan& p, const NsArgs& a, const NsLast& z, uint32_t batch, boo
     });
   }
   way<false>(p.apply, p.parts == 2, [&](auto s, auto ns, auto two) {
-    const dim3 grid((a.mp / s) * (a.np / s) * p.apply.splits, batch), block(tile_threads(s));
+    const dim3 grid((a.mp / s) * (a.np / s) * p.apply.splits * batch), block(tile_threads(s));
     if (!last) hipLaunchKernelGGL((apply_k<s, ns, two, false, false>), grid, block, 0, st, a, z, p.apply.splits);
     else if (!turn) hipLaunchKernelGGL((apply_k<s, ns, two, true, false>), grid, block, 0, st, a, z, p.apply.splits);
     else hipLaunchKernelGGL((apply_k<s, ns, two, true, true>), grid, block, 0, st, a, z, p.apply.splits);
@@ -624,6 +644,7 @@ hipError_t run_steps(const NsCall& c, const NsPlan& p, const NsSource& src, int 
   a.x_plane = two ? 64 : p.x_plane;
   a.x_batch = 2 * p.x_plane;
   a.o_batch = p.parts * p.o_plane;
+  a.batch = c.batch;
   a.mp = p.mp;
   a.np = p.np;
   a.m_stages = p.m_stages;
