@@ -726,9 +726,9 @@ template <class Tiles> static NsWay choose(uint32_t pad, bool two, bool square, 
     uint32_t tile, ns, per_cu;
     double alone, full, rest, join;  // microseconds
   };
-  static const Kind one[] = {{64, 4, 2, 0.23, 0.33, 4.0, 0.8}, {128, 4, 1, 0.45, 0.65, 5.5, 4.0}, {128, 2, 2, 0.62, 0.90, 5.5, 4.0},
+  static const Kind one[] = {{64, 4, 2, 0.23, 0.35, 3.4, 0.8}, {128, 4, 1, 0.55, 0.65, 5.5, 4.0}, {128, 2, 2, 0.62, 0.90, 6.7, 4.0},
                              {192, 3, 1, 0.98, 0.98, 20.0, 0.0}, {256, 2, 1, 1.43, 1.43, 14.0, 0.0}};
-  static const Kind parts2[] = {{64, 4, 2, 0.23, 0.42, 4.0, 0.8}, {128, 4, 1, 0.55, 0.75, 5.5, 4.0}, {128, 2, 2, 0.65, 1.04, 5.5, 4.0},
+  static const Kind parts2[] = {{64, 4, 2, 0.23, 0.37, 3.4, 0.8}, {128, 4, 1, 0.55, 0.65, 5.5, 4.0}, {128, 2, 2, 0.65, 1.23, 5.5, 4.0},
                                  {192, 3, 1, 1.60, 1.60, 20.0, 0.0}};
   const Kind* kinds = two ? parts2 : one;
   NsWay best{};
@@ -740,7 +740,7 @@ template <class Tiles> static NsWay choose(uint32_t pad, bool two, bool square, 
       const uint64_t groups = tiles(k.tile) * batch * splits, slots = 256 * k.per_cu, rounds = groups / slots, rest = groups % slots;
       if (splits > 1 && groups > 512) break;
       const double per = (stages + splits - 1) / splits;
-      const double last = rest ? per * (rest > 256 || rounds ? k.full : k.alone) + k.rest : 0.0;
+      const double last = rest ? per * (rest > 256 ? k.full : k.alone) + k.rest : 0.0;
       const double t = rounds * (per * k.full + k.rest) + last + (splits > 1 ? 2.0 + splits * k.join : 0.0);
       if (t < least) least = t, best = {k.tile, k.ns, splits, t};
     }
