@@ -299,8 +299,10 @@ __device__ __forceinline__ void finish(const QkArgs& a, const Walk& w, const Hea
 // One iteration a wave, which is a workgroup: the dispatcher hands them out in order, so that HBM
 // sees a narrow window that moves along, and all that a wave reads is asked for at once,
 // but for the angles, whose place the position gives.  For several ranks (8 ranks of 4096 tokens of
-// 48 heads of 128 bf16 88 us, 125 where waves walk over tokens), kAtOnce of them in flight, and for few
-// tokens.  K units a lane (1 but for heads without vectors).
+// 48 heads of 128 bf16 78 us, 125 where waves walk over tokens), and for few tokens.  G ranks' loads in
+// flight: 8, or as few as there are up to 4, whose registers leave room for more waves (2047 tokens
+// of 9 heads of 80 f16, 4 ranks, 9.7 us with 4 and 11.7 with 8; 4096 tokens of 48 heads of 128 bf16,
+// 2 ranks, 28 and 34).  K units a lane (1 but for heads without vectors).
 constexpr int kAtOnce = 8;
 
 // A lane's 2 V weights as they lie in memory, and widened.  No branch chooses between f32 and
@@ -336,9 +338,9 @@ template <int T, int V> struct RawWeights {
   }
 };
 
-template <int T, int V, int LPH, int K, bool RANKS, bool PAIRS, bool FULL, bool NT>
+template <int T, int V, int LPH, int K, int G, bool PAIRS, bool FULL, bool NT>
 __global__ void __launch_bounds__(64) qk_fwd_k(QkArgs a) {
-  constexpr int E = 2 * V, G = RANKS ? kAtOnce : 1;
+  constexpr int E = 2 * V;
   const int at_lane = threadIdx.x & (LPH - 1);
   const float inv = 1.0f / (float)a.dim;
   const uint32_t per = a.its[3], it = blockIdx.x % per;
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(64) qk_fwd_k(QkArgs a) {
       get_v<T, V>(raw[k][0][0], x[k]);
       get_v<T, V>(raw[k][0][1], x[k] + V);
     }
-    if constexpr (RANKS) {
+    if constexpr (G > 1) {
       for (int r0 = 0; r0 < a.nranks; r0 += G) {
         if (r0) fetch(r0);
 #pragma unroll
@@ -748,8 +750,9 @@ template <int T> void fwd(const QkArgs& a, hipStream_t s) {
       }
       const uint64_t rows = a.tokens < kMaxWaves / a.its[3] ? a.tokens : kMaxWaves / a.its[3];
       const dim3 grid((uint32_t)(a.its[3] * rows));
-      if (a.nranks > 1) hipLaunchKernelGGL((qk_fwd_k<T, v, lph, k, true, pairs, f, nt>), grid, dim3(64), 0, s, a);
-      else if constexpr (!nt) hipLaunchKernelGGL((qk_fwd_k<T, v, lph, k, false, pairs, f, false>), grid, dim3(64), 0, s, a);
+      if (a.nranks > kAtOnce / 2) hipLaunchKernelGGL((qk_fwd_k<T, v, lph, k, kAtOnce, pairs, f, nt>), grid, dim3(64), 0, s, a);
+      else if (a.nranks > 1) hipLaunchKernelGGL((qk_fwd_k<T, v, lph, k, kAtOnce / 2, pairs, f, nt>), grid, dim3(64), 0, s, a);
+      else if constexpr (!nt) hipLaunchKernelGGL((qk_fwd_k<T, v, lph, k, 1, pairs, f, false>), grid, dim3(64), 0, s, a);
     };
     shaped(v, lph, a, bytes > kCacheBytes, full);
   };
