@@ -1,11 +1,11 @@
-// mrr_gemm.hpp -- the tile product that the cross entropy kernels share: one workgroup
+// mrr_gemm.hpp -- the tile product that the cross entropy and Newton-Schulz kernels share: one workgroup
 // computes D[m][n] = sum over k of A[m][k] B[n][k] for a tile of S m by S n in f32, from
 // 16-bit operands, and hands each wave its part.
 //
 // An operand lies in memory either with k contiguous ("row": a row for each m)
 // or with m contiguous ("col": a row for each k).  Both reach LDS by loads that
 // bypass registers (16 bytes a lane, a wave's 1 KiB contiguous in LDS), 64 k a
-// stage, two stages.  A row operand is read from LDS 16 bytes a lane; a col
+// stage, two to four stages.  A row operand is read from LDS 16 bytes a lane; a col
 // operand with the transposing 64-bit read, so no operand is transposed in
 // memory.  Chunks are permuted within a stage (the permutation is made on the
 // global address, since the LDS side of the load is fixed) so that the lanes

@@ -300,9 +300,9 @@ __device__ __forceinline__ void finish(const QkArgs& a, const Walk& w, const Hea
 // sees a narrow window that moves along, and all that a wave reads is asked for at once,
 // but for the angles, whose place the position gives.  For several ranks (8 ranks of 4096 tokens of
 // 48 heads of 128 bf16 78 us, 125 where waves walk over tokens), and for few tokens.  G ranks' loads in
-// flight: 8, or as few as there are up to 4, whose registers leave room for more waves (2047 tokens
-// of 9 heads of 80 f16, 4 ranks, 9.7 us with 4 and 11.7 with 8; 4096 tokens of 48 heads of 128 bf16,
-// 2 ranks, 28 and 34).  K units a lane (1 but for heads without vectors).
+// flight: 8, 4 of up to 4, 2 of 2, as fewer registers leave room for more waves (2047 tokens of
+// 9 heads of 80 f16, 4 ranks, 9.7 us with 4 and 11.7 with 8; 4096 tokens of 48 heads of 128 bf16,
+// 2 ranks, 27 us with 2, 28 with 4, 34 with 8).  K units a lane (1 but for heads without vectors).
 constexpr int kAtOnce = 8;
 
 // A lane's 2 V weights as they lie in memory, and widened.  No branch chooses between f32 and
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(64) qk_fwd_k(QkArgs a) {
 
 // Many tokens of one rank: a wave takes all heads of a token in turn, its units, addresses and
 // angles worked out once, and asks for the next iteration's elements before it works on the
-// present one's.  16384 tokens of 48 heads of 128 bf16: 80 us, 5.0 TB/s; the above 85.
+// present one's.  16384 tokens of 48 heads of 128 bf16: 71 us, 5.7 TB/s; the above 85.
 template <int T, int V, int LPH, bool PAIRS, bool FULL>
 __global__ void __launch_bounds__(kThreads, 4) qk_walk_k(QkArgs a) {
   __shared__ float weights[2 * kMaxDim];
@@ -652,7 +652,7 @@ template <int T> __global__ void __launch_bounds__(kJoinCols * kJoinChains) qk_j
 // ---- launches -------------------------------------------------------------------------------
 // A backward's grid: as many workgroups as the card holds at once (3 a CU, of which
 // every wave then has as many tokens as the others: 16384 tokens of 48 heads of 128 bf16
-// 114 us, 132 with 1024), few tokens' heads dealt out over more of them.
+// 111 us, 132 with 1024), few tokens' heads dealt out over more of them.
 struct Shape {
   uint32_t x, y, chunk;
 };
@@ -751,7 +751,8 @@ template <int T> void fwd(const QkArgs& a, hipStream_t s) {
       const uint64_t rows = a.tokens < kMaxWaves / a.its[3] ? a.tokens : kMaxWaves / a.its[3];
       const dim3 grid((uint32_t)(a.its[3] * rows));
       if (a.nranks > kAtOnce / 2) hipLaunchKernelGGL((qk_fwd_k<T, v, lph, k, kAtOnce, pairs, f, nt>), grid, dim3(64), 0, s, a);
-      else if (a.nranks > 1) hipLaunchKernelGGL((qk_fwd_k<T, v, lph, k, kAtOnce / 2, pairs, f, nt>), grid, dim3(64), 0, s, a);
+      else if (a.nranks > 2) hipLaunchKernelGGL((qk_fwd_k<T, v, lph, k, kAtOnce / 2, pairs, f, nt>), grid, dim3(64), 0, s, a);
+      else if (a.nranks > 1) hipLaunchKernelGGL((qk_fwd_k<T, v, lph, k, 2, pairs, f, nt>), grid, dim3(64), 0, s, a);
       else if constexpr (!nt) hipLaunchKernelGGL((qk_fwd_k<T, v, lph, k, 1, pairs, f, false>), grid, dim3(64), 0, s, a);
     };
     shaped(v, lph, a, bytes > kCacheBytes, full);
