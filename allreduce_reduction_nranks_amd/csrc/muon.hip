@@ -698,13 +698,13 @@ bool ns_bounds(const float* co, int steps) {
     // a s + b s^3 + c s^5 over [0, top]: its ends, and where a + 3 b x + 5 c x^2 = 0
     auto value = [&](double x) { return fabs(sqrt(x) * (a + x * (b + x * c))); };
     double next = value(l);
+    // (the roots by their sum and product, which lose no digits where one is far from the other;
+    // where there is none, or c is 0, they are infinite or NaN and in no range)
     const double q = 9 * b * b - 20 * a * c;
-    if (c != 0.0 && q >= 0.0) {
-      for (const double r : {(-3 * b + sqrt(q)) / (10 * c), (-3 * b - sqrt(q)) / (10 * c)})
+    if (q >= 0.0) {
+      const double t = -(3 * b + copysign(sqrt(q), b)) / 2;
+      for (const double r : {t / (5 * c), a / t})
         if (r > 0.0 && r < l) next = fmax(next, value(r));
-    } else if (c == 0.0 && b != 0.0) {
-      const double r = -a / (3 * b);
-      if (r > 0.0 && r < l) next = fmax(next, value(r));
     }
     if (!(next < 1e30)) return false;
     top = 1.01 * next;
