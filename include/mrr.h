@@ -642,11 +642,14 @@ mrr_status mrr_qknorm_rope_bwd(const void* const* douts, const void* sum, const 
  * coefficients: host array of a, b, c of each step; NULL = 3.4445, -4.7750, 2.0315 at
  *          every step, which bring singular values from 0.01 of the norm up to within 0.7 and
  *          1.2 in 5 steps.
- * products: precision of the products.  F32: operands in two f16 parts (22 bits), three
- *          products of them for each: results as exact as f32 products give.  F16: operands
- *          of 11 bits, diagonals and what a step adds to in f32 beside them: results off
- *          by up to 1.1e-3 of their norm (bf16 itself rounds by 1.7e-3).  AUTO: F16 for
- *          BF16 results, else F32.  Matrices with a side of 64 or less always take F32.
+ * products: precision of the products.  F32 (AUTO): operands in two f16 parts (22 bits),
+ *          three products of them for each: results as exact as f32 products give (off by
+ *          1e-6 of their norm for noise, by up to 6e-5 where one direction stands alone, in 5
+ *          steps).  F16, where speed counts for more: operands of 11 bits, diagonals and what
+ *          a step adds to in f32 beside them.  Its results are off by some 1e-3 of their norm
+ *          for noise; equal rows round alike and their errors add, up to 3e-2 for blocks of
+ *          equal values (bf16 itself rounds by 1.7e-3).  Matrices with a side of 64 or
+ *          less always take F32.
  * Norms and sums are f32 or f64.  A matrix of zeros gives zeros; one that holds NaN or an
  * infinity gives NaN.  The same call gives the same bits.
  * out may be exactly in, with the same strides; any other overlap gives MRR_EOVERLAP, as do
@@ -688,7 +691,7 @@ mrr_status mrr_orthogonalize(const void* in, void* out, size_t rows, size_t cols
  * momentum, momentum_out: f32, laid out as the weights; momentum NULL = zeros (a first step).
  * weights_out[r] may be exactly weight, and momentum_out exactly momentum; any other overlap
  * of an output gives MRR_EOVERLAP.
- * products: as in mrr_orthogonalize, AUTO by wdtype.
+ * products: as in mrr_orthogonalize.
  * workspace: as there, mrr_muon_workspace_bytes(...) bytes at least.
  * Factors are values of the call: a captured graph replays those it was captured with.
  * Errors as there; MRR_EUNSUPPORTED for nranks outside [1, 32]; MRR_EINVAL for a factor that

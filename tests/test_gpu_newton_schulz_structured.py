@@ -1,0 +1,91 @@
+"""GPU checks of the products' precision on matrices whose roundings do not average out: equal rows, blocks of equal values, few
+directions.
+
+By default a result is off by no more than f32 products give, beside its own rounding.  The rounding model of
+test_gpu_muon, in two parts, run on the CPU over these kinds and sides up to 512, is off by 4e-7 to 9e-6 of the norm, and by up to
+5.6e-5 for one direction: there X's roundings of 2^-24 to 2^-23 lie in directions of no size, which each of 5 steps lets
+grow 3.4-fold (2^-24 3.4445^5 = 2.9e-5; f32 products give 1.3e-4).  LIMIT is four times that worst.  What an
+element is off beyond half a step of its type is held to it, in the norm of all elements.
+
+With products="f16" the header names 3e-2 as what blocks of equal values are off by; they are held to 4e-2.
+"""
+import pytest
+import torch
+
+import allreduce_reduction_nranks_amd as mrr
+from gpu_common import announce
+from test_gpu_muon import TYPES, exact, muon, orth, seeded
+
+pytestmark = pytest.mark.gpu
+
+LIMIT = 2.3e-4
+
+
+def matrix(kind, m, n):
+    g = seeded(m + n)
+
+    def randn(*s):
+        return torch.randn(*s, generator=g, device="cuda")
+
+    if kind == "noise":
+        return randn(m, n)
+    if kind == "ones":
+        return torch.ones(m, n, device="cuda")
+    if kind == "one direction":
+        return randn(m, 1) * randn(1, n)
+    if kind == "two rows equal":
+        x = randn(m, n)
+        x[m - 1] = x[0]
+        return x
+    if kind == "four rows":
+        return randn(4, n)[torch.randint(0, 4, (m,), generator=g, device="cuda")]
+    if kind == "diagonal":
+        return torch.eye(m, n, device="cuda")
+    blocks = int(kind.split()[0])
+    return torch.block_diag(*[torch.ones(m // blocks, n // blocks)] * blocks).cuda()
+
+
+KINDS = ["noise", "ones", "one direction", "two rows equal", "four rows", "diagonal", "4 blocks"]
+
+
+def beyond_half_a_step(got, want, t):
+    """The norm of what elements are off beyond half a step, over the norm of all."""
+    half = torch.exp2(torch.floor(torch.log2(want.abs().clamp(min=1e-30)))) * torch.finfo(TYPES[t]).eps / 2
+    return float(((got.double() - want).abs() - half).clamp(min=0).norm() / want.norm())
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("m,n", [(65, 65), (131, 131), (391, 500), (500, 391), (1024, 1024)])
+@pytest.mark.parametrize("kind", KINDS)
+def test_results_are_as_exact_as_f32_products_give(kind, m, n, t):
+    announce("orth structured", kind, m, n, t)
+    x = matrix(kind, m, n).to(TYPES[t])
+    out = torch.empty_like(x)
+    mrr.check(orth(x, out, x.shape[0], x.shape[1], 1, t))
+    off = beyond_half_a_step(out, exact(x), t)
+    assert off <= LIMIT, off
+
+
+@pytest.mark.parametrize("kind", ["noise", "ones", "four rows"])
+def test_updates_of_bf16_weights(kind):
+    announce("muon structured", kind)
+    m, n = 391, 500
+    x = matrix(kind, m, n).bfloat16()
+    w, new, momentum = torch.zeros_like(x), torch.empty_like(x), torch.empty(m, n, device="cuda")
+    mrr.check(muon([x], 1.0, None, momentum, 0.0, False, w, [new], -1.0, 0.0, m, n, 1, "bf16", "bf16"))
+    assert beyond_half_a_step(new, exact(x), "bf16") <= LIMIT
+
+
+@pytest.mark.parametrize("kind,m,n", [("noise", 256, 512), ("ones", 131, 131), ("four rows", 391, 500), ("4 blocks", 256, 512),
+                                      ("4 blocks", 1908, 5460), ("4 blocks", 448, 1372)])
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_products_of_11_bits_are_off_by_what_the_header_says(kind, m, n, t):
+    announce("orth structured f16", kind, m, n, t)
+    x = matrix(kind, m, n).to(TYPES[t])
+    out = torch.empty_like(x)
+    mrr.check(orth(x, out, x.shape[0], x.shape[1], 1, t, "f16"))
+    want = exact(x)
+    off = float((out.double() - want).norm() / want.norm())
+    print("off by %.2e" % off, flush=True)
+    half = torch.finfo(TYPES[t]).eps / 2
+    assert off <= (1.3e-3 if kind == "noise" else 4e-2) + half
