@@ -1363,7 +1363,9 @@ mrr_status mrr_orthogonalize(const void* in, void* out, size_t rows, size_t cols
 
 size_t mrr_muon_workspace_bytes(size_t rows, size_t cols, size_t batch, int nesterov, mrr_dtype wdtype, mrr_dtype products) {
   int parts;
-  if (batch == 0 || ns_shape("mrr_muon_workspace_bytes", rows, cols, batch, wdtype, products, &parts)) return 0;
+  // (AUTO stands for the gradients' type; no type needs more than another)
+  const int t = wdtype == MRR_AUTO ? kF32 : wdtype;
+  if (batch == 0 || ns_shape("mrr_muon_workspace_bytes", rows, cols, batch, t, products, &parts)) return 0;
   return ns_plan(rows, cols, batch, parts, nesterov != 0).bytes;
 }
 

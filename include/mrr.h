@@ -692,7 +692,7 @@ mrr_status mrr_orthogonalize(const void* in, void* out, size_t rows, size_t cols
  * weights_out[r] may be exactly weight, and momentum_out exactly momentum; any other overlap
  * of an output gives MRR_EOVERLAP.
  * products: as in mrr_orthogonalize.
- * workspace: as there, mrr_muon_workspace_bytes(...) bytes at least.
+ * workspace: as there, mrr_muon_workspace_bytes(...) bytes at least, which takes wdtype AUTO too.
  * Factors are values of the call: a captured graph replays those it was captured with.
  * Errors as there; MRR_EUNSUPPORTED for nranks outside [1, 32]; MRR_EINVAL for a factor that
  * is not finite.
