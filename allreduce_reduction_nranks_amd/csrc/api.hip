@@ -261,10 +261,11 @@ constexpr int kMaxSteps = 64;
 static bool float_type(int t) { return t == kF32 || t == kF16 || t == kBF16; }
 
 // A matrix that a call reads or writes: `rows` rows of `width` bytes, `pitch`
-// bytes apart.  Null or empty: absent.
+// bytes apart, of which, where `step` is not 0, each has units of `unit` bytes, `step` bytes
+// apart (a token's heads, a matrix's rows).  Null or empty: absent.
 struct Mat {
   const void* p;
-  size_t rows, width, pitch;
+  size_t rows, width, pitch, unit = 0, step = 0;
   Range range() const {
     return {(uintptr_t)p, (uintptr_t)p + (p && rows && width ? (rows - 1) * pitch + width : 0)};
   }
@@ -272,14 +273,25 @@ struct Mat {
 
 static Mat vec(const void* p, size_t bytes) { return {p, 1, bytes, bytes}; }
 
+// Whether two rows share a byte, the second beginning d bytes after the first.  Units of one
+// step may lie between each other's, and so may a whole row between units.
+static bool rows_meet(size_t d, const Mat& first, const Mat& second) {
+  if (d >= first.width) return false;
+  const size_t step = first.step ? first.step : second.step, at = step ? d % step : 0;
+  if (!step || (first.step && second.step && first.step != second.step)) return true;
+  return at < (first.step ? first.unit : first.width) || step - at < (second.step ? second.unit : second.width);
+}
+
 // Two matrices of one pitch whose rows lie side by side (columns of one wider
-// buffer) share no byte although their ranges overlap.
+// buffer) or between each other share no byte although their ranges overlap.
 static bool overlaps(const Mat& a, const Mat& b) {
   const Range x = a.range(), y = b.range();
   if (x.lo == x.hi || y.lo == y.hi || !overlaps(x, y)) return false;
+  const Mat &first = x.lo <= y.lo ? a : b, &second = x.lo <= y.lo ? b : a;
+  const uintptr_t d = x.lo <= y.lo ? y.lo - x.lo : x.lo - y.lo;
+  if (a.rows < 2 && b.rows < 2) return rows_meet(d, first, second);
   if (a.pitch != b.pitch || a.rows < 2 || b.rows < 2) return true;
-  const uintptr_t d = (y.lo >= x.lo ? y.lo - x.lo : a.pitch - (x.lo - y.lo) % a.pitch) % a.pitch;
-  return d < a.width || a.pitch - d < b.width;
+  return rows_meet(d % a.pitch, first, second) || rows_meet(a.pitch - d % a.pitch, second, first);
 }
 
 static bool same(const Mat& a, const Mat& b) {
@@ -323,10 +335,10 @@ static mrr_status norm_shape(const char* fn, size_t rows, size_t cols, size_t ld
 static bool heads_mat(const void* p, size_t tokens, size_t heads, size_t dim, size_t ld, size_t hs, size_t e, Mat* m) {
   const size_t across = (heads ? heads - 1 : 0) * hs + dim, along = (tokens ? tokens - 1 : 0) * ld + dim;
   if ((heads < 2 || hs >= dim) && (tokens < 2 || ld >= across)) {
-    *m = {p, tokens, heads ? across * e : 0, ld * e};
+    *m = {p, tokens, heads ? across * e : 0, ld * e, dim * e, heads > 1 && hs > dim ? hs * e : 0};
     return true;
   }
-  *m = {p, heads, tokens ? along * e : 0, hs * e};
+  *m = {p, heads, tokens ? along * e : 0, hs * e, dim * e, tokens > 1 && ld > dim ? ld * e : 0};
   return (tokens < 2 || ld >= dim) && (heads < 2 || hs >= along);
 }
 
@@ -382,12 +394,12 @@ static bool batch_mat(const void* p, size_t rows, size_t cols, size_t ld, size_t
     return true;
   }
   if (stride >= span) {
-    *m = {p, batch, span * e, stride * e};
+    *m = {p, batch, span * e, stride * e, cols * e, rows > 1 && ld > cols ? ld * e : 0};
     return true;
   }
   const size_t across = (batch - 1) * stride + cols;
   const bool fits = stride >= cols && (rows < 2 || ld >= across);
-  *m = fits ? Mat{p, rows, across * e, ld * e} : vec(p, ((batch - 1) * stride + span) * e);
+  *m = fits ? Mat{p, rows, across * e, ld * e, cols * e, stride > cols ? stride * e : 0} : vec(p, ((batch - 1) * stride + span) * e);
   return fits;
 }
 

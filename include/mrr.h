@@ -580,7 +580,8 @@ mrr_status mrr_linear_xent_bwd(const void* hidden, const void* const* weights, c
  *            token t lies at t * ld_outs[k] + j * head_strides[k] + d (so token by token
  *            or head by head, in a buffer of its own or as columns of a wider one).
  * sum may be exactly one of the inputs, and each of outs exactly its heads' columns of one;
- * any other overlap of an output gives MRR_EOVERLAP.  Pointers are aligned to their
+ * any other overlap of an output gives MRR_EOVERLAP.  Outputs of the same strides may lie
+ * between each other (query, key and value of head 0, then of head 1).  Pointers are aligned to their
  * element (MRR_EALIGN).  The same call gives the same bits.  tokens == 0 launches nothing.
  * Errors: MRR_EUNSUPPORTED for another type or nranks outside [1, 32]; MRR_EINVAL for null
  * pointers, head_dim 0 or over 512, rot_dim odd or over head_dim, a head count over
