@@ -575,16 +575,19 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_k(QkArgs a) {
           }
       }
       const float rs = 1.0f / __builtin_sqrtf(head_sum<LPH>(ss) * inv + a.eps);
-      // (a lane without a head adds nothing: it has the last one's elements, which are counted)
-      const float c = head_sum<LPH>(sg) * inv * rs * rs, live = h.live ? rs : 0.0f;
+      const float c = head_sum<LPH>(sg) * inv * rs * rs;
       auto add = [&](float (&to)[K][E]) __attribute__((always_inline)) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-          for (int e = 0; e < E; ++e) to[k][e] = __builtin_fmaf(u[k][e], x[k][e] * live, to[k][e]);
+          for (int e = 0; e < E; ++e) to[k][e] = __builtin_fmaf(u[k][e], x[k][e] * rs, to[k][e]);
       };
-      if (h.kind == 0) add(dw[0]);
-      else add(dw[1]);
+      // (a lane without a head adds nothing, not even zero times the last head's elements, which
+      // it holds: they may be infinite)
+      if (h.live) {
+        if (h.kind == 0) add(dw[0]);
+        else add(dw[1]);
+      }
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
