@@ -564,7 +564,10 @@ mrr_status mrr_linear_xent_bwd(const void* hidden, const void* const* weights, c
  * heads of head_dim elements, side by side.  R rotates the first rot_dim elements of a head
  * by the token's angles and leaves the others: a pair (a, b) becomes (a cos - b sin, b cos +
  * a sin).  pairs 0: element i < rot_dim / 2 pairs with i + rot_dim / 2; pairs 1: 2 i with
- * 2 i + 1.  All in f32, rounded once (a head of elements over 1.8e19 has no norm in f32).
+ * 2 i + 1.  All in f32, rounded once.  So are the squares: a head whose squares sum to more than
+ * f32 holds (all elements over 1.8e19 / sqrt(head_dim)) becomes zeros, and its gradients with it;
+ * without eps one of elements below 1e-18 loses digits, and one whose squares vanish (below
+ * 1e-23) becomes infinite, zeros NaN.
  *
  * inputs:    host array of nranks (1..32) device pointers to rows of dtype (F32 | F16 |
  *            BF16), one a token, ld_in elements apart; they may overlap each other.
