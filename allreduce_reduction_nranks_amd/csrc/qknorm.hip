@@ -671,8 +671,17 @@ Shape shape_of(uint64_t tokens, uint32_t its) {
   return {(uint32_t)x, (its + chunk - 1) / chunk, chunk};
 }
 
-// Calls that move more than the 256 MiB of the Infinity Cache go past the caches.
+// Calls that move more than the 256 MiB of the Infinity Cache go past the caches (48 heads of 128
+// bf16, one rank: 384 MiB forward 72 us, 84 through them, backward 79 and 86; 192 MiB that the cache still
+// holds forward 38 us, 35 through it, backward 46 and 42; 2 and 8 ranks alike).
 constexpr uint64_t kCacheBytes = 256ull << 20;
+// Elements of a token that a call moves: `reads` times its heads, and those of what it has of
+// the queries, keys and values.
+uint64_t token_moves(const QkArgs& a, uint64_t reads) {
+  uint64_t heads = reads * (a.heads[0] + a.heads[1] + (uint64_t)(a.skip_values ? 0 : a.heads[2]));
+  for (int k = 0; k < 3; ++k) heads += a.out[k] && !(k == 2 && a.skip_values) ? a.heads[k] : 0;
+  return heads * a.dim;
+}
 constexpr uint64_t kMaxWaves = 1u << 24, kMaxBlocks = 4096;  // tokens past them are walked in strides
 
 // Lanes a head, units a lane and elements a vector.
@@ -741,7 +750,7 @@ template <class V, class L, class Go> void shaped(V, L, const QkArgs& a, bool st
 }
 
 template <int T> void fwd(const QkArgs& a, hipStream_t s) {
-  const uint64_t bytes = a.tokens * (a.ld_in < 65536 ? a.ld_in : 65536) * Ty<T>::size * (a.nranks + 1 + (a.sum ? 1 : 0));
+  const uint64_t bytes = a.tokens * token_moves(a, a.nranks + (a.sum ? 1 : 0)) * Ty<T>::size;
   auto go = [&](auto v, auto lph, auto k, auto pairs) {
     auto full = [&](auto f, auto nt) {
       if constexpr (nt) {
@@ -766,7 +775,9 @@ template <int T> void fwd(const QkArgs& a, hipStream_t s) {
 }
 
 template <int T> void bwd(const QkArgs& a, const Shape& g, hipStream_t s) {
-  const uint64_t bytes = a.tokens * (a.ld_in < 65536 ? a.ld_in : 65536) * Ty<T>::size * 3;
+  // (the sum, of the queries and keys alone, its gradient, and the outputs')
+  const uint64_t sums = (a.heads[0] + (uint64_t)a.heads[1]) * a.dim;
+  const uint64_t bytes = a.tokens * (sums + token_moves(a, a.dsum ? 1 : 0)) * Ty<T>::size;
   auto go = [&](auto v, auto lph, auto k, auto pairs) {
     auto full = [&](auto f, auto nt) {
       hipLaunchKernelGGL((qk_bwd_k<T, v, lph, k, pairs, f, nt>), dim3(g.x, g.y), dim3(kThreads), 0, s, a);
