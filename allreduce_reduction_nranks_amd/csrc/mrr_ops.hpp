@@ -203,7 +203,7 @@ struct NsArgs {
   uint8_t* b;            // B beside its diagonal
   float* d;              // A's diagonal
   float* beta;           // a + B's
-  float* part;           // sums of the products' splits
+  float* part;           // sums of A's splits
   uint32_t* counter;     // splits that are done, of each tile
   uint64_t x_plane, x_batch, o_batch;  // bytes from upper to lower parts, and of a matrix
   uint32_t batch;
@@ -246,7 +246,8 @@ struct NsCall {
   void* workspace;
 };
 
-// How a product is done: side of its tiles, stages in flight, parts of k, and the time expected.
+// How a product is done: side of its tiles, stages in flight, parts of k (of A = X X^T alone), and the
+// time expected.
 struct NsWay {
   uint32_t tile, stages, splits;
   double us;

@@ -316,7 +316,7 @@ template <int T, bool TWO, bool TURN> __global__ void __launch_bounds__(kFewThre
 }
 
 // ---- the products -------------------------------------------------------------------
-// Of a workgroup: its matrix, and one of `splits` parts of k.  An XCD gets whole matrices, or as
+// Of a workgroup: its matrix, its tile, and one of `splits` parts of k.  An XCD gets whole matrices, or as
 // much of one, where there are several: 4 matrices of 1024 x 4096 bf16 525 us, 561 with each of
 // them spread over all XCDs.
 struct Part {
@@ -423,17 +423,16 @@ template <int S, int NS, bool TWO> __device__ __forceinline__ bool gram_tile(con
 }
 
 // B = b A + c A^2, tile (r, c): what lies beside the diagonal to B, a + its diagonal to beta.
-template <int S, int NS, bool TWO> __device__ __forceinline__ void poly_tile(const NsArgs& a, uint32_t mat, uint32_t r, uint32_t c, uint32_t split,
-                                                                             uint32_t splits, lds8* lds) {
+template <int S, int NS, bool TWO> __device__ __forceinline__ void poly_tile(const NsArgs& a, uint32_t mat, uint32_t r, uint32_t c, lds8* lds) {
   typedef Tile<kF16, false, false, S, NS, TWO> Prod;
-  const uint32_t m0 = r * S, n0 = c * S, side = (a.mp + S - 1) / S;
+  const uint32_t m0 = r * S, n0 = c * S;
   const uint8_t* o = a.o + mat * a.o_batch;
   uint8_t* b = a.b + mat * a.o_batch;
   const float* d = a.d + mat * a.mp;
   float* beta = a.beta + mat * a.mp;
   Prod p;
-  square_tile<Prod, S>(p, o, (uint64_t)a.mp * (TWO ? 4 : 2), a.m_stages, a.mp, m0, n0, split, splits, lds);
-  if (!whole<S>(p, a, mat, r * (r + 1) / 2 + c, side * (side + 1) / 2, split, splits, lds)) return;
+  square_tile<Prod, S>(p, o, (uint64_t)a.mp * (TWO ? 4 : 2), a.m_stages, a.mp, m0, n0, 0, 1, lds);
+  __syncthreads();
   constexpr float unscale = 1.0f / (kScaleA * kScaleA);
   struct In {
     Raw8 o;
@@ -476,14 +475,14 @@ template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_thread
   gram_tile<S, NS, TWO>(a, p.mat, r, c, p.split, splits, (lds8*)lds);
 }
 
-template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_threads(S)) square_k(NsArgs a, uint32_t splits) {
+template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_threads(S)) square_k(NsArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[square_lds<S, NS, TWO>()];
   const uint32_t side = (a.mp + S - 1) / S;
   uint32_t r, c;
   Part p;
-  if (!part_of(a, side * (side + 1) / 2, splits, p)) return;
+  if (!part_of(a, side * (side + 1) / 2, 1, p)) return;
   lower_tile(p.tile, side, r, c);
-  poly_tile<S, NS, TWO>(a, p.mat, r, c, p.split, splits, (lds8*)lds);
+  poly_tile<S, NS, TWO>(a, p.mat, r, c, (lds8*)lds);
 }
 
 // Both, of matrices that are one tile high: the workgroup that has A goes on to B (what it has
@@ -495,7 +494,7 @@ template <int NS, bool TWO> __global__ void __launch_bounds__(tile_threads(64)) 
   if (!part_of(a, 1, splits, p) || !gram_tile<64, NS, TWO>(a, p.mat, 0, 0, p.split, splits, (lds8*)lds)) return;
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  poly_tile<64, NS, TWO>(a, p.mat, 0, 0, 0, 1, (lds8*)lds);
+  poly_tile<64, NS, TWO>(a, p.mat, 0, 0, (lds8*)lds);
 }
 
 // Results of the last step: X, or the weights' update by it, of 8 values of a row of the
@@ -520,22 +519,21 @@ __device__ __forceinline__ void put_result(const NsLast& z, uint32_t mat, uint32
 
 // X <- (a + diag B) X + off(B) X, in parts (LAST false) or as the result, TURN: transposed.
 template <int S, int NS, bool TWO, bool LAST, bool TURN>
-__global__ void __launch_bounds__(tile_threads(S)) apply_k(NsArgs a, NsLast z, uint32_t splits) {
+__global__ void __launch_bounds__(tile_threads(S)) apply_k(NsArgs a, NsLast z) {
   typedef Tile<kF16, true, false, S, NS, TWO> Prod;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Prod::kLds];
   uint32_t mt, nt;
   Part at;
-  if (!part_of(a, a.np / S * (a.mp / S), splits, at)) return;
+  if (!part_of(a, a.np / S * (a.mp / S), 1, at)) return;
   tile_at(at.tile, a.np / S, a.mp / S, mt, nt);
-  const uint32_t mat = at.mat, split = at.split;
+  const uint32_t mat = at.mat;
   const uint32_t j0 = mt * S, i0 = nt * S;  // column and row of X
   const uint8_t* x = a.x + mat * a.x_batch;
   const uint8_t* b = a.b + mat * a.o_batch;
   const float* beta = a.beta + mat * a.mp;
   const int tid = threadIdx.x;
   const uint32_t ldx = a.np * (TWO ? 4 : 2), ldb = a.mp * (TWO ? 4 : 2);
-  uint32_t k = a.m_stages * split / splits;
-  const uint32_t k1 = a.m_stages * (split + 1) / splits;
+  uint32_t k = 0;
   auto src = [&](int s, const uint8_t*& pa, const uint8_t*& pb, uint32_t (&oa)[Prod::L], uint32_t (&ob)[Prod::L]) {
     if (s == 0) {
 #pragma unroll
@@ -550,8 +548,8 @@ __global__ void __launch_bounds__(tile_threads(S)) apply_k(NsArgs a, NsLast z, u
     ++k;
   };
   Prod p;
-  p.run((int)(k1 - k), (lds8*)lds, src);
-  if (!whole<S>(p, a, mat, mt * (a.mp / S) + nt, (a.np / S) * (a.mp / S), split, splits, (lds8*)lds)) return;
+  p.run((int)a.m_stages, (lds8*)lds, src);
+  __syncthreads();
   struct In {
     Raw8 x;
     float beta;
@@ -597,7 +595,7 @@ template <bool SQUARE, class Go> void way(const NsWay& w, bool two, Go&& go) {
 }
 
 void step(const NsPlan& p, const NsArgs& a, const NsLast& z, uint32_t batch, bool last, bool turn, hipStream_t st) {
-  auto lower = [&](const NsWay& w) {
+  auto lower = [&](const NsWay& w) {  // (with its splits)
     const uint64_t side = (a.mp + w.tile - 1) / w.tile;
     return dim3((uint32_t)(side * (side + 1) / 2 * w.splits * batch));
   };
@@ -609,14 +607,14 @@ void step(const NsPlan& p, const NsArgs& a, const NsLast& z, uint32_t batch, boo
       hipLaunchKernelGGL((gram_k<s, ns, two>), lower(p.gram), dim3(tile_threads(s)), 0, st, a, p.gram.splits);
     });
     way<true>(p.square, p.parts == 2, [&](auto s, auto ns, auto two) {
-      hipLaunchKernelGGL((square_k<s, ns, two>), lower(p.square), dim3(tile_threads(s)), 0, st, a, p.square.splits);
+      hipLaunchKernelGGL((square_k<s, ns, two>), lower(p.square), dim3(tile_threads(s)), 0, st, a);
     });
   }
   way<false>(p.apply, p.parts == 2, [&](auto s, auto ns, auto two) {
-    const dim3 grid((a.mp / s) * (a.np / s) * p.apply.splits * batch), block(tile_threads(s));
-    if (!last) hipLaunchKernelGGL((apply_k<s, ns, two, false, false>), grid, block, 0, st, a, z, p.apply.splits);
-    else if (!turn) hipLaunchKernelGGL((apply_k<s, ns, two, true, false>), grid, block, 0, st, a, z, p.apply.splits);
-    else hipLaunchKernelGGL((apply_k<s, ns, two, true, true>), grid, block, 0, st, a, z, p.apply.splits);
+    const dim3 grid((a.mp / s) * (a.np / s) * batch), block(tile_threads(s));
+    if (!last) hipLaunchKernelGGL((apply_k<s, ns, two, false, false>), grid, block, 0, st, a, z);
+    else if (!turn) hipLaunchKernelGGL((apply_k<s, ns, two, true, false>), grid, block, 0, st, a, z);
+    else hipLaunchKernelGGL((apply_k<s, ns, two, true, true>), grid, block, 0, st, a, z);
   });
 }
 
@@ -719,9 +717,10 @@ bool ns_bounds(const float* co, int steps) {
 // CU holds, and what a workgroup's launch, first loads and end take.  520 x 1600 f32: 156 us
 // with tiles of 64, 408 with 128; 2048 x 2048 bf16 394 with 64, 365 with 128 and four stages in
 // flight, 429 with two; 4096 x 4096 bf16 1815 with 128, 1490 with 256, 1450 with 192 for the
-// symmetric products (the 136 tiles of 256 leave CUs idle, the 253 of 192 do not).  Splits of k: 8192 x 256 bf16
-// 194 us without, 125 with 8 in the gram product.
-template <class Tiles> static NsWay choose(uint32_t pad, bool two, bool square, uint64_t batch, uint32_t stages, Tiles&& tiles) {
+// symmetric products (the 136 tiles of 256 leave CUs idle, the 253 of 192 do not).  Splits of k, up to `most`,
+// for A = X X^T alone, whose k is the longer side: 8192 x 256 bf16 194 us without, 125 with 8.  (The others' k is the
+// shorter side: few tiles mean a short k there, and no shape of 400000 between 1 and 65536 a side had a use for them.)
+template <class Tiles> static NsWay choose(uint32_t pad, bool two, bool square, uint64_t batch, uint32_t stages, uint32_t most, Tiles&& tiles) {
   struct Kind {
     uint32_t tile, ns, per_cu;
     double alone, full, rest, join;  // microseconds
@@ -736,7 +735,7 @@ template <class Tiles> static NsWay choose(uint32_t pad, bool two, bool square, 
   for (int i = 0; i < (two ? 4 : 5); ++i) {
     const Kind& k = kinds[i];
     if (k.tile == 192 ? !square : k.tile > pad) continue;
-    for (uint32_t splits = 1; splits <= (k.tile >= 192 ? 1u : 8u) && splits <= stages; splits *= 2) {
+    for (uint32_t splits = 1; splits <= (k.tile >= 192 ? 1u : most) && splits <= stages; splits *= 2) {
       const uint64_t groups = tiles(k.tile) * batch * splits, slots = 256 * k.per_cu, rounds = groups / slots, rest = groups % slots;
       if (splits > 1 && groups > 512) break;
       const double per = (stages + splits - 1) / splits;
@@ -760,8 +759,8 @@ NsPlan ns_plan(uint64_t rows, uint64_t cols, uint64_t batch, int parts, bool wit
   for (uint32_t pad = 64; pad <= (two ? 128u : 256u); pad *= 2) {
     const uint32_t mp = up(m, pad), np = up(n, pad);
     auto lower = [&](uint32_t s) { return (uint64_t)((mp + s - 1) / s) * ((mp + s - 1) / s + 1) / 2; };
-    const NsWay g = choose(pad, two, true, batch, p.n_stages, lower), q = choose(pad, two, true, batch, p.m_stages, lower),
-                x = choose(pad, two, false, batch, p.m_stages, [&](uint32_t s) { return (uint64_t)(mp / s) * (np / s); });
+    const NsWay g = choose(pad, two, true, batch, p.n_stages, 8, lower), q = choose(pad, two, true, batch, p.m_stages, 1, lower),
+                x = choose(pad, two, false, batch, p.m_stages, 1, [&](uint32_t s) { return (uint64_t)(mp / s) * (np / s); });
     const double t = g.us + q.us + x.us;
     if (t < least) least = t, p.gram = g, p.square = q, p.apply = x, p.mp = mp, p.np = np;
   }
@@ -769,14 +768,11 @@ NsPlan ns_plan(uint64_t rows, uint64_t cols, uint64_t batch, int parts, bool wit
   p.o_plane = (uint64_t)p.mp * p.mp * 2;
   p.x_bytes = 2 * p.x_plane * batch;
   const uint64_t o_bytes = parts * p.o_plane * batch;
-  auto part_bytes = [&](const NsWay& w, uint64_t tiles) {
-    if (w.splits < 2) return (uint64_t)0;
-    if (tiles > p.counters) p.counters = (uint32_t)tiles;
-    return tiles * batch * w.splits * w.tile * w.tile * 4;
-  };
-  auto lower = [&](const NsWay& w) { return part_bytes(w, (uint64_t)(p.mp / w.tile) * (p.mp / w.tile + 1) / 2); };
-  uint64_t most = lower(p.gram);
-  for (uint64_t b : {lower(p.square), part_bytes(p.apply, (uint64_t)(p.mp / p.apply.tile) * (p.np / p.apply.tile))}) most = b > most ? b : most;
+  uint64_t part_bytes = 0;
+  if (p.gram.splits > 1) {
+    p.counters = p.mp / p.gram.tile * (p.mp / p.gram.tile + 1) / 2;
+    part_bytes = (uint64_t)p.counters * batch * p.gram.splits * p.gram.tile * p.gram.tile * 4;
+  }
   uint64_t at = 0;
   auto take = [&](uint64_t bytes) {
     const uint64_t here = at;
@@ -789,7 +785,7 @@ NsPlan ns_plan(uint64_t rows, uint64_t cols, uint64_t batch, int parts, bool wit
   p.d = take((uint64_t)p.mp * 4 * batch);
   p.beta = take((uint64_t)p.mp * 4 * batch);
   p.partial = take((uint64_t)kMaxParts * 8 * batch);
-  p.part = take(most);
+  p.part = take(part_bytes);
   p.counter = take((uint64_t)p.counters * 4 * batch);
   p.u = with_u ? take(rows * cols * 4 * batch) : 0;
   p.bytes = at;
