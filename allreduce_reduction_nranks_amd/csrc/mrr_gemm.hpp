@@ -11,11 +11,12 @@
 // global address, since the LDS side of the load is fixed) so that the lanes
 // that LDS serves together touch different banks.
 //
-// Two sizes of tile, S x S.  256: 8 waves, 2 a SIMD, each with 128 x 64 accumulators;
+// Tiles are S x S.  256: 8 waves, 2 a SIMD, each with 128 x 64 accumulators;
 // a stage's products take 2048 cycles of a CU's matrix units against 1536 of LDS reads.
-// 128: 4 waves with 64 x 64 each, two workgroups a CU; as many cycles of LDS reads as of
-// products, but four times the workgroups, for calls with too few large tiles.  Of row
-// operands alone also 192 (4 waves with 96 x 96) and 64 (4 waves, 32 x 32).  Matrix
+// 128: 4 waves with 64 x 64 each, two workgroups a CU with two stages in flight, one with
+// four; as many cycles of LDS reads as of products, but four times the workgroups, for calls
+// with too few large tiles.  64: 4 waves with 32 x 32 each, two workgroups a CU with four
+// stages.  Of row operands alone also 192: 4 waves with 96 x 96 each, one workgroup.  Matrix
 // instructions are 32x32x16.  The fragments of the
 // next 16 k are read while those of the present ones multiply, over the end of a
 // stage as well: the one barrier of a stage stands before its last quarter, when

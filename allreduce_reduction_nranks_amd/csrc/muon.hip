@@ -265,8 +265,8 @@ template <int T, bool TWO> __global__ void __launch_bounds__(kSumThreads) turn_k
   }
 }
 
-// Both passes over a matrix of few elements, by one workgroup: a launch less (50 x 50 f32: 51 us
-// a call, 54 with two; 64 x 768, no less, and 768 x 64 half as long again).  TURN: the transpose,
+// Both passes over a matrix of few elements, by one workgroup: a launch less (50 x 50 f32: 47 us
+// a call, 49 with two; 64 x 768 76, 74 with two, and 768 x 64 115 and 75).  TURN: the transpose,
 // read element by element.
 constexpr int kFewThreads = 1024;
 constexpr uint64_t kFewElements = 16384;
@@ -317,8 +317,8 @@ template <int T, bool TWO, bool TURN> __global__ void __launch_bounds__(kFewThre
 
 // ---- the products -------------------------------------------------------------------
 // Of a workgroup: its matrix, its tile, and one of `splits` parts of k.  An XCD gets whole matrices, or as
-// much of one, where there are several: 4 matrices of 1024 x 4096 bf16 525 us, 561 with each of
-// them spread over all XCDs.
+// much of one, where there are several: 4 matrices of 1024 x 4096 in 11 bits 525 us, 561 with
+// each of them spread over all XCDs.
 struct Part {
   uint32_t mat, split, tile;
 };
@@ -486,8 +486,8 @@ template <int S, int NS, bool TWO> __global__ void __launch_bounds__(tile_thread
 }
 
 // Both, of matrices that are one tile high: the workgroup that has A goes on to B (what it has
-// stored it reads back past a barrier).  12 matrices of 64 x 768 f32: 95 us with two
-// launches a step, 89 with one.
+// stored it reads back past a barrier).  12 matrices of 64 x 768 f32: 88 us with two
+// launches a step, 80 with one.
 template <int NS, bool TWO> __global__ void __launch_bounds__(tile_threads(64)) short_k(NsArgs a, uint32_t splits) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[square_lds<64, NS, TWO>()];
   Part p;
@@ -714,11 +714,12 @@ bool ns_bounds(const float* co, int steps) {
 // in `stages` stages.  The times were measured with 256 CUs: a stage of a workgroup that has
 // its CU to itself (64: what one CU draws from beyond its L2, 16 KiB in 0.25 us, bounds
 // it, and neither more stages in flight nor fewer waits for LDS change that), of all that a
-// CU holds, and what a workgroup's launch, first loads and end take.  520 x 1600 f32: 156 us
-// with tiles of 64, 408 with 128; 2048 x 2048 bf16 394 with 64, 365 with 128 and four stages in
-// flight, 429 with two; 4096 x 4096 bf16 1815 with 128, 1490 with 256, 1450 with 192 for the
-// symmetric products (the 136 tiles of 256 leave CUs idle, the 253 of 192 do not).  Splits of k, up to `most`,
-// for A = X X^T alone, whose k is the longer side: 8192 x 256 bf16 194 us without, 125 with 8.  (The others' k is the
+// CU holds, and what a workgroup's launch, first loads and end take.  520 x 1600 f32: 142 us
+// with tiles of 64, 293 with 128; 2048 x 2048 in two parts 769 with 64, 648 with 128 and four stages in
+// flight, 743 with two (in 11 bits 375, 342, 411); 4096 x 4096 in two parts 4092 with 128, 3656 with 192 for
+// the symmetric products, in 11 bits 1807 with 128, 1481 with 256, 1467 with 192 for the symmetric
+// ones (the 136 tiles of 256 leave CUs idle, the 253 of 192 do not).  Splits of k, up to `most`,
+// for A = X X^T alone, whose k is the longer side: 8192 x 256 in two parts 309 us without, 148 with 8.  (The others' k is the
 // shorter side: few tiles mean a short k there, and no shape of 400000 between 1 and 65536 a side had a use for them.)
 template <class Tiles> static NsWay choose(uint32_t pad, bool two, bool square, uint64_t batch, uint32_t stages, uint32_t most, Tiles&& tiles) {
   struct Kind {

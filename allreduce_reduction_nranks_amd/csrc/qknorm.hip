@@ -299,10 +299,10 @@ __device__ __forceinline__ void finish(const QkArgs& a, const Walk& w, const Hea
 // One iteration a wave, which is a workgroup: the dispatcher hands them out in order, so that HBM
 // sees a narrow window that moves along, and all that a wave reads is asked for at once,
 // but for the angles, whose place the position gives.  For several ranks (8 ranks of 4096 tokens of
-// 48 heads of 128 bf16 78 us, 125 where waves walk over tokens), and for few tokens.  G ranks' loads in
-// flight: 8, 4 of up to 4, 2 of 2, as fewer registers leave room for more waves (2047 tokens of
-// 9 heads of 80 f16, 4 ranks, 9.7 us with 4 and 11.7 with 8; 4096 tokens of 48 heads of 128 bf16,
-// 2 ranks, 27 us with 2, 28 with 4, 34 with 8).  K units a lane (1 but for heads without vectors).
+// 48 heads of 128 bf16 and their sum 85 us, 112 where waves walk over tokens), and for few tokens.  G
+// ranks' loads in flight: 8, 4 of up to 4, 2 of 2, as fewer registers leave room for more waves (2047
+// tokens of 9 heads of 80 f16, 4 ranks, 9.9 us with 4 and 11.1 with 8; 4096 tokens of 48 heads of 128
+// bf16, 2 ranks and their sum, 32 us with 2 or 4, 37 with 8).  K units a lane (1 but for heads without vectors).
 constexpr int kAtOnce = 8;
 
 // A lane's 2 V weights as they lie in memory, and widened.  No branch chooses between f32 and
@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(64) qk_fwd_k(QkArgs a) {
 
 // Many tokens of one rank: a wave takes all heads of a token in turn, its units, addresses and
 // angles worked out once, and asks for the next iteration's elements before it works on the
-// present one's.  16384 tokens of 48 heads of 128 bf16: 71 us, 5.7 TB/s; the above 85.
+// present one's.  16384 tokens of 48 heads of 128 bf16: 72 us, 5.6 TB/s; the above
+// 84 (96 elements a head 82 and 86; where half of 128 rotate 92 and 87; 8192 tokens f32 77 and 71).
 template <int T, int V, int LPH, bool PAIRS, bool FULL>
 __global__ void __launch_bounds__(kThreads, 4) qk_walk_k(QkArgs a) {
   __shared__ float weights[2 * kMaxDim];
@@ -655,7 +656,8 @@ template <int T> __global__ void __launch_bounds__(kJoinCols * kJoinChains) qk_j
 // ---- launches -------------------------------------------------------------------------------
 // A backward's grid: as many workgroups as the card holds at once (3 a CU, of which
 // every wave then has as many tokens as the others: 16384 tokens of 48 heads of 128 bf16
-// 111 us, 132 with 1024), few tokens' heads dealt out over more of them.
+// 111 us, 128 with 1024 and 143 with 256; heads of 80 that rotate 32 in pairs 101, 115 and 166; 12 heads of
+// 512 f32 204, 210 and 264), few tokens' heads dealt out over more of them.
 struct Shape {
   uint32_t x, y, chunk;
 };

@@ -132,10 +132,11 @@ def test_gradient(t, heads, dim, rot, pairs, lanes):
 
 
 def check_large_backward(douts, h, weights, table, positions, dsum, dws, heads, dim, rot, pairs, t):
-    """check_backward, whose 256 steps of a weight's sum are for up to 128 terms of a lane: here up to `tokens` / 3072 tokens, each of
-    heads / (64 / lanes) iterations at most, follow each other in a lane.  Its tolerance holds for as many more."""
+    """check_backward, whose 256 steps of a weight's sum are for up to 128 terms of a lane: here as many of the tokens as fall to one
+    of 768 * 4 waves, each of heads / (64 / lanes) iterations at most, follow each other in a lane.  Its tolerance holds for
+    as many more."""
     import test_gpu_qknorm as q
-    terms = (len(h) / 3072 + 1) * (max(heads) + 1)
+    terms = (len(h) / (768 * 4) + 1) * (max(heads) + 1)
     want, tol, dw, tdw = q.backward_tolerances(douts, h, weights, table, positions, heads, dim, rot, pairs, t)
     q.close(dsum, want, tol, "dsum")
     for k in range(2):
