@@ -12,11 +12,11 @@
 //
 // Precision.  X is held in two f16 parts (22 bits), scaled so that neither loses bits: it is
 // what passes from step to step, and a small singular value, which grows a-fold a step, must
-// not carry the rounding of the large ones.  O and B have two parts as well (PL 2) and a product
+// not carry the rounding of the large ones.  O and B have two parts as well (TWO) and a product
 // is three of the parts', which leaves 2^-22 of each term.  The diagonals of A and B, which are
 // far larger than what lies beside them, stay in f32 and out of the products:  with A = D + O,
 //   A^2 = O O + D O + O D + D^2,   a X + B X = (a + diag B) X + off(B) X.
-// Callers that ask for F16 get products of the upper parts alone (PL 1), 11 bits: they reach X
+// Callers that ask for F16 get products of the upper parts alone (TWO false), 11 bits: they reach X
 // only as a correction B X beside a X, which is added in f32 from both parts.  Such results are off
 // by some 1e-3 of their norm for noise (1.5e-2 with X in one part and diagonals in f16), but rows
 // that repeat round alike and their errors add: 3e-3 for two equal ones, up to 3e-2 for blocks of

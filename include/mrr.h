@@ -647,9 +647,9 @@ mrr_status mrr_qknorm_rope_bwd(const void* const* douts, const void* sum, const 
  *          every step, which bring singular values from 0.01 of the norm up to within 0.68
  *          and 1.14 in 5 steps.
  * products: precision of the products.  F32 (AUTO): operands in two f16 parts (22 bits),
- *          three products of them for each: results as exact as f32 products give (off by
- *          1e-6 of their norm for noise, by up to 6e-5 where one direction stands alone, in 5
- *          steps).  F16, where speed counts for more: operands of 11 bits, diagonals and what
+ *          three products of them for each: results as exact as f32 products give (5 steps:
+ *          off by 1e-6 to 3e-6 of their norm for noise, and where one direction stands alone by
+ *          5e-5 for 65 a side, 3e-4 for 4096).  F16, where speed counts for more: operands of 11 bits, diagonals and what
  *          a step adds to in f32 beside them.  Its results are off by some 1e-3 of their norm
  *          for noise; equal rows round alike and their errors add, up to 3e-2 for blocks of
  *          equal values (bf16 itself rounds by 1.7e-3).  Matrices with a side of 64 or

@@ -14,7 +14,7 @@ import torch
 
 import allreduce_reduction_nranks_amd as mrr
 from gpu_common import announce
-from test_gpu_muon import TYPES, exact, muon, orth, seeded
+from test_gpu_muon import CO, TYPES, exact, muon, orth, seeded
 
 pytestmark = pytest.mark.gpu
 
@@ -89,6 +89,22 @@ def test_products_of_11_bits_are_off_by_what_the_header_says(kind, m, n, t):
     print("off by %.2e" % off, flush=True)
     half = torch.finfo(TYPES[t]).eps / 2
     assert off <= (1.3e-3 if kind == "noise" else 4e-2) + half
+
+
+@pytest.mark.parametrize("kind", ["noise", "ones", "one direction", "four rows", "4 blocks"])
+@pytest.mark.parametrize("m,n", [(1024, 4096), (4096, 4096)])
+def test_large_matrices_beside_f32_products(kind, m, n):
+    """Roundings in directions of no size are more in larger matrices, of f32 products as well: torch's are added to LIMIT."""
+    announce("orth structured large", kind, m, n)
+    x = matrix(kind, m, n)
+    out, want = torch.empty_like(x), exact(x)
+    mrr.check(orth(x, out, m, n, 1, "f32"))
+    y = x / (x.norm() + 1e-7)
+    for _ in range(5):
+        a = y @ y.T.contiguous()
+        y = CO[0] * y + (CO[1] * a + CO[2] * (a @ a)) @ y
+    off, plain = (float((v - want).norm() / want.norm()) for v in (out, y))
+    assert off <= LIMIT + plain, (off, plain)
 
 
 def test_what_the_default_coefficients_make_of_singular_values():
